@@ -48,8 +48,9 @@
 extern "C" {
 #endif
 
-/* Element types. VIT_F64 runs on the CUDA-core path only. */
-typedef enum { VIT_F32 = 0, VIT_BF16 = 1, VIT_F64 = 2 } vit_dtype;
+/* Element types. VIT_F64 runs on the CUDA-core path only. VIT_E4M3 (8-bit floating point,
+ * 4 exponent and 3 mantissa bits, largest value 448) is taken by the 8-bit stages alone. */
+typedef enum { VIT_F32 = 0, VIT_BF16 = 1, VIT_F64 = 2, VIT_E4M3 = 3 } vit_dtype;
 
 /* Status codes. */
 typedef enum {
@@ -392,6 +393,96 @@ int vit_linear(const void* a, const void* w, const void* bias, const void* resid
  */
 int vit_attention(const void* qkv, int64_t N, int64_t T, int64_t D, int64_t H, int dtype,
                   void* o, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * Serving stages: what a text decoder needs next to the encoder whose states it reads --
+ * the root-mean-square norm, products in 8 bits and cross attention. Forward only, like the
+ * rest of the library.
+ *
+ * 8-bit values: a block of 128 numbers y is held as e4m3 codes q and one fp32 scale,
+ *   scale = max(max|y| / 448, 2^-126),  q = e4m3(y / scale)  (nearest even),
+ * and stands for q * scale. Of activations (rows, K) a block is 128 columns of one row: scales
+ * (rows, ceil(K / 128)). Of weights it is 128 x 128: scales (ceil(N / 128), ceil(K / 128)). The
+ * last blocks of a row or column may be shorter. A NaN keeps its code; a block that holds an
+ * infinity has an infinite scale, and its values read back as NaN.
+ * ------------------------------------------------------------------------------ */
+
+/*
+ * vit_rmsnorm -- root-mean-square norm with the residual's addition, row by row:
+ *   s = x + residual,   out = s / sqrt(mean(s^2) + eps) * gamma,   sum = s
+ *   x         (rows, D) of x_dtype: BF16, F32 or F64
+ *   residual  (rows, D) of residual_dtype, nullable (then 0): x_dtype, or F32 with a BF16 x
+ *             (a residual stream kept in 32 bits)
+ *   gamma     (D) of gamma_dtype BF16 or F32 (F64 for F64), nullable (then 1)
+ *   sum       (rows, D) of residual_dtype, nullable; only with a residual. It may be the
+ *             residual itself (updated in place) or x itself where the types agree.
+ *   out       (rows, D) of out_dtype: BF16, F32 or E4M3 (F64 for F64); must not overlap an
+ *             input or sum
+ *   scales    (rows, ceil(D / 128)) fp32 with E4M3, else NULL
+ * s is formed and normalised in fp32 (fp64 for F64); out comes from s before it is rounded to
+ * sum. Any finite row of that type is normalised; squares below the fp32 range count as 0, so
+ * eps should be positive.
+ * Errors: VIT_ERR_ARG, VIT_ERR_DTYPE, VIT_ERR_CUDA.
+ */
+int vit_rmsnorm(const void* x, int x_dtype, const void* residual, int residual_dtype, int64_t rows,
+                int64_t D, double eps, const void* gamma, int gamma_dtype, void* sum, void* out,
+                int out_dtype, float* scales, void* stream);
+
+/*
+ * vit_quantize -- x (rows, K) of dtype BF16 or F32 -> q (rows, K) e4m3 and scales
+ * (rows, ceil(K / 128)). q and scales must not overlap x or each other.
+ * Errors: VIT_ERR_ARG, VIT_ERR_DTYPE, VIT_ERR_CUDA.
+ */
+int vit_quantize(const void* x, int dtype, int64_t rows, int64_t K, void* q, float* scales,
+                 void* stream);
+
+/*
+ * vit_quantize_weight -- a weight w (K, N), stored (in, out) like every weight of the library,
+ * of dtype BF16 or F32 -> q (N, K) e4m3, its transpose, and scales
+ * (ceil(N / 128), ceil(K / 128)): what vit_linear_fp8 takes. Made once per weight.
+ * Errors as vit_quantize.
+ */
+int vit_quantize_weight(const void* w, int dtype, int64_t K, int64_t N, void* q, float* scales,
+                        void* stream);
+
+/*
+ * vit_linear_fp8 -- out (M, N) = epilogue(z [+ bias]), z the product of 8-bit activations and
+ * weights:  z[m, n] = sum_b a_scales[m, b] w_scales[n / 128, b] sum_{k in b} a[m, k] w[n, k]
+ *   a, a_scales  (M, K) and (M, ceil(K / 128)), as vit_quantize or vit_rmsnorm leave them
+ *   w, w_scales  (N, K) and (ceil(N / 128), ceil(K / 128)), as vit_quantize_weight leaves them
+ *   bias         (N) of bias_dtype BF16 or F32, nullable
+ *   epilogue     a vit_epilogue; residual (M, N) of residual_dtype BF16 or F32 with
+ *                VIT_EPI_RESIDUAL, else NULL; it may be out itself where the types agree
+ *   out          (M, N) of out_dtype BF16, F32 or E4M3; out_scales (M, ceil(N / 128)) fp32 with
+ *                E4M3 (the next product's input), else NULL
+ * Sums are fp32. Tensor cores when K % 16 == 0 and a and w are 16-byte aligned, CUDA cores
+ * otherwise. Any M and N.
+ * Errors: VIT_ERR_ARG, VIT_ERR_DTYPE, VIT_ERR_CUDA.
+ */
+int vit_linear_fp8(const void* a, const float* a_scales, const void* w, const float* w_scales,
+                   const void* bias, int bias_dtype, const void* residual, int residual_dtype,
+                   int64_t M, int64_t K, int64_t N, int epilogue, void* out, int out_dtype,
+                   float* out_scales, void* stream);
+
+/*
+ * vit_cross_attention -- attention of queries to the states of another sequence:
+ *   o[b, t, h] = sum_{u < len_b} softmax_u(scale q[b, t, h] . k[b, u, h / G]) v[b, u, h / G]
+ *   q         (B, Tq, H, dh); k, v (B, Tk, Hkv, dh); o (B, Tq, H, dh), all of dtype (BF16, F32
+ *             or F64). H % Hkv == 0; G = H / Hkv query heads share one key head.
+ *   *_strides host arrays of three element strides (sequence, token, head), all >= 0; NULL:
+ *             contiguous. The dh elements of a head are contiguous. o is contiguous. K and V may
+ *             be views of one (B, Tk, 2, Hkv, dh) projection; o must not overlap what they span.
+ *   kv_lens   (B) device array, nullable (then Tk): sequence b sees its first kv_lens[b] keys,
+ *             clamped to [0, Tk]. With none its outputs are zero. Keys past the length may hold
+ *             anything, NaN included.
+ *   scale     any finite number; 1 / sqrt(dh) is usual
+ * Softmax in fp32 (fp64 for F64). dh up to 512.
+ * Errors: VIT_ERR_ARG, VIT_ERR_DTYPE, VIT_ERR_UNSUPPORTED (dh), VIT_ERR_NOMEM, VIT_ERR_CUDA.
+ */
+int vit_cross_attention(const void* q, const int64_t* q_strides, const void* k,
+                        const int64_t* k_strides, const void* v, const int64_t* v_strides,
+                        const int32_t* kv_lens, int64_t B, int64_t Tq, int64_t Tk, int64_t H,
+                        int64_t Hkv, int64_t dh, double scale, int dtype, void* o, void* stream);
 
 /* ------------------------------------------------------------------------------
  * Status, diagnostics and measurement

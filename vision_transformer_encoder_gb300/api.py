@@ -16,10 +16,13 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libvit_block.so")
 
-VIT_F32, VIT_BF16, VIT_F64 = 0, 1, 2
+VIT_F32, VIT_BF16, VIT_F64, VIT_E4M3 = 0, 1, 2, 3
 EPI_STORE, EPI_GELU, EPI_RESIDUAL = 0, 1, 2
 
 _DT = {torch.float32: VIT_F32, torch.bfloat16: VIT_BF16, torch.float64: VIT_F64}
+_F8 = torch.float8_e4m3fn
+_DT8 = dict(_DT)   # the types of the 8-bit stages' outputs
+_DT8[_F8] = VIT_E4M3
 
 LAYER_FIELDS = ("w_q", "w_k", "w_v", "w_o", "w_mlp1", "w_mlp2", "ln1_g", "ln1_b", "ln2_g", "ln2_b",
                 "b1", "b2", "b_q", "b_k", "b_v", "b_o")
@@ -54,6 +57,11 @@ SIGNATURES = {
     "vit_block_w": (_int, [_vp, _vp, _i64, _i64, _dbl, _vp, _vp]),
     "vit_block_w_host": (_int, [_vp, _vp, _i64, _i64, _dbl, _vp, _vp]),
     "vit_block_w_host_async": (_int, [_vp, _vp, _i64, _i64, _dbl, _vp, _vp]),
+    "vit_rmsnorm": (_int, [_vp, _int, _vp, _int, _i64, _i64, _dbl, _vp, _int, _vp, _vp, _int, _vp, _vp]),
+    "vit_quantize": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _vp]),
+    "vit_quantize_weight": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _vp]),
+    "vit_linear_fp8": (_int, [_vp] * 5 + [_int, _vp, _int] + [_i64] * 3 + [_int, _vp, _int, _vp, _vp]),
+    "vit_cross_attention": (_int, [_vp] * 7 + [_i64] * 6 + [_dbl, _int, _vp, _vp]),
     "vit_status_string": (ctypes.c_char_p, [_int]),
     "vit_device_error": (_int, [ctypes.POINTER(ctypes.c_uint32)]),
     "vit_launch_count": (_i64, []),
@@ -435,6 +443,250 @@ def attention(qkv, H, out=None, stream=None):
         rc = lib.vit_attention(_ptr(qkv), N, T, D, int(H), _dtype_code(qkv.dtype), _ptr(out),
                                _stream(stream))
     _check(rc, "vit_attention")
+    return out
+
+
+# ---- serving stages: rms norm, 8-bit products, cross attention -------------------------
+# These are called once per layer and token, so their marshalling is kept short: raw pointers
+# as integers, the device switched only when it is not current, one stream look-up.
+
+def _need(t, name, device, dtype, shape):
+    """t is a contiguous CUDA tensor on device, of dtype (None: any) and shape."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError("%s must be a CUDA tensor on %s" % (name, device))
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _operand(t, name, device=None):
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if device is not None and t.device != device:
+        raise ValueError("%s must be a CUDA tensor on %s" % (name, device))
+    return t.device
+
+
+def _code(dt, allowed, what):
+    if dt not in allowed:
+        raise ValueError("%s: unsupported dtype %s" % (what, dt))
+    return allowed[dt]
+
+
+def _alloc(shape, dtype, device, stream):
+    """An output of a call on `stream`, from that stream's memory."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_torch_stream(stream, device)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _torch_stream(stream, device):
+    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
+
+
+def _invoke(what, fn, device, stream, tensors, args):
+    """fn(*args, stream) with `device` current; raises on a non-zero status. With an explicit
+    stream the tensors are kept from reuse until the work queued there is done."""
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
+    else:
+        ts = _torch_stream(stream, device)
+        handle = ts.cuda_stream
+        for t in tensors:
+            if t is not None:
+                t.record_stream(ts)
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, handle)
+    if rc != 0:
+        raise VitError(rc, what)
+
+
+def _scale_shape(rows, cols):
+    return (rows, (cols + 127) // 128)
+
+
+def rmsnorm(x, eps, gamma=None, residual=None, out_dtype=None, out=None, scales=None, sum_out=None, stream=None):
+    """Root-mean-square norm of the last dimension of x (..., D) with the residual's addition:
+    s = x + residual, out = s / sqrt(mean(s^2) + eps) * gamma.
+
+    residual: shaped like x, of x's dtype, or fp32 with a bf16 x. gamma: (D), bf16 or fp32 (fp64
+    with fp64). out_dtype: x's dtype by default, bf16, fp32 or float8_e4m3fn, the last with fp32
+    scales (rows, ceil(D / 128)) of 128-column blocks. sum_out: where s goes, of the residual's
+    dtype (may be the residual or x itself); a new tensor when not given.
+    Returns out; (out, scales) in 8 bits; with a residual, also the sum as the last element."""
+    lib = _lib or load_library()
+    device = _operand(x, "x")
+    shape, xd = x.shape, x.dtype
+    if not shape or not x.numel():
+        raise ValueError("x must have at least one element and a last dimension")
+    D = shape[-1]
+    rows = x.numel() // D
+    xp = _need(x, "x", device, None, shape)
+    xc = _code(xd, _DT, "x")
+    od = out_dtype if out_dtype is not None else (out.dtype if out is not None else xd)
+    oc = _code(od, _DT8, "out")
+    gp, gc, rp, rc_, sp, cp = None, xc, None, xc, None, None
+    if gamma is not None:
+        gp, gc = _need(gamma, "gamma", device, None, (D,)), _code(gamma.dtype, _DT, "gamma")
+    if residual is not None:
+        rp, rc_ = _need(residual, "residual", device, None, shape), _code(residual.dtype, _DT, "residual")
+        if sum_out is None:
+            sum_out = _alloc(shape, residual.dtype, device, stream)
+        sp = _need(sum_out, "sum_out", device, residual.dtype, shape)
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual")
+    if out is None:
+        out = _alloc(shape, od, device, stream)
+    op = _need(out, "out", device, od, shape)
+    if oc == VIT_E4M3:
+        if scales is None:
+            scales = _alloc(_scale_shape(rows, D), torch.float32, device, stream)
+        cp = _need(scales, "scales", device, torch.float32, _scale_shape(rows, D))
+    elif scales is not None:
+        raise ValueError("scales belong to a float8_e4m3fn output")
+    _invoke("vit_rmsnorm", lib.vit_rmsnorm, device, stream, (x, residual, gamma, sum_out, out, scales),
+            (xp, xc, rp, rc_, rows, D, eps, gp, gc, sp, op, oc, cp))
+    if oc == VIT_E4M3:
+        return (out, scales) if residual is None else (out, scales, sum_out)
+    return out if residual is None else (out, sum_out)
+
+
+def quantize(x, out=None, scales=None, stream=None):
+    """x (..., K), bf16 or fp32, in 8 bits: (q (..., K) float8_e4m3fn, scales (rows, ceil(K / 128))
+    fp32), one scale for each 128 columns of a row; a value is q * scale."""
+    lib = _lib or load_library()
+    device = _operand(x, "x")
+    shape = x.shape
+    if not shape or not x.numel():
+        raise ValueError("x must have at least one element and a last dimension")
+    K = shape[-1]
+    rows = x.numel() // K
+    xp = _need(x, "x", device, None, shape)
+    xc = _code(x.dtype, _DT, "x")
+    if out is None:
+        out = _alloc(shape, _F8, device, stream)
+    if scales is None:
+        scales = _alloc(_scale_shape(rows, K), torch.float32, device, stream)
+    qp, sp = _need(out, "out", device, _F8, shape), _need(scales, "scales", device, torch.float32, _scale_shape(rows, K))
+    _invoke("vit_quantize", lib.vit_quantize, device, stream, (x, out, scales), (xp, xc, rows, K, qp, sp))
+    return out, scales
+
+
+def quantize_weight(w, out=None, scales=None, stream=None):
+    """A weight w (K, N), bf16 or fp32, as linear_fp8 takes it: (q (N, K) float8_e4m3fn, the
+    transpose, scales (ceil(N / 128), ceil(K / 128)) fp32), one scale for each 128 x 128 block."""
+    lib = _lib or load_library()
+    device = _operand(w, "w")
+    if w.dim() != 2 or not w.numel():
+        raise ValueError("w must be a matrix (K, N) with at least one element")
+    K, N = w.shape
+    wp = _need(w, "w", device, None, w.shape)
+    wc = _code(w.dtype, _DT, "w")
+    blocks = ((N + 127) // 128, (K + 127) // 128)
+    if out is None:
+        out = _alloc((N, K), _F8, device, stream)
+    if scales is None:
+        scales = _alloc(blocks, torch.float32, device, stream)
+    qp, sp = _need(out, "out", device, _F8, (N, K)), _need(scales, "scales", device, torch.float32, blocks)
+    _invoke("vit_quantize_weight", lib.vit_quantize_weight, device, stream, (w, out, scales), (wp, wc, K, N, qp, sp))
+    return out, scales
+
+
+def linear_fp8(a, a_scales, w, w_scales, bias=None, residual=None, epilogue=EPI_STORE, out_dtype=None, out=None,
+               out_scales=None, stream=None):
+    """epilogue(a @ w.T [+ bias]) of 8-bit activations a (..., K) with scales (rows, ceil(K / 128)),
+    as rmsnorm and quantize leave them, and a weight w (N, K) with scales
+    (ceil(N / 128), ceil(K / 128)), as quantize_weight leaves it.
+
+    bias (N) and residual (..., N): bf16 or fp32; the residual goes with EPI_RESIDUAL alone.
+    out_dtype: bf16 (default), fp32 or float8_e4m3fn. Returns out, or (out, out_scales) in 8 bits,
+    out_scales (rows, ceil(N / 128)). out may be the residual itself where the types agree."""
+    lib = _lib or load_library()
+    device = _operand(a, "a")
+    shape = a.shape
+    if not shape or not a.numel() or w.dim() != 2 or not w.numel():
+        raise ValueError("a must be (..., K) and w (N, K), with at least one element")
+    N, K = w.shape
+    if shape[-1] != K:
+        raise ValueError("a has %d columns, w %d" % (shape[-1], K))
+    M = a.numel() // K
+    kb, nb = (K + 127) // 128, (N + 127) // 128
+    oshape = shape[:-1] + (N,)
+    ap, wp = _need(a, "a", device, _F8, shape), _need(w, "w", device, _F8, w.shape)
+    asp = _need(a_scales, "a_scales", device, torch.float32, (M, kb))
+    wsp = _need(w_scales, "w_scales", device, torch.float32, (nb, kb))
+    bp, bc, rp, rc_, osp = None, 0, None, 0, None
+    if bias is not None:
+        bp, bc = _need(bias, "bias", device, None, (N,)), _code(bias.dtype, _DT, "bias")
+    if residual is not None:
+        rp, rc_ = _need(residual, "residual", device, None, oshape), _code(residual.dtype, _DT, "residual")
+    od = out_dtype if out_dtype is not None else (out.dtype if out is not None else torch.bfloat16)
+    oc = _code(od, _DT8, "out")
+    if out is None:
+        out = _alloc(oshape, od, device, stream)
+    op = _need(out, "out", device, od, oshape)
+    if oc == VIT_E4M3:
+        if out_scales is None:
+            out_scales = _alloc((M, nb), torch.float32, device, stream)
+        osp = _need(out_scales, "out_scales", device, torch.float32, (M, nb))
+    elif out_scales is not None:
+        raise ValueError("out_scales belong to a float8_e4m3fn output")
+    _invoke("vit_linear_fp8", lib.vit_linear_fp8, device, stream,
+            (a, a_scales, w, w_scales, bias, residual, out, out_scales),
+            (ap, asp, wp, wsp, bp, bc, rp, rc_, M, K, N, int(epilogue), op, oc, osp))
+    return (out, out_scales) if oc == VIT_E4M3 else out
+
+
+def _strided(t, name, device, dtype, own):
+    """Pointer and (sequence, token, head) strides of t (B, T, heads, dh); None when contiguous."""
+    if t.dim() != 4:
+        raise ValueError("%s must be (B, T, heads, dh)" % name)
+    _operand(t, name, device)
+    if t.dtype != dtype:
+        raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if t.is_contiguous():
+        return t.data_ptr(), None
+    st = t.stride()
+    if st[3] != 1 and own[3] != 1:
+        raise ValueError("%s: the elements of a head must be contiguous" % name)
+    return t.data_ptr(), (_i64 * 3)(st[0], st[1], st[2])
+
+
+def cross_attention(q, k, v, kv_lens=None, scale=None, out=None, stream=None):
+    """softmax(scale q k^T) v of queries q (B, Tq, H, dh) over the states of another sequence,
+    k and v (B, Tk, Hkv, dh); H / Hkv query heads share a key head. Returns (B, Tq, H, dh).
+
+    kv_lens: (B) int32 on the device, the keys that each sequence has (clamped to [0, Tk]; none:
+    zeros); all Tk when not given. scale: 1 / sqrt(dh) by default. q, k and v may be views with
+    any strides over sequences, tokens and heads, such as the halves of a fused key and value
+    projection; the elements of a head are contiguous."""
+    lib = _lib or load_library()
+    device = _operand(q, "q")
+    dt = q.dtype
+    if q.dim() != 4 or k.dim() != 4 or not q.numel() or not k.numel():
+        raise ValueError("q must be (B, Tq, H, dh) and k (B, Tk, Hkv, dh), with at least one element")
+    B, Tq, H, dh = q.shape
+    Tk, Hkv = k.shape[1], k.shape[2]
+    if k.shape != (B, Tk, Hkv, dh) or v.shape != k.shape:
+        raise ValueError("q %s, k %s and v %s do not fit" % (tuple(q.shape), tuple(k.shape), tuple(v.shape)))
+    code = _code(dt, _DT, "q")
+    qp, qs = _strided(q, "q", device, dt, q.shape)
+    kp, ks = _strided(k, "k", device, dt, k.shape)
+    vp, vs = _strided(v, "v", device, dt, v.shape)
+    lp = None if kv_lens is None else _need(kv_lens, "kv_lens", device, torch.int32, (B,))
+    if out is None:
+        out = _alloc((B, Tq, H, dh), dt, device, stream)
+    op = _need(out, "out", device, dt, (B, Tq, H, dh))
+    _invoke("vit_cross_attention", lib.vit_cross_attention, device, stream, (q, k, v, kv_lens, out),
+            (qp, qs, kp, ks, vp, vs, lp, B, Tq, Tk, H, Hkv, dh, dh ** -0.5 if scale is None else scale, code, op))
     return out
 
 

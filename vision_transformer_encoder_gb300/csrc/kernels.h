@@ -7,9 +7,9 @@
 namespace vit {
 
 // Element type tags (values match vit_dtype).
-enum Dt : int { DT_F32 = 0, DT_BF16 = 1, DT_F64 = 2 };
+enum Dt : int { DT_F32 = 0, DT_BF16 = 1, DT_F64 = 2, DT_E4M3 = 3 };
 
-inline size_t dt_size(int dt) { return dt == DT_F64 ? 8 : dt == DT_F32 ? 4 : 2; }
+inline size_t dt_size(int dt) { return dt == DT_F64 ? 8 : dt == DT_F32 ? 4 : dt == DT_E4M3 ? 1 : 2; }
 
 // Per-device facts the launchers need.
 struct DeviceInfo {
@@ -204,5 +204,54 @@ cudaError_t launch_attention_cls(const void* q, int64_t ldq, const void* k, cons
 // Any dtype (f32/bf16/f64 in and out, same type), any head width.
 cudaError_t launch_attention_simt(const void* qkv, int dt, void* o, int64_t N, int64_t T,
                                   int64_t D, int64_t H, cudaStream_t s);
+
+// ---- Root-mean-square norm (rmsnorm.cu) ----------------------------------------
+// s = x + residual, out = s / sqrt(mean(s^2) + eps) * gamma, sum = s. x, residual, gamma and
+// sum in their stated types (sum has residual_dt); out_dt DT_E4M3 writes scales too.
+struct RmsNormDesc {
+    const void* x; int x_dt;
+    const void* residual; int residual_dt;   // nullable
+    const void* gamma; int gamma_dt;         // nullable
+    void* sum;                               // nullable; may be x or residual itself
+    void* out; int out_dt;
+    float* scales;                           // (rows, ceil(D / 128)), out_dt DT_E4M3 only
+    int64_t rows, D;
+    double eps;
+};
+cudaError_t launch_rmsnorm(const RmsNormDesc& d, const DeviceInfo& dev, cudaStream_t s);
+
+// ---- 8-bit quantisation (quantize.cu) ------------------------------------------
+cudaError_t launch_quantize_rows(const void* x, int dt, int64_t rows, int64_t K, void* q, float* scales,
+                                 const DeviceInfo& dev, cudaStream_t s);
+cudaError_t launch_quantize_weight(const void* w, int dt, int64_t K, int64_t N, void* q, float* scales,
+                                   const DeviceInfo& dev, cudaStream_t s);
+
+// ---- 8-bit matrix product (gemm_fp8.cu) ----------------------------------------
+struct Fp8GemmDesc {
+    const uint8_t* a; const float* a_scales;   // (M, K) e4m3, (M, ceil(K / 128))
+    const uint8_t* w; const float* w_scales;   // (N, K) e4m3, (ceil(N / 128), ceil(K / 128))
+    const void* bias; bool bias_f32;           // (N), nullable
+    const void* residual; bool residual_f32;   // (M, N), TC_EPI_RESID only; may be out itself
+    int64_t M, K, N;
+    int epi;                                   // TcEpi
+    void* out; int out_dt;                     // DT_BF16, DT_F32 or DT_E4M3
+    float* out_scales;                         // (M, ceil(N / 128)), DT_E4M3 only
+};
+cudaError_t launch_gemm_fp8(const Fp8GemmDesc& d, const DeviceInfo& dev, cudaStream_t s);
+
+// ---- Cross attention (attention_cross.cu) --------------------------------------
+// Strides in elements: [0] sequence, [1] token, [2] head. o (B, Tq, H, dh) is contiguous.
+struct CrossDesc {
+    const void* q; int64_t qs[3];
+    const void* k; int64_t ks[3];
+    const void* v; int64_t vs[3];
+    const int32_t* kv_lens;                    // (B), nullable
+    int64_t B, Tq, Tk, H, Hkv, dh;
+    double scale;
+    int dt;
+    void* o;
+};
+constexpr int64_t kCrossMaxHead = 512;
+cudaError_t launch_cross_attention(const CrossDesc& d, const DeviceInfo& dev, cudaStream_t s);
 
 }  // namespace vit

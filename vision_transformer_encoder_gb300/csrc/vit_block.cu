@@ -152,6 +152,36 @@ bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
     return x < y + nb && y < x + na;
 }
 
+// Element counts are kept below this, so that no byte count or offset overflows.
+constexpr int64_t kMaxElements = (int64_t)1 << 46;
+
+// A null pointer, or one aligned to its elements.
+bool aligned_to(const void* p, int dt) { return reinterpret_cast<uintptr_t>(p) % dt_size(dt) == 0; }
+
+// Runs launch(device info, stream) for a single-stage call on the current device, counts it
+// and turns its outcome into a status; with VIT_DEBUG_SYNC=1 it waits for the stream and
+// reports what the device saw.
+template <class F>
+int enqueue(void* stream, F&& launch) {
+    DeviceState* st = nullptr;
+    const int rc = current_device(&st);
+    if (rc != VIT_OK) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = launch(st->info, s);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return status_from(e);
+    }
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    if (debug_sync()) {
+        if (cudaStreamSynchronize(s) != cudaSuccess) return VIT_ERR_CUDA;
+        uint32_t word = 0;
+        if (cudaMemcpyFromSymbol(&word, g_err_word, sizeof(word)) != cudaSuccess) return VIT_ERR_CUDA;
+        if (word) return VIT_ERR_TIMEOUT;
+    }
+    return VIT_OK;
+}
+
 // Column terms of both LayerNorm folds (and the gain-scaled weights), prepared once
 // per weight set by vit_weights_create.
 struct FoldTerms {
@@ -1715,6 +1745,129 @@ int vit_attention(const void* qkv, int64_t N, int64_t T, int64_t D, int64_t H, i
         return status_from(e);
     }
     return VIT_OK;
+}
+
+int vit_rmsnorm(const void* x, int x_dtype, const void* residual, int residual_dtype, int64_t rows, int64_t D,
+                double eps, const void* gamma, int gamma_dtype, void* sum, void* out, int out_dtype, float* scales,
+                void* stream) {
+    if (!x || !out || rows <= 0 || D <= 0 || (sum && !residual)) return VIT_ERR_ARG;
+    if (rows > kMaxElements / D) return VIT_ERR_ARG;
+    if (!residual) residual_dtype = x_dtype;
+    if (!gamma) gamma_dtype = x_dtype == DT_F64 ? DT_F64 : DT_F32;
+    if (x_dtype == DT_F64) {
+        if (residual_dtype != DT_F64 || gamma_dtype != DT_F64 || out_dtype != DT_F64) return VIT_ERR_DTYPE;
+    } else {
+        if (x_dtype != DT_F32 && x_dtype != DT_BF16) return VIT_ERR_DTYPE;
+        if (residual_dtype != DT_F32 && residual_dtype != x_dtype) return VIT_ERR_DTYPE;
+        if (gamma_dtype != DT_F32 && gamma_dtype != DT_BF16) return VIT_ERR_DTYPE;
+        if (out_dtype != DT_F32 && out_dtype != DT_BF16 && out_dtype != DT_E4M3) return VIT_ERR_DTYPE;
+    }
+    if ((out_dtype == DT_E4M3) != (scales != nullptr)) return VIT_ERR_ARG;
+    const size_t n = (size_t)(rows * D), xb = n * dt_size(x_dtype), rb = n * dt_size(residual_dtype);
+    const size_t gb = (size_t)D * dt_size(gamma_dtype), ob = n * dt_size(out_dtype);
+    const size_t sb = (size_t)(rows * ((D + 127) / 128)) * 4;
+    const struct { const void* p; size_t n; } in[] = {{x, xb}, {residual, rb}, {gamma, gb}};
+    for (const auto& i : in)
+        if (overlaps(out, ob, i.p, i.n) || overlaps(scales, sb, i.p, i.n)) return VIT_ERR_ARG;
+    if (overlaps(out, ob, scales, sb) || overlaps(out, ob, sum, rb) || overlaps(scales, sb, sum, rb) ||
+        overlaps(sum, rb, gamma, gb))
+        return VIT_ERR_ARG;
+    // the sum may replace x or the residual exactly, not shifted against it
+    if (overlaps(sum, rb, x, xb) && !(sum == x && residual_dtype == x_dtype)) return VIT_ERR_ARG;
+    if (overlaps(sum, rb, residual, rb) && sum != residual) return VIT_ERR_ARG;
+    if (!aligned_to(x, x_dtype) || !aligned_to(residual, residual_dtype) || !aligned_to(gamma, gamma_dtype) ||
+        !aligned_to(sum, residual_dtype) || !aligned_to(out, out_dtype) || !aligned_to(scales, DT_F32))
+        return VIT_ERR_ARG;
+    const RmsNormDesc d{x, x_dtype, residual, residual_dtype, gamma, gamma_dtype, sum, out, out_dtype, scales, rows, D,
+                        eps};
+    return enqueue(stream, [&](const DeviceInfo& dev, cudaStream_t s) { return launch_rmsnorm(d, dev, s); });
+}
+
+int vit_quantize(const void* x, int dtype, int64_t rows, int64_t K, void* q, float* scales, void* stream) {
+    if (!x || !q || !scales || rows <= 0 || K <= 0 || rows > kMaxElements / K) return VIT_ERR_ARG;
+    if (dtype != DT_F32 && dtype != DT_BF16) return VIT_ERR_DTYPE;
+    const size_t n = (size_t)(rows * K), xb = n * dt_size(dtype), sb = (size_t)(rows * ((K + 127) / 128)) * 4;
+    if (overlaps(q, n, x, xb) || overlaps(scales, sb, x, xb) || overlaps(q, n, scales, sb)) return VIT_ERR_ARG;
+    if (!aligned_to(x, dtype) || !aligned_to(scales, DT_F32)) return VIT_ERR_ARG;
+    return enqueue(stream, [&](const DeviceInfo& dev, cudaStream_t s) {
+        return launch_quantize_rows(x, dtype, rows, K, q, scales, dev, s);
+    });
+}
+
+int vit_quantize_weight(const void* w, int dtype, int64_t K, int64_t N, void* q, float* scales, void* stream) {
+    if (!w || !q || !scales || K <= 0 || N <= 0 || K > kMaxElements / N) return VIT_ERR_ARG;
+    if (dtype != DT_F32 && dtype != DT_BF16) return VIT_ERR_DTYPE;
+    const size_t n = (size_t)(K * N), wb = n * dt_size(dtype), sb = (size_t)(((N + 127) / 128) * ((K + 127) / 128)) * 4;
+    if (overlaps(q, n, w, wb) || overlaps(scales, sb, w, wb) || overlaps(q, n, scales, sb)) return VIT_ERR_ARG;
+    if (!aligned_to(w, dtype) || !aligned_to(scales, DT_F32)) return VIT_ERR_ARG;
+    return enqueue(stream, [&](const DeviceInfo& dev, cudaStream_t s) {
+        return launch_quantize_weight(w, dtype, K, N, q, scales, dev, s);
+    });
+}
+
+int vit_linear_fp8(const void* a, const float* a_scales, const void* w, const float* w_scales, const void* bias,
+                   int bias_dtype, const void* residual, int residual_dtype, int64_t M, int64_t K, int64_t N,
+                   int epilogue, void* out, int out_dtype, float* out_scales, void* stream) {
+    if (!a || !a_scales || !w || !w_scales || !out || M <= 0 || K <= 0 || N <= 0) return VIT_ERR_ARG;
+    if (M > kMaxElements / K || N > kMaxElements / K || M > kMaxElements / N) return VIT_ERR_ARG;
+    if (epilogue < VIT_EPI_STORE || epilogue > VIT_EPI_RESIDUAL) return VIT_ERR_ARG;
+    if ((epilogue == VIT_EPI_RESIDUAL) != (residual != nullptr)) return VIT_ERR_ARG;
+    if (out_dtype != DT_BF16 && out_dtype != DT_F32 && out_dtype != DT_E4M3) return VIT_ERR_DTYPE;
+    if (bias && bias_dtype != DT_BF16 && bias_dtype != DT_F32) return VIT_ERR_DTYPE;
+    if (residual && residual_dtype != DT_BF16 && residual_dtype != DT_F32) return VIT_ERR_DTYPE;
+    if ((out_dtype == DT_E4M3) != (out_scales != nullptr)) return VIT_ERR_ARG;
+    const int64_t kb = (K + 127) / 128, nb = (N + 127) / 128;
+    const size_t ob = (size_t)(M * N) * dt_size(out_dtype), osb = out_scales ? (size_t)(M * nb) * 4 : 0;
+    const size_t resb = residual ? (size_t)(M * N) * dt_size(residual_dtype) : 0;
+    const struct { const void* p; size_t n; } in[] = {
+        {a, (size_t)(M * K)}, {a_scales, (size_t)(M * kb) * 4}, {w, (size_t)(N * K)}, {w_scales, (size_t)(nb * kb) * 4},
+        {bias, bias ? (size_t)N * dt_size(bias_dtype) : 0}};
+    for (const auto& i : in)
+        if (overlaps(out, ob, i.p, i.n) || overlaps(out_scales, osb, i.p, i.n)) return VIT_ERR_ARG;
+    if (overlaps(out, ob, out_scales, osb) || overlaps(out_scales, osb, residual, resb)) return VIT_ERR_ARG;
+    // the output may replace the residual exactly, not shifted against it
+    if (overlaps(out, ob, residual, resb) && !(out == residual && out_dtype == residual_dtype)) return VIT_ERR_ARG;
+    if (!aligned_to(a_scales, DT_F32) || !aligned_to(w_scales, DT_F32) || !aligned_to(bias, bias_dtype) ||
+        !aligned_to(residual, residual_dtype) || !aligned_to(out, out_dtype) || !aligned_to(out_scales, DT_F32))
+        return VIT_ERR_ARG;
+    const Fp8GemmDesc d{static_cast<const uint8_t*>(a), a_scales, static_cast<const uint8_t*>(w), w_scales, bias,
+                        bias_dtype == DT_F32, residual, residual_dtype == DT_F32, M, K, N, epilogue, out, out_dtype,
+                        out_scales};
+    return enqueue(stream, [&](const DeviceInfo& dev, cudaStream_t s) { return launch_gemm_fp8(d, dev, s); });
+}
+
+int vit_cross_attention(const void* q, const int64_t* q_strides, const void* k, const int64_t* k_strides,
+                        const void* v, const int64_t* v_strides, const int32_t* kv_lens, int64_t B, int64_t Tq,
+                        int64_t Tk, int64_t H, int64_t Hkv, int64_t dh, double scale, int dtype, void* o,
+                        void* stream) {
+    if (!q || !k || !v || !o || B <= 0 || Tq <= 0 || Tk <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || dh <= 0)
+        return VIT_ERR_ARG;
+    if (!(scale - scale == 0.0)) return VIT_ERR_ARG;   // not finite
+    if (dtype != DT_F32 && dtype != DT_BF16 && dtype != DT_F64) return VIT_ERR_DTYPE;
+    if (dh > kCrossMaxHead) return VIT_ERR_UNSUPPORTED;
+    if (H > kMaxElements / dh || Tq > kMaxElements / (H * dh) || B > kMaxElements / (Tq * H * dh)) return VIT_ERR_ARG;
+    if (Tk > kMaxElements / (Hkv * dh) || B > kMaxElements / (Tk * Hkv * dh)) return VIT_ERR_ARG;
+    CrossDesc d{};
+    d.q = q; d.k = k; d.v = v; d.kv_lens = kv_lens; d.B = B; d.Tq = Tq; d.Tk = Tk; d.H = H; d.Hkv = Hkv; d.dh = dh;
+    d.scale = scale; d.dt = dtype; d.o = o;
+    const size_t es = dt_size(dtype), ob = (size_t)(B * Tq * H * dh) * es;
+    const struct { const void* p; const int64_t* given; int64_t* st; int64_t T, heads; } in[] = {
+        {q, q_strides, d.qs, Tq, H}, {k, k_strides, d.ks, Tk, Hkv}, {v, v_strides, d.vs, Tk, Hkv}};
+    for (const auto& i : in) {
+        const int64_t own[3] = {i.T * i.heads * dh, i.heads * dh, dh}, n[3] = {B, i.T, i.heads};
+        int64_t last = dh - 1;   // offset of the last element
+        for (int j = 0; j < 3; ++j) {
+            i.st[j] = i.given ? i.given[j] : own[j];
+            if (n[j] == 1) i.st[j] = own[j];   // never stepped along
+            if (i.st[j] < 0) return VIT_ERR_ARG;
+            if (n[j] > 1 && i.st[j] > (kMaxElements - last) / (n[j] - 1)) return VIT_ERR_ARG;
+            last += (n[j] - 1) * i.st[j];
+        }
+        if (overlaps(o, ob, i.p, (size_t)(last + 1) * es) || !aligned_to(i.p, dtype)) return VIT_ERR_ARG;
+    }
+    if (overlaps(o, ob, kv_lens, (size_t)B * 4) || !aligned_to(o, dtype) || !aligned_to(kv_lens, DT_F32))
+        return VIT_ERR_ARG;
+    return enqueue(stream, [&](const DeviceInfo& dev, cudaStream_t s) { return launch_cross_attention(d, dev, s); });
 }
 
 int vit_block_noalloc(const void* x, const void* w_q, const void* w_k, const void* w_v,
