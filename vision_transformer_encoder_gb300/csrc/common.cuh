@@ -132,6 +132,14 @@ __device__ __forceinline__ void gelu_tanh_fast2(float& a, float& b) {
     f2_unpack(f2_fma(hz, f2_pack(tanh_approx(u0), tanh_approx(u1)), hz), a, b);
 }
 
+// tanh-approximation GELU to fp32 accuracy (about 2^-20 relative for z > -4): with
+// u = sqrt(2/pi) (z + 0.044715 z^3), 0.5 z (1 + tanh u) = z / (1 + exp(-2u)). One base-2
+// exponential and one division, both hardware approximations good to 2^-22.
+__device__ __forceinline__ float gelu_tanh_exp(float z) {
+    const float c0 = -2.f * 0.7978845608028654f * 1.4426950408889634f;   // -2 sqrt(2/pi) log2(e)
+    return __fdividef(z, 1.f + exp2_approx(z * fmaf(c0 * 0.044715f, z * z, c0)));
+}
+
 // Accurate forms (library tanh) for the fp32 / fp64 paths.
 __device__ __forceinline__ float gelu_tanh_acc(float z) {
     const float k0 = 0.7978845608028654f;

@@ -5,24 +5,517 @@
 // fp32. Products of e4m3 values are exact in fp32; a block's sum and the sum over blocks are
 // fp32. An e4m3 output takes one scale for each 128 columns of a row (fp8.cuh).
 //
+// Pair kernel (many rows): a persistent CTA pair makes a 256 x BN tile with
+// tcgen05.mma.cta_group::2 kind::f8f6f4. One ring stage is one block of 128 along K, both operands
+// K-major with the 128-byte swizzle. A block's scales differ from row to row, so its sum cannot
+// stay in one accumulator with the others': each block gets an accumulator of its own in TMEM
+// (two, in turn), and the epilogue warps add scale * block sum to fp32 registers while the tensor
+// cores make the next block.
+//   warp 0       MMA issue (the leader CTA's lane 0)
+//   warps 1-3    TMA: A rows; B rows, first and second half
+//   warps 4-11   promotion and epilogue: warp (quarter, half) keeps 32 rows x BN / 2 columns in
+//                registers, one row per thread, so the row's scale is one register and an e4m3
+//                output's 128-column scale needs no exchange (BN 256)
+//
 // Generic kernel: CUDA cores, any size and alignment; a CTA makes 16 rows x 128 columns (one
 // output block per row), a thread eight columns of one row.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+
+#include <mutex>
 
 #include "common.cuh"
 #include "fp8.cuh"
 #include "kernels.h"
 #include "launch.cuh"
+#include "ptx.cuh"
 
 namespace vit {
 namespace {
 
-constexpr int GG_ROWS = 16, GG_COLS = 128, GG_THREADS = 256;
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn f8_encode_fn() {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* q = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &q, 12000, cudaEnableDefault, &r) == cudaSuccess &&
+            r == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(q);
+    });
+    return fn;
+}
+
+// Row-major (rows, cols) of `es`-byte elements; boxes of box_rows rows of 128 bytes, 128B swizzle.
+bool f8_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int es, int64_t rows, int64_t cols,
+            uint32_t box_rows, CUtensorMapL2promotion l2) {
+    EncodeTiledFn fn = f8_encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)(cols * es)};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / es), box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+CUtensorMapDataType f8_map_type(int dt) {
+    return dt == DT_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                        : dt == DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+}
 
 __device__ __forceinline__ float load_f32(const void* p, bool f32, int64_t i) {
     return f32 ? static_cast<const float*>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
 }
+
+__device__ __forceinline__ void f8_error(uint32_t* err, uint32_t bit) {
+    if (err) atomicOr(err, bit);
+}
+
+// ------------------------------------------------------------------------ pair kernel
+constexpr int FP_THREADS = 384, FP_EPI_WARPS = 8, FP_TILE_M = 256;
+constexpr int FP_A_BYTES = 128 * kFp8Block;      // this CTA's 128 rows of one block
+constexpr int FP_STG = 32 * 128;                 // staging: 32 rows of 128 bytes per warp
+constexpr int FP_REGS_IO = 56, FP_REGS_EPI = 224;   // of 168 x 3 warpgroups at launch
+
+template <int BN> struct FpLayout {
+    static constexpr int B_BYTES = BN / 2 * kFp8Block;
+    static constexpr int STAGE = FP_A_BYTES + B_BYTES;
+    static constexpr int STAGES = BN == 256 ? 5 : 6;
+    static constexpr int OFF_EPI = STAGES * STAGE;
+    static constexpr int OFF_MAX = OFF_EPI + FP_EPI_WARPS * FP_STG;   // row maxima, BN 128 with e4m3
+    static constexpr int OFF_BAR = OFF_MAX + 2 * 2 * 128 * 4;
+    static constexpr int SMEM = OFF_BAR + 256 + 1024;
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+struct FpParams {
+    Fp8GemmDesc d;
+    uint32_t* err;
+    int out_tma;
+};
+
+// 32 values of this thread's row from column `col` on: bias, GELU or residual.
+template <int EPI>
+__device__ __forceinline__ void f8_finish32(const Fp8GemmDesc& d, int64_t row, int64_t col, int lane, float (&v)[32]) {
+    if (d.bias) {
+        const float b = col + lane < d.N ? load_f32(d.bias, d.bias_f32, col + lane) : 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, b, j);
+    }
+    if constexpr (EPI == TC_EPI_GELU) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = gelu_tanh_exp(v[j]);
+    }
+    if constexpr (EPI == TC_EPI_RESID) {
+        if (row < d.M) {
+            const int64_t at = row * d.N + col;
+            const bool whole = col + 32 <= d.N;
+            if (d.residual_f32) {
+                const float* r = static_cast<const float*>(d.residual) + at;
+                if (whole && (reinterpret_cast<uintptr_t>(r) & 15) == 0) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 u = *reinterpret_cast<const float4*>(r + j);
+                        v[j] += u.x; v[j + 1] += u.y; v[j + 2] += u.z; v[j + 3] += u.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (col + j < d.N) v[j] += r[j];
+                }
+            } else {
+                const __nv_bfloat16* r = static_cast<const __nv_bfloat16*>(d.residual) + at;
+                if (whole && (reinterpret_cast<uintptr_t>(r) & 15) == 0) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8) {
+                        const uint4 u = *reinterpret_cast<const uint4*>(r + j);
+                        const float2 a = unpack_bf16x2(u.x), b = unpack_bf16x2(u.y), c = unpack_bf16x2(u.z),
+                                     e = unpack_bf16x2(u.w);
+                        v[j] += a.x; v[j + 1] += a.y; v[j + 2] += b.x; v[j + 3] += b.y;
+                        v[j + 4] += c.x; v[j + 5] += c.y; v[j + 6] += e.x; v[j + 7] += e.y;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (col + j < d.N) v[j] += __bfloat162float(r[j]);
+                }
+            }
+        }
+    }
+}
+
+// 16-byte unit u of staging row r, 128-byte rows with the 128-byte swizzle.
+__device__ __forceinline__ uint4* f8_unit(uint8_t* stage, int r, int u) {
+    return reinterpret_cast<uint4*>(stage + r * 128 + ((u ^ (r & 7)) << 4));
+}
+
+template <int BN, int EPI, int OUT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP_THREADS, 1)
+gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                     const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ FpParams p) {
+    using L = FpLayout<BN>;
+    constexpr int STAGES = L::STAGES, COLS = BN / 2;   // columns per epilogue warp
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+    uint64_t* empty = full + STAGES;
+    uint64_t* tfull = empty + STAGES;
+    uint64_t* tempty = tfull + 2;
+    uint64_t* done = tempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const Fp8GemmDesc& d = p.d;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = ptx::cluster_ctarank();
+    const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+    const int n_tiles = (int)((d.N + BN - 1) / BN);
+    const int tiles = (int)((d.M + FP_TILE_M - 1) / FP_TILE_M) * n_tiles;
+    const int kblocks = (int)((d.K + kFp8Block - 1) / kFp8Block);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            ptx::mbar_init(full + s, 1);
+            ptx::mbar_init(empty + s, 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            ptx::mbar_init(tfull + a, 1);
+            ptx::mbar_init(tempty + a, 2 * FP_EPI_WARPS);
+        }
+        ptx::mbar_init(done, 1);
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 1 && lane == 0) {
+        ptx::prefetch_tensormap(&tmA);
+        ptx::prefetch_tensormap(&tmB);
+        if (p.out_tma) ptx::prefetch_tensormap(&tmOut);
+    }
+    if (warp == 0) {
+        ptx::tmem_alloc_pair(tmem_slot, 2 * BN);
+        ptx::tmem_relinquish_pair();
+    }
+    ptx::tc_fence_before();
+    ptx::cluster_sync();   // barriers of both CTAs initialised before any remote arrive
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    griddep_wait();
+    griddep_launch_dependents();
+
+    if (warp < 4) {
+        ptx::setmaxnreg_dec<FP_REGS_IO>();
+        if (warp > 0 && lane == 0) {
+            // ------------------------------------------------ TMA producers (both CTAs)
+            const uint32_t full0 = ptx::mapa_shared(ptx::smem_addr(full), 0);   // the leader's
+            uint32_t it = 0;
+            bool ok = true;
+            for (int t = cluster; t < tiles && ok; t += nclusters) {
+                const int m0 = (t / n_tiles) * FP_TILE_M + (int)rank * 128;
+                const int n0 = (t % n_tiles) * BN + (int)rank * (BN / 2);
+                for (int kb = 0; kb < kblocks; ++kb, ++it) {
+                    const uint32_t s = it % STAGES, u = it / STAGES;
+                    if (!ptx::mbar_wait_bounded<true>(empty + s, (u & 1) ^ 1, abort_flag)) { ok = false; break; }
+                    if (warp == 1 && rank == 0) ptx::mbar_arrive_expect_tx(full + s, 2 * L::STAGE);
+                    uint8_t* st = smem + s * L::STAGE;
+                    if (warp == 1)
+                        ptx::tma_load_2d_pair(st, &tmA, full0 + s * 8, kb * kFp8Block, m0);
+                    else
+                        ptx::tma_load_2d_pair(st + FP_A_BYTES + (warp - 2) * (L::B_BYTES / 2), &tmB, full0 + s * 8,
+                                              kb * kFp8Block, n0 + (warp - 2) * (BN / 4));
+                }
+            }
+            if (!ok) {
+                f8_error(p.err, ERRBIT_TIMEOUT_PRODUCER);
+                *abort_flag = 1;
+            }
+            if (warp == 1 && rank == 0) {
+                // the copies of both CTAs complete on these barriers: let them land
+                for (uint32_t s = 0; s < (uint32_t)STAGES; ++s)
+                    if (it > s && !ptx::mbar_wait_bounded(full + s, ((it - 1 - s) / STAGES) & 1, nullptr))
+                        f8_error(p.err, ERRBIT_TIMEOUT_TEARDOWN);
+            }
+        } else if (warp == 0 && lane == 0 && rank == 0) {
+            // ------------------------------------------------ MMA issue (leader)
+            constexpr uint32_t idesc = ptx::idesc_e4m3_f32(FP_TILE_M, BN);
+            uint32_t it = 0;
+            bool ok = true;
+            for (int t = cluster; t < tiles && ok; t += nclusters) {
+                for (int kb = 0; kb < kblocks; ++kb, ++it) {
+                    const uint32_t s = it % STAGES, acc = it & 1;
+                    if (!ptx::mbar_wait_bounded(tempty + acc, ((it >> 1) & 1) ^ 1, abort_flag) ||
+                        !ptx::mbar_wait_bounded(full + s, (it / STAGES) & 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint32_t a = ptx::smem_addr(smem + s * L::STAGE), b = a + FP_A_BYTES;
+#pragma unroll
+                    for (int k = 0; k < kFp8Block / 32; ++k)
+                        ptx::mma_f8_ss_pair(tmem + acc * BN, ptx::smem_desc_sw128(a + k * 32, 16, 1024),
+                                            ptx::smem_desc_sw128(b + k * 32, 16, 1024), idesc, k != 0);
+                    ptx::mma_commit_pair_mc(empty + s, 0x3);
+                    ptx::mma_commit_pair_mc(tfull + acc, 0x3);
+                }
+            }
+            if (!ok) {
+                f8_error(p.err, ERRBIT_TIMEOUT_MMA);
+                *abort_flag = 1;
+            }
+            ptx::mma_commit_pair(done);
+            if (!ptx::mbar_wait_bounded(done, 0, nullptr)) f8_error(p.err, ERRBIT_TIMEOUT_TEARDOWN);
+        }
+    } else {
+        // ------------------------------------------------ promotion and epilogue
+        ptx::setmaxnreg_inc<FP_REGS_EPI>();
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t tempty0 = ptx::mapa_shared(ptx::smem_addr(tempty), 0);
+        const uint32_t t_lane = tmem + half * COLS + ((uint32_t)(quarter * 32) << 16);
+        uint8_t* stage = smem + L::OFF_EPI + (warp - 4) * FP_STG;
+        const int64_t nblk = (d.N + kFp8Block - 1) / kFp8Block;
+        uint32_t it = 0, tcount = 0;
+        bool failed = false;   // a wait ran out: go on without waiting, store nothing
+        // scales of block kb of tile t for this thread's row and this warp's columns
+        auto scale_of = [&](int t, int kb) -> float {
+            if (t >= tiles || kb >= kblocks) return 0.f;
+            const int64_t row = (int64_t)(t / n_tiles) * FP_TILE_M + rank * 128 + quarter * 32 + lane;
+            int64_t nb = ((int64_t)(t % n_tiles) * BN + half * COLS) / kFp8Block;
+            if (nb > nblk - 1) nb = nblk - 1;
+            const float sa = row < d.M ? __ldg(d.a_scales + row * kblocks + kb) : 0.f;
+            return sa * __ldg(d.w_scales + nb * kblocks + kb);
+        };
+        float s0 = scale_of(cluster, 0), s1 = scale_of(cluster, 1);
+        for (int t = cluster; t < tiles; t += nclusters, ++tcount) {
+            const int64_t row0 = (int64_t)(t / n_tiles) * FP_TILE_M + rank * 128 + quarter * 32, row = row0 + lane;
+            const int64_t n0 = (int64_t)(t % n_tiles) * BN + half * COLS;
+            unsigned long long acc[COLS / 2];
+#pragma unroll
+            for (int j = 0; j < COLS / 2; ++j) acc[j] = 0ull;
+            for (int kb = 0; kb < kblocks; ++kb, ++it) {
+                const uint32_t buf = it & 1;
+                const float s2 = scale_of(t, kb + 2);   // two blocks ahead
+                if (!failed && !__all_sync(0xffffffffu, ptx::mbar_wait_bounded(tfull + buf, (it >> 1) & 1, abort_flag))) {
+                    failed = true;
+                    if (lane == 0) f8_error(p.err, ERRBIT_TIMEOUT_EPILOGUE);
+                    *abort_flag = 1;
+                }
+                ptx::tc_fence_after();
+                const unsigned long long ss = f2_pack(s0, s0);
+#pragma unroll
+                for (int c = 0; c < COLS / 32; ++c) {
+                    uint32_t r[32];
+                    ptx::tmem_ld_32x32b_x32(t_lane + buf * BN + c * 32, r);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        acc[c * 16 + j] = f2_fma(f2_pack(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), ss,
+                                                 acc[c * 16 + j]);
+                }
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_cluster_relaxed(tempty0 + buf * 8);   // orders TMEM reads only
+                s0 = s1;
+                s1 = s2;
+            }
+            // the next tile's first scales travel while this one is stored
+            s0 = scale_of(t + nclusters, 0);
+            s1 = scale_of(t + nclusters, 1);
+            if (n0 >= d.N && !(OUT == DT_E4M3 && BN == 128)) continue;   // (there the two halves meet below)
+            if constexpr (OUT == DT_E4M3) {
+                float amax = 0.f;
+#pragma unroll
+                for (int c = 0; c < COLS / 32; ++c) {
+                    float v[32];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) f2_unpack(acc[c * 16 + j], v[2 * j], v[2 * j + 1]);
+                    f8_finish32<EPI>(d, row, n0 + c * 32, lane, v);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (n0 + c * 32 + j < d.N) amax = fmaxf(amax, fabsf(v[j]));
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) acc[c * 16 + j] = f2_pack(v[2 * j], v[2 * j + 1]);
+                }
+                if constexpr (BN == 128) {   // a block of 128 columns is two warps' halves
+                    float* mx = reinterpret_cast<float*>(smem + L::OFF_MAX) + (tcount & 1) * 256;
+                    mx[half * 128 + quarter * 32 + lane] = amax;
+                    ptx::named_bar_sync(1 + quarter, 64);
+                    amax = fmaxf(amax, mx[(half ^ 1) * 128 + quarter * 32 + lane]);
+                }
+                const float sc = fp8_block_scale(amax), inv = __frcp_rn(sc);
+                if (row < d.M && n0 < d.N && (BN == 256 || half == 0) && !failed)
+                    d.out_scales[row * nblk + n0 / kFp8Block] = sc;
+                if (p.out_tma) {
+                    if (lane == 0) ptx::bulk_wait_group_read<0>();
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int u = 0; u < COLS / 16; ++u) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float a, b, c, e;
+                        f2_unpack(acc[u * 8 + q * 2], a, b);
+                        f2_unpack(acc[u * 8 + q * 2 + 1], c, e);
+                        w[q] = fp8_pack4(a * inv, b * inv, c * inv, e * inv);
+                    }
+                    if (p.out_tma) {
+                        if constexpr (BN == 256) *f8_unit(stage, lane, u) = make_uint4(w[0], w[1], w[2], w[3]);
+                        else   // rows of 64 bytes, 64-byte swizzle
+                            *reinterpret_cast<uint4*>(stage + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4)) =
+                                make_uint4(w[0], w[1], w[2], w[3]);
+                    } else if (row < d.M && !failed) {
+                        uint8_t* o = static_cast<uint8_t*>(d.out) + row * d.N + n0 + u * 16;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (n0 + u * 16 + j < d.N) o[j] = (uint8_t)(w[j >> 2] >> ((j & 3) * 8));
+                    }
+                }
+                if (p.out_tma) {
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && !failed && n0 < d.N) {
+                        ptx::tma_store_2d(&tmOut, stage, (int32_t)n0, (int32_t)row0);
+                        ptx::bulk_commit_group();
+                    }
+                }
+            } else {
+                // 128 bytes of each row at a time: 32 fp32 or 64 bf16 columns
+                constexpr int UNIT = OUT == DT_F32 ? 32 : 64;
+#pragma unroll
+                for (int c = 0; c < COLS / 32; ++c) {
+                    float v[32];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) f2_unpack(acc[c * 16 + j], v[2 * j], v[2 * j + 1]);
+                    const int64_t col = n0 + c * 32;
+                    f8_finish32<EPI>(d, row, col, lane, v);
+                    if (p.out_tma) {
+                        if ((c * 32) % UNIT == 0) {
+                            if (lane == 0) ptx::bulk_wait_group_read<0>();
+                            __syncwarp();
+                        }
+                        if constexpr (OUT == DT_F32) {
+#pragma unroll
+                            for (int u = 0; u < 8; ++u)
+                                *f8_unit(stage, lane, u) =
+                                    make_uint4(__float_as_uint(v[4 * u]), __float_as_uint(v[4 * u + 1]),
+                                               __float_as_uint(v[4 * u + 2]), __float_as_uint(v[4 * u + 3]));
+                        } else {
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                *f8_unit(stage, lane, (c & 1) * 4 + u) =
+                                    make_uint4(pack_bf16x2(v[8 * u], v[8 * u + 1]), pack_bf16x2(v[8 * u + 2], v[8 * u + 3]),
+                                               pack_bf16x2(v[8 * u + 4], v[8 * u + 5]),
+                                               pack_bf16x2(v[8 * u + 6], v[8 * u + 7]));
+                        }
+                        if ((c * 32 + 32) % UNIT == 0) {
+                            ptx::fence_proxy_async_smem();
+                            __syncwarp();
+                            const int64_t first = n0 + c * 32 + 32 - UNIT;
+                            if (lane == 0 && !failed && first < d.N) {
+                                ptx::tma_store_2d(&tmOut, stage, (int32_t)first, (int32_t)row0);
+                                ptx::bulk_commit_group();
+                            }
+                        }
+                    } else if (row < d.M && !failed) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            if (col + j >= d.N) continue;
+                            if constexpr (OUT == DT_F32) static_cast<float*>(d.out)[row * d.N + col + j] = v[j];
+                            else static_cast<__nv_bfloat16*>(d.out)[row * d.N + col + j] = __float2bfloat16_rn(v[j]);
+                        }
+                    }
+                }
+            }
+        }
+        if (lane == 0) ptx::bulk_wait_group<0>();   // stores complete before the CTA exits
+    }
+
+    __syncthreads();
+    ptx::cluster_sync();   // no CTA leaves while its peer may still touch its memory
+    if (warp == 0) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc_pair(tmem, 2 * BN);
+    }
+}
+
+// A row stride that TMA takes, from a 16-byte aligned base.
+inline bool f8_tma_ok(const void* p, int64_t row_bytes) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && row_bytes % 16 == 0;
+}
+
+template <int BN, int EPI, int OUT>
+cudaError_t launch_pair_inst(const Fp8GemmDesc& d, const DeviceInfo& dev, cudaStream_t s) {
+    using L = FpLayout<BN>;
+    auto k = gemm_fp8_pair_kernel<BN, EPI, OUT>;
+    // setmaxnreg hands out the registers of the launch: the split must fit in them
+    static const bool fits = [&] {
+        cudaFuncAttributes a;
+        return cudaFuncGetAttributes(&a, k) == cudaSuccess &&
+               a.numRegs * 3 >= FP_REGS_IO + 2 * FP_REGS_EPI;
+    }();
+    if (!fits) return cudaErrorNotSupported;
+    static std::atomic<uint64_t> attr{0};
+    cudaError_t e = set_smem_limit_once(k, L::SMEM, attr);
+    if (e != cudaSuccess) return e;
+    alignas(64) CUtensorMap ma, mb, mo;
+    if (!f8_map(&ma, d.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, d.M, d.K, 128, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
+        !f8_map(&mb, d.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, d.N, d.K, BN / 4, CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+        return cudaErrorInvalidValue;
+    FpParams p{d, dev.err_word, 0};
+    const int es = (int)dt_size(OUT);
+    mo = ma;
+    if (f8_tma_ok(d.out, d.N * es)) {
+        p.out_tma = 1;
+        if (OUT == DT_E4M3 && BN == 128) {
+            const cuuint64_t dims[2] = {(cuuint64_t)d.N, (cuuint64_t)d.M};
+            const cuuint64_t strides[1] = {(cuuint64_t)d.N};
+            const cuuint32_t box[2] = {64, 32}, estr[2] = {1, 1};
+            if (f8_encode_fn()(&mo, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, d.out, dims, strides, box, estr,
+                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+                return cudaErrorInvalidValue;
+        } else if (!f8_map(&mo, d.out, f8_map_type(OUT), es, d.M, d.N, 32, CU_TENSOR_MAP_L2_PROMOTION_NONE)) {
+            return cudaErrorInvalidValue;
+        }
+    }
+    const int64_t tiles = ((d.M + FP_TILE_M - 1) / FP_TILE_M) * ((d.N + BN - 1) / BN);
+    const int64_t clusters = tiles < dev.num_sms / 2 ? tiles : dev.num_sms / 2;
+    return launch_dependent(k, dim3((unsigned)(2 * clusters)), dim3(FP_THREADS), L::SMEM, s, ma, mb, mo, p);
+}
+
+template <int BN, int EPI>
+cudaError_t launch_pair_out(const Fp8GemmDesc& d, const DeviceInfo& dev, cudaStream_t s) {
+    switch (d.out_dt) {
+        case DT_BF16: return launch_pair_inst<BN, EPI, DT_BF16>(d, dev, s);
+        case DT_F32: return launch_pair_inst<BN, EPI, DT_F32>(d, dev, s);
+        case DT_E4M3: return launch_pair_inst<BN, EPI, DT_E4M3>(d, dev, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+template <int BN> cudaError_t launch_pair(const Fp8GemmDesc& d, const DeviceInfo& dev, cudaStream_t s) {
+    switch (d.epi) {
+        case TC_EPI_STORE: return launch_pair_out<BN, TC_EPI_STORE>(d, dev, s);
+        case TC_EPI_GELU: return launch_pair_out<BN, TC_EPI_GELU>(d, dev, s);
+        case TC_EPI_RESID: return launch_pair_out<BN, TC_EPI_RESID>(d, dev, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+// Tensor-core kernels: 16-byte aligned operands and rows, extents and tile counts in 32 bits.
+bool f8_tc_ok(const Fp8GemmDesc& d, const DeviceInfo& dev) {
+    const int64_t lim = 0x7fffffff - 512;
+    return f8_tma_ok(d.a, d.K) && f8_tma_ok(d.w, d.K) && d.M <= lim && d.N <= lim && d.K <= lim &&
+           ((d.M + 255) / 256) * ((d.N + 127) / 128) <= lim && dev.num_sms >= 2 && f8_encode_fn() != nullptr;
+}
+
+// ------------------------------------------------------------------------ generic kernel
+constexpr int GG_ROWS = 16, GG_COLS = 128, GG_THREADS = 256;
 
 __global__ void __launch_bounds__(GG_THREADS)
 gemm_fp8_generic_kernel(const Fp8GemmDesc d) {
@@ -93,6 +586,12 @@ gemm_fp8_generic_kernel(const Fp8GemmDesc d) {
 }  // namespace
 
 cudaError_t launch_gemm_fp8(const Fp8GemmDesc& d, const DeviceInfo& dev, cudaStream_t s) {
+    if (f8_tc_ok(d, dev)) {
+        // 256-wide tiles halve the operand traffic per product; 128-wide ones when the wide tiles
+        // leave CTA pairs without work
+        const int64_t wide = ((d.M + FP_TILE_M - 1) / FP_TILE_M) * ((d.N + 255) / 256);
+        return wide >= dev.num_sms / 2 ? launch_pair<256>(d, dev, s) : launch_pair<128>(d, dev, s);
+    }
     int64_t grid = ((d.M + GG_ROWS - 1) / GG_ROWS) * ((d.N + GG_COLS - 1) / GG_COLS);
     if (grid > 8 * (int64_t)dev.num_sms) grid = 8 * (int64_t)dev.num_sms;
     return launch_dependent(gemm_fp8_generic_kernel, dim3((unsigned)grid), dim3(GG_THREADS), 0, s, d);
