@@ -1,0 +1,567 @@
+// attention_cross_tc.cu -- cross attention of many queries on the sm_103a tensor cores
+// (tcgen05 / TMEM / TMA), bf16 in and out, fp32 softmax: the mathematics of
+// attention_cross.cu for head widths 64, 80, 96 and 128.
+//
+// A tile is up to 128 query rows of ONE key head: TT tokens x the G query heads that share it
+// (TT = 128 / G), packed row = token * G + head by one 4-D TMA box, so K and V are read once for
+// the whole head group. A work item is (sequence, key head, pair of tiles); a persistent CTA per
+// SM walks the items.
+//   warps 10, 11  TMA: Q and K tiles, V tiles, 128 keys each, rings of their own
+//   warps 1, 0    MMA issue for softmax group 0, 1: S = Q K^T (M 128, N 128, K dh), then
+//                 O += P V (M 128, N dh, K 128) with P read from TMEM and V MN-major
+//   warps 2-5, 6-9  softmax groups 0 and 1, one query row per thread
+// Heads wider than 64 columns are two 64-column boxes; columns past dh are zero-filled on load and
+// cut off on store by the tensor map, so 80 and 96 run as they are. For dh 64, P has columns of its
+// own in TMEM and S of the next key tile is made while P V of this one runs; for wider heads
+// S, O and P do not fit side by side, so P overwrites S and the two groups take turns on the
+// tensor cores instead.
+//
+// The running maximum is only raised when a row's scores exceed it by more than 8 (in log2): until
+// then weights of up to 2^8 are carried, exactly as good in bf16 and far inside fp32, and the
+// accumulator in TMEM is not touched. Keys past the sequence's length get weight 0 by position,
+// and the V rows that the last tile holds past it are cleared before they meet those zeros.
+// Every wait is bounded; on expiry the kernel records an error bit and unwinds.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdlib>
+#include <mutex>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "launch.cuh"
+#include "ptx.cuh"
+
+namespace vit {
+namespace {
+
+constexpr int CT_ROWS = 128, CT_KEYS = 128, CT_THREADS = 384;
+constexpr int CT_BOX = CT_ROWS * 128;      // 64 columns x 128 rows: 16 KB
+constexpr float CT_SLACK = 8.f;            // log2 of the weights that are carried before a rescale
+
+template <int DH> struct CtLayout {
+    static_assert(DH % 16 == 0 && DH >= 64 && DH <= 128, "head width");
+    static constexpr int NCH = (DH + 63) / 64;           // 64-column boxes per tile
+    static constexpr bool ALIAS = DH > 64;               // P overwrites S
+    static constexpr int TILE = NCH * CT_BOX;
+    static constexpr int QBUF = ALIAS ? 1 : 2;           // buffers of two query tiles
+    static constexpr int KVS = ALIAS ? 2 : 4;            // stages of each ring
+    static constexpr int OFF_K = QBUF * 2 * TILE;
+    static constexpr int OFF_V = OFF_K + KVS * TILE;
+    static constexpr int OFF_O = OFF_V + KVS * TILE;     // per group: one 64-column box of O on its way out
+    static constexpr int OFF_BAR = OFF_O + 2 * CT_BOX;
+    static constexpr int SMEM = OFF_BAR + 512 + 1024;
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+struct CtParams {
+    const int32_t* kv_lens;
+    int B, Tq, Tk, Hkv, G, TT;
+    int npairs, items;
+    int kb, kh, vb, vh, qb;      // 0 where the tensor has one sequence (key head) for all
+    float scale_log2;
+    uint32_t* err;
+};
+
+struct CtBars {
+    uint64_t q_full[2], q_empty[2];
+    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+    uint64_t s_full[2], s_read[2], p_full[2], o_done[2], o_free[2], ost_full[2], ost_free[2];
+    uint64_t done;
+    uint32_t tmem_slot;
+    int abort_flag;
+};
+static_assert(sizeof(CtBars) <= 512, "barriers");
+
+__device__ __forceinline__ void ct_error(uint32_t* err, uint32_t bit) {
+    if (err) atomicOr(err, bit);
+}
+
+struct CtItem {
+    int b, h, t0, nact, len, nkt;
+};
+
+__device__ __forceinline__ CtItem ct_item(const CtParams& p, int item) {
+    CtItem x;
+    const int pair = item % p.npairs, bh = item / p.npairs;
+    x.h = bh % p.Hkv;
+    x.b = bh / p.Hkv;
+    x.t0 = pair * 2 * p.TT;
+    x.nact = x.t0 + p.TT < p.Tq ? 2 : 1;
+    x.len = p.kv_lens ? min(max(__ldg(p.kv_lens + x.b), 0), p.Tk) : p.Tk;
+    x.nkt = (x.len + CT_KEYS - 1) / CT_KEYS;
+    return x;
+}
+
+template <int DH>
+__global__ void __launch_bounds__(CT_THREADS, 1)
+cross_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, const CtParams p) {
+    using L = CtLayout<DH>;
+    constexpr int KVS = L::KVS, QB = L::QBUF, NCH = L::NCH;
+    constexpr bool ALIAS = L::ALIAS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t* sQ = smem;
+    uint8_t* sK = smem + L::OFF_K;
+    uint8_t* sV = smem + L::OFF_V;
+    CtBars* bars = reinterpret_cast<CtBars*>(smem + L::OFF_BAR);
+    volatile int* abort_flag = &bars->abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&bars->q_full[i], 1);
+            ptx::mbar_init(&bars->q_empty[i], 2);     // both MMA issuers
+            ptx::mbar_init(&bars->s_full[i], 1);
+            ptx::mbar_init(&bars->s_read[i], 4);      // one arrival per softmax warp
+            ptx::mbar_init(&bars->p_full[i], 4);
+            ptx::mbar_init(&bars->o_done[i], 1);
+            ptx::mbar_init(&bars->o_free[i], 4);
+            ptx::mbar_init(&bars->ost_full[i], 4);
+            ptx::mbar_init(&bars->ost_free[i], 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            ptx::mbar_init(&bars->k_full[i], 1);
+            ptx::mbar_init(&bars->k_empty[i], 2);
+            ptx::mbar_init(&bars->v_full[i], 1);
+            ptx::mbar_init(&bars->v_empty[i], 2);
+        }
+        ptx::mbar_init(&bars->done, 2);
+        bars->abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 10 && lane == 0) {
+        ptx::prefetch_tensormap(&tmQ);
+        ptx::prefetch_tensormap(&tmK);
+        ptx::prefetch_tensormap(&tmV);
+        ptx::prefetch_tensormap(&tmO);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(&bars->tmem_slot, 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = bars->tmem_slot;
+    griddep_wait();
+    griddep_launch_dependents();
+    // TMEM columns: S_g at 128 g; O_g at 256 + 128 g; P_g over S_g, or for dh 64 behind O_g
+
+    if (warp >= 10) {
+        if (lane == 0) {
+            // ------------------------------------------------ TMA producers
+            const bool kq = warp == 10;
+            uint64_t* full = kq ? bars->k_full : bars->v_full;
+            uint64_t* empty = kq ? bars->k_empty : bars->v_empty;
+            uint8_t* ring = kq ? sK : sV;
+            const CUtensorMap* tm = kq ? &tmK : &tmV;
+            uint32_t it = 0, ii = 0;
+            bool ok = true;
+            for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x) {
+                const CtItem x = ct_item(p, item);
+                if (x.nkt == 0) continue;
+                if (kq) {
+                    const uint32_t qb = ii % QB;
+                    if (!ptx::mbar_wait_bounded<true>(&bars->q_empty[qb], ((ii / QB) & 1) ^ 1, abort_flag)) { ok = false; break; }
+                    ptx::mbar_arrive_expect_tx(&bars->q_full[qb], x.nact * NCH * p.G * p.TT * 128);
+                    for (int g = 0; g < x.nact; ++g)
+                        for (int c = 0; c < NCH; ++c)
+                            ptx::tma_load_4d(sQ + (qb * 2 + g) * L::TILE + c * CT_BOX, &tmQ, &bars->q_full[qb], c * 64,
+                                             x.h * p.G, x.t0 + g * p.TT, x.b * p.qb);
+                }
+                ++ii;
+                const int b = x.b * (kq ? p.kb : p.vb), h = x.h * (kq ? p.kh : p.vh);
+                for (int j = 0; j < x.nkt; ++j, ++it) {
+                    const uint32_t st = it % KVS;
+                    if (!ptx::mbar_wait_bounded<true>(empty + st, ((it / KVS) & 1) ^ 1, abort_flag)) { ok = false; break; }
+                    ptx::mbar_arrive_expect_tx(full + st, L::TILE);
+                    for (int c = 0; c < NCH; ++c)
+                        ptx::tma_load_4d(ring + st * L::TILE + c * CT_BOX, tm, full + st, c * 64, h, j * CT_KEYS, b);
+                }
+            }
+            if (!ok) {
+                ct_error(p.err, ERRBIT_TIMEOUT_ATTENTION);
+                *abort_flag = 1;
+            }
+            // copies in flight land before the CTA can exit
+            if (kq)
+                for (uint32_t i = 0; i < (uint32_t)QB; ++i)
+                    if (ii > i && !ptx::mbar_wait_bounded(&bars->q_full[(ii - 1 - i) % QB], ((ii - 1 - i) / QB) & 1, nullptr))
+                        ct_error(p.err, ERRBIT_TIMEOUT_TEARDOWN);
+            for (uint32_t i = 0; i < (uint32_t)KVS; ++i)
+                if (it > i && !ptx::mbar_wait_bounded(full + (it - 1 - i) % KVS, ((it - 1 - i) / KVS) & 1, nullptr))
+                    ct_error(p.err, ERRBIT_TIMEOUT_TEARDOWN);
+        }
+    } else if (warp <= 1) {
+        // ---------------------------------------------------- MMA issue, lane 0; the other lanes
+        // wait alongside and help to clear V rows
+        const int g = warp == 1 ? 0 : 1;
+        constexpr uint32_t idS = ptx::idesc_bf16_f32(CT_ROWS, CT_KEYS, false, false);
+        constexpr uint32_t idO = ptx::idesc_bf16_f32(CT_ROWS, DH, false, true);
+        const uint32_t tS = tmem + g * CT_KEYS, tO = tmem + 256 + g * 128, tP = ALIAS ? tS : tO + 64;
+        uint32_t base = 0, ii = 0, pc = 0, ic = 0;
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+            return __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, parity, abort_flag));
+        };
+        auto issue_S = [&](int j, uint32_t qb) -> bool {
+            const uint32_t it = base + j, st = it % KVS;
+            if (!wait(&bars->k_full[st], (it / KVS) & 1)) return false;
+            ptx::tc_fence_after();
+            if (lane == 0) {
+                const uint32_t qa = ptx::smem_addr(sQ + (qb * 2 + g) * L::TILE), ka = ptx::smem_addr(sK + st * L::TILE);
+#pragma unroll
+                for (int kk = 0; kk < DH / 16; ++kk) {
+                    const uint32_t off = (kk >> 2) * CT_BOX + (kk & 3) * 32;
+                    ptx::mma_bf16_ss(tS, ptx::smem_desc(qa + off, 16, 1024, ptx::kLayoutSw128),
+                                     ptx::smem_desc(ka + off, 16, 1024, ptx::kLayoutSw128), idS, kk > 0);
+                }
+                ptx::mma_commit(&bars->s_full[g]);
+                ptx::mma_commit(&bars->k_empty[st]);
+            }
+            return true;
+        };
+        for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x) {
+            const CtItem x = ct_item(p, item);
+            if (x.nkt == 0) continue;
+            const uint32_t qb = ii % QB;
+            ok = wait(&bars->q_full[qb], (ii / QB) & 1);
+            ++ii;
+            if (!ok) break;
+            if (g >= x.nact) {
+                // no tile for this group: release what the other issuer uses, each once it has landed
+                if (lane == 0) ptx::mma_commit(&bars->q_empty[qb]);
+                for (int j = 0; j < x.nkt && ok; ++j) {
+                    const uint32_t it = base + j, st = it % KVS;
+                    ok = wait(&bars->k_full[st], (it / KVS) & 1);
+                    if (ok && lane == 0) ptx::mma_commit(&bars->k_empty[st]);
+                    ok = ok && wait(&bars->v_full[st], (it / KVS) & 1);
+                    if (ok && lane == 0) ptx::mma_commit(&bars->v_empty[st]);
+                }
+                base += x.nkt;
+                continue;
+            }
+            ok = issue_S(0, qb);
+            if (ok && x.nkt == 1 && lane == 0) ptx::mma_commit(&bars->q_empty[qb]);
+            for (int j = 0; j < x.nkt && ok; ++j, ++pc) {
+                if (!ALIAS) {
+                    // S of the next tile as soon as the softmax holds this one in registers
+                    if (!(ok = wait(&bars->s_read[g], pc & 1))) break;
+                    if (j + 1 < x.nkt) {
+                        if (!(ok = issue_S(j + 1, qb))) break;
+                        if (j + 2 == x.nkt && lane == 0) ptx::mma_commit(&bars->q_empty[qb]);
+                    }
+                }
+                const uint32_t it = base + j, st = it % KVS;
+                if (!(ok = wait(&bars->v_full[st], (it / KVS) & 1))) break;
+                const int valid = x.len - j * CT_KEYS;
+                if (valid < CT_KEYS) {
+                    // rows past the length may hold anything, and 0 * NaN is NaN. Both issuers clear
+                    // the same rows: the second finds zeros and writes zeros.
+                    for (int i = valid * 8 + lane; i < CT_KEYS * 8; i += 32)
+#pragma unroll
+                        for (int c = 0; c < NCH; ++c)
+                            *reinterpret_cast<uint4*>(sV + st * L::TILE + c * CT_BOX + i * 16) = make_uint4(0, 0, 0, 0);
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (!(ok = wait(&bars->p_full[g], pc & 1))) break;
+                if (j == 0 && ic > 0 && !(ok = wait(&bars->o_free[g], (ic - 1) & 1))) break;
+                ptx::tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t va = ptx::smem_addr(sV + st * L::TILE);
+#pragma unroll
+                    for (int kk = 0; kk < CT_KEYS / 16; ++kk)   // 16 keys: 16 rows of V, 8 columns of bf16 pairs of P
+                        ptx::mma_bf16_ts(tO, tP + kk * 8, ptx::smem_desc(va + kk * 2048, CT_BOX, 1024, ptx::kLayoutSw128),
+                                         idO, j > 0 || kk > 0);
+                    ptx::mma_commit(&bars->o_done[g]);
+                    ptx::mma_commit(&bars->v_empty[st]);
+                }
+                __syncwarp();
+                if (ALIAS && j + 1 < x.nkt) {
+                    // S of the next tile overwrites P: after P V has read it
+                    if (!(ok = wait(&bars->o_done[g], pc & 1))) break;
+                    if (!(ok = issue_S(j + 1, qb))) break;
+                    if (j + 2 == x.nkt && lane == 0) ptx::mma_commit(&bars->q_empty[qb]);
+                }
+            }
+            ++ic;
+            base += x.nkt;
+        }
+        if (!ok && lane == 0) {
+            ct_error(p.err, ERRBIT_TIMEOUT_MMA);
+            *abort_flag = 1;
+        }
+        if (lane == 0) {
+            ptx::mma_commit(&bars->done);
+            if (!ptx::mbar_wait_bounded(&bars->done, 0, nullptr)) ct_error(p.err, ERRBIT_TIMEOUT_TEARDOWN);
+        }
+    } else {
+        // ---------------------------------------------------- softmax groups
+        const int g = (warp - 2) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+        const uint32_t tS = tmem + g * CT_KEYS + lane_off, tO = tmem + 256 + g * 128 + lane_off;
+        const uint32_t tP = ALIAS ? tS : tO + 64;
+        uint8_t* stage = smem + L::OFF_O + g * CT_BOX;
+        const bool storer = quarter == 2 && lane == 0;
+        const float sl2 = p.scale_log2;
+        uint32_t tt = 0, sc = 0;   // key tiles, staged boxes of this group so far
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+            return __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, parity, abort_flag));
+        };
+        for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x) {
+            const CtItem x = ct_item(p, item);
+            if (g >= x.nact) continue;
+            const int t0 = x.t0 + g * p.TT;
+            // a warp whose 32 rows hold no query only keeps the barrier protocol
+            const bool live = quarter * 32 < min(p.TT, p.Tq - t0) * p.G;
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < x.nkt; ++j, ++tt) {
+                if (!(ok = wait(&bars->s_full[g], tt & 1))) break;
+                ptx::tc_fence_after();
+                uint32_t sv[CT_KEYS];   // S, then P packed in place
+                float alpha = 1.f, lsum = 0.f;
+                if (live) {
+#pragma unroll
+                    for (int c = 0; c < CT_KEYS / 32; ++c)
+                        ptx::tmem_ld_32x32b_x32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[c * 32]));
+                    ptx::tmem_ld_wait();
+                }
+                if (!ALIAS) {
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&bars->s_read[g]);
+                }
+                if (live) {
+                    const int valid = x.len - j * CT_KEYS;
+                    if (valid < CT_KEYS) {
+#pragma unroll
+                        for (int e = 0; e < CT_KEYS; ++e)
+                            if (e >= valid) sv[e] = __float_as_uint(-INFINITY);
+                    }
+                    float mx[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) mx[e] = __uint_as_float(sv[e]);
+#pragma unroll
+                    for (int e = 8; e < CT_KEYS; ++e) mx[e & 7] = fmaxf(mx[e & 7], __uint_as_float(sv[e]));
+                    const float mrow = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                             fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * sl2;
+                    if (mrow > m + CT_SLACK || m == -INFINITY) {   // raise the maximum
+                        const float m_new = fmaxf(m, mrow);
+                        if (m_new > -INFINITY) alpha = exp2_approx(m - m_new);
+                        m = m_new;
+                    }
+                    const float base = m == -INFINITY ? 0.f : m;   // only infinite scores so far: weights of zero
+                    const unsigned long long s2 = f2_pack(sl2, sl2), nm = f2_pack(-base, -base);
+                    unsigned long long ls[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+                    for (int e = 0; e < CT_KEYS; e += 2) {
+                        float x0, x1;
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), s2, nm), x0, x1);
+                        const float p0 = exp2_approx(x0), p1 = exp2_approx(x1);
+                        ls[(e >> 1) & 3] = f2_add(ls[(e >> 1) & 3], f2_pack(p0, p1));
+                        sv[e >> 1] = pack_bf16x2(p0, p1);
+                    }
+                    float a0, a1, b0, b1;
+                    f2_unpack(f2_add(ls[0], ls[1]), a0, a1);
+                    f2_unpack(f2_add(ls[2], ls[3]), b0, b1);
+                    lsum = (a0 + a1) + (b0 + b1);
+                }
+                if (!ALIAS && j > 0) {   // P V of the previous tile reads P and writes O
+                    if (!(ok = wait(&bars->o_done[g], (tt - 1) & 1))) break;
+                    ptx::tc_fence_after();
+                }
+                if (live) {
+                    if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+                        for (int c = 0; c < DH / 16; ++c) {
+                            uint32_t ov[16];
+                            ptx::tmem_ld_32x32b_x16(tO + c * 16, ov);
+                            ptx::tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                            ptx::tmem_st_32x32b_x16(tO + c * 16, ov);
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < CT_KEYS / 64; ++c)
+                        ptx::tmem_st_32x32b_x32(tP + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[c * 32]));
+                    l = l * alpha + lsum;
+                    ptx::tmem_st_wait();
+                }
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&bars->p_full[g]);
+            }
+            if (!ok) break;
+            if (x.nkt > 0) {
+                if (!(ok = wait(&bars->o_done[g], (tt - 1) & 1))) break;
+                ptx::tc_fence_after();
+            }
+            const float inv = 1.f / l;
+#pragma unroll 1
+            for (int c = 0; c < NCH; ++c, ++sc) {
+                // the previous store has read the staging box
+                if (sc > 0 && !(ok = wait(&bars->ost_free[g], (sc - 1) & 1))) break;
+                constexpr int W = DH < 64 ? DH : 64;
+                if (live) {
+#pragma unroll
+                    for (int u = 0; u < W / 16; ++u) {
+                        uint32_t ov[16];
+                        if (x.nkt > 0 && c * 64 + u * 16 < DH) {
+                            ptx::tmem_ld_32x32b_x16(tO + c * 64 + u * 16, ov);
+                            ptx::tmem_ld_wait();
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) ov[e] = 0u;
+                        }
+                        uint32_t w[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float lo = __uint_as_float(ov[2 * e]), hi = __uint_as_float(ov[2 * e + 1]);
+                            w[e] = x.nkt > 0 ? pack_bf16x2(lo * inv, hi * inv) : 0u;
+                        }
+                        // 16-byte unit i of row r at i ^ (r % 8)
+                        *reinterpret_cast<uint4*>(stage + r * 128 + (((2 * u) ^ (r & 7)) << 4)) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4*>(stage + r * 128 + (((2 * u + 1) ^ (r & 7)) << 4)) =
+                            make_uint4(w[4], w[5], w[6], w[7]);
+                    }
+                }
+                ptx::fence_proxy_async_smem();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (c == NCH - 1 && x.nkt > 0) ptx::mbar_arrive(&bars->o_free[g]);   // O has been read
+                    ptx::mbar_arrive(&bars->ost_full[g]);
+                }
+                bool sok = true;
+                if (storer) {
+                    sok = ptx::mbar_wait_bounded(&bars->ost_full[g], sc & 1, abort_flag);
+                    if (sok) {
+                        ptx::tma_store_4d(&tmO, stage, c * 64, x.h * p.G, t0, x.b);
+                        ptx::bulk_commit_group();
+                        ptx::bulk_wait_group_read<0>();
+                        ptx::mbar_arrive(&bars->ost_free[g]);
+                    }
+                }
+                if (!(ok = __all_sync(0xffffffffu, sok))) break;
+            }
+        }
+        if (storer) ptx::bulk_wait_group<0>();   // the group's last store has completed
+        if (!ok) {
+            if (lane == 0) ct_error(p.err, ERRBIT_TIMEOUT_ATTENTION);
+            *abort_flag = 1;
+        }
+    }
+
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn ct_encode_fn() {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* q = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &q, 12000, cudaEnableDefault, &r) == cudaSuccess &&
+            r == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(q);
+    });
+    return fn;
+}
+
+// (B, T, heads, dh) with element strides st (sequence, token, head); boxes of 64 columns x
+// box_heads x box_tokens. A sequence or head stride of 0 becomes an extent of 1.
+bool ct_map(CUtensorMap* m, const void* base, const int64_t st[3], int64_t B, int64_t T, int64_t heads, int64_t dh,
+            uint32_t box_heads, uint32_t box_tokens, CUtensorMapL2promotion l2) {
+    const cuuint64_t dims[4] = {(cuuint64_t)dh, (cuuint64_t)(st[2] ? heads : 1), (cuuint64_t)T, (cuuint64_t)(st[0] ? B : 1)};
+    const cuuint64_t strides[3] = {(cuuint64_t)((st[2] ? st[2] : dh) * 2), (cuuint64_t)(st[1] * 2),
+                                   (cuuint64_t)((st[0] ? st[0] : dh) * 2)};
+    const cuuint32_t box[4] = {64, box_heads, box_tokens, 1}, estr[4] = {1, 1, 1, 1};
+    return ct_encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, l2,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// 16-byte aligned rows, and strides that a tensor map takes.
+bool ct_strides_ok(const void* base, const int64_t st[3], int64_t T) {
+    if (reinterpret_cast<uintptr_t>(base) & 15) return false;
+    for (int i = 0; i < 3; ++i)
+        if (st[i] % 8 != 0 || st[i] >= ((int64_t)1 << 38)) return false;
+    return T == 1 || st[1] > 0;
+}
+
+template <int DH>
+cudaError_t launch_ct(const CrossDesc& d, const DeviceInfo& dev, cudaStream_t s) {
+    using L = CtLayout<DH>;
+    const int G = (int)(d.H / d.Hkv), TT = CT_ROWS / G;
+    const int64_t os[3] = {d.Tq * d.H * d.dh, d.H * d.dh, d.dh};
+    alignas(64) CUtensorMap mq, mk, mv, mo;
+    if (!ct_map(&mq, d.q, d.qs, d.B, d.Tq, d.H, d.dh, G, TT, CU_TENSOR_MAP_L2_PROMOTION_L2_128B) ||
+        !ct_map(&mk, d.k, d.ks, d.B, d.Tk, d.Hkv, d.dh, 1, CT_KEYS, CU_TENSOR_MAP_L2_PROMOTION_L2_128B) ||
+        !ct_map(&mv, d.v, d.vs, d.B, d.Tk, d.Hkv, d.dh, 1, CT_KEYS, CU_TENSOR_MAP_L2_PROMOTION_L2_128B) ||
+        !ct_map(&mo, d.o, os, d.B, d.Tq, d.H, d.dh, G, TT, CU_TENSOR_MAP_L2_PROMOTION_NONE))
+        return cudaErrorInvalidValue;
+    CtParams p;
+    p.kv_lens = d.kv_lens;
+    p.B = (int)d.B;
+    p.Tq = (int)d.Tq;
+    p.Tk = (int)d.Tk;
+    p.Hkv = (int)d.Hkv;
+    p.G = G;
+    p.TT = TT;
+    p.npairs = (int)((d.Tq + 2 * TT - 1) / (2 * TT));
+    p.items = (int)(d.B * d.Hkv * p.npairs);
+    p.qb = d.qs[0] != 0;
+    p.kb = d.ks[0] != 0;
+    p.kh = d.ks[2] != 0;
+    p.vb = d.vs[0] != 0;
+    p.vh = d.vs[2] != 0;
+    p.scale_log2 = (float)(d.scale * 1.4426950408889634);
+    p.err = dev.err_word;
+    static std::atomic<uint64_t> attr{0};
+    const cudaError_t e = set_smem_limit_once(cross_tc_kernel<DH>, L::SMEM, attr);
+    if (e != cudaSuccess) return e;
+    const int grid = p.items < dev.num_sms ? p.items : dev.num_sms;
+    return launch_dependent(cross_tc_kernel<DH>, dim3(grid), dim3(CT_THREADS), L::SMEM, s, mq, mk, mv, mo, p);
+}
+
+}  // namespace
+
+bool cross_tc_supported(const CrossDesc& d) {
+    if (d.dt != DT_BF16 || (d.dh != 64 && d.dh != 80 && d.dh != 96 && d.dh != 128)) return false;
+    const int64_t G = d.H / d.Hkv, lim = 0x7fffffff;
+    // positive scales only: the row maximum is taken before scaling
+    if (!((float)(d.scale * 1.4426950408889634) > 0.f) || !(d.scale < 1e30) || G > CT_ROWS) return false;
+    if (d.Tq > lim - 1024 || d.Tk > lim - 1024 || d.H > lim || d.B > lim) return false;
+    if (d.B > lim / (d.Hkv * ((d.Tq * G + 1) / 2 + 1))) return false;   // items, at two rows each
+    if (d.H > 1 && d.qs[2] == 0) return false;
+    const int64_t os[3] = {d.Tq * d.H * d.dh, d.H * d.dh, d.dh};
+    return ct_strides_ok(d.q, d.qs, d.Tq) && ct_strides_ok(d.k, d.ks, d.Tk) && ct_strides_ok(d.v, d.vs, d.Tk) &&
+           ct_strides_ok(d.o, os, d.Tq) && ct_encode_fn() != nullptr;
+}
+
+cudaError_t launch_cross_tc(const CrossDesc& d, const DeviceInfo& dev, cudaStream_t s) {
+    switch (d.dh) {
+        case 64: return launch_ct<64>(d, dev, s);
+        case 80: return launch_ct<80>(d, dev, s);
+        case 96: return launch_ct<96>(d, dev, s);
+        case 128: return launch_ct<128>(d, dev, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace vit

@@ -252,6 +252,9 @@ struct CrossDesc {
     void* o;
 };
 constexpr int64_t kCrossMaxHead = 512;
+// Many queries on the tensor cores (attention_cross_tc.cu): bf16, head widths 64, 80, 96 and 128.
+bool cross_tc_supported(const CrossDesc& d);
+cudaError_t launch_cross_tc(const CrossDesc& d, const DeviceInfo& dev, cudaStream_t s);
 cudaError_t launch_cross_attention(const CrossDesc& d, const DeviceInfo& dev, cudaStream_t s);
 
 }  // namespace vit
