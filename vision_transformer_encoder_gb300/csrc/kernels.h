@@ -252,6 +252,9 @@ struct CrossDesc {
     void* o;
 };
 constexpr int64_t kCrossMaxHead = 512;
+// Few queries (attention_cross_rows.cu): bf16, at most 16 query rows per key head.
+bool cross_rows_supported(const CrossDesc& d);
+cudaError_t launch_cross_rows(const CrossDesc& d, const DeviceInfo& dev, cudaStream_t s);
 // Many queries on the tensor cores (attention_cross_tc.cu): bf16, head widths 64, 80, 96 and 128.
 bool cross_tc_supported(const CrossDesc& d);
 cudaError_t launch_cross_tc(const CrossDesc& d, const DeviceInfo& dev, cudaStream_t s);
