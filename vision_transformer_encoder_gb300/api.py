@@ -447,28 +447,31 @@ def attention(qkv, H, out=None, stream=None):
 
 
 # ---- serving stages: rms norm, 8-bit products, cross attention -------------------------
-# These are called once per layer and token, so their marshalling is kept short: raw pointers
-# as integers, the device switched only when it is not current, one stream look-up.
+# These are called once per layer and token, and a call costs the host more than the GPU: the
+# marshalling checks each operand once, leaves tensors that it has just made unchecked, passes raw
+# pointers as integers and switches the device only when it is not current.
 
-def _need(t, name, device, dtype, shape):
-    """t is a contiguous CUDA tensor on device, of dtype (None: any) and shape."""
-    if not t.is_cuda or t.device != device:
-        raise ValueError("%s must be a CUDA tensor on %s" % (name, device))
+def _fits(t, dtype, shape, index):
+    """t is a contiguous CUDA tensor of this dtype and shape on device `index`."""
+    return t.get_device() == index and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+
+
+def _refuse(name, t, dtype, shape, index):
+    """The reason why t does not fit."""
+    if t.get_device() != index or index < 0:
+        raise ValueError("%s must be a CUDA tensor%s" % (name, " on cuda:%d" % index if index >= 0 else ""))
     if dtype is not None and t.dtype != dtype:
         raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
     if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
+    raise ValueError("%s must be contiguous" % name)
+
+
+def _given(t, name, dtype, shape, index):
+    """Pointer of an operand of known dtype."""
+    if not _fits(t, dtype, shape, index):
+        _refuse(name, t, dtype, shape, index)
     return t.data_ptr()
-
-
-def _operand(t, name, device=None):
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
-    if device is not None and t.device != device:
-        raise ValueError("%s must be a CUDA tensor on %s" % (name, device))
-    return t.device
 
 
 def _code(dt, allowed, what):
@@ -477,40 +480,36 @@ def _code(dt, allowed, what):
     return allowed[dt]
 
 
+def _torch_stream(stream, index):
+    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=index)
+
+
 def _alloc(shape, dtype, device, stream):
     """An output of a call on `stream`, from that stream's memory."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(_torch_stream(stream, device)):
+    with torch.cuda.stream(_torch_stream(stream, device.index)):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _torch_stream(stream, device):
-    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
-
-
-def _invoke(what, fn, device, stream, tensors, args):
-    """fn(*args, stream) with `device` current; raises on a non-zero status. With an explicit
+def _invoke(what, fn, index, stream, tensors, args):
+    """fn(*args, stream) with device `index` current; raises on a non-zero status. With an explicit
     stream the tensors are kept from reuse until the work queued there is done."""
     if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(device.index)
+        handle = torch._C._cuda_getCurrentRawStream(index)
     else:
-        ts = _torch_stream(stream, device)
+        ts = _torch_stream(stream, index)
         handle = ts.cuda_stream
         for t in tensors:
             if t is not None:
                 t.record_stream(ts)
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == index:
         rc = fn(*args, handle)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             rc = fn(*args, handle)
     if rc != 0:
         raise VitError(rc, what)
-
-
-def _scale_shape(rows, cols):
-    return (rows, (cols + 127) // 128)
 
 
 def rmsnorm(x, eps, gamma=None, residual=None, out_dtype=None, out=None, scales=None, sum_out=None, stream=None):
@@ -523,60 +522,83 @@ def rmsnorm(x, eps, gamma=None, residual=None, out_dtype=None, out=None, scales=
     dtype (may be the residual or x itself); a new tensor when not given.
     Returns out; (out, scales) in 8 bits; with a residual, also the sum as the last element."""
     lib = _lib or load_library()
-    device = _operand(x, "x")
-    shape, xd = x.shape, x.dtype
-    if not shape or not x.numel():
+    shape, xd, index = x.shape, x.dtype, x.get_device()
+    n = x.numel()
+    if not shape or not n:
         raise ValueError("x must have at least one element and a last dimension")
-    D = shape[-1]
-    rows = x.numel() // D
-    xp = _need(x, "x", device, None, shape)
     xc = _code(xd, _DT, "x")
+    if index < 0 or not x.is_contiguous():
+        _refuse("x", x, None, shape, index)
+    device = x.device
+    D = shape[-1]
+    rows = n // D
     od = out_dtype if out_dtype is not None else (out.dtype if out is not None else xd)
     oc = _code(od, _DT8, "out")
-    gp, gc, rp, rc_, sp, cp = None, xc, None, xc, None, None
+    gp = rp = sp = cp = None
+    gc = rc = xc
     if gamma is not None:
-        gp, gc = _need(gamma, "gamma", device, None, (D,)), _code(gamma.dtype, _DT, "gamma")
+        gc = _code(gamma.dtype, _DT, "gamma")
+        gp = _given(gamma, "gamma", gamma.dtype, (D,), index)
     if residual is not None:
-        rp, rc_ = _need(residual, "residual", device, None, shape), _code(residual.dtype, _DT, "residual")
+        rd = residual.dtype
+        rc = _code(rd, _DT, "residual")
+        rp = _given(residual, "residual", rd, shape, index)
         if sum_out is None:
-            sum_out = _alloc(shape, residual.dtype, device, stream)
-        sp = _need(sum_out, "sum_out", device, residual.dtype, shape)
+            sum_out = _alloc(shape, rd, device, stream)
+            sp = sum_out.data_ptr()
+        else:
+            sp = _given(sum_out, "sum_out", rd, shape, index)
     elif sum_out is not None:
         raise ValueError("sum_out needs a residual")
     if out is None:
         out = _alloc(shape, od, device, stream)
-    op = _need(out, "out", device, od, shape)
+        op = out.data_ptr()
+    else:
+        op = _given(out, "out", od, shape, index)
     if oc == VIT_E4M3:
         if scales is None:
-            scales = _alloc(_scale_shape(rows, D), torch.float32, device, stream)
-        cp = _need(scales, "scales", device, torch.float32, _scale_shape(rows, D))
+            scales = _alloc((rows, (D + 127) // 128), torch.float32, device, stream)
+            cp = scales.data_ptr()
+        else:
+            cp = _given(scales, "scales", torch.float32, (rows, (D + 127) // 128), index)
     elif scales is not None:
         raise ValueError("scales belong to a float8_e4m3fn output")
-    _invoke("vit_rmsnorm", lib.vit_rmsnorm, device, stream, (x, residual, gamma, sum_out, out, scales),
-            (xp, xc, rp, rc_, rows, D, eps, gp, gc, sp, op, oc, cp))
+    _invoke("vit_rmsnorm", lib.vit_rmsnorm, index, stream, (x, residual, gamma, sum_out, out, scales),
+            (x.data_ptr(), xc, rp, rc, rows, D, eps, gp, gc, sp, op, oc, cp))
     if oc == VIT_E4M3:
         return (out, scales) if residual is None else (out, scales, sum_out)
     return out if residual is None else (out, sum_out)
+
+
+def _quantized(x, oshape, sshape, out, scales, stream, index):
+    """The outputs of a quantisation, made or checked, and their pointers."""
+    if out is None:
+        out = _alloc(oshape, _F8, x.device, stream)
+        op = out.data_ptr()
+    else:
+        op = _given(out, "out", _F8, oshape, index)
+    if scales is None:
+        scales = _alloc(sshape, torch.float32, x.device, stream)
+        sp = scales.data_ptr()
+    else:
+        sp = _given(scales, "scales", torch.float32, sshape, index)
+    return out, scales, op, sp
 
 
 def quantize(x, out=None, scales=None, stream=None):
     """x (..., K), bf16 or fp32, in 8 bits: (q (..., K) float8_e4m3fn, scales (rows, ceil(K / 128))
     fp32), one scale for each 128 columns of a row; a value is q * scale."""
     lib = _lib or load_library()
-    device = _operand(x, "x")
-    shape = x.shape
-    if not shape or not x.numel():
+    shape, index, n = x.shape, x.get_device(), x.numel()
+    if not shape or not n:
         raise ValueError("x must have at least one element and a last dimension")
-    K = shape[-1]
-    rows = x.numel() // K
-    xp = _need(x, "x", device, None, shape)
     xc = _code(x.dtype, _DT, "x")
-    if out is None:
-        out = _alloc(shape, _F8, device, stream)
-    if scales is None:
-        scales = _alloc(_scale_shape(rows, K), torch.float32, device, stream)
-    qp, sp = _need(out, "out", device, _F8, shape), _need(scales, "scales", device, torch.float32, _scale_shape(rows, K))
-    _invoke("vit_quantize", lib.vit_quantize, device, stream, (x, out, scales), (xp, xc, rows, K, qp, sp))
+    if index < 0 or not x.is_contiguous():
+        _refuse("x", x, None, shape, index)
+    K = shape[-1]
+    rows = n // K
+    out, scales, op, sp = _quantized(x, shape, (rows, (K + 127) // 128), out, scales, stream, index)
+    _invoke("vit_quantize", lib.vit_quantize, index, stream, (x, out, scales), (x.data_ptr(), xc, rows, K, op, sp))
     return out, scales
 
 
@@ -584,19 +606,16 @@ def quantize_weight(w, out=None, scales=None, stream=None):
     """A weight w (K, N), bf16 or fp32, as linear_fp8 takes it: (q (N, K) float8_e4m3fn, the
     transpose, scales (ceil(N / 128), ceil(K / 128)) fp32), one scale for each 128 x 128 block."""
     lib = _lib or load_library()
-    device = _operand(w, "w")
-    if w.dim() != 2 or not w.numel():
+    shape, index = w.shape, w.get_device()
+    if len(shape) != 2 or not w.numel():
         raise ValueError("w must be a matrix (K, N) with at least one element")
-    K, N = w.shape
-    wp = _need(w, "w", device, None, w.shape)
     wc = _code(w.dtype, _DT, "w")
-    blocks = ((N + 127) // 128, (K + 127) // 128)
-    if out is None:
-        out = _alloc((N, K), _F8, device, stream)
-    if scales is None:
-        scales = _alloc(blocks, torch.float32, device, stream)
-    qp, sp = _need(out, "out", device, _F8, (N, K)), _need(scales, "scales", device, torch.float32, blocks)
-    _invoke("vit_quantize_weight", lib.vit_quantize_weight, device, stream, (w, out, scales), (wp, wc, K, N, qp, sp))
+    if index < 0 or not w.is_contiguous():
+        _refuse("w", w, None, shape, index)
+    K, N = shape
+    out, scales, op, sp = _quantized(w, (N, K), ((N + 127) // 128, (K + 127) // 128), out, scales, stream, index)
+    _invoke("vit_quantize_weight", lib.vit_quantize_weight, index, stream, (w, out, scales),
+            (w.data_ptr(), wc, K, N, op, sp))
     return out, scales
 
 
@@ -610,54 +629,62 @@ def linear_fp8(a, a_scales, w, w_scales, bias=None, residual=None, epilogue=EPI_
     out_dtype: bf16 (default), fp32 or float8_e4m3fn. Returns out, or (out, out_scales) in 8 bits,
     out_scales (rows, ceil(N / 128)). out may be the residual itself where the types agree."""
     lib = _lib or load_library()
-    device = _operand(a, "a")
-    shape = a.shape
-    if not shape or not a.numel() or w.dim() != 2 or not w.numel():
+    shape, wshape, index, n = a.shape, w.shape, a.get_device(), a.numel()
+    if not shape or not n or len(wshape) != 2 or not w.numel():
         raise ValueError("a must be (..., K) and w (N, K), with at least one element")
-    N, K = w.shape
+    N, K = wshape
     if shape[-1] != K:
         raise ValueError("a has %d columns, w %d" % (shape[-1], K))
-    M = a.numel() // K
+    if index < 0:
+        _refuse("a", a, _F8, shape, index)
+    M = n // K
     kb, nb = (K + 127) // 128, (N + 127) // 128
     oshape = shape[:-1] + (N,)
-    ap, wp = _need(a, "a", device, _F8, shape), _need(w, "w", device, _F8, w.shape)
-    asp = _need(a_scales, "a_scales", device, torch.float32, (M, kb))
-    wsp = _need(w_scales, "w_scales", device, torch.float32, (nb, kb))
-    bp, bc, rp, rc_, osp = None, 0, None, 0, None
+    ap, wp = _given(a, "a", _F8, shape, index), _given(w, "w", _F8, wshape, index)
+    asp = _given(a_scales, "a_scales", torch.float32, (M, kb), index)
+    wsp = _given(w_scales, "w_scales", torch.float32, (nb, kb), index)
+    bp = rp = osp = None
+    bc = rc = 0
     if bias is not None:
-        bp, bc = _need(bias, "bias", device, None, (N,)), _code(bias.dtype, _DT, "bias")
+        bc = _code(bias.dtype, _DT, "bias")
+        bp = _given(bias, "bias", bias.dtype, (N,), index)
     if residual is not None:
-        rp, rc_ = _need(residual, "residual", device, None, oshape), _code(residual.dtype, _DT, "residual")
+        rc = _code(residual.dtype, _DT, "residual")
+        rp = _given(residual, "residual", residual.dtype, oshape, index)
     od = out_dtype if out_dtype is not None else (out.dtype if out is not None else torch.bfloat16)
     oc = _code(od, _DT8, "out")
     if out is None:
-        out = _alloc(oshape, od, device, stream)
-    op = _need(out, "out", device, od, oshape)
+        out = _alloc(oshape, od, a.device, stream)
+        op = out.data_ptr()
+    else:
+        op = _given(out, "out", od, oshape, index)
     if oc == VIT_E4M3:
         if out_scales is None:
-            out_scales = _alloc((M, nb), torch.float32, device, stream)
-        osp = _need(out_scales, "out_scales", device, torch.float32, (M, nb))
+            out_scales = _alloc((M, nb), torch.float32, a.device, stream)
+            osp = out_scales.data_ptr()
+        else:
+            osp = _given(out_scales, "out_scales", torch.float32, (M, nb), index)
     elif out_scales is not None:
         raise ValueError("out_scales belong to a float8_e4m3fn output")
-    _invoke("vit_linear_fp8", lib.vit_linear_fp8, device, stream,
+    _invoke("vit_linear_fp8", lib.vit_linear_fp8, index, stream,
             (a, a_scales, w, w_scales, bias, residual, out, out_scales),
-            (ap, asp, wp, wsp, bp, bc, rp, rc_, M, K, N, int(epilogue), op, oc, osp))
+            (ap, asp, wp, wsp, bp, bc, rp, rc, M, K, N, int(epilogue), op, oc, osp))
     return (out, out_scales) if oc == VIT_E4M3 else out
 
 
-def _strided(t, name, device, dtype, own):
+_Strides = _i64 * 3
+
+
+def _strided(t, name, dtype, index):
     """Pointer and (sequence, token, head) strides of t (B, T, heads, dh); None when contiguous."""
-    if t.dim() != 4:
-        raise ValueError("%s must be (B, T, heads, dh)" % name)
-    _operand(t, name, device)
-    if t.dtype != dtype:
-        raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if t.get_device() != index or t.dtype is not dtype:
+        _refuse(name, t, dtype, t.shape, index)
     if t.is_contiguous():
         return t.data_ptr(), None
-    st = t.stride()
-    if st[3] != 1 and own[3] != 1:
+    b, u, h, c = t.stride()
+    if c != 1 and t.shape[3] != 1:
         raise ValueError("%s: the elements of a head must be contiguous" % name)
-    return t.data_ptr(), (_i64 * 3)(st[0], st[1], st[2])
+    return t.data_ptr(), _Strides(b, u, h)
 
 
 def cross_attention(q, k, v, kv_lens=None, scale=None, out=None, stream=None):
@@ -669,23 +696,26 @@ def cross_attention(q, k, v, kv_lens=None, scale=None, out=None, stream=None):
     any strides over sequences, tokens and heads, such as the halves of a fused key and value
     projection; the elements of a head are contiguous."""
     lib = _lib or load_library()
-    device = _operand(q, "q")
-    dt = q.dtype
-    if q.dim() != 4 or k.dim() != 4 or not q.numel() or not k.numel():
+    dt, index, qshape, kshape = q.dtype, q.get_device(), q.shape, k.shape
+    if len(qshape) != 4 or len(kshape) != 4 or not q.numel() or not k.numel():
         raise ValueError("q must be (B, Tq, H, dh) and k (B, Tk, Hkv, dh), with at least one element")
-    B, Tq, H, dh = q.shape
-    Tk, Hkv = k.shape[1], k.shape[2]
-    if k.shape != (B, Tk, Hkv, dh) or v.shape != k.shape:
-        raise ValueError("q %s, k %s and v %s do not fit" % (tuple(q.shape), tuple(k.shape), tuple(v.shape)))
+    B, Tq, H, dh = qshape
+    kb, Tk, Hkv, kd = kshape
+    if kb != B or kd != dh or v.shape != kshape:
+        raise ValueError("q %s, k %s and v %s do not fit" % (tuple(qshape), tuple(kshape), tuple(v.shape)))
     code = _code(dt, _DT, "q")
-    qp, qs = _strided(q, "q", device, dt, q.shape)
-    kp, ks = _strided(k, "k", device, dt, k.shape)
-    vp, vs = _strided(v, "v", device, dt, v.shape)
-    lp = None if kv_lens is None else _need(kv_lens, "kv_lens", device, torch.int32, (B,))
+    if index < 0:
+        _refuse("q", q, dt, qshape, index)
+    qp, qs = _strided(q, "q", dt, index)
+    kp, ks = _strided(k, "k", dt, index)
+    vp, vs = _strided(v, "v", dt, index)
+    lp = None if kv_lens is None else _given(kv_lens, "kv_lens", torch.int32, (B,), index)
     if out is None:
-        out = _alloc((B, Tq, H, dh), dt, device, stream)
-    op = _need(out, "out", device, dt, (B, Tq, H, dh))
-    _invoke("vit_cross_attention", lib.vit_cross_attention, device, stream, (q, k, v, kv_lens, out),
+        out = _alloc(qshape, dt, q.device, stream)
+        op = out.data_ptr()
+    else:
+        op = _given(out, "out", dt, qshape, index)
+    _invoke("vit_cross_attention", lib.vit_cross_attention, index, stream, (q, k, v, kv_lens, out),
             (qp, qs, kp, ks, vp, vs, lp, B, Tq, Tk, H, Hkv, dh, dh ** -0.5 if scale is None else scale, code, op))
     return out
 
