@@ -16,8 +16,17 @@ namespace vit {
 
 constexpr int kFp8Block = 128;   // columns (and, for weights, rows) that share one scale
 
+// The quotient as a product with the rounded 1 / 448, at most one unit in the last place off, and
+// the codes from the hardware reciprocal of the scale, likewise: IEEE division and reciprocal
+// cost the HBM-bound kernels a third of their time (norm of 16400 x 1280 to e4m3: 37.6 us).
 __device__ __forceinline__ float fp8_block_scale(float amax) {
-    return fmaxf(__fdiv_rn(amax, 448.f), 1.17549435e-38f);
+    return fmaxf(amax * (1.f / 448.f), 1.17549435e-38f);
+}
+// 1 / scale; scales lie between 2^-126 and 2^120, or are infinite.
+__device__ __forceinline__ float fp8_inverse(float scale) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(scale));
+    return r;
 }
 
 // Two floats as two e4m3 codes, a in the low byte.

@@ -346,7 +346,7 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                     ptx::named_bar_sync(1 + quarter, 64);
                     amax = fmaxf(amax, mx[(half ^ 1) * 128 + quarter * 32 + lane]);
                 }
-                const float sc = fp8_block_scale(amax), inv = __frcp_rn(sc);
+                const float sc = fp8_block_scale(amax), inv = fp8_inverse(sc);
                 if (row < d.M && n0 < d.N && (BN == 256 || half == 0) && !failed)
                     d.out_scales[row * nblk + n0 / kFp8Block] = sc;
                 if (p.out_tma) {
@@ -576,7 +576,7 @@ gemm_fp8_generic_kernel(const Fp8GemmDesc d) {
             const int64_t n = n0 + c + 16 * j;
             if (m >= d.M || n >= d.N) continue;
             const int64_t at = m * d.N + n;
-            if (d.out_dt == DT_E4M3) static_cast<uint8_t*>(d.out)[at] = fp8_pack1(__fdiv_rn(acc[j], sc));
+            if (d.out_dt == DT_E4M3) static_cast<uint8_t*>(d.out)[at] = fp8_pack1(acc[j] * fp8_inverse(sc));
             else if (d.out_dt == DT_F32) static_cast<float*>(d.out)[at] = acc[j];
             else static_cast<__nv_bfloat16*>(d.out)[at] = __float2bfloat16_rn(acc[j]);
         }

@@ -5,6 +5,13 @@
 // new residual stream; sums of squares are fp32 over at most a few hundred terms per thread and
 // then a tree, so their relative error stays far below one bf16 step.
 //
+// Fast kernel (D % 8 == 0, 16-byte aligned, D up to 16384): a row is read once, by the threads of a
+// group of 1 to 16 warps, 8 elements per thread and step, and stays in registers as fp32 sums until
+// its mean square is known. Sixteen neighbouring threads hold 128 columns, so an e4m3 block's
+// scale is a maximum over half a warp. Bound by HBM: with many rows one warp takes a row of up to
+// 2048, so nothing is exchanged between warps and the loads of many rows overlap; with few rows
+// more warps share a row, because latency counts.
+//
 // Generic kernel: one CTA per row, any width, alignment and type. Two passes over x and the
 // residual; an element is read and then overwritten by the same thread, so the sum may be
 // stored in place of either.
@@ -105,7 +112,7 @@ rmsnorm_generic_kernel(const TX* x, const TR* residual, int64_t rows, int64_t D,
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int64_t c = b * kFp8Block + i * 32 + lane;
-                    if (c < D) out[row * D + c] = fp8_pack1(__fdiv_rn((float)y[i], sc));
+                    if (c < D) out[row * D + c] = fp8_pack1((float)y[i] * fp8_inverse(sc));
                 }
             } else {
 #pragma unroll
@@ -118,6 +125,166 @@ rmsnorm_generic_kernel(const TX* x, const TR* residual, int64_t rows, int64_t D,
     }
 }
 
+// 8 consecutive elements, 16-byte aligned. x may be overwritten by the same thread later, so
+// these are plain loads.
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const float2 a = unpack_bf16x2(u.x), b = unpack_bf16x2(u.y), c = unpack_bf16x2(u.z), d = unpack_bf16x2(u.w);
+    v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+    v[4] = c.x; v[5] = c.y; v[6] = d.x; v[7] = d.y;
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                              pack_bf16x2(v[6], v[7]));
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// G warps per row, NV steps of 8 columns per thread; blockDim.x = 32 G times the rows of a CTA
+// (one row when G > 1).
+template <typename TX, typename TR, typename TO, int NV>
+__global__ void __launch_bounds__(512, NV <= 5 ? 2 : 1)   // 64 registers up to 1280 columns per warp: 32 warps per SM
+rmsnorm_fast_kernel(const TX* x, const TR* residual, int64_t rows, int D, float eps, const void* __restrict__ gamma,
+                    int gamma_dt, TR* sum, TO* out, float* __restrict__ scales, int G) {
+    constexpr bool Q = std::is_same<TO, uint8_t>::value;
+    __shared__ float part[2][16];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, threads = 32 * G;
+    const int t = G == 1 ? lane : (int)threadIdx.x;
+    const int64_t row = G == 1 ? (int64_t)blockIdx.x * (blockDim.x >> 5) + warp : (int64_t)blockIdx.x;
+    if (row >= rows) return;   // whole warps, and whole CTAs when warps share a row
+    const int64_t at = row * D;
+    float v[NV][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * threads + t) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+        if (c < D) {
+            load8(x + at + c, v[i]);
+            if (residual) {
+                float r[8];
+                load8(residual + at + c, r);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[i][j] += r[j];
+            }
+        }
+    }
+    auto total = [&](float w, int round) {
+        w = warp_sum(w);
+        if (G > 1) {
+            if (lane == 0) part[round][warp] = w;
+            __syncthreads();
+            w = lane < G ? part[round][lane] : 0.f;
+            w = warp_sum(w);
+        }
+        return w;
+    };
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+    if (sum) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * threads + t) * 8;
+            if (c < D) store8(sum + at + c, v[i]);
+        }
+    }
+    ss = total(ss, 0);
+    float e = eps;
+    if (ss > kSquaresLimit) {   // squares past the fp32 range: again from scaled values
+        float s2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[i][j] *= kPreScale;
+                s2 = fmaf(v[i][j], v[i][j], s2);
+            }
+        ss = total(s2, 1);
+        e = 0.f;   // far below half a unit of the scaled mean square
+    }
+    const float r = 1.f / sqrtf(ss / (float)D + e);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * threads + t) * 8;
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = v[i][j] * r;
+        if (gamma && c < D) {
+            float g[8];
+            if (gamma_dt == DT_BF16) load8(static_cast<const __nv_bfloat16*>(gamma) + c, g);
+            else load8(static_cast<const float*>(gamma) + c, g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] *= g[j];
+        }
+        if constexpr (Q) {
+            // NaN must not hide: fmaxf drops it, but its code below is NaN whatever the scale
+            float amax = fmaxf(fmaxf(fmaxf(fabsf(y[0]), fabsf(y[1])), fmaxf(fabsf(y[2]), fabsf(y[3]))),
+                               fmaxf(fmaxf(fabsf(y[4]), fabsf(y[5])), fmaxf(fabsf(y[6]), fabsf(y[7]))));
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            const float sc = fp8_block_scale(amax), inv = fp8_inverse(sc);
+            if (c < D) {
+                if ((lane & 15) == 0) scales[row * ((D + kFp8Block - 1) / kFp8Block) + c / kFp8Block] = sc;
+                *reinterpret_cast<uint2*>(out + at + c) =
+                    make_uint2(fp8_pack4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+                               fp8_pack4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+            }
+        } else {
+            if (c < D) store8(out + at + c, y);
+        }
+    }
+}
+
+template <typename TX, typename TR, typename TO, int NV>
+cudaError_t fast_inst(const RmsNormDesc& d, int G, cudaStream_t s) {
+    const int per = G == 1 ? 8 : 1;   // rows per CTA
+    return launch_dependent(rmsnorm_fast_kernel<TX, TR, TO, NV>, dim3((unsigned)((d.rows + per - 1) / per)),
+                            dim3(32 * G * per), 0, s, static_cast<const TX*>(d.x), static_cast<const TR*>(d.residual),
+                            d.rows, (int)d.D, (float)d.eps, d.gamma, d.gamma_dt, static_cast<TR*>(d.sum),
+                            static_cast<TO*>(d.out), d.scales, G);
+}
+
+template <typename TX, typename TR, typename TO>
+cudaError_t fast(const RmsNormDesc& d, const DeviceInfo& dev, cudaStream_t s) {
+    // a warp per row while the rows fill the GPU's warp slots; otherwise as many warps as
+    // leave every thread one step, up to 16
+    const int steps = (int)((d.D + 255) / 256);   // of one warp
+    int G = 1;
+    const bool few = d.rows < 16 * (int64_t)dev.num_sms;
+    while (G < 16 && (steps > 8 * G || (few && steps > G))) G *= 2;
+    const int nv = (steps + G - 1) / G;
+    switch (nv) {
+        case 1: return fast_inst<TX, TR, TO, 1>(d, G, s);
+        case 2: return fast_inst<TX, TR, TO, 2>(d, G, s);
+        case 3: return fast_inst<TX, TR, TO, 3>(d, G, s);
+        case 4: return fast_inst<TX, TR, TO, 4>(d, G, s);
+        case 5: return fast_inst<TX, TR, TO, 5>(d, G, s);
+        case 6: return fast_inst<TX, TR, TO, 6>(d, G, s);
+        case 7: return fast_inst<TX, TR, TO, 7>(d, G, s);
+        case 8: return fast_inst<TX, TR, TO, 8>(d, G, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+bool fast_ok(const RmsNormDesc& d) {
+    const void* ps[] = {d.x, d.residual, d.gamma, d.sum, d.out};
+    for (const void* p : ps)
+        if (reinterpret_cast<uintptr_t>(p) & 15) return false;
+    return d.D % 8 == 0 && d.D <= 16384 && d.rows <= 0x7fffffff;
+}
+
 template <typename TX, typename TR, typename TO, typename A>
 cudaError_t generic(const RmsNormDesc& d, cudaStream_t s) {
     const unsigned grid = (unsigned)(d.rows < (1 << 20) ? d.rows : (1 << 20));
@@ -127,7 +294,12 @@ cudaError_t generic(const RmsNormDesc& d, cudaStream_t s) {
 }
 
 template <typename TX, typename TR>
-cudaError_t by_out(const RmsNormDesc& d, cudaStream_t s) {
+cudaError_t by_out(const RmsNormDesc& d, const DeviceInfo& dev, cudaStream_t s) {
+    if (fast_ok(d)) switch (d.out_dt) {
+        case DT_BF16: return fast<TX, TR, __nv_bfloat16>(d, dev, s);
+        case DT_F32: return fast<TX, TR, float>(d, dev, s);
+        case DT_E4M3: return fast<TX, TR, uint8_t>(d, dev, s);
+    }
     switch (d.out_dt) {
         case DT_BF16: return generic<TX, TR, __nv_bfloat16, float>(d, s);
         case DT_F32: return generic<TX, TR, float, float>(d, s);
@@ -140,8 +312,9 @@ cudaError_t by_out(const RmsNormDesc& d, cudaStream_t s) {
 
 cudaError_t launch_rmsnorm(const RmsNormDesc& d, const DeviceInfo& dev, cudaStream_t s) {
     if (d.x_dt == DT_F64) return generic<double, double, double, double>(d, s);
-    if (d.x_dt == DT_F32) return by_out<float, float>(d, s);
-    return d.residual_dt == DT_F32 ? by_out<__nv_bfloat16, float>(d, s) : by_out<__nv_bfloat16, __nv_bfloat16>(d, s);
+    if (d.x_dt == DT_F32) return by_out<float, float>(d, dev, s);
+    return d.residual_dt == DT_F32 ? by_out<__nv_bfloat16, float>(d, dev, s)
+                                     : by_out<__nv_bfloat16, __nv_bfloat16>(d, dev, s);
 }
 
 }  // namespace vit
