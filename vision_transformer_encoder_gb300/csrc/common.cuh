@@ -132,12 +132,19 @@ __device__ __forceinline__ void gelu_tanh_fast2(float& a, float& b) {
     f2_unpack(f2_fma(hz, f2_pack(tanh_approx(u0), tanh_approx(u1)), hz), a, b);
 }
 
-// tanh-approximation GELU to fp32 accuracy (about 2^-20 relative for z > -4): with
-// u = sqrt(2/pi) (z + 0.044715 z^3), 0.5 z (1 + tanh u) = z / (1 + exp(-2u)). One base-2
-// exponential and one division, both hardware approximations good to 2^-22.
-__device__ __forceinline__ float gelu_tanh_exp(float z) {
+// tanh-approximation GELU of a pair to fp32 accuracy (about 2^-20 relative): with
+// u = sqrt(2/pi) (z + 0.044715 z^3), 0.5 z (1 + tanh u) = z / (1 + exp(-2u)). The two quotients
+// share one hardware reciprocal, 1/a = b / (a b) and 1/b = a / (a b); exp is cut off at 2^60,
+// where the result is below 2^-53 |z| and the product of the denominators still in range.
+__device__ __forceinline__ unsigned long long gelu_tanh_exp2(unsigned long long z) {
     const float c0 = -2.f * 0.7978845608028654f * 1.4426950408889634f;   // -2 sqrt(2/pi) log2(e)
-    return __fdividef(z, 1.f + exp2_approx(z * fmaf(c0 * 0.044715f, z * z, c0)));
+    const float c1 = c0 * 0.044715f;
+    const unsigned long long t = f2_mul(z, f2_fma(f2_mul(z, z), f2_pack(c1, c1), f2_pack(c0, c0)));
+    float u0, u1, a0, a1, r;
+    f2_unpack(t, u0, u1);
+    f2_unpack(f2_add(f2_pack(exp2_approx(fminf(u0, 60.f)), exp2_approx(fminf(u1, 60.f))), f2_pack(1.f, 1.f)), a0, a1);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a0 * a1));
+    return f2_mul(z, f2_mul(f2_pack(r, r), f2_pack(a1, a0)));
 }
 
 // Accurate forms (library tanh) for the fp32 / fp64 paths.

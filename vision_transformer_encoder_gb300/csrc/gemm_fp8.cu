@@ -12,7 +12,9 @@
 // (two, in turn), and the epilogue warps add scale * block sum to fp32 registers while the tensor
 // cores make the next block.
 //   warp 0       MMA issue (the leader CTA's lane 0)
-//   warps 1-3    TMA: A rows; B rows, first and second half
+//   warps 1-3    TMA: a stage is four boxes, A and B rows in halves, dealt out to the three warps in
+//                turn (one thread's copies run one after another: with A's 16 KB on one warp the
+//                stages came in at half the rate)
 //   warps 4-11   promotion and epilogue: warp (quarter, half) keeps 32 rows x BN / 2 columns in
 //                registers, one row per thread, so the row's scale is one register and an e4m3
 //                output's 128-column scale needs no exchange (BN 256)
@@ -89,7 +91,8 @@ template <int BN> struct FpLayout {
     static constexpr int STAGES = BN == 256 ? 5 : 6;
     static constexpr int OFF_EPI = STAGES * STAGE;
     static constexpr int OFF_MAX = OFF_EPI + FP_EPI_WARPS * FP_STG;   // row maxima, BN 128 with e4m3
-    static constexpr int OFF_BAR = OFF_MAX + 2 * 2 * 128 * 4;
+    static constexpr int OFF_BIAS = OFF_MAX + 2 * 2 * 128 * 4;        // per warp: its columns' bias
+    static constexpr int OFF_BAR = OFF_BIAS + FP_EPI_WARPS * BN / 2 * 4;
     static constexpr int SMEM = OFF_BAR + 256 + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
@@ -100,17 +103,12 @@ struct FpParams {
     int out_tma;
 };
 
-// 32 values of this thread's row from column `col` on: bias, GELU or residual.
+// 32 sums of this thread's row from column `col` on, as 16 packed pairs: GELU or residual.
 template <int EPI>
-__device__ __forceinline__ void f8_finish32(const Fp8GemmDesc& d, int64_t row, int64_t col, int lane, float (&v)[32]) {
-    if (d.bias) {
-        const float b = col + lane < d.N ? load_f32(d.bias, d.bias_f32, col + lane) : 0.f;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, b, j);
-    }
+__device__ __forceinline__ void f8_finish32(const Fp8GemmDesc& d, int64_t row, int64_t col, unsigned long long (&v)[16]) {
     if constexpr (EPI == TC_EPI_GELU) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = gelu_tanh_exp(v[j]);
+        for (int j = 0; j < 16; ++j) v[j] = gelu_tanh_exp2(v[j]);
     }
     if constexpr (EPI == TC_EPI_RESID) {
         if (row < d.M) {
@@ -120,30 +118,32 @@ __device__ __forceinline__ void f8_finish32(const Fp8GemmDesc& d, int64_t row, i
                 const float* r = static_cast<const float*>(d.residual) + at;
                 if (whole && (reinterpret_cast<uintptr_t>(r) & 15) == 0) {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const float4 u = *reinterpret_cast<const float4*>(r + j);
-                        v[j] += u.x; v[j + 1] += u.y; v[j + 2] += u.z; v[j + 3] += u.w;
+                    for (int j = 0; j < 16; j += 2) {
+                        const float4 u = *reinterpret_cast<const float4*>(r + 2 * j);
+                        v[j] = f2_add(v[j], f2_pack(u.x, u.y));
+                        v[j + 1] = f2_add(v[j + 1], f2_pack(u.z, u.w));
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (col + j < d.N) v[j] += r[j];
+                    for (int j = 0; j < 16; ++j)
+                        v[j] = f2_add(v[j], f2_pack(col + 2 * j < d.N ? r[2 * j] : 0.f, col + 2 * j + 1 < d.N ? r[2 * j + 1] : 0.f));
                 }
             } else {
                 const __nv_bfloat16* r = static_cast<const __nv_bfloat16*>(d.residual) + at;
                 if (whole && (reinterpret_cast<uintptr_t>(r) & 15) == 0) {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
-                        const uint4 u = *reinterpret_cast<const uint4*>(r + j);
-                        const float2 a = unpack_bf16x2(u.x), b = unpack_bf16x2(u.y), c = unpack_bf16x2(u.z),
-                                     e = unpack_bf16x2(u.w);
-                        v[j] += a.x; v[j + 1] += a.y; v[j + 2] += b.x; v[j + 3] += b.y;
-                        v[j + 4] += c.x; v[j + 5] += c.y; v[j + 6] += e.x; v[j + 7] += e.y;
+                    for (int j = 0; j < 16; j += 4) {
+                        const uint4 u = *reinterpret_cast<const uint4*>(r + 2 * j);
+                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            v[j + q] = f2_add(v[j + q], f2_pack(__uint_as_float(w[q] << 16), __uint_as_float(w[q] & 0xFFFF0000u)));
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (col + j < d.N) v[j] += __bfloat162float(r[j]);
+                    for (int j = 0; j < 16; ++j)
+                        v[j] = f2_add(v[j], f2_pack(col + 2 * j < d.N ? __bfloat162float(r[2 * j]) : 0.f,
+                                                    col + 2 * j + 1 < d.N ? __bfloat162float(r[2 * j + 1]) : 0.f));
                 }
             }
         }
@@ -223,11 +223,15 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                     if (!ptx::mbar_wait_bounded<true>(empty + s, (u & 1) ^ 1, abort_flag)) { ok = false; break; }
                     if (warp == 1 && rank == 0) ptx::mbar_arrive_expect_tx(full + s, 2 * L::STAGE);
                     uint8_t* st = smem + s * L::STAGE;
-                    if (warp == 1)
-                        ptx::tma_load_2d_pair(st, &tmA, full0 + s * 8, kb * kFp8Block, m0);
-                    else
-                        ptx::tma_load_2d_pair(st + FP_A_BYTES + (warp - 2) * (L::B_BYTES / 2), &tmB, full0 + s * 8,
-                                              kb * kFp8Block, n0 + (warp - 2) * (BN / 4));
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {   // A rows 0-63, 64-127, then B's halves
+                        if ((it * 4 + x) % 3 != (uint32_t)(warp - 1)) continue;
+                        if (x < 2)
+                            ptx::tma_load_2d_pair(st + x * (FP_A_BYTES / 2), &tmA, full0 + s * 8, kb * kFp8Block, m0 + x * 64);
+                        else
+                            ptx::tma_load_2d_pair(st + FP_A_BYTES + (x - 2) * (L::B_BYTES / 2), &tmB, full0 + s * 8,
+                                                  kb * kFp8Block, n0 + (x - 2) * (BN / 4));
+                    }
                 }
             }
             if (!ok) {
@@ -278,7 +282,7 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         const uint32_t t_lane = tmem + half * COLS + ((uint32_t)(quarter * 32) << 16);
         uint8_t* stage = smem + L::OFF_EPI + (warp - 4) * FP_STG;
         const int64_t nblk = (d.N + kFp8Block - 1) / kFp8Block;
-        uint32_t it = 0, tcount = 0;
+        uint32_t it = 0, tcount = 0;   // block sums, tiles so far
         bool failed = false;   // a wait ran out: go on without waiting, store nothing
         // scales of block kb of tile t for this thread's row and this warp's columns
         auto scale_of = [&](int t, int kb) -> float {
@@ -290,55 +294,101 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             return sa * __ldg(d.w_scales + nb * kblocks + kb);
         };
         float s0 = scale_of(cluster, 0), s1 = scale_of(cluster, 1);
+        float bl[COLS / 32];
+        auto load_bias = [&](int t) {
+            if (!d.bias || t >= tiles) return;
+#pragma unroll
+            for (int j = 0; j < COLS / 32; ++j) {
+                const int64_t c = (int64_t)(t % n_tiles) * BN + half * COLS + lane * (COLS / 32) + j;
+                bl[j] = c < d.N ? load_f32(d.bias, d.bias_f32, c) : 0.f;
+            }
+        };
+        load_bias(cluster);
         for (int t = cluster; t < tiles; t += nclusters, ++tcount) {
             const int64_t row0 = (int64_t)(t / n_tiles) * FP_TILE_M + rank * 128 + quarter * 32, row = row0 + lane;
             const int64_t n0 = (int64_t)(t % n_tiles) * BN + half * COLS;
+            // sums start from the bias, COLS / 32 columns per lane, which arrived during the last tile
             unsigned long long acc[COLS / 2];
+            if (d.bias) {
+                float* sb = reinterpret_cast<float*>(smem + L::OFF_BIAS) + (warp - 4) * COLS;
+                __syncwarp();   // the previous tile's have been read
 #pragma unroll
-            for (int j = 0; j < COLS / 2; ++j) acc[j] = 0ull;
-            for (int kb = 0; kb < kblocks; ++kb, ++it) {
-                const uint32_t buf = it & 1;
-                const float s2 = scale_of(t, kb + 2);   // two blocks ahead
-                if (!failed && !__all_sync(0xffffffffu, ptx::mbar_wait_bounded(tfull + buf, (it >> 1) & 1, abort_flag))) {
+                for (int j = 0; j < COLS / 32; ++j) sb[lane * (COLS / 32) + j] = bl[j];
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < COLS / 4; ++j) {
+                    const float4 b = *reinterpret_cast<const float4*>(sb + 4 * j);
+                    acc[2 * j] = f2_pack(b.x, b.y);
+                    acc[2 * j + 1] = f2_pack(b.z, b.w);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < COLS / 2; ++j) acc[j] = 0ull;
+            }
+            // 32 columns at a time; the next 32 (of this block sum or of the next) are on their way
+            // from TMEM while these are added
+            constexpr int CH = COLS / 32;
+            uint32_t ra[32], rb[32];
+            auto ready = [&]() {   // the next block's sum is complete
+                if (!failed && !__all_sync(0xffffffffu, ptx::mbar_wait_bounded(tfull + (it & 1), (it >> 1) & 1, abort_flag))) {
                     failed = true;
                     if (lane == 0) f8_error(p.err, ERRBIT_TIMEOUT_EPILOGUE);
                     *abort_flag = 1;
                 }
                 ptx::tc_fence_after();
+            };
+            auto add = [&](int c, const uint32_t (&r)[32], unsigned long long ss) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    acc[c * 16 + j] = f2_fma(f2_pack(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), ss,
+                                             acc[c * 16 + j]);
+            };
+            ready();
+            ptx::tmem_ld_32x32b_x32(t_lane + (it & 1) * BN, ra);
+            for (int kb = 0; kb < kblocks; ++kb) {
+                const float s2 = scale_of(t, kb + 2);   // two blocks ahead
                 const unsigned long long ss = f2_pack(s0, s0);
 #pragma unroll
-                for (int c = 0; c < COLS / 32; ++c) {
-                    uint32_t r[32];
-                    ptx::tmem_ld_32x32b_x32(t_lane + buf * BN + c * 32, r);
-                    ptx::tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        acc[c * 16 + j] = f2_fma(f2_pack(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), ss,
-                                                 acc[c * 16 + j]);
+                for (int c = 0; c < CH; ++c) {
+                    uint32_t(&cur)[32] = (c & 1) ? rb : ra;
+                    uint32_t(&nxt)[32] = (c & 1) ? ra : rb;
+                    ptx::tmem_ld_wait_for(cur);
+                    if (c + 1 < CH) {
+                        ptx::tmem_ld_32x32b_x32(t_lane + (it & 1) * BN + (c + 1) * 32, nxt);
+                    } else {
+                        // this sum is in registers: its accumulator is free
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive_cluster_relaxed(tempty0 + (it & 1) * 8);   // orders TMEM reads only
+                        ++it;
+                        if (kb + 1 < kblocks) {
+                            ready();
+                            ptx::tmem_ld_32x32b_x32(t_lane + (it & 1) * BN, nxt);
+                        }
+                    }
+                    add(c, cur, ss);
                 }
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_cluster_relaxed(tempty0 + buf * 8);   // orders TMEM reads only
                 s0 = s1;
                 s1 = s2;
             }
-            // the next tile's first scales travel while this one is stored
+            // the next tile's first scales and bias travel while this one is stored
             s0 = scale_of(t + nclusters, 0);
             s1 = scale_of(t + nclusters, 1);
+            load_bias(t + nclusters);
             if (n0 >= d.N && !(OUT == DT_E4M3 && BN == 128)) continue;   // (there the two halves meet below)
             if constexpr (OUT == DT_E4M3) {
                 float amax = 0.f;
 #pragma unroll
                 for (int c = 0; c < COLS / 32; ++c) {
-                    float v[32];
+                    unsigned long long(&v)[16] = *reinterpret_cast<unsigned long long(*)[16]>(&acc[c * 16]);
+                    f8_finish32<EPI>(d, row, n0 + c * 32, v);
+                    // columns past N are products with zero rows: 0 (or NaN, which fmaxf drops)
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) f2_unpack(acc[c * 16 + j], v[2 * j], v[2 * j + 1]);
-                    f8_finish32<EPI>(d, row, n0 + c * 32, lane, v);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (n0 + c * 32 + j < d.N) amax = fmaxf(amax, fabsf(v[j]));
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) acc[c * 16 + j] = f2_pack(v[2 * j], v[2 * j + 1]);
+                    for (int j = 0; j < 16; ++j) {
+                        float a, b;
+                        f2_unpack(v[j], a, b);
+                        amax = fmaxf(amax, fmaxf(fabsf(a), fabsf(b)));
+                    }
                 }
                 if constexpr (BN == 128) {   // a block of 128 columns is two warps' halves
                     float* mx = reinterpret_cast<float*>(smem + L::OFF_MAX) + (tcount & 1) * 256;
@@ -347,6 +397,7 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                     amax = fmaxf(amax, mx[(half ^ 1) * 128 + quarter * 32 + lane]);
                 }
                 const float sc = fp8_block_scale(amax), inv = fp8_inverse(sc);
+                const unsigned long long inv2 = f2_pack(inv, inv);
                 if (row < d.M && n0 < d.N && (BN == 256 || half == 0) && !failed)
                     d.out_scales[row * nblk + n0 / kFp8Block] = sc;
                 if (p.out_tma) {
@@ -359,9 +410,9 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         float a, b, c, e;
-                        f2_unpack(acc[u * 8 + q * 2], a, b);
-                        f2_unpack(acc[u * 8 + q * 2 + 1], c, e);
-                        w[q] = fp8_pack4(a * inv, b * inv, c * inv, e * inv);
+                        f2_unpack(f2_mul(acc[u * 8 + q * 2], inv2), a, b);
+                        f2_unpack(f2_mul(acc[u * 8 + q * 2 + 1], inv2), c, e);
+                        w[q] = fp8_pack4(a, b, c, e);
                     }
                     if (p.out_tma) {
                         if constexpr (BN == 256) *f8_unit(stage, lane, u) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -388,11 +439,11 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 constexpr int UNIT = OUT == DT_F32 ? 32 : 64;
 #pragma unroll
                 for (int c = 0; c < COLS / 32; ++c) {
+                    const int64_t col = n0 + c * 32;
+                    f8_finish32<EPI>(d, row, col, *reinterpret_cast<unsigned long long(*)[16]>(&acc[c * 16]));
                     float v[32];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) f2_unpack(acc[c * 16 + j], v[2 * j], v[2 * j + 1]);
-                    const int64_t col = n0 + c * 32;
-                    f8_finish32<EPI>(d, row, col, lane, v);
                     if (p.out_tma) {
                         if ((c * 32) % UNIT == 0) {
                             if (lane == 0) ptx::bulk_wait_group_read<0>();
@@ -463,7 +514,7 @@ cudaError_t launch_pair_inst(const Fp8GemmDesc& d, const DeviceInfo& dev, cudaSt
     cudaError_t e = set_smem_limit_once(k, L::SMEM, attr);
     if (e != cudaSuccess) return e;
     alignas(64) CUtensorMap ma, mb, mo;
-    if (!f8_map(&ma, d.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, d.M, d.K, 128, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
+    if (!f8_map(&ma, d.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, d.M, d.K, 64, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
         !f8_map(&mb, d.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, d.N, d.K, BN / 4, CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
         return cudaErrorInvalidValue;
     FpParams p{d, dev.err_word, 0};
