@@ -99,7 +99,7 @@ cudaError_t generic(const CrossDesc& d, const DeviceInfo& dev, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_cross_attention(const CrossDesc& d, const DeviceInfo& dev, cudaStream_t s) {
-    if (cross_f32_supported(d)) return launch_cross_f32(d, s);
+    if (cross_f32_supported(d)) return launch_cross_f32(d, dev, s);
     if (cross_rows_supported(d)) return launch_cross_rows(d, dev, s);
     if (cross_tc_supported(d)) return launch_cross_tc(d, dev, s);
     if (d.dt == DT_F64) return generic<double, double>(d, dev, s);

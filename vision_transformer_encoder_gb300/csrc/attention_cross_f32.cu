@@ -1,225 +1,368 @@
-// attention_cross_f32.cu -- cross attention in fp32 on the CUDA cores: the mathematics of
-// attention_cross.cu for head widths 32, 48, 64, 80, 96, 112 and 128.
+// attention_cross_f32.cu -- cross attention in fp32: the mathematics of attention_cross.cu for head
+// widths up to 128 in steps of 4.
 //
-// A CTA of four warps takes 64 packed query rows (row = token * G + head of the group) of one key
-// head and walks the keys 64 at a time, K and V tiles arriving by cp.async a tile ahead. A thread
-// makes an 8 x 4 piece of S (rows 8 g .. 8 g + 7, keys c, c + 16, c + 32, c + 48) and the same rows
-// of O in columns c, c + 16, ...; the sixteen threads of a row group are half a warp, so the row
-// maxima are shuffles and P goes through shared memory inside one warp. 32 products need 12
-// shared-memory words: bound by the FP32 pipe. Warps whose sixteen rows hold no query skip the
-// arithmetic.
+// Products are 3xTF32 (hi hi + hi lo + lo hi, hi the 11 leading bits that the tensor cores read, lo the
+// rest) on mma.m16n8k8: relative to the sum of magnitudes off by 2^-20 or so, where fp32 chains of
+// this length are off by more. CUDA cores came out at half the rate: a thread's 8 x 8 piece needs
+// one product per cycle and scheduler and its operands from shared memory at 128 bytes a cycle
+// per SM, and reached half of either (8 x 197 queries over 288 to 577 keys of 12 heads of 64: 103 us).
+//
+// A CTA of four warps walks the keys of one (sequence, key head) 64 at a time, K and V tiles by TMA in
+// a ring that all warps read. Query rows are the n side of the products, S^T = K Q^T and
+// O^T = V^T P^T, eight or sixteen to a warp (packed row = token * G + head of the group):
+//   many rows (SPLIT false): 64 rows per CTA, sixteen to each warp; warps without rows skip the work
+//   few rows  (SPLIT true):  the same eight or sixteen rows in every warp, which takes 16 of the 64
+//                            keys; joined at the end through shared memory
+// Operands are read 16 bytes at a time from the 128-byte swizzled tiles without bank conflicts:
+// the order of the columns in a dot product is free, so thread c takes four consecutive columns
+// of its key for two k-steps; so is which column a row of V^T means; and P^T comes out of S^T by
+// 8 x 8 transposes of its upper and lower halves.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "cross_maps.cuh"
 #include "kernels.h"
 #include "launch.cuh"
+#include "ptx.cuh"
 
 namespace vit {
 namespace {
 
-constexpr int CF_ROWS = 64, CF_KEYS = 64, CF_THREADS = 128;
+constexpr int CF_KEYS = 64, CF_WARPS = 4, CF_BOX = CF_KEYS * 128;   // a box: 32 columns of 64 keys
 
-template <int DH> struct CfLayout {
-    static constexpr int LD = DH + 4;             // padded rows: 16-byte columns of eight keys in different banks
-    static constexpr int LDP = CF_KEYS + 4;
-    static constexpr int TILE = CF_KEYS * LD;     // floats of one K or V tile
-    static constexpr int OFF_Q = 0;
-    static constexpr int OFF_K = OFF_Q + CF_ROWS * LD;
-    static constexpr int OFF_V = OFF_K + 2 * TILE;
-    static constexpr int OFF_P = OFF_V + 2 * TILE;
-    static constexpr int SMEM = (OFF_P + CF_ROWS * LDP) * 4;
+template <int DHT> struct CfLayout {
+    static constexpr int NB = DHT / 32;                 // boxes of a K or V tile
+    static constexpr int STAGE = 2 * NB * CF_BOX;
+    static constexpr int STAGES = DHT <= 64 ? 3 : 2;
+    static constexpr int SMEM = STAGES * STAGE + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
-// 16 bytes global -> shared, zeros when !ok (nothing is read then).
-__device__ __forceinline__ void cp_async16(float* dst, const float* src, bool ok) {
-    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(ok ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int DH>
-__global__ void __launch_bounds__(CF_THREADS)
-cross_f32_kernel(const __grid_constant__ CrossDesc d, float scale_log2, int qtiles) {
-    using L = CfLayout<DH>;
-    constexpr int LD = L::LD, NC = DH / 16, V4 = DH / 4;
-    extern __shared__ __align__(16) float sm[];
-    float* sQ = sm + L::OFF_Q;
-    float* sK = sm + L::OFF_K;
-    float* sV = sm + L::OFF_V;
-    float* sP = sm + L::OFF_P;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = lane & 15, r0 = warp * 16 + (lane >> 4) * 8;
-    const int G = (int)(d.H / d.Hkv);
-    const int64_t rows = d.Tq * G;   // packed rows of one key head
-    const int qt = blockIdx.x % qtiles;
-    const int64_t bh = blockIdx.x / qtiles, b = bh / d.Hkv, h = bh % d.Hkv, first = (int64_t)qt * CF_ROWS;
+__device__ __forceinline__ uint32_t lo_bits(uint32_t x) { return __float_as_uint(tf32_low_part(__uint_as_float(x))); }
+
+// Lane (r, c) holds row r, columns 2c and 2c + 1 of an 8 x 8 matrix: the same of the transpose.
+__device__ __forceinline__ void transpose_8x8_f32(float& x, float& y) {
+    const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+    uint32_t l = __byte_perm(a, b, 0x5410), h = __byte_perm(a, b, 0x7632);
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %0;" : "+r"(l));
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %0;" : "+r"(h));
+    x = __uint_as_float(__byte_perm(l, h, 0x5410));
+    y = __uint_as_float(__byte_perm(l, h, 0x7632));
+}
+
+template <int DHT, int NR, bool SPLIT>
+__global__ void __launch_bounds__(CF_WARPS * 32, DHT <= 64 ? 2 : 1)
+cross_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                 const __grid_constant__ CrossDesc d, float scale_log2, int qtiles, uint32_t* err) {
+    using L = CfLayout<DHT>;
+    constexpr int NB = L::NB, STAGES = L::STAGES, ROWS = SPLIT ? NR * 8 : CF_WARPS * NR * 8;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full[STAGES], empty[STAGES];
+    __shared__ int abort_word;
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    volatile int* abort_flag = &abort_word;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c4 = lane & 3, r8 = lane >> 2;
+    const int G = (int)(d.H / d.Hkv), dh = (int)d.dh, qt = blockIdx.x % qtiles, bh = blockIdx.x / qtiles;
+    const int b = bh / (int)d.Hkv, h = bh % (int)d.Hkv;
+    const int64_t rows = d.Tq * G, first = (int64_t)qt * ROWS + (SPLIT ? 0 : warp * NR * 8);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            ptx::mbar_init(full + i, 1);
+            ptx::mbar_init(empty + i, CF_WARPS);
+        }
+        abort_word = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tensormap(&tmK);
+        ptx::prefetch_tensormap(&tmV);
+    }
+    __syncthreads();
     griddep_wait();
     griddep_launch_dependents();
 
-    const float* k = static_cast<const float*>(d.k) + b * d.ks[0] + h * d.ks[2];
-    const float* v = static_cast<const float*>(d.v) + b * d.vs[0] + h * d.vs[2];
-    int64_t len = d.Tk;
-    if (d.kv_lens) len = min((int64_t)max(__ldg(d.kv_lens + b), 0), d.Tk);
-    const int tiles = (int)((len + CF_KEYS - 1) / CF_KEYS);
-    auto fetch = [&](int tile) {
-        float* dk = sK + (tile & 1) * L::TILE;
-        float* dv = sV + (tile & 1) * L::TILE;
-        for (int i = tid; i < CF_KEYS * V4; i += CF_THREADS) {
-            const int u = i / V4, x = (i - u * V4) * 4;
-            const int64_t key = (int64_t)tile * CF_KEYS + u;
-            const bool ok = key < len;   // rows past the length are zeros, whatever they hold
-            cp_async16(dk + u * LD + x, k + (ok ? key : 0) * d.ks[1] + x, ok);
-            cp_async16(dv + u * LD + x, v + (ok ? key : 0) * d.vs[1] + x, ok);
+    int len = (int)d.Tk;
+    if (d.kv_lens) len = min(max(__ldg(d.kv_lens + b), 0), (int)d.Tk);
+    const int tiles = (len + CF_KEYS - 1) / CF_KEYS;
+    const int kb = d.ks[0] ? b : 0, kh = d.ks[2] ? h : 0, vb = d.vs[0] ? b : 0, vh = d.vs[2] ? h : 0;
+    auto request = [&](int t) {   // thread 0
+        uint8_t* dst = smem + (t % STAGES) * L::STAGE;
+        uint64_t* bar = full + t % STAGES;
+        ptx::mbar_arrive_expect_tx(bar, L::STAGE);
+#pragma unroll
+        for (int x = 0; x < NB; ++x) {
+            ptx::tma_load_4d(dst + x * CF_BOX, &tmK, bar, x * 32, kh, t * CF_KEYS, kb);
+            ptx::tma_load_4d(dst + (NB + x) * CF_BOX, &tmV, bar, x * 32, vh, t * CF_KEYS, vb);
         }
-        cp_async_commit();
     };
-    if (tiles > 0) fetch(0);
-    for (int i = tid; i < CF_ROWS * V4; i += CF_THREADS) {
-        const int r = i / V4, x = (i - r * V4) * 4;
-        const int64_t row = first + r;
-        float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (row < rows)
-            q = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(d.q) + b * d.qs[0] + (row / G) * d.qs[1] +
-                                                      (h * G + row % G) * d.qs[2] + x));
-        *reinterpret_cast<float4*>(sQ + r * LD + x) = q;
+    if (threadIdx.x == 0)
+        for (int t = 0; t < STAGES && t < tiles; ++t) request(t);
+
+    // query rows first + 8 i + r8: columns 32 x + 4 (2 c4 + u) + {0 .. 3}
+    uint4 q[NR][2 * NB];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        const int64_t r = first + 8 * i + r8;
+        const float* qr = static_cast<const float*>(d.q) + b * d.qs[0] + (r / G) * d.qs[1] + (h * G + r % G) * d.qs[2];
+#pragma unroll
+        for (int c = 0; c < 2 * NB; ++c) {
+            const int col = (c >> 1) * 32 + (2 * c4 + (c & 1)) * 4;
+            q[i][c] = r < rows && col < dh ? __ldg(reinterpret_cast<const uint4*>(qr + col)) : make_uint4(0, 0, 0, 0);
+        }
+    }
+    // rows 8 i + 2 c4 + e: maximum, this thread's part of the sum; O^T of the two m-tiles of each box
+    float o[NR][2 * NB][4], m[NR][2], l[NR][2];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        m[i][0] = m[i][1] = -INFINITY;
+        l[i][0] = l[i][1] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 2 * NB; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][j][e] = 0.f;
+    }
+    const bool live = first < rows;
+    bool ok = true;
+    int t = 0;
+    for (; t < tiles; ++t) {
+        const uint32_t st = t % STAGES, par = (t / STAGES) & 1;
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(full + st, par, abort_flag));
+        if (!ok) break;
+        const uint8_t* sk = smem + st * L::STAGE;
+        const uint8_t* sv = sk + NB * CF_BOX;
+        // 16 keys at a time; the key groups of a warp
+        const int g0 = SPLIT ? warp : 0, g1 = SPLIT ? warp + 1 : CF_KEYS / 16;
+#pragma unroll 1
+        for (int g = g0; g < g1; ++g) {
+            const int valid = len - t * CF_KEYS - g * 16;
+            if (!live || valid <= 0) break;
+            float s[NR][4] = {}, s2[NR][4] = {};   // hi hi; the cross terms
+#pragma unroll
+            for (int c = 0; c < 2 * NB; ++c) {
+                // 16-byte unit i of key u at i ^ (u % 8)
+                const uint8_t* at = sk + (c >> 1) * CF_BOX + (g * 16 + r8) * 128 + (((2 * c4 + (c & 1)) ^ r8) << 4);
+                const uint4 k0 = *reinterpret_cast<const uint4*>(at), k1 = *reinterpret_cast<const uint4*>(at + 1024);
+                const uint32_t a0[4] = {k0.x, k1.x, k0.y, k1.y}, a1[4] = {k0.z, k1.z, k0.w, k1.w};
+                const uint32_t l0[4] = {lo_bits(a0[0]), lo_bits(a0[1]), lo_bits(a0[2]), lo_bits(a0[3])};
+                const uint32_t l1[4] = {lo_bits(a1[0]), lo_bits(a1[1]), lo_bits(a1[2]), lo_bits(a1[3])};
+#pragma unroll
+                for (int i = 0; i < NR; ++i) {
+                    const uint4 x = q[i][c];
+                    mma_tf32(s[i], a0, x.x, x.y);
+                    mma_tf32(s2[i], l0, x.x, x.y);
+                    mma_tf32(s2[i], a0, lo_bits(x.x), lo_bits(x.y));
+                    mma_tf32(s[i], a1, x.z, x.w);
+                    mma_tf32(s2[i], l1, x.z, x.w);
+                    mma_tf32(s2[i], a1, lo_bits(x.z), lo_bits(x.w));
+                }
+            }
+            bool grew = false;
+            float alpha[NR][2];
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                float mx[2] = {m[i][0], m[i][1]};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {   // key r8 + 8 (e / 2), row 2 c4 + e % 2
+                    // an infinite hi hi stands as it is: the low part of an infinity is NaN
+                    const float x = fabsf(s[i][e]) < INFINITY ? s[i][e] + s2[i][e] : s[i][e];
+                    s[i][e] = r8 + 8 * (e >> 1) < valid ? x * scale_log2 : -INFINITY;
+                    mx[e & 1] = fmaxf(mx[e & 1], s[i][e]);
+                }
+#pragma unroll
+                for (int w = 4; w < 32; w *= 2) {
+                    mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], w));
+                    mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], w));
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    alpha[i][e] = mx[e] > m[i][e] ? exp2_approx(m[i][e] - mx[e]) : 1.f;
+                    grew = grew || mx[e] > m[i][e];
+                    m[i][e] = mx[e];
+                    if (mx[e] == -INFINITY) mx[e] = 0.f;   // only infinite scores so far: weights of zero
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[i][e] = exp2_approx(s[i][e] - mx[e & 1]);
+                l[i][0] = l[i][0] * alpha[i][0] + (s[i][0] + s[i][2]);
+                l[i][1] = l[i][1] * alpha[i][1] + (s[i][1] + s[i][3]);
+                transpose_8x8_f32(s[i][0], s[i][1]);   // now row r8, keys 2 c4 and 2 c4 + 1
+                transpose_8x8_f32(s[i][2], s[i][3]);   // and 8 on
+            }
+            if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                for (int i = 0; i < NR; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2 * NB; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[i][j][e] *= alpha[i][e & 1];
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k)   // eight keys
+#pragma unroll
+                for (int x = 0; x < NB; ++x) {
+                    const int u = g * 16 + k * 8 + 2 * c4;
+                    const uint8_t* at = sv + x * CF_BOX + u * 128;
+                    uint4 v0 = *reinterpret_cast<const uint4*>(at + ((r8 ^ (u & 7)) << 4));
+                    uint4 v1 = *reinterpret_cast<const uint4*>(at + 128 + ((r8 ^ ((u + 1) & 7)) << 4));
+                    if (valid < 16) {   // rows past the length may hold anything, and 0 * NaN is NaN
+                        if (k * 8 + 2 * c4 >= valid) v0 = make_uint4(0, 0, 0, 0);
+                        if (k * 8 + 2 * c4 + 1 >= valid) v1 = make_uint4(0, 0, 0, 0);
+                    }
+                    const uint32_t a0[4] = {v0.x, v0.y, v1.x, v1.y}, a1[4] = {v0.z, v0.w, v1.z, v1.w};
+                    const uint32_t l0[4] = {lo_bits(a0[0]), lo_bits(a0[1]), lo_bits(a0[2]), lo_bits(a0[3])};
+                    const uint32_t l1[4] = {lo_bits(a1[0]), lo_bits(a1[1]), lo_bits(a1[2]), lo_bits(a1[3])};
+#pragma unroll
+                    for (int i = 0; i < NR; ++i) {
+                        const uint32_t p0 = __float_as_uint(s[i][2 * k]), p1 = __float_as_uint(s[i][2 * k + 1]);
+                        const uint32_t n0 = lo_bits(p0), n1 = lo_bits(p1);
+                        mma_tf32(o[i][2 * x], a0, p0, p1);
+                        mma_tf32(o[i][2 * x + 1], a1, p0, p1);
+                        mma_tf32(o[i][2 * x], l0, p0, p1);
+                        mma_tf32(o[i][2 * x + 1], l1, p0, p1);
+                        mma_tf32(o[i][2 * x], a0, n0, n1);
+                        mma_tf32(o[i][2 * x + 1], a1, n0, n1);
+                    }
+                }
+        }
+        __syncwarp();   // this warp has read the stage
+        if (lane == 0) ptx::mbar_arrive(empty + st);
+        if (threadIdx.x == 0 && t > 0 && t - 1 + STAGES < tiles) {   // the tile before: the other warps are done too
+            ok = ptx::mbar_wait_bounded(empty + (t - 1) % STAGES, ((t - 1) / STAGES) & 1, abort_flag);
+            if (ok) request(t - 1 + STAGES);
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+    }
+    if (!ok) {
+        if (lane == 0 && err) atomicOr(err, ERRBIT_TIMEOUT_ATTENTION);
+        *abort_flag = 1;
+        // copies in flight land before the CTA can exit
+        if (threadIdx.x == 0)
+            for (int i = t; i < t + STAGES && i < tiles; ++i)
+                ptx::mbar_wait_bounded(full + i % STAGES, (i / STAGES) & 1, nullptr);
     }
 
-    const bool live = first + warp * 16 < rows;
-    float o[8][NC], m[8], l[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        m[i] = -INFINITY;
-        l[i] = 0.f;
+    for (int i = 0; i < NR; ++i)
 #pragma unroll
-        for (int j = 0; j < NC; ++j) o[i][j] = 0.f;
-    }
-    for (int t = 0; t < tiles; ++t) {
-        if (t + 1 < tiles) {
-            fetch(t + 1);
-            cp_async_wait<1>();
-        } else {
-            cp_async_wait<0>();
-        }
-        __syncthreads();   // this tile (and, the first time, Q) is in place
-        if (live) {
-            const float* tk = sK + (t & 1) * L::TILE;
-            const float* tv = sV + (t & 1) * L::TILE;
-            float s[8][4] = {};
-#pragma unroll 4
-            for (int x = 0; x < DH; x += 4) {
-                float4 kv[4];
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(tk + (c + 16 * j) * LD + x);
+            for (int w = 4; w < 32; w *= 2) l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], w);
+    auto out = [&](int64_t r) {
+        return static_cast<float*>(d.o) + ((b * d.Tq + r / G) * d.H + h * G + r % G) * dh;
+    };
+    // [0] and [2] of m-tile j are columns 16 j' ..: 32 x + 4 r8 + 2 (j % 2) and the next, row 2 c4; [1] and [3]
+    // the same of row 2 c4 + 1
+    if constexpr (!SPLIT) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float4 q = *reinterpret_cast<const float4*>(sQ + (r0 + i) * LD + x);
+        for (int i = 0; i < NR; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        s[i][j] = fmaf(q.x, kv[j].x, s[i][j]);
-                        s[i][j] = fmaf(q.y, kv[j].y, s[i][j]);
-                        s[i][j] = fmaf(q.z, kv[j].z, s[i][j]);
-                        s[i][j] = fmaf(q.w, kv[j].w, s[i][j]);
-                    }
+            for (int e = 0; e < 2; ++e) {
+                const int64_t r = first + 8 * i + 2 * c4 + e;
+                if (r >= rows) continue;
+                const float inv = tiles > 0 ? 1.f / l[i][e] : 0.f;
+                float* at = out(r);
+#pragma unroll
+                for (int x = 0; x < NB; ++x) {
+                    const int col = 32 * x + 4 * r8;
+                    const float v[4] = {o[i][2 * x][e], o[i][2 * x][2 + e], o[i][2 * x + 1][e], o[i][2 * x + 1][2 + e]};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (col + j < dh) at[col + j] = tiles > 0 ? v[j] * inv : 0.f;
                 }
             }
-            const int64_t valid = len - (int64_t)t * CF_KEYS;
+    } else {
+        // join the warps: O, m and l of each over the ring, which nobody reads any more
+        constexpr int PIECE = NR * 8 * (DHT + 2);
+        float* sm = reinterpret_cast<float*>(smem);
+        static_assert(CF_WARPS * PIECE * 4 <= L::STAGES * L::STAGE, "join");
+        __syncthreads();
+        float* w0 = sm + warp * PIECE;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float mx = m[i];
+        for (int i = 0; i < NR; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    s[i][j] = c + 16 * j < valid ? s[i][j] * scale_log2 : -INFINITY;
-                    mx = fmaxf(mx, s[i][j]);
+            for (int e = 0; e < 2; ++e) {
+                const int r = 8 * i + 2 * c4 + e;
+#pragma unroll
+                for (int x = 0; x < NB; ++x) {
+                    float* at = w0 + r * DHT + 32 * x + 4 * r8;
+                    at[0] = o[i][2 * x][e];
+                    at[1] = o[i][2 * x][2 + e];
+                    at[2] = o[i][2 * x + 1][e];
+                    at[3] = o[i][2 * x + 1][2 + e];
                 }
-#pragma unroll
-                for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-                const float base = mx == -INFINITY ? 0.f : mx;   // only infinite scores so far: weights of zero
-                const float alpha = exp2_approx(m[i] - base);
-                m[i] = mx;
-                float sum = 0.f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float p = exp2_approx(s[i][j] - base);
-                    sum += p;
-                    sP[(r0 + i) * L::LDP + c + 16 * j] = p;
-                }
-                l[i] = l[i] * alpha + sum;   // this thread's keys; joined at the end
-#pragma unroll
-                for (int j = 0; j < NC; ++j) o[i][j] *= alpha;
-            }
-            __syncwarp();
-#pragma unroll 2
-            for (int u = 0; u < CF_KEYS; u += 4) {
-                float vv[4][NC];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                    for (int j = 0; j < NC; ++j) vv[e][j] = tv[(u + e) * LD + c + 16 * j];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float4 p = *reinterpret_cast<const float4*>(sP + (r0 + i) * L::LDP + u);
-#pragma unroll
-                    for (int j = 0; j < NC; ++j) {
-                        o[i][j] = fmaf(p.x, vv[0][j], o[i][j]);
-                        o[i][j] = fmaf(p.y, vv[1][j], o[i][j]);
-                        o[i][j] = fmaf(p.z, vv[2][j], o[i][j]);
-                        o[i][j] = fmaf(p.w, vv[3][j], o[i][j]);
-                    }
+                if (r8 == 0) {
+                    w0[NR * 8 * DHT + r] = m[i][e];
+                    w0[NR * 8 * DHT + NR * 8 + r] = l[i][e];
                 }
             }
-        }
-        __syncthreads();   // the tile has been read: its buffer takes the one after the next
-    }
+        __syncthreads();
+        for (int x = threadIdx.x; x < (int)rows * dh; x += CF_WARPS * 32) {
+            const int r = x / dh, c = x - r * dh;
+            float mw[CF_WARPS], mx = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+            for (int w = 0; w < CF_WARPS; ++w) {
+                mw[w] = sm[w * PIECE + NR * 8 * DHT + r];
+                mx = fmaxf(mx, mw[w]);
+            }
+            const float base = mx == -INFINITY ? 0.f : mx;
+            float acc = 0.f, sum = 0.f;
 #pragma unroll
-        for (int w = 8; w > 0; w >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
-        const int64_t row = first + r0 + i;
-        if (row < rows) {
-            float* at = static_cast<float*>(d.o) + ((b * d.Tq + row / G) * d.H + h * G + row % G) * DH;
-            const float inv = 1.f / l[i];
-#pragma unroll
-            for (int j = 0; j < NC; ++j) at[c + 16 * j] = tiles > 0 ? o[i][j] * inv : 0.f;
+            for (int w = 0; w < CF_WARPS; ++w) {
+                const float f = exp2_approx(mw[w] - base);
+                acc = fmaf(f, sm[w * PIECE + r * DHT + c], acc);
+                sum = fmaf(f, sm[w * PIECE + NR * 8 * DHT + NR * 8 + r], sum);
+            }
+            out(r)[c] = tiles > 0 ? acc / sum : 0.f;
         }
     }
 }
 
-template <int DH> cudaError_t launch_cf(const CrossDesc& d, cudaStream_t s) {
-    using L = CfLayout<DH>;
+template <int DHT, int NR, bool SPLIT>
+cudaError_t launch_cf_inst(const CrossDesc& d, const DeviceInfo& dev, cudaStream_t s) {
+    using L = CfLayout<DHT>;
+    auto k = cross_f32_kernel<DHT, NR, SPLIT>;
     static std::atomic<uint64_t> attr{0};
-    const cudaError_t e = set_smem_limit_once(cross_f32_kernel<DH>, L::SMEM, attr);
+    const cudaError_t e = set_smem_limit_once(k, L::SMEM, attr);
     if (e != cudaSuccess) return e;
-    const int64_t qtiles = (d.Tq * (d.H / d.Hkv) + CF_ROWS - 1) / CF_ROWS;
-    return launch_dependent(cross_f32_kernel<DH>, dim3((unsigned)(d.B * d.Hkv * qtiles)), dim3(CF_THREADS), L::SMEM, s, d,
-                            (float)(d.scale * 1.4426950408889634), (int)qtiles);
+    alignas(64) CUtensorMap mk, mv;
+    if (!ct_map_f32(&mk, d.k, d.ks, d.B, d.Tk, d.Hkv, d.dh, CF_KEYS) ||
+        !ct_map_f32(&mv, d.v, d.vs, d.B, d.Tk, d.Hkv, d.dh, CF_KEYS))
+        return cudaErrorInvalidValue;
+    const int rows = SPLIT ? NR * 8 : CF_WARPS * NR * 8;
+    const int64_t qtiles = (d.Tq * (d.H / d.Hkv) + rows - 1) / rows;
+    return launch_dependent(k, dim3((unsigned)(d.B * d.Hkv * qtiles)), dim3(CF_WARPS * 32), L::SMEM, s, mk, mv, d,
+                            (float)(d.scale * 1.4426950408889634), (int)qtiles, dev.err_word);
+}
+
+template <int DHT> cudaError_t launch_cf(const CrossDesc& d, const DeviceInfo& dev, cudaStream_t s) {
+    const int64_t rows = d.Tq * (d.H / d.Hkv);
+    if (rows <= 8) return launch_cf_inst<DHT, 1, true>(d, dev, s);
+    if (rows <= 16) return launch_cf_inst<DHT, 2, true>(d, dev, s);
+    return launch_cf_inst<DHT, 2, false>(d, dev, s);
 }
 
 }  // namespace
 
 bool cross_f32_supported(const CrossDesc& d) {
-    if (d.dt != DT_F32 || d.dh % 16 != 0 || d.dh < 32 || d.dh > 128) return false;
-    const int64_t lim = 0x7fffffff, qtiles = (d.Tq * (d.H / d.Hkv) + CF_ROWS - 1) / CF_ROWS;
-    if (d.Tk > lim - 65536 || qtiles > lim || d.B > lim / (d.Hkv * qtiles) || d.Hkv > lim / qtiles) return false;
-    const struct { const void* p; const int64_t* st; } in[] = {{d.q, d.qs}, {d.k, d.ks}, {d.v, d.vs}};
-    for (const auto& i : in)
-        if ((reinterpret_cast<uintptr_t>(i.p) & 15) || i.st[0] % 4 || i.st[1] % 4 || i.st[2] % 4) return false;
-    return true;
+    if (d.dt != DT_F32 || d.dh % 4 != 0 || d.dh > 128) return false;
+    const int64_t lim = 0x7fffffff, qtiles = (d.Tq * (d.H / d.Hkv) + 63) / 64;
+    if (d.Tk > lim - 65536 || qtiles > lim || d.Hkv > lim / qtiles || d.B > lim / (d.Hkv * qtiles)) return false;
+    if ((reinterpret_cast<uintptr_t>(d.q) & 15) || d.qs[0] % 4 || d.qs[1] % 4 || d.qs[2] % 4) return false;
+    return ct_strides_ok(d.k, d.ks, d.Tk, 4) && ct_strides_ok(d.v, d.vs, d.Tk, 4) && ct_encode_fn() != nullptr;
 }
 
-cudaError_t launch_cross_f32(const CrossDesc& d, cudaStream_t s) {
-    switch (d.dh) {
-        case 32: return launch_cf<32>(d, s);
-        case 48: return launch_cf<48>(d, s);
-        case 64: return launch_cf<64>(d, s);
-        case 80: return launch_cf<80>(d, s);
-        case 96: return launch_cf<96>(d, s);
-        case 112: return launch_cf<112>(d, s);
-        case 128: return launch_cf<128>(d, s);
-    }
-    return cudaErrorInvalidValue;
+cudaError_t launch_cross_f32(const CrossDesc& d, const DeviceInfo& dev, cudaStream_t s) {
+    if (d.dh <= 32) return launch_cf<32>(d, dev, s);
+    if (d.dh <= 64) return launch_cf<64>(d, dev, s);
+    if (d.dh <= 96) return launch_cf<96>(d, dev, s);
+    return launch_cf<128>(d, dev, s);
 }
 
 }  // namespace vit

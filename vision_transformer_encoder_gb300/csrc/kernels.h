@@ -252,9 +252,9 @@ struct CrossDesc {
     void* o;
 };
 constexpr int64_t kCrossMaxHead = 512;
-// fp32 on the CUDA cores (attention_cross_f32.cu): head widths 32 to 128 in steps of 16.
+// fp32, three TF32 products per step (attention_cross_f32.cu): head widths up to 128 in steps of 4.
 bool cross_f32_supported(const CrossDesc& d);
-cudaError_t launch_cross_f32(const CrossDesc& d, cudaStream_t s);
+cudaError_t launch_cross_f32(const CrossDesc& d, const DeviceInfo& dev, cudaStream_t s);
 // Few queries (attention_cross_rows.cu): bf16, at most 16 query rows per key head.
 bool cross_rows_supported(const CrossDesc& d);
 cudaError_t launch_cross_rows(const CrossDesc& d, const DeviceInfo& dev, cudaStream_t s);
