@@ -10,9 +10,10 @@
 // A CTA of four warps walks the keys of one (sequence, key head) 64 at a time, K and V tiles by TMA in
 // a ring that all warps read. Query rows are the n side of the products, S^T = K Q^T and
 // O^T = V^T P^T, eight or sixteen to a warp (packed row = token * G + head of the group):
-//   many rows (SPLIT false): 64 rows per CTA, sixteen to each warp; warps without rows skip the work
-//   few rows  (SPLIT true):  the same eight or sixteen rows in every warp, which takes 16 of the 64
-//                            keys; joined at the end through shared memory
+//   64 rows per CTA, sixteen to each warp; warps without rows skip the work;
+//   a CTA with at most sixteen rows (decoding, or the last of a head) is split along the keys: the
+//   same rows in every warp, which takes 16 of the 64 keys, joined at the end through shared
+//   memory. The last five of 197 rows took three quarters of a full CTA's time before.
 // Operands are read 16 bytes at a time from the 128-byte swizzled tiles without bank conflicts:
 // the order of the columns in a dot product is free, so thread c takes four consecutive columns
 // of its key for two k-steps; so is which column a row of V^T means; and P^T comes out of S^T by
@@ -29,7 +30,7 @@
 namespace vit {
 namespace {
 
-constexpr int CF_KEYS = 64, CF_WARPS = 4, CF_BOX = CF_KEYS * 128;   // a box: 32 columns of 64 keys
+constexpr int CF_KEYS = 64, CF_WARPS = 4, CF_ROWS = 64, CF_BOX = CF_KEYS * 128;   // a box: 32 columns of 64 keys
 
 template <int DHT> struct CfLayout {
     static constexpr int NB = DHT / 32;                 // boxes of a K or V tile
@@ -59,12 +60,12 @@ __device__ __forceinline__ void transpose_8x8_f32(float& x, float& y) {
     y = __uint_as_float(__byte_perm(l, h, 0x7632));
 }
 
-template <int DHT, int NR, bool SPLIT>
+template <int DHT, int NR>
 __global__ void __launch_bounds__(CF_WARPS * 32, DHT <= 64 ? 2 : 1)
 cross_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                  const __grid_constant__ CrossDesc d, float scale_log2, int qtiles, uint32_t* err) {
     using L = CfLayout<DHT>;
-    constexpr int NB = L::NB, STAGES = L::STAGES, ROWS = SPLIT ? NR * 8 : CF_WARPS * NR * 8;
+    constexpr int NB = L::NB, STAGES = L::STAGES;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[STAGES], empty[STAGES];
     __shared__ int abort_word;
@@ -73,7 +74,9 @@ cross_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c4 = lane & 3, r8 = lane >> 2;
     const int G = (int)(d.H / d.Hkv), dh = (int)d.dh, qt = blockIdx.x % qtiles, bh = blockIdx.x / qtiles;
     const int b = bh / (int)d.Hkv, h = bh % (int)d.Hkv;
-    const int64_t rows = d.Tq * G, first = (int64_t)qt * ROWS + (SPLIT ? 0 : warp * NR * 8);
+    const int64_t rows = d.Tq * G, tile0 = (int64_t)qt * CF_ROWS;
+    const bool split = rows - tile0 <= NR * 8;
+    const int64_t first = tile0 + (split ? 0 : warp * NR * 8);
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
             ptx::mbar_init(full + i, 1);
@@ -138,12 +141,13 @@ cross_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         const uint8_t* sk = smem + st * L::STAGE;
         const uint8_t* sv = sk + NB * CF_BOX;
         // 16 keys at a time; the key groups of a warp
-        const int g0 = SPLIT ? warp : 0, g1 = SPLIT ? warp + 1 : CF_KEYS / 16;
+        const int g0 = split ? warp : 0, g1 = split ? warp + 1 : CF_KEYS / 16;
 #pragma unroll 1
         for (int g = g0; g < g1; ++g) {
             const int valid = len - t * CF_KEYS - g * 16;
             if (!live || valid <= 0) break;
-            float s[NR][4] = {}, s2[NR][4] = {};   // hi hi; the cross terms
+            // hi hi, lo hi and hi lo apart: shorter chains of dependent products
+            float s[NR][4] = {}, s2[NR][4] = {}, s3[NR][4] = {};
 #pragma unroll
             for (int c = 0; c < 2 * NB; ++c) {
                 // 16-byte unit i of key u at i ^ (u % 8)
@@ -157,10 +161,10 @@ cross_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                     const uint4 x = q[i][c];
                     mma_tf32(s[i], a0, x.x, x.y);
                     mma_tf32(s2[i], l0, x.x, x.y);
-                    mma_tf32(s2[i], a0, lo_bits(x.x), lo_bits(x.y));
+                    mma_tf32(s3[i], a0, lo_bits(x.x), lo_bits(x.y));
                     mma_tf32(s[i], a1, x.z, x.w);
                     mma_tf32(s2[i], l1, x.z, x.w);
-                    mma_tf32(s2[i], a1, lo_bits(x.z), lo_bits(x.w));
+                    mma_tf32(s3[i], a1, lo_bits(x.z), lo_bits(x.w));
                 }
             }
             bool grew = false;
@@ -171,7 +175,7 @@ cross_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {   // key r8 + 8 (e / 2), row 2 c4 + e % 2
                     // an infinite hi hi stands as it is: the low part of an infinity is NaN
-                    const float x = fabsf(s[i][e]) < INFINITY ? s[i][e] + s2[i][e] : s[i][e];
+                    const float x = fabsf(s[i][e]) < INFINITY ? s[i][e] + (s2[i][e] + s3[i][e]) : s[i][e];
                     s[i][e] = r8 + 8 * (e >> 1) < valid ? x * scale_log2 : -INFINITY;
                     mx[e & 1] = fmaxf(mx[e & 1], s[i][e]);
                 }
@@ -259,7 +263,7 @@ cross_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     };
     // [0] and [2] of m-tile j are columns 16 j' ..: 32 x + 4 r8 + 2 (j % 2) and the next, row 2 c4; [1] and [3]
     // the same of row 2 c4 + 1
-    if constexpr (!SPLIT) {
+    if (!split) {
 #pragma unroll
         for (int i = 0; i < NR; ++i)
 #pragma unroll
@@ -303,7 +307,7 @@ cross_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                 }
             }
         __syncthreads();
-        for (int x = threadIdx.x; x < (int)rows * dh; x += CF_WARPS * 32) {
+        for (int x = threadIdx.x; x < (int)(rows - tile0) * dh; x += CF_WARPS * 32) {
             const int r = x / dh, c = x - r * dh;
             float mw[CF_WARPS], mx = -INFINITY;
 #pragma unroll
@@ -319,15 +323,14 @@ cross_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                 acc = fmaf(f, sm[w * PIECE + r * DHT + c], acc);
                 sum = fmaf(f, sm[w * PIECE + NR * 8 * DHT + NR * 8 + r], sum);
             }
-            out(r)[c] = tiles > 0 ? acc / sum : 0.f;
+            out(tile0 + r)[c] = tiles > 0 ? acc / sum : 0.f;
         }
     }
 }
 
-template <int DHT, int NR, bool SPLIT>
-cudaError_t launch_cf_inst(const CrossDesc& d, const DeviceInfo& dev, cudaStream_t s) {
+template <int DHT, int NR> cudaError_t launch_cf_inst(const CrossDesc& d, const DeviceInfo& dev, cudaStream_t s) {
     using L = CfLayout<DHT>;
-    auto k = cross_f32_kernel<DHT, NR, SPLIT>;
+    auto k = cross_f32_kernel<DHT, NR>;
     static std::atomic<uint64_t> attr{0};
     const cudaError_t e = set_smem_limit_once(k, L::SMEM, attr);
     if (e != cudaSuccess) return e;
@@ -335,24 +338,20 @@ cudaError_t launch_cf_inst(const CrossDesc& d, const DeviceInfo& dev, cudaStream
     if (!ct_map_f32(&mk, d.k, d.ks, d.B, d.Tk, d.Hkv, d.dh, CF_KEYS) ||
         !ct_map_f32(&mv, d.v, d.vs, d.B, d.Tk, d.Hkv, d.dh, CF_KEYS))
         return cudaErrorInvalidValue;
-    const int rows = SPLIT ? NR * 8 : CF_WARPS * NR * 8;
-    const int64_t qtiles = (d.Tq * (d.H / d.Hkv) + rows - 1) / rows;
+    const int64_t qtiles = (d.Tq * (d.H / d.Hkv) + CF_ROWS - 1) / CF_ROWS;
     return launch_dependent(k, dim3((unsigned)(d.B * d.Hkv * qtiles)), dim3(CF_WARPS * 32), L::SMEM, s, mk, mv, d,
                             (float)(d.scale * 1.4426950408889634), (int)qtiles, dev.err_word);
 }
 
 template <int DHT> cudaError_t launch_cf(const CrossDesc& d, const DeviceInfo& dev, cudaStream_t s) {
-    const int64_t rows = d.Tq * (d.H / d.Hkv);
-    if (rows <= 8) return launch_cf_inst<DHT, 1, true>(d, dev, s);
-    if (rows <= 16) return launch_cf_inst<DHT, 2, true>(d, dev, s);
-    return launch_cf_inst<DHT, 2, false>(d, dev, s);
+    return d.Tq * (d.H / d.Hkv) <= 8 ? launch_cf_inst<DHT, 1>(d, dev, s) : launch_cf_inst<DHT, 2>(d, dev, s);
 }
 
 }  // namespace
 
 bool cross_f32_supported(const CrossDesc& d) {
     if (d.dt != DT_F32 || d.dh % 4 != 0 || d.dh > 128) return false;
-    const int64_t lim = 0x7fffffff, qtiles = (d.Tq * (d.H / d.Hkv) + 63) / 64;
+    const int64_t lim = 0x7fffffff, qtiles = (d.Tq * (d.H / d.Hkv) + CF_ROWS - 1) / CF_ROWS;
     if (d.Tk > lim - 65536 || qtiles > lim || d.Hkv > lim / qtiles || d.B > lim / (d.Hkv * qtiles)) return false;
     if ((reinterpret_cast<uintptr_t>(d.q) & 15) || d.qs[0] % 4 || d.qs[1] % 4 || d.qs[2] % 4) return false;
     return ct_strides_ok(d.k, d.ks, d.Tk, 4) && ct_strides_ok(d.v, d.vs, d.Tk, 4) && ct_encode_fn() != nullptr;
