@@ -20,9 +20,6 @@ VIT_F32, VIT_BF16, VIT_F64, VIT_E4M3 = 0, 1, 2, 3
 EPI_STORE, EPI_GELU, EPI_RESIDUAL = 0, 1, 2
 
 _DT = {torch.float32: VIT_F32, torch.bfloat16: VIT_BF16, torch.float64: VIT_F64}
-_F8 = torch.float8_e4m3fn
-_DT8 = dict(_DT)   # the types of the 8-bit stages' outputs
-_DT8[_F8] = VIT_E4M3
 
 LAYER_FIELDS = ("w_q", "w_k", "w_v", "w_o", "w_mlp1", "w_mlp2", "ln1_g", "ln1_b", "ln2_g", "ln2_b",
                 "b1", "b2", "b_q", "b_k", "b_v", "b_o")
@@ -447,69 +444,47 @@ def attention(qkv, H, out=None, stream=None):
 
 
 # ---- serving stages: rms norm, 8-bit products, cross attention -------------------------
-# These are called once per layer and token, and a call costs the host more than the GPU: the
-# marshalling checks each operand once, leaves tensors that it has just made unchecked, passes raw
-# pointers as integers and switches the device only when it is not current.
+# Called once per layer and token, where marshalling in Python costs several times what the
+# kernels take: csrc/binding.cpp checks the tensors, makes the outputs and calls the library.
 
-def _fits(t, dtype, shape, index):
-    """t is a contiguous CUDA tensor of this dtype and shape on device `index`."""
-    return t.get_device() == index and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+_native = None
 
 
-def _refuse(name, t, dtype, shape, index):
-    """The reason why t does not fit."""
-    if t.get_device() != index or index < 0:
-        raise ValueError("%s must be a CUDA tensor%s" % (name, " on cuda:%d" % index if index >= 0 else ""))
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
-    if t.shape != shape:
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    raise ValueError("%s must be contiguous" % name)
+def _serving():
+    global _native
+    if _native is None:
+        lib = load_library()
+        try:
+            from . import _serving as native
+        except ImportError as e:
+            raise RuntimeError("the serving binding is not built (%s); run "
+                               "python -m vision_transformer_encoder_gb300.build" % e)
+
+        def on_error(status, what):
+            raise VitError(status, what)
+
+        native.set_entry(on_error, *[ctypes.cast(getattr(lib, name), _vp).value for name in (
+            "vit_rmsnorm", "vit_quantize", "vit_quantize_weight", "vit_linear_fp8", "vit_cross_attention")])
+        _native = native
+    return _native
 
 
-def _given(t, name, dtype, shape, index):
-    """Pointer of an operand of known dtype."""
-    if not _fits(t, dtype, shape, index):
-        _refuse(name, t, dtype, shape, index)
-    return t.data_ptr()
-
-
-def _code(dt, allowed, what):
-    if dt not in allowed:
-        raise ValueError("%s: unsupported dtype %s" % (what, dt))
-    return allowed[dt]
-
-
-def _torch_stream(stream, index):
-    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=index)
-
-
-def _alloc(shape, dtype, device, stream):
-    """An output of a call on `stream`, from that stream's memory."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(_torch_stream(stream, device.index)):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _invoke(what, fn, index, stream, tensors, args):
-    """fn(*args, stream) with device `index` current; raises on a non-zero status. With an explicit
-    stream the tensors are kept from reuse until the work queued there is done."""
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(index)
-    else:
-        ts = _torch_stream(stream, index)
-        handle = ts.cuda_stream
-        for t in tensors:
-            if t is not None:
-                t.record_stream(ts)
-    if torch._C._cuda_getDevice() == index:
-        rc = fn(*args, handle)
-    else:
-        with torch.cuda.device(index):
-            rc = fn(*args, handle)
-    if rc != 0:
-        raise VitError(rc, what)
+def _on(stream, tensors, fn, *args):
+    """fn(*args) on an explicit stream: outputs come from that stream's memory, and the tensors are
+    kept from reuse until the work queued there is done."""
+    device = tensors[0].get_device()
+    if device < 0:
+        return fn(*args)   # refuses
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream.device_index != device:
+        raise ValueError("the stream is on cuda:%d, the tensors on cuda:%d" % (stream.device_index, device))
+    with torch.cuda.stream(stream):
+        r = fn(*args)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    return r
 
 
 def rmsnorm(x, eps, gamma=None, residual=None, out_dtype=None, out=None, scales=None, sum_out=None, stream=None):
@@ -521,102 +496,29 @@ def rmsnorm(x, eps, gamma=None, residual=None, out_dtype=None, out=None, scales=
     scales (rows, ceil(D / 128)) of 128-column blocks. sum_out: where s goes, of the residual's
     dtype (may be the residual or x itself); a new tensor when not given.
     Returns out; (out, scales) in 8 bits; with a residual, also the sum as the last element."""
-    lib = _lib or load_library()
-    shape, xd, index = x.shape, x.dtype, x.get_device()
-    n = x.numel()
-    if not shape or not n:
-        raise ValueError("x must have at least one element and a last dimension")
-    xc = _code(xd, _DT, "x")
-    if index < 0 or not x.is_contiguous():
-        _refuse("x", x, None, shape, index)
-    device = x.device
-    D = shape[-1]
-    rows = n // D
-    od = out_dtype if out_dtype is not None else (out.dtype if out is not None else xd)
-    oc = _code(od, _DT8, "out")
-    gp = rp = sp = cp = None
-    gc = rc = xc
-    if gamma is not None:
-        gc = _code(gamma.dtype, _DT, "gamma")
-        gp = _given(gamma, "gamma", gamma.dtype, (D,), index)
-    if residual is not None:
-        rd = residual.dtype
-        rc = _code(rd, _DT, "residual")
-        rp = _given(residual, "residual", rd, shape, index)
-        if sum_out is None:
-            sum_out = _alloc(shape, rd, device, stream)
-            sp = sum_out.data_ptr()
-        else:
-            sp = _given(sum_out, "sum_out", rd, shape, index)
-    elif sum_out is not None:
-        raise ValueError("sum_out needs a residual")
-    if out is None:
-        out = _alloc(shape, od, device, stream)
-        op = out.data_ptr()
-    else:
-        op = _given(out, "out", od, shape, index)
-    if oc == VIT_E4M3:
-        if scales is None:
-            scales = _alloc((rows, (D + 127) // 128), torch.float32, device, stream)
-            cp = scales.data_ptr()
-        else:
-            cp = _given(scales, "scales", torch.float32, (rows, (D + 127) // 128), index)
-    elif scales is not None:
-        raise ValueError("scales belong to a float8_e4m3fn output")
-    _invoke("vit_rmsnorm", lib.vit_rmsnorm, index, stream, (x, residual, gamma, sum_out, out, scales),
-            (x.data_ptr(), xc, rp, rc, rows, D, eps, gp, gc, sp, op, oc, cp))
-    if oc == VIT_E4M3:
-        return (out, scales) if residual is None else (out, scales, sum_out)
-    return out if residual is None else (out, sum_out)
-
-
-def _quantized(x, oshape, sshape, out, scales, stream, index):
-    """The outputs of a quantisation, made or checked, and their pointers."""
-    if out is None:
-        out = _alloc(oshape, _F8, x.device, stream)
-        op = out.data_ptr()
-    else:
-        op = _given(out, "out", _F8, oshape, index)
-    if scales is None:
-        scales = _alloc(sshape, torch.float32, x.device, stream)
-        sp = scales.data_ptr()
-    else:
-        sp = _given(scales, "scales", torch.float32, sshape, index)
-    return out, scales, op, sp
+    fn = (_native or _serving()).rmsnorm
+    if stream is None:
+        return fn(x, eps, gamma, residual, out_dtype, out, scales, sum_out)
+    return _on(stream, (x, gamma, residual, out, scales, sum_out), fn, x, eps, gamma, residual, out_dtype, out, scales,
+               sum_out)
 
 
 def quantize(x, out=None, scales=None, stream=None):
     """x (..., K), bf16 or fp32, in 8 bits: (q (..., K) float8_e4m3fn, scales (rows, ceil(K / 128))
     fp32), one scale for each 128 columns of a row; a value is q * scale."""
-    lib = _lib or load_library()
-    shape, index, n = x.shape, x.get_device(), x.numel()
-    if not shape or not n:
-        raise ValueError("x must have at least one element and a last dimension")
-    xc = _code(x.dtype, _DT, "x")
-    if index < 0 or not x.is_contiguous():
-        _refuse("x", x, None, shape, index)
-    K = shape[-1]
-    rows = n // K
-    out, scales, op, sp = _quantized(x, shape, (rows, (K + 127) // 128), out, scales, stream, index)
-    _invoke("vit_quantize", lib.vit_quantize, index, stream, (x, out, scales), (x.data_ptr(), xc, rows, K, op, sp))
-    return out, scales
+    fn = (_native or _serving()).quantize
+    if stream is None:
+        return fn(x, out, scales)
+    return _on(stream, (x, out, scales), fn, x, out, scales)
 
 
 def quantize_weight(w, out=None, scales=None, stream=None):
     """A weight w (K, N), bf16 or fp32, as linear_fp8 takes it: (q (N, K) float8_e4m3fn, the
     transpose, scales (ceil(N / 128), ceil(K / 128)) fp32), one scale for each 128 x 128 block."""
-    lib = _lib or load_library()
-    shape, index = w.shape, w.get_device()
-    if len(shape) != 2 or not w.numel():
-        raise ValueError("w must be a matrix (K, N) with at least one element")
-    wc = _code(w.dtype, _DT, "w")
-    if index < 0 or not w.is_contiguous():
-        _refuse("w", w, None, shape, index)
-    K, N = shape
-    out, scales, op, sp = _quantized(w, (N, K), ((N + 127) // 128, (K + 127) // 128), out, scales, stream, index)
-    _invoke("vit_quantize_weight", lib.vit_quantize_weight, index, stream, (w, out, scales),
-            (w.data_ptr(), wc, K, N, op, sp))
-    return out, scales
+    fn = (_native or _serving()).quantize_weight
+    if stream is None:
+        return fn(w, out, scales)
+    return _on(stream, (w, out, scales), fn, w, out, scales)
 
 
 def linear_fp8(a, a_scales, w, w_scales, bias=None, residual=None, epilogue=EPI_STORE, out_dtype=None, out=None,
@@ -628,63 +530,11 @@ def linear_fp8(a, a_scales, w, w_scales, bias=None, residual=None, epilogue=EPI_
     bias (N) and residual (..., N): bf16 or fp32; the residual goes with EPI_RESIDUAL alone.
     out_dtype: bf16 (default), fp32 or float8_e4m3fn. Returns out, or (out, out_scales) in 8 bits,
     out_scales (rows, ceil(N / 128)). out may be the residual itself where the types agree."""
-    lib = _lib or load_library()
-    shape, wshape, index, n = a.shape, w.shape, a.get_device(), a.numel()
-    if not shape or not n or len(wshape) != 2 or not w.numel():
-        raise ValueError("a must be (..., K) and w (N, K), with at least one element")
-    N, K = wshape
-    if shape[-1] != K:
-        raise ValueError("a has %d columns, w %d" % (shape[-1], K))
-    if index < 0:
-        _refuse("a", a, _F8, shape, index)
-    M = n // K
-    kb, nb = (K + 127) // 128, (N + 127) // 128
-    oshape = shape[:-1] + (N,)
-    ap, wp = _given(a, "a", _F8, shape, index), _given(w, "w", _F8, wshape, index)
-    asp = _given(a_scales, "a_scales", torch.float32, (M, kb), index)
-    wsp = _given(w_scales, "w_scales", torch.float32, (nb, kb), index)
-    bp = rp = osp = None
-    bc = rc = 0
-    if bias is not None:
-        bc = _code(bias.dtype, _DT, "bias")
-        bp = _given(bias, "bias", bias.dtype, (N,), index)
-    if residual is not None:
-        rc = _code(residual.dtype, _DT, "residual")
-        rp = _given(residual, "residual", residual.dtype, oshape, index)
-    od = out_dtype if out_dtype is not None else (out.dtype if out is not None else torch.bfloat16)
-    oc = _code(od, _DT8, "out")
-    if out is None:
-        out = _alloc(oshape, od, a.device, stream)
-        op = out.data_ptr()
-    else:
-        op = _given(out, "out", od, oshape, index)
-    if oc == VIT_E4M3:
-        if out_scales is None:
-            out_scales = _alloc((M, nb), torch.float32, a.device, stream)
-            osp = out_scales.data_ptr()
-        else:
-            osp = _given(out_scales, "out_scales", torch.float32, (M, nb), index)
-    elif out_scales is not None:
-        raise ValueError("out_scales belong to a float8_e4m3fn output")
-    _invoke("vit_linear_fp8", lib.vit_linear_fp8, index, stream,
-            (a, a_scales, w, w_scales, bias, residual, out, out_scales),
-            (ap, asp, wp, wsp, bp, bc, rp, rc, M, K, N, int(epilogue), op, oc, osp))
-    return (out, out_scales) if oc == VIT_E4M3 else out
-
-
-_Strides = _i64 * 3
-
-
-def _strided(t, name, dtype, index):
-    """Pointer and (sequence, token, head) strides of t (B, T, heads, dh); None when contiguous."""
-    if t.get_device() != index or t.dtype is not dtype:
-        _refuse(name, t, dtype, t.shape, index)
-    if t.is_contiguous():
-        return t.data_ptr(), None
-    b, u, h, c = t.stride()
-    if c != 1 and t.shape[3] != 1:
-        raise ValueError("%s: the elements of a head must be contiguous" % name)
-    return t.data_ptr(), _Strides(b, u, h)
+    fn = (_native or _serving()).linear_fp8
+    if stream is None:
+        return fn(a, a_scales, w, w_scales, bias, residual, epilogue, out_dtype, out, out_scales)
+    return _on(stream, (a, a_scales, w, w_scales, bias, residual, out, out_scales), fn, a, a_scales, w, w_scales, bias,
+               residual, epilogue, out_dtype, out, out_scales)
 
 
 def cross_attention(q, k, v, kv_lens=None, scale=None, out=None, stream=None):
@@ -695,29 +545,12 @@ def cross_attention(q, k, v, kv_lens=None, scale=None, out=None, stream=None):
     zeros); all Tk when not given. scale: 1 / sqrt(dh) by default. q, k and v may be views with
     any strides over sequences, tokens and heads, such as the halves of a fused key and value
     projection; the elements of a head are contiguous."""
-    lib = _lib or load_library()
-    dt, index, qshape, kshape = q.dtype, q.get_device(), q.shape, k.shape
-    if len(qshape) != 4 or len(kshape) != 4 or not q.numel() or not k.numel():
-        raise ValueError("q must be (B, Tq, H, dh) and k (B, Tk, Hkv, dh), with at least one element")
-    B, Tq, H, dh = qshape
-    kb, Tk, Hkv, kd = kshape
-    if kb != B or kd != dh or v.shape != kshape:
-        raise ValueError("q %s, k %s and v %s do not fit" % (tuple(qshape), tuple(kshape), tuple(v.shape)))
-    code = _code(dt, _DT, "q")
-    if index < 0:
-        _refuse("q", q, dt, qshape, index)
-    qp, qs = _strided(q, "q", dt, index)
-    kp, ks = _strided(k, "k", dt, index)
-    vp, vs = _strided(v, "v", dt, index)
-    lp = None if kv_lens is None else _given(kv_lens, "kv_lens", torch.int32, (B,), index)
-    if out is None:
-        out = _alloc(qshape, dt, q.device, stream)
-        op = out.data_ptr()
-    else:
-        op = _given(out, "out", dt, qshape, index)
-    _invoke("vit_cross_attention", lib.vit_cross_attention, index, stream, (q, k, v, kv_lens, out),
-            (qp, qs, kp, ks, vp, vs, lp, B, Tq, Tk, H, Hkv, dh, dh ** -0.5 if scale is None else scale, code, op))
-    return out
+    fn = (_native or _serving()).cross_attention
+    if scale is None:
+        scale = (q.shape[-1] or 1) ** -0.5
+    if stream is None:
+        return fn(q, k, v, kv_lens, scale, out)
+    return _on(stream, (q, k, v, kv_lens, out), fn, q, k, v, kv_lens, scale, out)
 
 
 def device_error() -> int:

@@ -1,17 +1,20 @@
-"""Build the CUDA library in-tree: csrc/*.cu -> libvit_block.so (sm_103a only).
+"""Build in-tree: csrc/*.cu -> libvit_block.so (sm_103a only), the CUDA library, and
+csrc/binding.cpp -> _serving.so, the Python marshalling of its serving stages.
 
-Each translation unit is compiled in parallel with nvcc, then linked into one shared
-library next to this file. A rebuild happens only when a source or header is newer
-than the library. Usage: ``python -m vision_transformer_encoder_gb300.build``.
+Each translation unit is compiled in parallel, with nvcc or g++, then linked next to this
+file. A rebuild happens only when a source or header is newer than what is built. Usage:
+``python -m vision_transformer_encoder_gb300.build``.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -19,6 +22,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libvit_block.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING_PATH = os.path.join(HERE, "_serving.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
@@ -37,14 +42,14 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
+    return _sources() + [BINDING_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
         os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -64,14 +69,32 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stdout + r.stderr)
         return obj
 
+    def run(cmd, what):
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError("%s:\n%s%s" % (what, r.stdout, r.stderr))
+
+    def build_binding():
+        # torch is only located here, not imported; its libraries are in the process before the
+        # module is loaded
+        torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+        include = os.path.join(torch_dir, "include")
+        tmp = BINDING_PATH + ".%d.tmp" % os.getpid()
+        run([os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE, "-I", include,
+             "-I", os.path.join(include, "torch", "csrc", "api", "include"),
+             "-I", os.path.join(os.path.dirname(os.path.dirname(cc)), "include"),
+             "-I", sysconfig.get_paths()["include"], BINDING_SRC, "-o", tmp, "-L", os.path.join(torch_dir, "lib"),
+             "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"], "g++ failed on %s" % BINDING_SRC)
+        os.replace(tmp, BINDING_PATH)
+
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(build_binding)
         objs = list(ex.map(compile_one, srcs))
+        binding.result()
     tmp = LIB_PATH + ".%d.tmp" % os.getpid()
     cmd = [cc] + ARCH + ["-shared", "-o", tmp] + objs
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("link failed:\n%s%s" % (r.stdout, r.stderr))
+    run(cmd, "link failed")
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 
