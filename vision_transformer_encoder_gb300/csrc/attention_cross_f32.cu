@@ -1,11 +1,12 @@
 // attention_cross_f32.cu -- cross attention in fp32: the mathematics of attention_cross.cu for head
 // widths up to 128 in steps of 4.
 //
-// Products are 3xTF32 (hi hi + hi lo + lo hi, hi the 11 leading bits that the tensor cores read, lo the
-// rest) on mma.m16n8k8: relative to the sum of magnitudes off by 2^-20 or so, where fp32 chains of
-// this length are off by more. CUDA cores came out at half the rate: a thread's 8 x 8 piece needs
-// one product per cycle and scheduler and its operands from shared memory at 128 bytes a cycle
-// per SM, and reached half of either (8 x 197 queries over 288 to 577 keys of 12 heads of 64: 103 us).
+// Products are 3xTF32 (hi hi + hi lo + lo hi, hi rounded to the 11 bits that the tensor cores read,
+// lo the rest) on mma.m16n8k8, and sums longer than 16 keys are fp32 additions: the outputs of 8 x 197
+// queries over 288 to 577 keys are off by 3.6e-7 in the 2-norm, and by 3.3e-6 when O is summed on the
+// tensor cores, which cut sums off instead of rounding them. Bound by the tensor pipe (44 %
+// active); 55 us at 12 heads of 64 (35 TFLOP/s). A CUDA-core kernel took 103 us: one warp per
+// scheduler issues a product every other cycle.
 //
 // A CTA of four warps walks the keys of one (sequence, key head) 64 at a time, K and V tiles by TMA in
 // a ring that all warps read. Query rows are the n side of the products, S^T = K Q^T and
@@ -48,7 +49,15 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t lo_bits(uint32_t x) { return __float_as_uint(tf32_low_part(__uint_as_float(x))); }
+// x as hi + lo: hi its 11 leading bits, rounded to nearest (an infinity stays one), lo exact.
+__device__ __forceinline__ void split_tf32(uint32_t x, uint32_t& hi, uint32_t& lo) {
+    hi = (x + 0x1000u) & 0xFFFFE000u;
+    lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi));
+}
+__device__ __forceinline__ void split_tf32(const uint32_t (&x)[4], uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split_tf32(x[i], hi[i], lo[i]);
+}
 
 // Lane (r, c) holds row r, columns 2c and 2c + 1 of an 8 x 8 matrix: the same of the transpose.
 __device__ __forceinline__ void transpose_8x8_f32(float& x, float& y) {
@@ -153,21 +162,21 @@ cross_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                 // 16-byte unit i of key u at i ^ (u % 8)
                 const uint8_t* at = sk + (c >> 1) * CF_BOX + (g * 16 + r8) * 128 + (((2 * c4 + (c & 1)) ^ r8) << 4);
                 const uint4 k0 = *reinterpret_cast<const uint4*>(at), k1 = *reinterpret_cast<const uint4*>(at + 1024);
-                const uint32_t a0[4] = {k0.x, k1.x, k0.y, k1.y}, a1[4] = {k0.z, k1.z, k0.w, k1.w};
-                const uint32_t l0[4] = {lo_bits(a0[0]), lo_bits(a0[1]), lo_bits(a0[2]), lo_bits(a0[3])};
-                const uint32_t l1[4] = {lo_bits(a1[0]), lo_bits(a1[1]), lo_bits(a1[2]), lo_bits(a1[3])};
+                uint32_t a0[4], a1[4], l0[4], l1[4];
+                split_tf32({k0.x, k1.x, k0.y, k1.y}, a0, l0);
+                split_tf32({k0.z, k1.z, k0.w, k1.w}, a1, l1);
 #pragma unroll
                 for (int i = 0; i < NR; ++i) {
-                    const uint4 x = q[i][c];
-                    mma_tf32(s[i], a0, x.x, x.y);
-                    mma_tf32(s2[i], l0, x.x, x.y);
-                    mma_tf32(s3[i], a0, lo_bits(x.x), lo_bits(x.y));
-                    mma_tf32(s[i], a1, x.z, x.w);
-                    mma_tf32(s2[i], l1, x.z, x.w);
-                    mma_tf32(s3[i], a1, lo_bits(x.z), lo_bits(x.w));
+                    uint32_t x[4], y[4];
+                    split_tf32({q[i][c].x, q[i][c].y, q[i][c].z, q[i][c].w}, x, y);
+                    mma_tf32(s[i], a0, x[0], x[1]);
+                    mma_tf32(s2[i], l0, x[0], x[1]);
+                    mma_tf32(s3[i], a0, y[0], y[1]);
+                    mma_tf32(s[i], a1, x[2], x[3]);
+                    mma_tf32(s2[i], l1, x[2], x[3]);
+                    mma_tf32(s3[i], a1, y[2], y[3]);
                 }
             }
-            bool grew = false;
             float alpha[NR][2];
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
@@ -175,9 +184,8 @@ cross_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {   // key r8 + 8 (e / 2), row 2 c4 + e % 2
                     // an infinite hi hi stands as it is: the low part of an infinity is NaN
-                    const float x = fabsf(s[i][e]) < INFINITY ? s[i][e] + (s2[i][e] + s3[i][e]) : s[i][e];
-                    s[i][e] = r8 + 8 * (e >> 1) < valid ? x * scale_log2 : -INFINITY;
-                    mx[e & 1] = fmaxf(mx[e & 1], s[i][e]);
+                    if (fabsf(s[i][e]) < INFINITY) s[i][e] += s2[i][e] + s3[i][e];
+                    if (r8 + 8 * (e >> 1) < valid) mx[e & 1] = fmaxf(mx[e & 1], s[i][e] * scale_log2);
                 }
 #pragma unroll
                 for (int w = 4; w < 32; w *= 2) {
@@ -187,29 +195,24 @@ cross_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     alpha[i][e] = mx[e] > m[i][e] ? exp2_approx(m[i][e] - mx[e]) : 1.f;
-                    grew = grew || mx[e] > m[i][e];
                     m[i][e] = mx[e];
                     if (mx[e] == -INFINITY) mx[e] = 0.f;   // only infinite scores so far: weights of zero
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[i][e] = exp2_approx(s[i][e] - mx[e & 1]);
+                for (int e = 0; e < 4; ++e)
+                    s[i][e] = r8 + 8 * (e >> 1) < valid ? exp2_approx(fmaf(s[i][e], scale_log2, -mx[e & 1])) : 0.f;
                 l[i][0] = l[i][0] * alpha[i][0] + (s[i][0] + s[i][2]);
                 l[i][1] = l[i][1] * alpha[i][1] + (s[i][1] + s[i][3]);
                 transpose_8x8_f32(s[i][0], s[i][1]);   // now row r8, keys 2 c4 and 2 c4 + 1
                 transpose_8x8_f32(s[i][2], s[i][3]);   // and 8 on
             }
-            if (__any_sync(0xffffffffu, grew)) {
+            // the tensor cores cut sums off instead of rounding them, which adds up over hundreds of
+            // keys: the 16 keys' products start from zero and are added to O here
 #pragma unroll
-                for (int i = 0; i < NR; ++i)
+            for (int x = 0; x < NB; ++x) {
+                float y[NR][2][4] = {};
 #pragma unroll
-                    for (int j = 0; j < 2 * NB; ++j)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[i][j][e] *= alpha[i][e & 1];
-            }
-#pragma unroll
-            for (int k = 0; k < 2; ++k)   // eight keys
-#pragma unroll
-                for (int x = 0; x < NB; ++x) {
+                for (int k = 0; k < 2; ++k) {   // eight keys
                     const int u = g * 16 + k * 8 + 2 * c4;
                     const uint8_t* at = sv + x * CF_BOX + u * 128;
                     uint4 v0 = *reinterpret_cast<const uint4*>(at + ((r8 ^ (u & 7)) << 4));
@@ -218,21 +221,30 @@ cross_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                         if (k * 8 + 2 * c4 >= valid) v0 = make_uint4(0, 0, 0, 0);
                         if (k * 8 + 2 * c4 + 1 >= valid) v1 = make_uint4(0, 0, 0, 0);
                     }
-                    const uint32_t a0[4] = {v0.x, v0.y, v1.x, v1.y}, a1[4] = {v0.z, v0.w, v1.z, v1.w};
-                    const uint32_t l0[4] = {lo_bits(a0[0]), lo_bits(a0[1]), lo_bits(a0[2]), lo_bits(a0[3])};
-                    const uint32_t l1[4] = {lo_bits(a1[0]), lo_bits(a1[1]), lo_bits(a1[2]), lo_bits(a1[3])};
+                    uint32_t a0[4], a1[4], l0[4], l1[4];
+                    split_tf32({v0.x, v0.y, v1.x, v1.y}, a0, l0);
+                    split_tf32({v0.z, v0.w, v1.z, v1.w}, a1, l1);
 #pragma unroll
                     for (int i = 0; i < NR; ++i) {
-                        const uint32_t p0 = __float_as_uint(s[i][2 * k]), p1 = __float_as_uint(s[i][2 * k + 1]);
-                        const uint32_t n0 = lo_bits(p0), n1 = lo_bits(p1);
-                        mma_tf32(o[i][2 * x], a0, p0, p1);
-                        mma_tf32(o[i][2 * x + 1], a1, p0, p1);
-                        mma_tf32(o[i][2 * x], l0, p0, p1);
-                        mma_tf32(o[i][2 * x + 1], l1, p0, p1);
-                        mma_tf32(o[i][2 * x], a0, n0, n1);
-                        mma_tf32(o[i][2 * x + 1], a1, n0, n1);
+                        uint32_t p0, p1, n0, n1;
+                        split_tf32(__float_as_uint(s[i][2 * k]), p0, n0);
+                        split_tf32(__float_as_uint(s[i][2 * k + 1]), p1, n1);
+                        mma_tf32(y[i][0], l0, p0, p1);
+                        mma_tf32(y[i][1], l1, p0, p1);
+                        mma_tf32(y[i][0], a0, n0, n1);
+                        mma_tf32(y[i][1], a1, n0, n1);
+                        mma_tf32(y[i][0], a0, p0, p1);
+                        mma_tf32(y[i][1], a1, p0, p1);
                     }
                 }
+#pragma unroll
+                for (int i = 0; i < NR; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            o[i][2 * x + j][e] = fmaf(o[i][2 * x + j][e], alpha[i][e & 1], y[i][j][e]);
+            }
         }
         __syncwarp();   // this warp has read the stage
         if (lane == 0) ptx::mbar_arrive(empty + st);
