@@ -7,14 +7,17 @@
 // the whole head group. A work item is (sequence, key head, pair of tiles); a persistent CTA per
 // SM walks the items.
 //   warps 10, 11  TMA: Q and K tiles, V tiles, 128 keys each, rings of their own
-//   warps 1, 0    MMA issue for softmax group 0, 1: S = Q K^T (M 128, N 128, K dh), then
-//                 O += P V (M 128, N dh, K 128) with P read from TMEM and V MN-major
+//   warps 1, 0    MMA issue for softmax group 0, 1, 64 keys (half a tile) at a time: S = Q K^T
+//                 (M 128, N 64, K dh), then O += P V (M 128, N dh, K 64) with P read from TMEM and V
+//                 MN-major
 //   warps 2-5, 6-9  softmax groups 0 and 1, one query row per thread
+// Each group has two S buffers of 64 columns in TMEM, and P overwrites the S that it came from: while
+// the softmax works on one half tile, the scores of the next are there already and P V of the one
+// before runs. (With 128 keys at a time S, P and O of both groups fill TMEM, so that the scores
+// wait for P V and the softmax for the scores: a pair of tiles of 128 x 128 took 3960 cycles at dh 128
+// where its products take 2048.)
 // Heads wider than 64 columns are two 64-column boxes; columns past dh are zero-filled on load and
-// cut off on store by the tensor map, so 80 and 96 run as they are. For dh 64, P has columns of its
-// own in TMEM and S of the next key tile is made while P V of this one runs; for wider heads
-// S, O and P do not fit side by side, so P overwrites S and the two groups take turns on the
-// tensor cores instead.
+// cut off on store by the tensor map, so 80 and 96 run as they are.
 //
 // The running maximum is only raised when a row's scores exceed it by more than 8 (in log2): until
 // then weights of up to 2^8 are carried, exactly as good in bf16 and far inside fp32, and the
@@ -34,17 +37,16 @@
 namespace vit {
 namespace {
 
-constexpr int CT_ROWS = 128, CT_KEYS = 128, CT_THREADS = 384;
+constexpr int CT_ROWS = 128, CT_KEYS = 128, CT_SUB = 64, CT_THREADS = 384;
 constexpr int CT_BOX = CT_ROWS * 128;      // 64 columns x 128 rows: 16 KB
 constexpr float CT_SLACK = 8.f;            // log2 of the weights that are carried before a rescale
 
 template <int DH> struct CtLayout {
     static_assert(DH % 16 == 0 && DH >= 64 && DH <= 128, "head width");
     static constexpr int NCH = (DH + 63) / 64;           // 64-column boxes per tile
-    static constexpr bool ALIAS = DH > 64;               // P overwrites S
     static constexpr int TILE = NCH * CT_BOX;
-    static constexpr int QBUF = ALIAS ? 1 : 2;           // buffers of two query tiles
-    static constexpr int KVS = ALIAS ? 2 : 4;            // stages of each ring
+    static constexpr int QBUF = NCH == 2 ? 1 : 2;        // buffers of two query tiles
+    static constexpr int KVS = NCH == 2 ? 2 : 4;         // stages of each ring
     static constexpr int OFF_K = QBUF * 2 * TILE;
     static constexpr int OFF_V = OFF_K + KVS * TILE;
     static constexpr int OFF_O = OFF_V + KVS * TILE;     // per group: one 64-column box of O on its way out
@@ -65,7 +67,8 @@ struct CtParams {
 struct CtBars {
     uint64_t q_full[2], q_empty[2];
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-    uint64_t s_full[2], s_read[2], p_full[2], o_done[2], o_free[2], ost_full[2], ost_free[2];
+    // two of each for the half tiles in turn: a waiter may be one phase behind, never two
+    uint64_t s_full[2][2], p_full[2][2], o_done[2][2], o_free[2], ost_full[2], ost_free[2];
     uint64_t done;
     uint32_t tmem_slot;
     int abort_flag;
@@ -77,7 +80,8 @@ __device__ __forceinline__ void ct_error(uint32_t* err, uint32_t bit) {
 }
 
 struct CtItem {
-    int b, h, t0, nact, len, nkt;
+    int b, h, t0, nact, len;
+    int nkt, nst;   // key tiles, half tiles
 };
 
 __device__ __forceinline__ CtItem ct_item(const CtParams& p, int item) {
@@ -89,6 +93,7 @@ __device__ __forceinline__ CtItem ct_item(const CtParams& p, int item) {
     x.nact = x.t0 + p.TT < p.Tq ? 2 : 1;
     x.len = p.kv_lens ? min(max(__ldg(p.kv_lens + x.b), 0), p.Tk) : p.Tk;
     x.nkt = (x.len + CT_KEYS - 1) / CT_KEYS;
+    x.nst = (x.len + CT_SUB - 1) / CT_SUB;
     return x;
 }
 
@@ -98,7 +103,6 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, const CtParams p) {
     using L = CtLayout<DH>;
     constexpr int KVS = L::KVS, QB = L::QBUF, NCH = L::NCH;
-    constexpr bool ALIAS = L::ALIAS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t* sQ = smem;
@@ -112,10 +116,11 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&bars->q_full[i], 1);
             ptx::mbar_init(&bars->q_empty[i], 2);     // both MMA issuers
-            ptx::mbar_init(&bars->s_full[i], 1);
-            ptx::mbar_init(&bars->s_read[i], 4);      // one arrival per softmax warp
-            ptx::mbar_init(&bars->p_full[i], 4);
-            ptx::mbar_init(&bars->o_done[i], 1);
+            for (int b = 0; b < 2; ++b) {
+                ptx::mbar_init(&bars->s_full[i][b], 1);
+                ptx::mbar_init(&bars->p_full[i][b], 4);   // one arrival per softmax warp
+                ptx::mbar_init(&bars->o_done[i][b], 1);
+            }
             ptx::mbar_init(&bars->o_free[i], 4);
             ptx::mbar_init(&bars->ost_full[i], 4);
             ptx::mbar_init(&bars->ost_free[i], 1);
@@ -143,10 +148,10 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    const uint32_t tmem = bars->tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_slot, 0);
     griddep_wait();
     griddep_launch_dependents();
-    // TMEM columns: S_g at 128 g; O_g at 256 + 128 g; P_g over S_g, or for dh 64 behind O_g
+    // TMEM columns: S_g at 128 g, two buffers of 64 with P over each; O_g at 256 + 128 g
 
     if (warp >= 10) {
         if (lane == 0) {
@@ -194,32 +199,37 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     ct_error(p.err, ERRBIT_TIMEOUT_TEARDOWN);
         }
     } else if (warp <= 1) {
-        // ---------------------------------------------------- MMA issue, lane 0; the other lanes
-        // wait alongside and help to clear V rows
+        // ---------------------------------------------------- MMA issue, one lane; the others wait
+        // alongside and help to clear V rows
         const int g = warp == 1 ? 0 : 1;
-        constexpr uint32_t idS = ptx::idesc_bf16_f32(CT_ROWS, CT_KEYS, false, false);
+        constexpr uint32_t idS = ptx::idesc_bf16_f32(CT_ROWS, CT_SUB, false, false);
         constexpr uint32_t idO = ptx::idesc_bf16_f32(CT_ROWS, DH, false, true);
-        const uint32_t tS = tmem + g * CT_KEYS, tO = tmem + 256 + g * 128, tP = ALIAS ? tS : tO + 64;
-        uint32_t base = 0, ii = 0, pc = 0, ic = 0;
+        const uint32_t tS = tmem + g * 128, tO = tmem + 256 + g * 128;
+        uint32_t base = 0, ii = 0, pc = 0, ic = 0;   // key tiles, items with keys, half tiles, own items so far
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
             return __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, parity, abort_flag));
         };
-        auto issue_S = [&](int j, uint32_t qb) -> bool {
-            const uint32_t it = base + j, st = it % KVS;
+        // S of half tile j of this item, n half tiles after the first of this group
+        auto issue_S = [&](int j, uint32_t n, uint32_t qb, bool last_of_stage) -> bool {
+            const uint32_t it = base + (j >> 1), st = it % KVS;
             if (!wait(&bars->k_full[st], (it / KVS) & 1)) return false;
             ptx::tc_fence_after();
-            if (lane == 0) {
-                const uint32_t qa = ptx::smem_addr(sQ + (qb * 2 + g) * L::TILE), ka = ptx::smem_addr(sK + st * L::TILE);
+            // descriptors count 16-byte units: those of later steps are sums
+            const uint64_t qd = ptx::smem_desc(ptx::smem_addr(sQ + (qb * 2 + g) * L::TILE), 16, 1024, ptx::kLayoutSw128);
+            const uint64_t kd = ptx::smem_desc(ptx::smem_addr(sK + st * L::TILE + (j & 1) * (CT_SUB * 128)), 16, 1024,
+                                               ptx::kLayoutSw128);
+            const uint32_t tD = tS + (n & 1) * CT_SUB;
+            if (ptx::elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < DH / 16; ++kk) {
-                    const uint32_t off = (kk >> 2) * CT_BOX + (kk & 3) * 32;
-                    ptx::mma_bf16_ss(tS, ptx::smem_desc(qa + off, 16, 1024, ptx::kLayoutSw128),
-                                     ptx::smem_desc(ka + off, 16, 1024, ptx::kLayoutSw128), idS, kk > 0);
+                    const uint64_t off = ((kk >> 2) * CT_BOX + (kk & 3) * 32) >> 4;
+                    ptx::mma_bf16_ss(tD, qd + off, kd + off, idS, kk > 0);
                 }
-                ptx::mma_commit(&bars->s_full[g]);
-                ptx::mma_commit(&bars->k_empty[st]);
+                ptx::mma_commit(&bars->s_full[g][n & 1]);
+                if (last_of_stage) ptx::mma_commit(&bars->k_empty[st]);
             }
+            __syncwarp();
             return true;
         };
         for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x) {
@@ -231,69 +241,68 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             if (!ok) break;
             if (g >= x.nact) {
                 // no tile for this group: release what the other issuer uses, each once it has landed
-                if (lane == 0) ptx::mma_commit(&bars->q_empty[qb]);
+                if (ptx::elect_one()) ptx::mma_commit(&bars->q_empty[qb]);
                 for (int j = 0; j < x.nkt && ok; ++j) {
                     const uint32_t it = base + j, st = it % KVS;
                     ok = wait(&bars->k_full[st], (it / KVS) & 1);
-                    if (ok && lane == 0) ptx::mma_commit(&bars->k_empty[st]);
+                    if (ok && ptx::elect_one()) ptx::mma_commit(&bars->k_empty[st]);
                     ok = ok && wait(&bars->v_full[st], (it / KVS) & 1);
-                    if (ok && lane == 0) ptx::mma_commit(&bars->v_empty[st]);
+                    if (ok && ptx::elect_one()) ptx::mma_commit(&bars->v_empty[st]);
                 }
                 base += x.nkt;
                 continue;
             }
-            ok = issue_S(0, qb);
-            if (ok && x.nkt == 1 && lane == 0) ptx::mma_commit(&bars->q_empty[qb]);
-            for (int j = 0; j < x.nkt && ok; ++j, ++pc) {
-                if (!ALIAS) {
-                    // S of the next tile as soon as the softmax holds this one in registers
-                    if (!(ok = wait(&bars->s_read[g], pc & 1))) break;
-                    if (j + 1 < x.nkt) {
-                        if (!(ok = issue_S(j + 1, qb))) break;
-                        if (j + 2 == x.nkt && lane == 0) ptx::mma_commit(&bars->q_empty[qb]);
-                    }
-                }
-                const uint32_t it = base + j, st = it % KVS;
+            auto scores = [&](int j) -> bool {   // and what their last user releases
+                if (!issue_S(j, pc + j, qb, (j & 1) || j + 1 == x.nst)) return false;
+                if (j + 1 == x.nst && ptx::elect_one()) ptx::mma_commit(&bars->q_empty[qb]);
+                return true;
+            };
+            // the first scores overwrite the last item's P: after its last P V has read it
+            ok = (pc == 0 || wait(&bars->o_done[g][(pc - 1) & 1], ((pc - 1) >> 1) & 1)) && scores(0) && (x.nst < 2 || scores(1));
+            for (int j = 0; j < x.nst && ok; ++j) {
+                const uint32_t it = base + (j >> 1), st = it % KVS, n = pc + j;
                 if (!(ok = wait(&bars->v_full[st], (it / KVS) & 1))) break;
-                const int valid = x.len - j * CT_KEYS;
-                if (valid < CT_KEYS) {
+                const int valid = x.len - j * CT_SUB;
+                uint8_t* v = sV + st * L::TILE + (j & 1) * (CT_SUB * 128);
+                if (valid < CT_SUB) {
                     // rows past the length may hold anything, and 0 * NaN is NaN. Both issuers clear
                     // the same rows: the second finds zeros and writes zeros.
-                    for (int i = valid * 8 + lane; i < CT_KEYS * 8; i += 32)
+                    for (int i = valid * 8 + lane; i < CT_SUB * 8; i += 32)
 #pragma unroll
                         for (int c = 0; c < NCH; ++c)
-                            *reinterpret_cast<uint4*>(sV + st * L::TILE + c * CT_BOX + i * 16) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4*>(v + c * CT_BOX + i * 16) = make_uint4(0, 0, 0, 0);
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                 }
-                if (!(ok = wait(&bars->p_full[g], pc & 1))) break;
+                if (!(ok = wait(&bars->p_full[g][n & 1], (n >> 1) & 1))) break;
                 if (j == 0 && ic > 0 && !(ok = wait(&bars->o_free[g], (ic - 1) & 1))) break;
                 ptx::tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t va = ptx::smem_addr(sV + st * L::TILE);
+                const uint64_t vd = ptx::smem_desc(ptx::smem_addr(v), CT_BOX, 1024, ptx::kLayoutSw128);
+                const uint32_t tP = tS + (n & 1) * CT_SUB;
+                if (ptx::elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < CT_KEYS / 16; ++kk)   // 16 keys: 16 rows of V, 8 columns of bf16 pairs of P
-                        ptx::mma_bf16_ts(tO, tP + kk * 8, ptx::smem_desc(va + kk * 2048, CT_BOX, 1024, ptx::kLayoutSw128),
-                                         idO, j > 0 || kk > 0);
-                    ptx::mma_commit(&bars->o_done[g]);
-                    ptx::mma_commit(&bars->v_empty[st]);
+                    for (int kk = 0; kk < CT_SUB / 16; ++kk)   // 16 keys: 16 rows of V, 8 columns of bf16 pairs of P
+                        ptx::mma_bf16_ts(tO, tP + kk * 8, vd + kk * (2048 >> 4), idO, j > 0 || kk > 0);
+                    ptx::mma_commit(&bars->o_done[g][n & 1]);
+                    if ((j & 1) || j + 1 == x.nst) ptx::mma_commit(&bars->v_empty[st]);
                 }
                 __syncwarp();
-                if (ALIAS && j + 1 < x.nkt) {
-                    // S of the next tile overwrites P: after P V has read it
-                    if (!(ok = wait(&bars->o_done[g], pc & 1))) break;
-                    if (!(ok = issue_S(j + 1, qb))) break;
-                    if (j + 2 == x.nkt && lane == 0) ptx::mma_commit(&bars->q_empty[qb]);
+                if (j + 2 < x.nst) {
+                    // the scores two on overwrite P: after P V has read it; the next ones are there
+                    if (!(ok = wait(&bars->o_done[g][n & 1], (n >> 1) & 1))) break;
+                    ok = scores(j + 2);
                 }
             }
             ++ic;
+            pc += x.nst;
             base += x.nkt;
         }
         if (!ok && lane == 0) {
             ct_error(p.err, ERRBIT_TIMEOUT_MMA);
             *abort_flag = 1;
         }
-        if (lane == 0) {
+        __syncwarp();
+        if (ptx::elect_one()) {
             ptx::mma_commit(&bars->done);
             if (!ptx::mbar_wait_bounded(&bars->done, 0, nullptr)) ct_error(p.err, ERRBIT_TIMEOUT_TEARDOWN);
         }
@@ -301,12 +310,11 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         // ---------------------------------------------------- softmax groups
         const int g = (warp - 2) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-        const uint32_t tS = tmem + g * CT_KEYS + lane_off, tO = tmem + 256 + g * 128 + lane_off;
-        const uint32_t tP = ALIAS ? tS : tO + 64;
+        const uint32_t tO = tmem + 256 + g * 128 + lane_off;
         uint8_t* stage = smem + L::OFF_O + g * CT_BOX;
         const bool storer = quarter == 2 && lane == 0;
         const float sl2 = p.scale_log2;
-        uint32_t tt = 0, sc = 0;   // key tiles, staged boxes of this group so far
+        uint32_t tt = 0, sc = 0;   // half tiles, staged boxes of this group so far
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
             return __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, parity, abort_flag));
@@ -318,63 +326,38 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             // a warp whose 32 rows hold no query only keeps the barrier protocol
             const bool live = quarter * 32 < min(p.TT, p.Tq - t0) * p.G;
             float m = -INFINITY, l = 0.f;
-            for (int j = 0; j < x.nkt; ++j, ++tt) {
-                if (!(ok = wait(&bars->s_full[g], tt & 1))) break;
+            for (int j = 0; j < x.nst; ++j, ++tt) {
+                if (!(ok = wait(&bars->s_full[g][tt & 1], (tt >> 1) & 1))) break;
                 ptx::tc_fence_after();
-                uint32_t sv[CT_KEYS];   // S, then P packed in place
-                float alpha = 1.f, lsum = 0.f;
+                const uint32_t tS = tmem + g * 128 + (tt & 1) * CT_SUB + lane_off;
                 if (live) {
-#pragma unroll
-                    for (int c = 0; c < CT_KEYS / 32; ++c)
-                        ptx::tmem_ld_32x32b_x32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[c * 32]));
+                    uint32_t sv[CT_SUB];   // S, then P packed in place
+                    ptx::tmem_ld_32x32b_x32(tS, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+                    ptx::tmem_ld_32x32b_x32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
                     ptx::tmem_ld_wait();
-                }
-                if (!ALIAS) {
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&bars->s_read[g]);
-                }
-                if (live) {
-                    const int valid = x.len - j * CT_KEYS;
-                    if (valid < CT_KEYS) {
+                    const int valid = x.len - j * CT_SUB;
+                    if (valid < CT_SUB) {
 #pragma unroll
-                        for (int e = 0; e < CT_KEYS; ++e)
+                        for (int e = 0; e < CT_SUB; ++e)
                             if (e >= valid) sv[e] = __float_as_uint(-INFINITY);
                     }
                     float mx[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) mx[e] = __uint_as_float(sv[e]);
 #pragma unroll
-                    for (int e = 8; e < CT_KEYS; ++e) mx[e & 7] = fmaxf(mx[e & 7], __uint_as_float(sv[e]));
+                    for (int e = 8; e < CT_SUB; ++e) mx[e & 7] = fmaxf(mx[e & 7], __uint_as_float(sv[e]));
                     const float mrow = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
                                              fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * sl2;
+                    float alpha = 1.f;
                     if (mrow > m + CT_SLACK || m == -INFINITY) {   // raise the maximum
                         const float m_new = fmaxf(m, mrow);
                         if (m_new > -INFINITY) alpha = exp2_approx(m - m_new);
                         m = m_new;
                     }
-                    const float base = m == -INFINITY ? 0.f : m;   // only infinite scores so far: weights of zero
-                    const unsigned long long s2 = f2_pack(sl2, sl2), nm = f2_pack(-base, -base);
-                    unsigned long long ls[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-                    for (int e = 0; e < CT_KEYS; e += 2) {
-                        float x0, x1;
-                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), s2, nm), x0, x1);
-                        const float p0 = exp2_approx(x0), p1 = exp2_approx(x1);
-                        ls[(e >> 1) & 3] = f2_add(ls[(e >> 1) & 3], f2_pack(p0, p1));
-                        sv[e >> 1] = pack_bf16x2(p0, p1);
-                    }
-                    float a0, a1, b0, b1;
-                    f2_unpack(f2_add(ls[0], ls[1]), a0, a1);
-                    f2_unpack(f2_add(ls[2], ls[3]), b0, b1);
-                    lsum = (a0 + a1) + (b0 + b1);
-                }
-                if (!ALIAS && j > 0) {   // P V of the previous tile reads P and writes O
-                    if (!(ok = wait(&bars->o_done[g], (tt - 1) & 1))) break;
-                    ptx::tc_fence_after();
-                }
-                if (live) {
                     if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                        // P V of the half tile before writes O
+                        if (!(ok = wait(&bars->o_done[g][(tt - 1) & 1], ((tt - 1) >> 1) & 1))) break;
+                        ptx::tc_fence_after();
 #pragma unroll
                         for (int c = 0; c < DH / 16; ++c) {
                             uint32_t ov[16];
@@ -385,19 +368,31 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                             ptx::tmem_st_32x32b_x16(tO + c * 16, ov);
                         }
                     }
+                    const float base = m == -INFINITY ? 0.f : m;   // only infinite scores so far: weights of zero
+                    const unsigned long long s2 = f2_pack(sl2, sl2), nm = f2_pack(-base, -base);
+                    unsigned long long ls[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-                    for (int c = 0; c < CT_KEYS / 64; ++c)
-                        ptx::tmem_st_32x32b_x32(tP + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[c * 32]));
-                    l = l * alpha + lsum;
+                    for (int e = 0; e < CT_SUB; e += 2) {
+                        float x0, x1;
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), s2, nm), x0, x1);
+                        const float p0 = exp2_approx(x0), p1 = exp2_approx(x1);
+                        ls[(e >> 1) & 3] = f2_add(ls[(e >> 1) & 3], f2_pack(p0, p1));
+                        sv[e >> 1] = pack_bf16x2(p0, p1);
+                    }
+                    ptx::tmem_st_32x32b_x32(tS, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+                    float a0, a1, b0, b1;
+                    f2_unpack(f2_add(ls[0], ls[1]), a0, a1);
+                    f2_unpack(f2_add(ls[2], ls[3]), b0, b1);
+                    l = l * alpha + ((a0 + a1) + (b0 + b1));
                     ptx::tmem_st_wait();
                 }
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&bars->p_full[g]);
+                if (lane == 0) ptx::mbar_arrive(&bars->p_full[g][tt & 1]);
             }
             if (!ok) break;
             if (x.nkt > 0) {
-                if (!(ok = wait(&bars->o_done[g], (tt - 1) & 1))) break;
+                if (!(ok = wait(&bars->o_done[g][(tt - 1) & 1], ((tt - 1) >> 1) & 1))) break;
                 ptx::tc_fence_after();
             }
             const float inv = 1.f / l;
