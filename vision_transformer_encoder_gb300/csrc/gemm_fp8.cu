@@ -244,35 +244,46 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                     if (it > s && !ptx::mbar_wait_bounded(full + s, ((it - 1 - s) / STAGES) & 1, nullptr))
                         f8_error(p.err, ERRBIT_TIMEOUT_TEARDOWN);
             }
-        } else if (warp == 0 && lane == 0 && rank == 0) {
-            // ------------------------------------------------ MMA issue (leader)
+        } else if (warp == 0 && rank == 0) {
+            // ------------------------------------------------ MMA issue (leader), one lane of a warp
+            // that stays together (see elect_one): from lane 0 alone each issue took some 100 cycles
             constexpr uint32_t idesc = ptx::idesc_e4m3_f32(FP_TILE_M, BN);
-            uint32_t it = 0;
+            const uint64_t a0 = ptx::smem_desc_sw128(ptx::smem_addr(smem), 16, 1024);
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            uint32_t it = 0, s = 0, round = 0;
             bool ok = true;
             for (int t = cluster; t < tiles && ok; t += nclusters) {
                 for (int kb = 0; kb < kblocks; ++kb, ++it) {
-                    const uint32_t s = it % STAGES, acc = it & 1;
-                    if (!ptx::mbar_wait_bounded(tempty + acc, ((it >> 1) & 1) ^ 1, abort_flag) ||
-                        !ptx::mbar_wait_bounded(full + s, (it / STAGES) & 1, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
+                    const uint32_t acc = it & 1;
+                    ok = ptx::mbar_wait_bounded(tempty + acc, ((it >> 1) & 1) ^ 1, abort_flag) &&
+                         ptx::mbar_wait_bounded(full + s, round & 1, abort_flag);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
                     ptx::tc_fence_after();
-                    const uint32_t a = ptx::smem_addr(smem + s * L::STAGE), b = a + FP_A_BYTES;
+                    // descriptors count 16-byte units
+                    const uint64_t ad = a0 + s * (L::STAGE >> 4), bd = ad + (FP_A_BYTES >> 4);
+                    if (ptx::elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kFp8Block / 32; ++k)
-                        ptx::mma_f8_ss_pair(tmem + acc * BN, ptx::smem_desc_sw128(a + k * 32, 16, 1024),
-                                            ptx::smem_desc_sw128(b + k * 32, 16, 1024), idesc, k != 0);
-                    ptx::mma_commit_pair_mc(empty + s, 0x3);
-                    ptx::mma_commit_pair_mc(tfull + acc, 0x3);
+                        for (int k = 0; k < kFp8Block / 32; ++k)
+                            ptx::mma_f8_ss_pair(tm + acc * BN, ad + k * 2, bd + k * 2, idesc, k != 0);
+                        ptx::mma_commit_pair_mc(empty + s, 0x3);
+                        ptx::mma_commit_pair_mc(tfull + acc, 0x3);
+                    }
+                    __syncwarp();
+                    if (++s == (uint32_t)STAGES) {
+                        s = 0;
+                        ++round;
+                    }
                 }
             }
-            if (!ok) {
-                f8_error(p.err, ERRBIT_TIMEOUT_MMA);
-                *abort_flag = 1;
+            if (ptx::elect_one()) {
+                if (!ok) {
+                    f8_error(p.err, ERRBIT_TIMEOUT_MMA);
+                    *abort_flag = 1;
+                }
+                ptx::mma_commit_pair(done);
+                if (!ptx::mbar_wait_bounded(done, 0, nullptr)) f8_error(p.err, ERRBIT_TIMEOUT_TEARDOWN);
             }
-            ptx::mma_commit_pair(done);
-            if (!ptx::mbar_wait_bounded(done, 0, nullptr)) f8_error(p.err, ERRBIT_TIMEOUT_TEARDOWN);
         }
     } else {
         // ------------------------------------------------ promotion and epilogue
