@@ -147,6 +147,12 @@ __device__ __forceinline__ unsigned long long gelu_tanh_exp2(unsigned long long 
     return f2_mul(z, f2_mul(f2_pack(r, r), f2_pack(a1, a0)));
 }
 
+// The same of one value.
+__device__ __forceinline__ float gelu_tanh_exp1(float z) {
+    const float c0 = -2.f * 0.7978845608028654f * 1.4426950408889634f;
+    return __fdividef(z, 1.f + exp2_approx(fminf(z * fmaf(c0 * 0.044715f, z * z, c0), 60.f)));
+}
+
 // Accurate forms (library tanh) for the fp32 / fp64 paths.
 __device__ __forceinline__ float gelu_tanh_acc(float z) {
     const float k0 = 0.7978845608028654f;

@@ -19,6 +19,12 @@
 //                registers, one row per thread, so the row's scale is one register and an e4m3
 //                output's 128-column scale needs no exchange (BN 256)
 //
+// Rows kernel (few rows): bound by the weight's bytes and by latency. The weight is the M side,
+// out^T = w a^T: a CTA takes 128 weight rows (one scale block) against 16 or 32 rows of a, and a
+// cluster of CTAs shares the blocks along K, so that a decoding step's product streams its weight
+// with most of the SMs. The CTAs' fp32 sums meet in distributed shared memory and are added in
+// rank order: no workspace, one launch, the same result every time.
+//
 // Generic kernel: CUDA cores, any size and alignment; a CTA makes 16 rows x 128 columns (one
 // output block per row), a thread eight columns of one row.
 #include <cuda.h>
@@ -576,6 +582,331 @@ bool f8_tc_ok(const Fp8GemmDesc& d, const DeviceInfo& dev) {
            ((d.M + 255) / 256) * ((d.N + 127) / 128) <= lim && dev.num_sms >= 2 && f8_encode_fn() != nullptr;
 }
 
+// ------------------------------------------------------------------------ rows kernel
+constexpr int FR_THREADS = 224;   // warp 0: weight loads, 1: MMA, 2-5: sums and epilogue, 6: loads of a
+constexpr int FR_BUFS = 4;        // block sums in TMEM
+constexpr int FR_MAXZ = 8;
+
+template <int TN> struct FrLayout {
+    static constexpr int W_BYTES = 128 * kFp8Block;
+    static constexpr int STAGE = W_BYTES + TN * kFp8Block;
+    static constexpr int STAGES = 8;
+    static constexpr int OFF_SC = STAGES * STAGE;                    // per warp: two sets of TN scales
+    static constexpr int OFF_MAX = OFF_SC + 4 * 2 * TN * 4;          // per token: four warps' maxima
+    static constexpr int OFF_BAR = OFF_MAX + 4 * TN * 4;
+    static constexpr int SMEM = OFF_BAR + 512 + 1024;
+    static_assert(TN * 128 * 4 <= STAGES * STAGE, "sums over the ring");
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ float fr_ld_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    return v;
+}
+
+template <int TN, int EPI, int OUT>
+__global__ void __launch_bounds__(FR_THREADS, 1)
+gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
+                     const __grid_constant__ FpParams p, int Z, int mtiles) {
+    using L = FrLayout<TN>;
+    constexpr int STAGES = L::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+    uint64_t* empty = full + STAGES;
+    uint64_t* tfull = empty + STAGES;
+    uint64_t* tempty = tfull + FR_BUFS;
+    uint64_t* done = tempty + FR_BUFS;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const Fp8GemmDesc& d = p.d;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int z = Z > 1 ? (int)ptx::cluster_ctarank() : 0, tile = blockIdx.x / Z;
+    const int nt = tile / mtiles, mt = tile - nt * mtiles;
+    const int kblocks = (int)((d.K + kFp8Block - 1) / kFp8Block);
+    // this CTA's share of the blocks
+    const int per = (kblocks + Z - 1) / Z, kb0 = min(z * per, kblocks), nkb = min(kb0 + per, kblocks) - kb0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            ptx::mbar_init(full + s, 2);
+            ptx::mbar_init(empty + s, 1);
+        }
+        for (int b = 0; b < FR_BUFS; ++b) {
+            ptx::mbar_init(tfull + b, 1);
+            ptx::mbar_init(tempty + b, 4);
+        }
+        ptx::mbar_init(done, 1);
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tensormap(&tmW);
+        ptx::prefetch_tensormap(&tmA);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(tmem_slot, FR_BUFS * TN);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+    griddep_wait();
+    griddep_launch_dependents();
+
+    bool failed = false;
+    float acc[TN];
+    if (warp == 0 || warp == 6) {
+        if (lane == 0) {
+            bool ok = true;
+            int i = 0;
+            for (; i < nkb; ++i) {
+                const int s = i % STAGES;
+                if (!ptx::mbar_wait_bounded<true>(empty + s, ((i / STAGES) & 1) ^ 1, abort_flag)) { ok = false; break; }
+                uint8_t* st = smem + s * L::STAGE;
+                if (warp == 0) {
+                    ptx::mbar_arrive_expect_tx(full + s, L::W_BYTES);
+                    ptx::tma_load_2d(st, &tmW, full + s, (kb0 + i) * kFp8Block, nt * 128);
+                } else {
+                    ptx::mbar_arrive_expect_tx(full + s, TN * kFp8Block);
+                    ptx::tma_load_2d(st + L::W_BYTES, &tmA, full + s, (kb0 + i) * kFp8Block, mt * TN);
+                }
+            }
+            if (!ok) {
+                f8_error(p.err, ERRBIT_TIMEOUT_PRODUCER);
+                *abort_flag = 1;
+                // copies in flight land before the CTA can exit
+                for (int j = i > STAGES ? i - STAGES : 0; j < i; ++j)
+                    if (!ptx::mbar_wait_bounded(full + j % STAGES, (j / STAGES) & 1, nullptr))
+                        f8_error(p.err, ERRBIT_TIMEOUT_TEARDOWN);
+            }
+        }
+    } else if (warp == 1) {
+        constexpr uint32_t idesc = ptx::idesc_e4m3_f32(128, TN);
+        const uint64_t w0 = ptx::smem_desc_sw128(ptx::smem_addr(smem), 16, 1024);
+        bool ok = true;
+        for (int i = 0; i < nkb; ++i) {
+            const uint32_t s = i % STAGES, buf = i % FR_BUFS;
+            ok = ptx::mbar_wait_bounded(tempty + buf, ((i / FR_BUFS) & 1) ^ 1, abort_flag) &&
+                 ptx::mbar_wait_bounded(full + s, (i / STAGES) & 1, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const uint64_t wd = w0 + s * (L::STAGE >> 4), ad = wd + (L::W_BYTES >> 4);
+            if (ptx::elect_one()) {
+#pragma unroll
+                for (int k = 0; k < kFp8Block / 32; ++k)
+                    ptx::mma_f8_ss(tmem + buf * TN, wd + k * 2, ad + k * 2, idesc, k != 0);
+                ptx::mma_commit(empty + s);
+                ptx::mma_commit(tfull + buf);
+            }
+            __syncwarp();
+        }
+        if (ptx::elect_one()) {
+            if (!ok) {
+                f8_error(p.err, ERRBIT_TIMEOUT_MMA);
+                *abort_flag = 1;
+            }
+            ptx::mma_commit(done);
+            if (!ptx::mbar_wait_bounded(done, 0, nullptr)) f8_error(p.err, ERRBIT_TIMEOUT_TEARDOWN);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------ sums: a weight row per thread, TN tokens
+        const int quarter = warp & 3;
+        const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
+        float* sc = reinterpret_cast<float*>(smem + L::OFF_SC) + quarter * 2 * TN;
+        constexpr int PER = (TN + 31) / 32;
+        // products of a block's scales for this lane's tokens
+        auto scales = [&](int i, float (&v)[PER]) {
+            const float w = i < nkb ? __ldg(d.w_scales + (int64_t)nt * kblocks + kb0 + i) : 0.f;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                const int64_t m = (int64_t)mt * TN + j * 32 + lane;
+                v[j] = i < nkb && j * 32 + lane < TN && m < d.M ? w * __ldg(d.a_scales + m * kblocks + kb0 + i) : 0.f;
+            }
+        };
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[j] = 0.f;
+        float v0[PER], v1[PER];
+        scales(0, v0);
+        scales(1, v1);
+        for (int i = 0; i < nkb; ++i) {
+            const uint32_t buf = i % FR_BUFS;
+            float* set = sc + (i & 1) * TN;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                if (j * 32 + lane < TN) set[j * 32 + lane] = v0[j];
+                v0[j] = v1[j];
+            }
+            scales(i + 2, v1);
+            __syncwarp();   // two sets in turn: nobody is still reading the one that is written next
+            if (!failed && !__all_sync(0xffffffffu, ptx::mbar_wait_bounded(tfull + buf, (i / FR_BUFS) & 1, abort_flag))) {
+                failed = true;
+                if (lane == 0) f8_error(p.err, ERRBIT_TIMEOUT_EPILOGUE);
+                *abort_flag = 1;
+            }
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < TN / 16; ++c) {
+                uint32_t r[16];
+                ptx::tmem_ld_32x32b_x16(t_lane + buf * TN + c * 16, r);
+                ptx::tmem_ld_wait_for(r);
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(set + c * 16 + j);
+                    acc[c * 16 + j] = fmaf(f.x, __uint_as_float(r[j]), acc[c * 16 + j]);
+                    acc[c * 16 + j + 1] = fmaf(f.y, __uint_as_float(r[j + 1]), acc[c * 16 + j + 1]);
+                    acc[c * 16 + j + 2] = fmaf(f.z, __uint_as_float(r[j + 2]), acc[c * 16 + j + 2]);
+                    acc[c * 16 + j + 3] = fmaf(f.w, __uint_as_float(r[j + 3]), acc[c * 16 + j + 3]);
+                }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(tempty + buf);
+        }
+    }
+    // ---------------------------------------------------- the CTAs' sums over the ring, [token][weight row]
+    float* part = reinterpret_cast<float*>(smem);
+    __syncthreads();   // every block of this CTA has been multiplied and added
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, FR_BUFS * TN);
+    }
+    const bool sums = warp >= 2 && warp <= 5;
+    const int n = (warp & 3) * 32 + lane;
+    if (sums && Z > 1) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) part[j * 128 + n] = acc[j];
+    }
+    if (Z > 1) ptx::cluster_sync();
+    if (sums) {
+        const int64_t col = (int64_t)nt * 128 + n, nblk = (d.N + kFp8Block - 1) / kFp8Block;
+        const float bias = d.bias && col < d.N ? load_f32(d.bias, d.bias_f32, col) : 0.f;
+        float* mx = reinterpret_cast<float*>(smem + L::OFF_MAX);
+        // this CTA's tokens: all of them, or its share of the cluster's
+        const int share = (TN + Z - 1) / Z, j0 = z * share, j1 = min(j0 + share, TN);
+        auto finish = [&](int j, float v) -> float {
+            const int64_t m = (int64_t)mt * TN + j;
+            v += bias;
+            if constexpr (EPI == TC_EPI_GELU) v = gelu_tanh_exp1(v);
+            if constexpr (EPI == TC_EPI_RESID)
+                if (m < d.M && col < d.N) v += load_f32(d.residual, d.residual_f32, m * d.N + col);
+            return v;
+        };
+        auto store = [&](int j, float v) {
+            const int64_t m = (int64_t)mt * TN + j;
+            if (m >= d.M || col >= d.N || failed) return;
+            if constexpr (OUT == DT_F32) static_cast<float*>(d.out)[m * d.N + col] = v;
+            else if constexpr (OUT == DT_BF16) static_cast<__nv_bfloat16*>(d.out)[m * d.N + col] = __float2bfloat16_rn(v);
+            else static_cast<uint8_t*>(d.out)[m * d.N + col] = fp8_pack1(v);
+        };
+        if (Z == 1) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                acc[j] = finish(j, acc[j]);
+                if constexpr (OUT == DT_E4M3) {
+                    const float w = warp_max(fabsf(acc[j]));
+                    if (lane == 0) mx[(warp & 3) * TN + j] = w;
+                } else {
+                    store(j, acc[j]);
+                }
+            }
+            if constexpr (OUT == DT_E4M3) {
+                ptx::named_bar_sync(1, 128);
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    const float s = fp8_block_scale(fmaxf(fmaxf(mx[j], mx[TN + j]), fmaxf(mx[2 * TN + j], mx[3 * TN + j])));
+                    const int64_t m = (int64_t)mt * TN + j;
+                    if (n == 0 && m < d.M && !failed) d.out_scales[m * nblk + nt] = s;
+                    store(j, acc[j] * fp8_inverse(s));
+                }
+            }
+        } else {
+            // the cluster's sums in rank order, four tokens' values asked for at once
+            uint32_t at[FR_MAXZ];
+#pragma unroll
+            for (int y = 0; y < FR_MAXZ; ++y) at[y] = ptx::mapa_shared(ptx::smem_addr(part + n), y < Z ? y : 0);
+            for (int j4 = j0; j4 < j1; j4 += 4) {
+                float v[4][FR_MAXZ];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int y = 0; y < FR_MAXZ; ++y)
+                        v[e][y] = y < Z && j4 + e < j1 ? fr_ld_cluster(at[y] + (j4 + e) * 512) : 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = j4 + e;
+                    if (j >= j1) break;
+                    float t = 0.f;
+#pragma unroll
+                    for (int y = 0; y < FR_MAXZ; ++y)
+                        if (y < Z) t += v[e][y];
+                    t = finish(j, t);
+                    if constexpr (OUT == DT_E4M3) {
+                        part[j * 128 + n] = t;   // of this CTA's sums of this token, only this thread read [n]
+                        const float w = warp_max(fabsf(t));
+                        if (lane == 0) mx[(warp & 3) * TN + j] = w;
+                    } else {
+                        store(j, t);
+                    }
+                }
+            }
+            if constexpr (OUT == DT_E4M3) {
+                ptx::named_bar_sync(1, 128);
+                for (int j = j0; j < j1; ++j) {
+                    const float s = fp8_block_scale(fmaxf(fmaxf(mx[j], mx[TN + j]), fmaxf(mx[2 * TN + j], mx[3 * TN + j])));
+                    const int64_t m = (int64_t)mt * TN + j;
+                    if (n == 0 && m < d.M && !failed) d.out_scales[m * nblk + nt] = s;
+                    store(j, part[j * 128 + n] * fp8_inverse(s));
+                }
+            }
+        }
+    }
+    if (Z > 1) ptx::cluster_sync();   // no CTA leaves while another reads its sums
+}
+
+template <int TN, int EPI, int OUT>
+cudaError_t launch_rows_inst(const Fp8GemmDesc& d, const DeviceInfo& dev, int Z, cudaStream_t s) {
+    using L = FrLayout<TN>;
+    auto k = gemm_fp8_rows_kernel<TN, EPI, OUT>;
+    static std::atomic<uint64_t> attr{0};
+    const cudaError_t e = set_smem_limit_once(k, L::SMEM, attr);
+    if (e != cudaSuccess) return e;
+    alignas(64) CUtensorMap mw, ma;
+    if (!f8_map(&mw, d.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, d.N, d.K, 128, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
+        !f8_map(&ma, d.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, d.M, d.K, TN, CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+        return cudaErrorInvalidValue;
+    const FpParams p{d, dev.err_word, 0};
+    const int mtiles = (int)((d.M + TN - 1) / TN);
+    const int64_t tiles = mtiles * ((d.N + 127) / 128);
+    if (Z == 1)
+        return launch_dependent(k, dim3((unsigned)tiles), dim3(FR_THREADS), L::SMEM, s, mw, ma, p, 1, mtiles);
+    return launch_dependent_cluster(k, dim3((unsigned)(tiles * Z)), dim3(FR_THREADS), Z, L::SMEM, s, mw, ma, p, Z, mtiles);
+}
+
+template <int TN, int EPI> cudaError_t launch_rows_out(const Fp8GemmDesc& d, const DeviceInfo& dev, int Z, cudaStream_t s) {
+    switch (d.out_dt) {
+        case DT_BF16: return launch_rows_inst<TN, EPI, DT_BF16>(d, dev, Z, s);
+        case DT_F32: return launch_rows_inst<TN, EPI, DT_F32>(d, dev, Z, s);
+        case DT_E4M3: return launch_rows_inst<TN, EPI, DT_E4M3>(d, dev, Z, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+template <int TN> cudaError_t launch_rows(const Fp8GemmDesc& d, const DeviceInfo& dev, cudaStream_t s) {
+    // as many CTAs per tile as SMs allow, each with a block along K at least
+    const int64_t tiles = ((d.M + TN - 1) / TN) * ((d.N + 127) / 128), kblocks = (d.K + kFp8Block - 1) / kFp8Block;
+    int Z = 1;
+    while (Z < FR_MAXZ && tiles * Z * 2 <= dev.num_sms && kblocks >= Z * 2) Z *= 2;
+    switch (d.epi) {
+        case TC_EPI_STORE: return launch_rows_out<TN, TC_EPI_STORE>(d, dev, Z, s);
+        case TC_EPI_GELU: return launch_rows_out<TN, TC_EPI_GELU>(d, dev, Z, s);
+        case TC_EPI_RESID: return launch_rows_out<TN, TC_EPI_RESID>(d, dev, Z, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
 // ------------------------------------------------------------------------ generic kernel
 constexpr int GG_ROWS = 16, GG_COLS = 128, GG_THREADS = 256;
 
@@ -649,6 +980,13 @@ gemm_fp8_generic_kernel(const Fp8GemmDesc d) {
 
 cudaError_t launch_gemm_fp8(const Fp8GemmDesc& d, const DeviceInfo& dev, cudaStream_t s) {
     if (f8_tc_ok(d, dev)) {
+        // Up to 32 rows the rows kernel reads the weight once, with every SM. Beyond, 32 rows at a time,
+        // while its tiles are one wave of CTAs: it then has more CTAs than the pair kernel has pairs
+        // with work. Measured, rows / pair kernel, us (rows x K x N): 8 x 5120 x 5120 10.0 / 19.5;
+        // 100 x 4096 x 1024 7.2 / 15.7; 512 x 1024 x 1024 5.5 / 6.7; and past one wave
+        // 200 x 1024 x 4096 10.4 / 6.7; 1000 x 1280 x 1280 16.9 / 7.8.
+        if (d.M <= 16) return launch_rows<16>(d, dev, s);
+        if (d.M <= 32 || ((d.M + 31) / 32) * ((d.N + 127) / 128) <= dev.num_sms) return launch_rows<32>(d, dev, s);
         // 256-wide tiles halve the operand traffic per product; 128-wide ones when the wide tiles
         // leave CTA pairs without work
         const int64_t wide = ((d.M + FP_TILE_M - 1) / FP_TILE_M) * ((d.N + 255) / 256);
