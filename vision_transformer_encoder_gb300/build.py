@@ -84,7 +84,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
              "-I", os.path.join(include, "torch", "csrc", "api", "include"),
              "-I", os.path.join(os.path.dirname(os.path.dirname(cc)), "include"),
              "-I", sysconfig.get_paths()["include"], BINDING_SRC, "-o", tmp, "-L", os.path.join(torch_dir, "lib"),
-             "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"], "g++ failed on %s" % BINDING_SRC)
+             "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"], "g++ failed on %s" % BINDING_SRC)
         os.replace(tmp, BINDING_PATH)
 
     srcs = _sources()

@@ -9,7 +9,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -88,7 +88,7 @@ void* output(PyObject* given, const char* name, at::ScalarType dt, at::IntArrayR
         *keep = given;
         return p;
     }
-    at::Tensor t = at::empty(shape, like.options().dtype(dt).requires_grad(false));
+    at::Tensor t = at::detail::empty_cuda(shape, dt, like.device(), std::nullopt);
     void* p = t.data_ptr();
     *keep = THPVariable_Wrap(std::move(t));
     if (!*keep) throw python_error();

@@ -590,7 +590,7 @@ constexpr int FR_MAXZ = 8;
 template <int TN> struct FrLayout {
     static constexpr int W_BYTES = 128 * kFp8Block;
     static constexpr int STAGE = W_BYTES + TN * kFp8Block;
-    static constexpr int STAGES = 8;
+    static constexpr int STAGES = 5;   // two CTAs fit an SM
     static constexpr int OFF_SC = STAGES * STAGE;                    // per warp: two sets of TN scales
     static constexpr int OFF_MAX = OFF_SC + 4 * 2 * TN * 4;          // per token: four warps' maxima
     static constexpr int OFF_BAR = OFF_MAX + 4 * TN * 4;
@@ -895,10 +895,14 @@ template <int TN, int EPI> cudaError_t launch_rows_out(const Fp8GemmDesc& d, con
 }
 
 template <int TN> cudaError_t launch_rows(const Fp8GemmDesc& d, const DeviceInfo& dev, cudaStream_t s) {
-    // as many CTAs per tile as SMs allow, each with a block along K at least
+    // One block along K at least for each CTA; a second CTA on an SM only for eight or more (us with
+    // one / two per SM: 8 x 5120 x 5120 10.1 / 7.9, 256 x 4096 x 1024 11.0 / 9.1, but 512 x 1024 x 1024,
+    // four blocks each, 5.5 / 8.3).
     const int64_t tiles = ((d.M + TN - 1) / TN) * ((d.N + 127) / 128), kblocks = (d.K + kFp8Block - 1) / kFp8Block;
     int Z = 1;
-    while (Z < FR_MAXZ && tiles * Z * 2 <= dev.num_sms && kblocks >= Z * 2) Z *= 2;
+    while (Z < FR_MAXZ && tiles * Z * 2 <= 2 * (int64_t)dev.num_sms &&
+           kblocks >= Z * 2 * (tiles * Z * 2 <= dev.num_sms ? 1 : 8))
+        Z *= 2;
     switch (d.epi) {
         case TC_EPI_STORE: return launch_rows_out<TN, TC_EPI_STORE>(d, dev, Z, s);
         case TC_EPI_GELU: return launch_rows_out<TN, TC_EPI_GELU>(d, dev, Z, s);
