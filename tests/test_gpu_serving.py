@@ -352,6 +352,20 @@ def test_cross_attention(shape, dt, ragged):
     check_cross(q, k, v, lens_of(shape[0], shape[2]) if ragged else None)
 
 
+@pytest.mark.parametrize("Tq", [1, 3, 20, 130, 260])
+@pytest.mark.parametrize("dh", [64, 80, 96, 128])
+def test_cross_attention_of_few_queries_over_many_keys(dh, Tq):
+    """Parts of the keys go to different CTAs: lengths that leave some of them, or all but one key, without."""
+    B, Tk, H, Hkv = 3, 2500, 6, 2
+    q, k, v = make_cross(B, Tq, Tk, H, Hkv, dh)
+    for lens in ([2500, 1, 0], [1300, 129, 2177]):
+        check_cross(q, k, v, torch.tensor(lens, dtype=torch.int32, device=DEV))
+    check_cross(q[:1], k[:1], v[:1])
+    got = check_cross(q, k, v)
+    for _ in range(3):
+        assert torch.equal(api.cross_attention(q, k, v), got)
+
+
 @pytest.mark.parametrize("dh", [1, 8, 17, 32, 48, 72, 160, 256, 512])
 @pytest.mark.parametrize("dt", [BF, F32, F64], ids=str)
 def test_cross_attention_other_head_widths(dh, dt):

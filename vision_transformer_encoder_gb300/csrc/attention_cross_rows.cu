@@ -51,12 +51,6 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
     return r;
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
-    return v;
-}
-
 // DHT: the head width rounded up to 64 or 128; columns past dh are zeros.
 template <int DHT, int NR, int NW, int KEYS, int CR_STAGES, int MINB>
 __global__ void __launch_bounds__(NW * 32, MINB)
@@ -332,10 +326,10 @@ cross_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 #pragma unroll
             for (int y = 0; y < CR_MAXZ; ++y) {
                 const uint32_t at = ptx::mapa_shared(own, y < Z ? y : 0);
-                mz[y] = ld_cluster_f32(at + (R * dh + r) * 4);
-                lz[y] = ld_cluster_f32(at + (R * dh + R + r) * 4);
-                oz[y].x = ld_cluster_f32(at + i * 4);
-                oz[y].y = ld_cluster_f32(at + i * 4 + 4);
+                mz[y] = ptx::ld_cluster_f32(at + (R * dh + r) * 4);
+                lz[y] = ptx::ld_cluster_f32(at + (R * dh + R + r) * 4);
+                oz[y].x = ptx::ld_cluster_f32(at + i * 4);
+                oz[y].y = ptx::ld_cluster_f32(at + i * 4 + 4);
                 if (y >= Z) mz[y] = -INFINITY;
             }
             float mx = -INFINITY;
@@ -354,6 +348,7 @@ cross_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             const float inv = 1.f / sum;
             store(r, i - r * dh, len > 0 ? ax * inv : 0.f, len > 0 ? ay * inv : 0.f);
         }
+        __syncwarp();
         ptx::cluster_sync();   // no CTA leaves while another reads its shared memory
     }
 }

@@ -26,6 +26,9 @@
 // then weights of up to 2^8 are carried, exactly as good in bf16 and far inside fp32, and the
 // accumulator in TMEM is not touched. Keys past the sequence's length get weight 0 by position,
 // and the V rows that the last tile holds past it are cleared before they meet those zeros.
+//
+// Few items over many keys (SPLIT): the CTAs of a cluster take a part of an item's key tiles each and
+// join O, the maxima and the sums through distributed shared memory, every CTA a share of the rows.
 // Every wait is bounded; on expiry the kernel records an error bit and unwinds.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -42,6 +45,7 @@ namespace {
 
 constexpr int CT_ROWS = 128, CT_KEYS = 128, CT_SUB = 64, CT_THREADS = 384;
 constexpr int CT_BOX = CT_ROWS * 128;      // 64 columns x 128 rows: 16 KB
+constexpr int CT_MAXZ = 8;
 constexpr float CT_SLACK = 8.f;            // log2 of the weights that are carried before a rescale
 
 template <int DH> struct CtLayout {
@@ -63,6 +67,9 @@ struct CtParams {
     int B, Tq, Tk, Hkv, G, TT;
     int npairs, items;
     int kb, kh, vb, vh, qb;      // 0 where the tensor has one sequence (key head) for all
+    int Z;                       // CTAs per item (SPLIT)
+    int H;
+    __nv_bfloat16* o;            // SPLIT: rows are stored directly
     float scale_log2;
     uint32_t* err;
 };
@@ -85,9 +92,11 @@ __device__ __forceinline__ void ct_error(uint32_t* err, uint32_t bit) {
 struct CtItem {
     int b, h, t0, nact, len;
     int nkt, nst;   // key tiles, half tiles
+    int kt0;        // first key tile (SPLIT)
+    bool any;       // the sequence has keys at all
 };
 
-__device__ __forceinline__ CtItem ct_item(const CtParams& p, int item) {
+template <bool SPLIT> __device__ __forceinline__ CtItem ct_item(const CtParams& p, int item) {
     CtItem x;
     const int pair = item % p.npairs, bh = item / p.npairs;
     x.h = bh % p.Hkv;
@@ -95,12 +104,19 @@ __device__ __forceinline__ CtItem ct_item(const CtParams& p, int item) {
     x.t0 = pair * 2 * p.TT;
     x.nact = x.t0 + p.TT < p.Tq ? 2 : 1;
     x.len = p.kv_lens ? min(max(__ldg(p.kv_lens + x.b), 0), p.Tk) : p.Tk;
+    x.any = x.len > 0;
+    x.kt0 = 0;
+    if (SPLIT) {   // this CTA's part of the tiles
+        const int all = (x.len + CT_KEYS - 1) / CT_KEYS, per = (all + p.Z - 1) / p.Z;
+        x.kt0 = min((int)ptx::cluster_ctarank() * per, all);
+        x.len = min(x.len - x.kt0 * CT_KEYS, per * CT_KEYS);
+    }
     x.nkt = (x.len + CT_KEYS - 1) / CT_KEYS;
     x.nst = (x.len + CT_SUB - 1) / CT_SUB;
     return x;
 }
 
-template <int DH>
+template <int DH, bool SPLIT>
 __global__ void __launch_bounds__(CT_THREADS, 1)
 cross_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, const CtParams p) {
@@ -154,6 +170,8 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_slot, 0);
     griddep_wait();
     griddep_launch_dependents();
+    const int item0 = SPLIT ? blockIdx.x / p.Z : blockIdx.x, step = SPLIT ? p.items : gridDim.x;
+    float m = -INFINITY, l = 0.f;   // softmax warps: this row's maximum and sum
     // TMEM columns: S_g at 128 g, two buffers of 64 with P over each; O_g at 256 + 128 g
 
     if (warp >= 10) {
@@ -166,8 +184,8 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             const CUtensorMap* tm = kq ? &tmK : &tmV;
             uint32_t it = 0, ii = 0;
             bool ok = true;
-            for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x) {
-                const CtItem x = ct_item(p, item);
+            for (int item = item0; item < p.items && ok; item += step) {
+                const CtItem x = ct_item<SPLIT>(p, item);
                 if (x.nkt == 0) continue;
                 if (kq) {
                     const uint32_t qb = ii % QB;
@@ -185,7 +203,7 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     if (!ptx::mbar_wait_bounded<true>(empty + st, ((it / KVS) & 1) ^ 1, abort_flag)) { ok = false; break; }
                     ptx::mbar_arrive_expect_tx(full + st, L::TILE);
                     for (int c = 0; c < NCH; ++c)
-                        ptx::tma_load_4d(ring + st * L::TILE + c * CT_BOX, tm, full + st, c * 64, h, j * CT_KEYS, b);
+                        ptx::tma_load_4d(ring + st * L::TILE + c * CT_BOX, tm, full + st, c * 64, h, (x.kt0 + j) * CT_KEYS, b);
                 }
             }
             if (!ok) {
@@ -235,8 +253,8 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             __syncwarp();
             return true;
         };
-        for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x) {
-            const CtItem x = ct_item(p, item);
+        for (int item = item0; item < p.items && ok; item += step) {
+            const CtItem x = ct_item<SPLIT>(p, item);
             if (x.nkt == 0) continue;
             const uint32_t qb = ii % QB;
             ok = wait(&bars->q_full[qb], (ii / QB) & 1);
@@ -322,13 +340,14 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
             return __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, parity, abort_flag));
         };
-        for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x) {
-            const CtItem x = ct_item(p, item);
+        for (int item = item0; item < p.items && ok; item += step) {
+            const CtItem x = ct_item<SPLIT>(p, item);
             if (g >= x.nact) continue;
             const int t0 = x.t0 + g * p.TT;
             // a warp whose 32 rows hold no query only keeps the barrier protocol
             const bool live = quarter * 32 < min(p.TT, p.Tq - t0) * p.G;
-            float m = -INFINITY, l = 0.f;
+            m = -INFINITY;
+            l = 0.f;
             for (int j = 0; j < x.nst; ++j, ++tt) {
                 if (!(ok = wait(&bars->s_full[g][tt & 1], (tt >> 1) & 1))) break;
                 ptx::tc_fence_after();
@@ -398,6 +417,7 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 if (!(ok = wait(&bars->o_done[g][(tt - 1) & 1], ((tt - 1) >> 1) & 1))) break;
                 ptx::tc_fence_after();
             }
+            if (SPLIT) continue;   // joined below
             const float inv = 1.f / l;
 #pragma unroll 1
             for (int c = 0; c < NCH; ++c, ++sc) {
@@ -456,6 +476,76 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     }
 
     __syncthreads();
+    if constexpr (SPLIT) {
+        // O, m and l of both groups over the K and V rings, which nobody reads any more; rows of
+        // DH + 4 floats keep the 16-byte writes of eight rows in different banks
+        constexpr int LD = DH + 4;
+        float* jO = reinterpret_cast<float*>(sK);
+        float* jm = jO + 2 * CT_ROWS * LD;
+        static_assert((2 * CT_ROWS * LD + 4 * CT_ROWS) * 4 <= L::OFF_BAR - L::OFF_K, "join");
+        const CtItem x = ct_item<true>(p, item0);
+        if (warp >= 2 && warp <= 9) {
+            const int g = (warp - 2) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+            float* row = jO + (g * CT_ROWS + r) * LD;
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < DH / 16; ++c) {
+                uint32_t ov[16];
+                ptx::tmem_ld_32x32b_x16(tmem + 256 + g * 128 + ((uint32_t)(quarter * 32) << 16) + c * 16, ov);
+                ptx::tmem_ld_wait_for(ov);
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {   // a part without keys adds nothing
+                    const uint4 v = x.nkt > 0 ? make_uint4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]) : make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(row + c * 16 + e) = v;
+                }
+            }
+            jm[g * CT_ROWS + r] = m;
+            jm[2 * CT_ROWS + g * CT_ROWS + r] = l;
+            ptx::tc_fence_before();
+        }
+        ptx::cluster_sync();   // every part is in place
+        const uint32_t own = ptx::smem_addr(jO), own_m = ptx::smem_addr(jm);
+        const int rows = x.nact * CT_ROWS, share = (rows + p.Z - 1) / p.Z, z = (int)ptx::cluster_ctarank();
+        const bool clean = *abort_flag == 0;
+        for (int i = threadIdx.x; i < share * (DH / 4); i += CT_THREADS) {
+            const int gr = z * share + i / (DH / 4), c = (i % (DH / 4)) * 4;   // group * 128 + row, column
+            const int r = gr % CT_ROWS, t = x.t0 + (gr / CT_ROWS) * p.TT + r / p.G;
+            if (gr >= rows || r >= p.TT * p.G || t >= p.Tq) continue;
+            float mz[CT_MAXZ], lz[CT_MAXZ];
+            float4 oz[CT_MAXZ];
+#pragma unroll
+            for (int y = 0; y < CT_MAXZ; ++y) {
+                if (y >= p.Z) break;
+                mz[y] = ptx::ld_cluster_f32(ptx::mapa_shared(own_m + gr * 4, y));
+                lz[y] = ptx::ld_cluster_f32(ptx::mapa_shared(own_m + (2 * CT_ROWS + gr) * 4, y));
+                oz[y] = ptx::ld_cluster_f32x4(ptx::mapa_shared(own + (gr * LD + c) * 4, y));
+            }
+            float mx = -INFINITY;
+#pragma unroll
+            for (int y = 0; y < CT_MAXZ; ++y)
+                if (y < p.Z) mx = fmaxf(mx, mz[y]);
+            const float base = mx == -INFINITY ? 0.f : mx;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            float sum = 0.f;
+#pragma unroll
+            for (int y = 0; y < CT_MAXZ; ++y) {
+                if (y >= p.Z) break;
+                const float f = exp2_approx(mz[y] - base);
+                acc.x = fmaf(f, oz[y].x, acc.x);
+                acc.y = fmaf(f, oz[y].y, acc.y);
+                acc.z = fmaf(f, oz[y].z, acc.z);
+                acc.w = fmaf(f, oz[y].w, acc.w);
+                sum = fmaf(f, lz[y], sum);
+            }
+            const float inv = 1.f / sum;
+            if (clean)
+                *reinterpret_cast<uint2*>(p.o + (((int64_t)x.b * p.Tq + t) * p.H + x.h * p.G + r % p.G) * DH + c) =
+                    x.any ? make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv))
+                          : make_uint2(0u, 0u);
+        }
+        __syncwarp();
+        ptx::cluster_sync();   // no CTA leaves while another reads its shared memory
+    }
     if (warp == 1) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, 512);
@@ -490,11 +580,26 @@ cudaError_t launch_ct(const CrossDesc& d, const DeviceInfo& dev, cudaStream_t s)
     p.vh = d.vs[2] != 0;
     p.scale_log2 = (float)(d.scale * 1.4426950408889634);
     p.err = dev.err_word;
+    p.H = (int)d.H;
+    p.o = static_cast<__nv_bfloat16*>(d.o);
+    // Items that fill at most half the SMs are split along the keys, each part four tiles at least. CTAs
+    // fill an SM each, and clusters of eight of them do not pack into the GPU's SM groups.
+    const int64_t nkt = (d.Tk + CT_KEYS - 1) / CT_KEYS;
+    int Z = 1;
+    while (Z < CT_MAXZ && (int64_t)p.items * Z * 2 <= (Z < 4 ? dev.num_sms : dev.num_sms / 2) && nkt >= Z * 2 * 4) Z *= 2;
+    p.Z = Z;
+    if (Z > 1) {
+        static std::atomic<uint64_t> attr{0};
+        const cudaError_t e = set_smem_limit_once(cross_tc_kernel<DH, true>, L::SMEM, attr);
+        if (e != cudaSuccess) return e;
+        return launch_dependent_cluster(cross_tc_kernel<DH, true>, dim3(p.items * Z), dim3(CT_THREADS), Z, L::SMEM, s, mq, mk,
+                                        mv, mo, p);
+    }
     static std::atomic<uint64_t> attr{0};
-    const cudaError_t e = set_smem_limit_once(cross_tc_kernel<DH>, L::SMEM, attr);
+    const cudaError_t e = set_smem_limit_once(cross_tc_kernel<DH, false>, L::SMEM, attr);
     if (e != cudaSuccess) return e;
     const int grid = p.items < dev.num_sms ? p.items : dev.num_sms;
-    return launch_dependent(cross_tc_kernel<DH>, dim3(grid), dim3(CT_THREADS), L::SMEM, s, mq, mk, mv, mo, p);
+    return launch_dependent(cross_tc_kernel<DH, false>, dim3(grid), dim3(CT_THREADS), L::SMEM, s, mq, mk, mv, mo, p);
 }
 
 }  // namespace

@@ -599,12 +599,6 @@ template <int TN> struct FrLayout {
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
-__device__ __forceinline__ float fr_ld_cluster(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
-    return v;
-}
-
 template <int TN, int EPI, int OUT>
 __global__ void __launch_bounds__(FR_THREADS, 1)
 gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
@@ -833,7 +827,7 @@ gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
                 for (int e = 0; e < 4; ++e)
 #pragma unroll
                     for (int y = 0; y < FR_MAXZ; ++y)
-                        v[e][y] = y < Z && j4 + e < j1 ? fr_ld_cluster(at[y] + (j4 + e) * 512) : 0.f;
+                        v[e][y] = y < Z && j4 + e < j1 ? ptx::ld_cluster_f32(at[y] + (j4 + e) * 512) : 0.f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int j = j4 + e;
@@ -863,6 +857,7 @@ gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
             }
         }
     }
+    __syncwarp();
     if (Z > 1) ptx::cluster_sync();   // no CTA leaves while another reads its sums
 }
 
