@@ -301,6 +301,23 @@ def cross_ref(q, k, v, lens, scale):
     live = torch.arange(Tk, device=q.device)[None] < (lens[:, None] if lens is not None else Tk)
     kd, vd = (torch.where(live[:, None, :, None], t, 0.0) for t in (kd, vd))
     x = torch.where(live[:, None, None], scale * (qd @ kd.transpose(2, 3)), -math.inf)
+@pytest.mark.parametrize("ot", [BF, F32, F8], ids=str)
+@pytest.mark.parametrize("M,K", [(4, 256), (40, 256), (600, 256), (4, 255)])   # rows, pairs, generic
+def test_linear_fp8_gelu_of_large_values(M, K, ot):
+    """GELU of -1e25 is zero and of 1e25 is itself, beside rows of ordinary size."""
+    a, sa, w, sw = make_product(M, K, 256)
+    sa = sa.clone()
+    sa[1::2] *= 1e25
+    z = linear_ref(a, sa, w, sw)[0]
+    got = api.linear_fp8(a, sa, w, sw, epilogue=api.EPI_GELU, out_dtype=ot)
+    v = got[0].double() * spread(got[1], 256) if ot == F8 else got.double()
+    below, above = z < -1e23, z > 1e23
+    assert below.any() and above.any() and (v[below] == 0).all()
+    # e4m3: half a step of the block's scale, at most 448 of which are the largest value
+    tol = (2.0 ** -4 if ot == F8 else 2.0 ** -7) * z[above].abs() + (2.0 ** -17 * z.abs().max() if ot == F8 else 0)
+    close(v[above], z[above], tol)
+
+
     p = torch.where(live[:, None, None].any(3, keepdim=True), torch.softmax(x, 3), 0.0)
     mag = abs(scale) * (qd.abs() @ kd.abs().transpose(2, 3)).amax(3, keepdim=True)
     return [t.permute(0, 2, 1, 3) for t in (p @ vd, p @ vd.abs(), mag)]
