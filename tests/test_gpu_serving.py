@@ -151,6 +151,16 @@ def test_rmsnorm_special_rows():
     close(out[3:], ref[3:], 2.0 ** -7 * ref[3:].abs())
 
 
+@pytest.mark.parametrize("rows,D", [(3, 8), (1500, 264), (2, 5)])   # registers, many rows, generic
+def test_rmsnorm_large_rows_and_eps(rows, D):
+    """Squares past the fp32 range beside an eps of their size: mean square 1e38, eps 1e38."""
+    x = torch.full((rows, D), 1e19, device=DEV)
+    x[:, ::2] *= -1
+    for eps in (1e38, 1e-6):
+        y = norm_ref(x, None, None, eps)[1]
+        close(api.rmsnorm(x, eps), y, 2.0 ** -19 * y.abs())
+
+
 def test_rmsnorm_leading_dimensions_and_no_gain():
     x = rand(2, 3, 5, 64, seed=5, dtype=BF)
     out = api.rmsnorm(x, 1e-5)

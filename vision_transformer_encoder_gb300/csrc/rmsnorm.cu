@@ -90,7 +90,7 @@ rmsnorm_generic_kernel(const TX* x, const TR* residual, int64_t rows, int64_t D,
                 ss += v * v;
             }
             ss = block_sum(ss, part);
-            eps_row = 0;   // far below half a unit of the scaled mean square
+            eps_row = eps * pre * pre;
         }
         A r;
         if constexpr (std::is_same<A, double>::value) r = 1.0 / sqrt(ss / (A)D + eps_row);
@@ -216,7 +216,7 @@ rmsnorm_fast_kernel(const TX* x, const TR* residual, int64_t rows, int D, float 
                 s2 = fmaf(v[i][j], v[i][j], s2);
             }
         ss = total(s2, 1);
-        e = 0.f;   // far below half a unit of the scaled mean square
+        e = eps * kPreScale * kPreScale;
     }
     const float r = 1.f / sqrtf(ss / (float)D + e);
 #pragma unroll
@@ -361,7 +361,7 @@ rmsnorm_rows_kernel(const TX* x, const TR* residual, int64_t rows, int D, float 
                 }
             f2_unpack(s2, a, b);
             ss = total(a + b);
-            e = 0.f;   // far below half a unit of the scaled mean square
+            e = eps * kPreScale * kPreScale;
         }
         const float r = 1.f / sqrtf(ss * inv_d + e);
         const unsigned long long r2 = f2_pack(r, r);
