@@ -154,7 +154,7 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
 // G warps per row, NV steps of 8 columns per thread; blockDim.x = 32 G times the rows of a CTA
 // (one row when G > 1).
 template <typename TX, typename TR, typename TO, int NV>
-__global__ void __launch_bounds__(512, NV <= 5 ? 2 : 1)   // 64 registers up to 1280 columns per warp: 32 warps per SM
+__global__ void __launch_bounds__(512, 2)   // 64 registers: 32 warps per SM
 rmsnorm_fast_kernel(const TX* x, const TR* residual, int64_t rows, int D, float eps, const void* __restrict__ gamma,
                     int gamma_dt, TR* sum, TO* out, float* __restrict__ scales, int G) {
     constexpr bool Q = std::is_same<TO, uint8_t>::value;
@@ -426,9 +426,10 @@ cudaError_t rows_nv(const RmsNormDesc& d, const DeviceInfo& dev, int nv, int G, 
     // steps whose two rows (one as stored, one in fp32) fit in registers
     constexpr int MAXNV = 20 / (sizeof(TX) + (RES ? sizeof(TR) : 0)) < 5 ? 20 / (sizeof(TX) + (RES ? sizeof(TR) : 0)) : 5;
     constexpr int N3 = MAXNV < 3 ? MAXNV : 3, N4 = MAXNV < 4 ? MAXNV : 4;
+    // a row that more warps than one share fills more than half of the steps of each
+    constexpr int W2 = MAXNV == 5 ? 3 : 2;
     if (G > 1) switch (nv) {
-        case 1: return rows_inst<TX, TR, TO, 1, RES, true>(d, dev, 32 * G, s);
-        case 2: return rows_inst<TX, TR, TO, 2, RES, true>(d, dev, 32 * G, s);
+        case 2: return rows_inst<TX, TR, TO, W2, RES, true>(d, dev, 32 * G, s);
         case 3: return rows_inst<TX, TR, TO, N3, RES, true>(d, dev, 32 * G, s);
         case 4: return rows_inst<TX, TR, TO, N4, RES, true>(d, dev, 32 * G, s);
         case 5: return rows_inst<TX, TR, TO, MAXNV, RES, true>(d, dev, 32 * G, s);
@@ -462,7 +463,10 @@ cudaError_t fast(const RmsNormDesc& d, const DeviceInfo& dev, cudaStream_t s) {
     while (G < 16 && steps > most * G) G *= 2;
     if (steps <= most * G && d.rows * G >= 32 * (int64_t)dev.num_sms) {
         const int nv = (steps + G - 1) / G;
-        return d.residual ? rows_nv<TX, TR, TO, true>(d, dev, nv, G, s) : rows_nv<TX, TR, TO, false>(d, dev, nv, G, s);
+        // (without a residual its type is x's)
+        if constexpr (std::is_same<TX, TR>::value)
+            if (!d.residual) return rows_nv<TX, TR, TO, false>(d, dev, nv, G, s);
+        return rows_nv<TX, TR, TO, true>(d, dev, nv, G, s);
     }
     // fewer: as many warps as leave every thread one step, up to 16
     G = 1;
@@ -473,10 +477,6 @@ cudaError_t fast(const RmsNormDesc& d, const DeviceInfo& dev, cudaStream_t s) {
         case 2: return fast_inst<TX, TR, TO, 2>(d, G, s);
         case 3: return fast_inst<TX, TR, TO, 3>(d, G, s);
         case 4: return fast_inst<TX, TR, TO, 4>(d, G, s);
-        case 5: return fast_inst<TX, TR, TO, 5>(d, G, s);
-        case 6: return fast_inst<TX, TR, TO, 6>(d, G, s);
-        case 7: return fast_inst<TX, TR, TO, 7>(d, G, s);
-        case 8: return fast_inst<TX, TR, TO, 8>(d, G, s);
     }
     return cudaErrorInvalidValue;
 }
