@@ -475,10 +475,10 @@ int vit_linear_fp8(const void* a, const float* a_scales, const void* w, const fl
  *   kv_lens   (B) device array, nullable (then Tk): sequence b sees its first kv_lens[b] keys,
  *             clamped to [0, Tk]. With none its outputs are zero. Keys past the length may hold
  *             anything, NaN included.
- *   scale     any finite number; 1 / sqrt(dh) is usual
+ *   scale     any finite number, of magnitude up to 1e30 unless F64; 1 / sqrt(dh) is usual
  * Softmax in fp32 (fp64 for F64); F32 products as three TF32 products per step for dh <= 128
- * (an infinite value then gives NaN). dh up to 512.
- * Errors: VIT_ERR_ARG, VIT_ERR_DTYPE, VIT_ERR_UNSUPPORTED (dh), VIT_ERR_NOMEM, VIT_ERR_CUDA.
+ * (an infinite value, or one above 3.4e38, then gives NaN). dh up to 512.
+ * Errors: VIT_ERR_ARG, VIT_ERR_DTYPE, VIT_ERR_UNSUPPORTED (dh), VIT_ERR_CUDA.
  */
 int vit_cross_attention(const void* q, const int64_t* q_strides, const void* k,
                         const int64_t* k_strides, const void* v, const int64_t* v_strides,

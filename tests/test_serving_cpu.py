@@ -97,6 +97,12 @@ def test_cross_attention_refuses(lib, kw, code):
     assert cross(lib, **kw) == code
 
 
+@pytest.mark.parametrize("d", [BF16, F32])
+@pytest.mark.parametrize("scale", [1e300, -1e39, 3e38])
+def test_cross_attention_refuses_scales_past_fp32(lib, d, scale):
+    assert cross(lib, scale=scale, d=d) == ARG
+
+
 def test_without_a_device_the_stages_report_a_cuda_error(lib):
     if torch.cuda.is_available():
         pytest.skip("a CUDA device is present")

@@ -423,10 +423,9 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             for (int c = 0; c < NCH; ++c, ++sc) {
                 // the previous store has read the staging box
                 if (sc > 0 && !(ok = wait(&bars->ost_free[g], (sc - 1) & 1))) break;
-                constexpr int W = DH < 64 ? DH : 64;
                 if (live) {
 #pragma unroll
-                    for (int u = 0; u < W / 16; ++u) {
+                    for (int u = 0; u < 4; ++u) {
                         uint32_t ov[16];
                         if (x.nkt > 0 && c * 64 + u * 16 < DH) {
                             ptx::tmem_ld_32x32b_x16(tO + c * 64 + u * 16, ov);
@@ -608,8 +607,9 @@ bool cross_tc_supported(const CrossDesc& d) {
     if (d.dt != DT_BF16 || (d.dh != 64 && d.dh != 80 && d.dh != 96 && d.dh != 128)) return false;
     const int64_t G = d.H / d.Hkv, lim = 0x7fffffff;
     // positive scales only: the row maximum is taken before scaling
-    if (!((float)(d.scale * 1.4426950408889634) > 0.f) || !(d.scale < 1e30) || G > CT_ROWS) return false;
-    if (d.Tq > lim - 1024 || d.Tk > lim - 1024 || d.H > lim || d.B > lim) return false;
+    if (!((float)(d.scale * 1.4426950408889634) > 0.f) || G > CT_ROWS) return false;
+    // the query producer may wait for a whole item: 2^26 keys take half of the wait's limit
+    if (d.Tq > lim - 1024 || d.Tk > (1 << 26) || d.H > lim || d.B > lim) return false;
     if (d.B > lim / (d.Hkv * ((d.Tq * G + 1) / 2 + 1))) return false;   // items, at two rows each
     if (d.H > 1 && d.qs[2] == 0) return false;
     const int64_t os[3] = {d.Tq * d.H * d.dh, d.H * d.dh, d.dh};

@@ -22,6 +22,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
@@ -1844,6 +1845,7 @@ int vit_cross_attention(const void* q, const int64_t* q_strides, const void* k, 
         return VIT_ERR_ARG;
     if (!(scale - scale == 0.0)) return VIT_ERR_ARG;   // not finite
     if (dtype != DT_F32 && dtype != DT_BF16 && dtype != DT_F64) return VIT_ERR_DTYPE;
+    if (dtype != DT_F64 && std::fabs(scale) > 1e30) return VIT_ERR_ARG;   // fp32 holds it, and its products
     if (dh > kCrossMaxHead) return VIT_ERR_UNSUPPORTED;
     if (H > kMaxElements / dh || Tq > kMaxElements / (H * dh) || B > kMaxElements / (Tq * H * dh)) return VIT_ERR_ARG;
     if (Tk > kMaxElements / (Hkv * dh) || B > kMaxElements / (Tk * Hkv * dh)) return VIT_ERR_ARG;
