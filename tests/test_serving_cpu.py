@@ -124,3 +124,10 @@ def test_the_binding_refuses_host_tensors():
         api.linear_fp8(q, s, q, s)
     with pytest.raises(ValueError):
         api.cross_attention(x.view(1, 4, 4, 64), x.view(1, 4, 4, 64), x.view(1, 4, 4, 64))
+
+
+@pytest.mark.parametrize("epilogue", [1 << 32, (1 << 32) + 1, -(1 << 32)])
+def test_the_binding_refuses_epilogues_past_32_bits(epilogue):
+    q = torch.empty(4, 256, dtype=torch.float8_e4m3fn, device="meta")
+    with pytest.raises(ValueError, match="epilogue"):
+        api.linear_fp8(q, q, q, q, epilogue=epilogue)

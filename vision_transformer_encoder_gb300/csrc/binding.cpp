@@ -230,6 +230,8 @@ PyObject* quantize_weight(PyObject* const* a) {
 // ---- (a, a_scales, w, w_scales, bias, residual, epilogue, out_dtype, out, out_scales)
 PyObject* linear_fp8(PyObject* const* a) {
     const at::Tensor &x = tensor(a[0], "a"), &w = tensor(a[2], "w");
+    const int64_t epi = integer(a[6]);
+    if (epi < VIT_EPI_STORE || epi > VIT_EPI_RESIDUAL) refuse("epilogue", " must be EPI_STORE, EPI_GELU or EPI_RESIDUAL");
     int64_t M, K;
     matrix_of(x, "a", &M, &K);
     if (w.dim() != 2 || w.numel() == 0) refuse("w", " must be a matrix (N, K) with at least one element");
@@ -255,7 +257,6 @@ PyObject* linear_fp8(PyObject* const* a) {
         rc = code_of(r.scalar_type(), false, "residual");
         rp = fits(r, "residual", r.scalar_type(), shape, dev);
     }
-    const int64_t epi = integer(a[6]);
     const at::ScalarType od = dtype_arg(a[7], a[8], at::kBFloat16);
     const int oc = code_of(od, true, "out");
     const bool e4m3 = oc == VIT_E4M3;
