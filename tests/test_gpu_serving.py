@@ -301,16 +301,6 @@ def test_linear_fp8_special_values(M):
     assert (zero[0].float() == 0).all() and (zero[1] == TINY).all()
 
 
-# -------------------------------------------------------------------------- cross attention
-def cross_ref(q, k, v, lens, scale):
-    """o, the sum of weights times |v|, and the largest sum of magnitudes in a row's scores."""
-    B, Tq, H, dh = q.shape
-    Tk, G = k.shape[1], H // k.shape[2]
-    qd = q.double().permute(0, 2, 1, 3)
-    kd, vd = (t.double().repeat_interleave(G, 2).permute(0, 2, 1, 3) for t in (k, v))
-    live = torch.arange(Tk, device=q.device)[None] < (lens[:, None] if lens is not None else Tk)
-    kd, vd = (torch.where(live[:, None, :, None], t, 0.0) for t in (kd, vd))
-    x = torch.where(live[:, None, None], scale * (qd @ kd.transpose(2, 3)), -math.inf)
 @pytest.mark.parametrize("ot", [BF, F32, F8], ids=str)
 @pytest.mark.parametrize("M,K", [(4, 256), (40, 256), (600, 256), (4, 255)])   # rows, pairs, generic
 def test_linear_fp8_gelu_of_large_values(M, K, ot):
@@ -328,6 +318,16 @@ def test_linear_fp8_gelu_of_large_values(M, K, ot):
     close(v[above], z[above], tol)
 
 
+# -------------------------------------------------------------------------- cross attention
+def cross_ref(q, k, v, lens, scale):
+    """o, the sum of weights times |v|, and the largest sum of magnitudes in a row's scores."""
+    B, Tq, H, dh = q.shape
+    Tk, G = k.shape[1], H // k.shape[2]
+    qd = q.double().permute(0, 2, 1, 3)
+    kd, vd = (t.double().repeat_interleave(G, 2).permute(0, 2, 1, 3) for t in (k, v))
+    live = torch.arange(Tk, device=q.device)[None] < (lens[:, None] if lens is not None else Tk)
+    kd, vd = (torch.where(live[:, None, :, None], t, 0.0) for t in (kd, vd))
+    x = torch.where(live[:, None, None], scale * (qd @ kd.transpose(2, 3)), -math.inf)
     p = torch.where(live[:, None, None].any(3, keepdim=True), torch.softmax(x, 3), 0.0)
     mag = abs(scale) * (qd.abs() @ kd.abs().transpose(2, 3)).amax(3, keepdim=True)
     return [t.permute(0, 2, 1, 3) for t in (p @ vd, p @ vd.abs(), mag)]
