@@ -464,6 +464,104 @@ def test_cross_attention_special_scores(Tq, dt):
     assert torch.equal(got[1], keep[1]) and torch.equal(got[0, :, 0], keep[0, :, 0])
 
 
+# ----------------------------------------------------------------------- limits of outputs, offsets
+def inside(shape, dt, lead, fn):
+    """fn(out) with out a contiguous tensor between two margins (the first of `lead` bytes); nothing outside it changes."""
+    n = math.prod(shape) * torch.empty(0, dtype=dt).element_size()
+    buf = torch.full((lead + n + 4096,), 0x5A, dtype=torch.uint8, device=DEV)
+    fn(buf[lead:lead + n].view(dt).view(shape))
+    assert (buf[:lead] == 0x5A).all() and (buf[lead + n:] == 0x5A).all()
+
+
+@pytest.mark.parametrize("lead", [4096, 4104])
+def test_nothing_outside_the_outputs_is_written(lead):
+    for rows, D in ((3, 264), (5, 129), (1501, 1032)):
+        x = rand(rows, D, dtype=BF)
+        blocks = (rows, (D + 127) // 128)
+        inside((rows, D), BF, lead, lambda t: api.rmsnorm(x, 1e-6, out=t))
+        inside((rows, D), F8, lead, lambda t: api.rmsnorm(x, 1e-6, out=t))
+        inside(blocks, F32, lead, lambda t: api.rmsnorm(x, 1e-6, out_dtype=F8, scales=t))
+        inside((rows, D), F32, lead, lambda t: api.rmsnorm(x, 1e-6, residual=x.float(), sum_out=t))
+        inside((rows, D), F8, lead, lambda t: api.quantize(x, out=t))
+        inside(blocks, F32, lead, lambda t: api.quantize(x, scales=t))
+        inside((D, rows), F8, lead, lambda t: api.quantize_weight(x, out=t))
+    for M in (3, 29, 45, 333):
+        for N in (136, 400, 1032, 5):
+            ops = make_product(M, 272, N)
+            for dt in (BF, F32, F8):
+                inside((M, N), dt, lead, lambda t: api.linear_fp8(*ops, out=t))
+            inside((M, (N + 127) // 128), F32, lead, lambda t: api.linear_fp8(*ops, out_dtype=F8, out_scales=t))
+    for dt in (BF, F32):
+        for Tq, H, Hkv, dh in ((1, 4, 2, 64), (3, 6, 2, 80), (131, 6, 2, 64), (150, 2, 2, 96), (37, 5, 1, 128), (7, 3, 3, 40)):
+            q, k, v = make_cross(2, Tq, 333, H, Hkv, dh, dt=dt)
+            inside(tuple(q.shape), dt, lead, lambda t: api.cross_attention(q, k, v, out=t))
+
+
+def big(*shape, dtype=BF):
+    return torch.empty(shape, dtype=dtype, device=DEV).normal_(generator=torch.Generator(DEV).manual_seed(sum(shape)))
+
+
+def test_rows_past_32_bit_offsets():
+    """More than 2^32 elements: the last rows and blocks come out as they do alone."""
+    x = big((1 << 21) + 3, 2056)
+    q, s = api.quantize(x)
+    qe, se = api.quantize(x[-3:])
+    assert torch.equal(q[-3:].view(torch.uint8), qe.view(torch.uint8)) and torch.equal(s[-3:], se)
+    q, s = api.rmsnorm(x, 1e-6, out=q, scales=s)
+    for part in (slice(0, 3), slice(-3, None)):
+        y = norm_ref(x[part], None, None, 1e-6)[1]
+        close8(q[part], s[part], y, (math.ceil(2056 / 256) + 26) * U * y.abs())
+    del x, q, s
+    w = big(65544, 65544)
+    q, s = api.quantize_weight(w)
+    qe, se = api.quantize_weight(w[65408:, 65408:].contiguous())
+    assert torch.equal(q[65408:, 65408:].contiguous().view(torch.uint8), qe.view(torch.uint8))
+    assert torch.equal(s[511:, 511:], se)
+
+
+@pytest.mark.parametrize("ot", [BF, F8], ids=str)
+def test_product_past_32_bit_offsets(ot):
+    a, sa, w, sw = make_product((1 << 17) + 5, 128, 32784)
+    got = api.linear_fp8(a, sa, w, sw, out_dtype=ot)
+    ref = api.linear_fp8(a[-261:], sa[-261:], w, sw, out_dtype=ot)   # the last whole tile and what is behind it
+    for g, r in zip(got, ref) if ot == F8 else ((got, ref),):
+        assert torch.equal(g[-261:].view(torch.uint8), r.view(torch.uint8))
+    del got, ref
+    # a weight of more than 2^32 elements under few rows
+    n0, N, K = 1 << 20, (1 << 20) + 72, 4096
+    a, sa = api.quantize(rand(3, K))
+    w = torch.zeros(N, K, dtype=torch.uint8, device=DEV)
+    w[n0:] = api.quantize(rand(72, K, seed=1))[0].view(torch.uint8)
+    w, sw = w.view(F8), torch.rand(N // 128 + 1, K // 128, device=DEV) * 1e-3
+    got = api.linear_fp8(a, sa, w, sw, out_dtype=F32)
+    z, mag = linear_ref(a, sa, w[n0:].contiguous(), sw[n0 // 128:])
+    close(got[:, n0:], z, 2 * U * (128 + 32 + 8) * mag)
+    assert (got[:, :n0] == 0).all()
+
+
+@pytest.mark.parametrize("dt,Tq,dh", [(BF, 1, 64), (BF, 150, 128), (F32, 1, 64), (F32, 40, 64), (BF, 20, 72), (F64, 2, 64)], ids=str)
+def test_cross_attention_past_32_bit_offsets(dt, Tq, dh):
+    """A cache whose sequences, or tokens, lie more than 2^32 elements apart."""
+    q, k, v = make_cross(2, Tq, 300, 4, 2, dh, dt=dt)
+    lens = torch.tensor([300, 211], dtype=torch.int32, device=DEV)
+    for b, t in (((1 << 32) + 64, 2 * dh), (2 * dh, 1 << 24)):
+        buf = torch.empty(b + 299 * t + 2 * dh, dtype=dt, device=DEV)
+        far = buf.as_strided((2, 300, 2, dh), (b, t, dh, 1))
+        far.copy_(k)
+        assert torch.equal(api.cross_attention(q, far, v, kv_lens=lens), api.cross_attention(q, k, v, kv_lens=lens))
+        far.copy_(v)
+        assert torch.equal(api.cross_attention(q, k, far, kv_lens=lens), api.cross_attention(q, k, v, kv_lens=lens))
+        del buf, far
+
+
+@pytest.mark.parametrize("dt,Tq", [(BF, 1 << 21), (F32, 1 << 20)], ids=str)
+def test_cross_attention_outputs_past_32_bit_offsets(dt, Tq):
+    q = big(1, Tq + 8, 16, 128, dtype=dt)
+    _, k, v = make_cross(1, 1, 40, 16, 1, 128, dt=dt)
+    got = api.cross_attention(q, k, v)
+    assert torch.equal(got[:, -520:], api.cross_attention(q[:, -520:], k, v))
+
+
 # ------------------------------------------------------------------------------- together
 def decoder_layer(p, x, states_kv, lens, H, out=None):
     """One reading layer of a text decoder: x + cross attention over the encoder's states, then the
