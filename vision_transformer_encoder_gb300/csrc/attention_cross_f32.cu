@@ -4,8 +4,8 @@
 // Products are 3xTF32 (hi hi + hi lo + lo hi, hi rounded to the 11 bits that the tensor cores read,
 // lo the rest) on mma.m16n8k8, and sums longer than 16 keys are fp32 additions: the outputs of 8 x 197
 // queries over 288 to 577 keys are off by 3.6e-7 in the 2-norm, and by 3.3e-6 when O is summed on the
-// tensor cores, which cut sums off instead of rounding them. Bound by the tensor pipe (44 %
-// active); 55 us at 12 heads of 64 (35 TFLOP/s). A CUDA-core kernel took 103 us: one warp per
+// tensor cores, which cut sums off instead of rounding them. Bound by the tensor pipe (50 %
+// active); 53 us at 12 heads of 64 (36 TFLOP/s). A CUDA-core kernel took 103 us: one warp per
 // scheduler issues a product every other cycle.
 //
 // A CTA of four warps walks the keys of one (sequence, key head) 64 at a time, K and V tiles by TMA in
@@ -14,7 +14,8 @@
 //   64 rows per CTA, sixteen to each warp; warps without rows skip the work;
 //   a CTA with at most sixteen rows (decoding, or the last of a head) is split along the keys: the
 //   same rows in every warp, which takes 16 of the 64 keys, joined at the end through shared
-//   memory. The last five of 197 rows took three quarters of a full CTA's time before.
+//   memory. The last five of 197 rows took three quarters of a full CTA's time before. The last tiles
+//   of all heads come last in the grid, where they fill the end of it: 32 x 197 queries 177 -> 166 us.
 // Operands are read 16 bytes at a time from the 128-byte swizzled tiles without bank conflicts:
 // the order of the columns in a dot product is free, so thread c takes four consecutive columns
 // of its key for two k-steps; so is which column a row of V^T means; and P^T comes out of S^T by
@@ -72,7 +73,7 @@ __device__ __forceinline__ void transpose_8x8_f32(float& x, float& y) {
 template <int DHT, int NR>
 __global__ void __launch_bounds__(CF_WARPS * 32, DHT <= 64 ? 2 : 1)
 cross_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                 const __grid_constant__ CrossDesc d, float scale_log2, int qtiles, uint32_t* err) {
+                 const __grid_constant__ CrossDesc d, float scale_log2, uint32_t* err) {
     using L = CfLayout<DHT>;
     constexpr int NB = L::NB, STAGES = L::STAGES;
     extern __shared__ uint8_t smem_raw[];
@@ -81,7 +82,8 @@ cross_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     volatile int* abort_flag = &abort_word;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c4 = lane & 3, r8 = lane >> 2;
-    const int G = (int)(d.H / d.Hkv), dh = (int)d.dh, qt = blockIdx.x % qtiles, bh = blockIdx.x / qtiles;
+    const int G = (int)(d.H / d.Hkv), dh = (int)d.dh, heads = (int)(d.B * d.Hkv);
+    const int qt = blockIdx.x / heads, bh = blockIdx.x - qt * heads;
     const int b = bh / (int)d.Hkv, h = bh % (int)d.Hkv;
     const int64_t rows = d.Tq * G, tile0 = (int64_t)qt * CF_ROWS;
     const bool split = rows - tile0 <= NR * 8;
@@ -352,7 +354,7 @@ template <int DHT, int NR> cudaError_t launch_cf_inst(const CrossDesc& d, const 
         return cudaErrorInvalidValue;
     const int64_t qtiles = (d.Tq * (d.H / d.Hkv) + CF_ROWS - 1) / CF_ROWS;
     return launch_dependent(k, dim3((unsigned)(d.B * d.Hkv * qtiles)), dim3(CF_WARPS * 32), L::SMEM, s, mk, mv, d,
-                            (float)(d.scale * 1.4426950408889634), (int)qtiles, dev.err_word);
+                            (float)(d.scale * 1.4426950408889634), dev.err_word);
 }
 
 template <int DHT> cudaError_t launch_cf(const CrossDesc& d, const DeviceInfo& dev, cudaStream_t s) {
