@@ -9,8 +9,12 @@
 // tcgen05.mma.cta_group::2 kind::f8f6f4. One ring stage is one block of 128 along K, both operands
 // K-major with the 128-byte swizzle. A block's scales differ from row to row, so its sum cannot
 // stay in one accumulator with the others': each block gets an accumulator of its own in TMEM
-// (two, in turn), and the epilogue warps add scale * block sum to fp32 registers while the tensor
-// cores make the next block.
+// (512 / BN, in turn), and the epilogue warps add scale * block sum to fp32 registers while the
+// tensor cores make the next ones. With four in turn instead of two 577 x 5120 -> 5120 (BN 128) takes
+// 34.1 us instead of 34.7. At BN 256 that addition is what bounds it, some 1160 cycles per block of which the products
+// need 512 (36928 x 4096 -> 4096: 563 us, 2.20 PFLOP/s, near the power limit). Measured and slower: loads of 64
+// columns, 642 us; sixteen epilogue warps of 64 columns each with loads of 16, 780 us; products of 128 columns with
+// accumulators handed over by halves, 573 us.
 //   warp 0       MMA issue (the leader CTA's lane 0)
 //   warps 1-3    TMA: a stage is four boxes, A and B rows in halves, dealt out to the three warps in
 //                turn (one thread's copies run one after another: with A's 16 KB on one warp the
@@ -95,6 +99,7 @@ template <int BN> struct FpLayout {
     static constexpr int B_BYTES = BN / 2 * kFp8Block;
     static constexpr int STAGE = FP_A_BYTES + B_BYTES;
     static constexpr int STAGES = BN == 256 ? 5 : 6;
+    static constexpr int NB = 512 / BN;                  // block sums in TMEM
     static constexpr int OFF_EPI = STAGES * STAGE;
     static constexpr int OFF_MAX = OFF_EPI + FP_EPI_WARPS * FP_STG;   // row maxima, BN 128 with e4m3
     static constexpr int OFF_BIAS = OFF_MAX + 2 * 2 * 128 * 4;        // per warp: its columns' bias
@@ -166,14 +171,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FP_THREADS, 1)
 gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ FpParams p) {
     using L = FpLayout<BN>;
-    constexpr int STAGES = L::STAGES, COLS = BN / 2;   // columns per epilogue warp
+    constexpr int STAGES = L::STAGES, NB = L::NB, COLS = BN / 2;   // columns per epilogue warp
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
     uint64_t* empty = full + STAGES;
     uint64_t* tfull = empty + STAGES;
-    uint64_t* tempty = tfull + 2;
-    uint64_t* done = tempty + 2;
+    uint64_t* tempty = tfull + NB;
+    uint64_t* done = tempty + NB;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -190,7 +195,7 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             ptx::mbar_init(full + s, 1);
             ptx::mbar_init(empty + s, 1);
         }
-        for (int a = 0; a < 2; ++a) {
+        for (int a = 0; a < NB; ++a) {
             ptx::mbar_init(tfull + a, 1);
             ptx::mbar_init(tempty + a, 2 * FP_EPI_WARPS);
         }
@@ -204,7 +209,7 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         if (p.out_tma) ptx::prefetch_tensormap(&tmOut);
     }
     if (warp == 0) {
-        ptx::tmem_alloc_pair(tmem_slot, 2 * BN);
+        ptx::tmem_alloc_pair(tmem_slot, 512);
         ptx::tmem_relinquish_pair();
     }
     ptx::tc_fence_before();
@@ -260,8 +265,8 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             bool ok = true;
             for (int t = cluster; t < tiles && ok; t += nclusters) {
                 for (int kb = 0; kb < kblocks; ++kb, ++it) {
-                    const uint32_t acc = it & 1;
-                    ok = ptx::mbar_wait_bounded(tempty + acc, ((it >> 1) & 1) ^ 1, abort_flag) &&
+                    const uint32_t acc = it % NB;
+                    ok = ptx::mbar_wait_bounded(tempty + acc, ((it / NB) & 1) ^ 1, abort_flag) &&
                          ptx::mbar_wait_bounded(full + s, round & 1, abort_flag);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
@@ -347,7 +352,7 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             constexpr int CH = COLS / 32;
             uint32_t ra[32], rb[32];
             auto ready = [&]() {   // the next block's sum is complete
-                if (!failed && !__all_sync(0xffffffffu, ptx::mbar_wait_bounded(tfull + (it & 1), (it >> 1) & 1, abort_flag))) {
+                if (!failed && !__all_sync(0xffffffffu, ptx::mbar_wait_bounded(tfull + it % NB, (it / NB) & 1, abort_flag))) {
                     failed = true;
                     if (lane == 0) f8_error(p.err, ERRBIT_TIMEOUT_EPILOGUE);
                     *abort_flag = 1;
@@ -361,7 +366,7 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                                              acc[c * 16 + j]);
             };
             ready();
-            ptx::tmem_ld_32x32b_x32(t_lane + (it & 1) * BN, ra);
+            ptx::tmem_ld_32x32b_x32(t_lane + it % NB * BN, ra);
             for (int kb = 0; kb < kblocks; ++kb) {
                 const float s2 = scale_of(t, kb + 2);   // two blocks ahead
                 const unsigned long long ss = f2_pack(s0, s0);
@@ -371,16 +376,16 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                     uint32_t(&nxt)[32] = (c & 1) ? ra : rb;
                     ptx::tmem_ld_wait_for(cur);
                     if (c + 1 < CH) {
-                        ptx::tmem_ld_32x32b_x32(t_lane + (it & 1) * BN + (c + 1) * 32, nxt);
+                        ptx::tmem_ld_32x32b_x32(t_lane + it % NB * BN + (c + 1) * 32, nxt);
                     } else {
                         // this sum is in registers: its accumulator is free
                         ptx::tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive_cluster_relaxed(tempty0 + (it & 1) * 8);   // orders TMEM reads only
+                        if (lane == 0) ptx::mbar_arrive_cluster_relaxed(tempty0 + it % NB * 8);   // orders TMEM reads only
                         ++it;
                         if (kb + 1 < kblocks) {
                             ready();
-                            ptx::tmem_ld_32x32b_x32(t_lane + (it & 1) * BN, nxt);
+                            ptx::tmem_ld_32x32b_x32(t_lane + it % NB * BN, nxt);
                         }
                     }
                     add(c, cur, ss);
@@ -507,7 +512,7 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     ptx::cluster_sync();   // no CTA leaves while its peer may still touch its memory
     if (warp == 0) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc_pair(tmem, 2 * BN);
+        ptx::tmem_dealloc_pair(tmem, 512);
     }
 }
 
