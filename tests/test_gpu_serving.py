@@ -250,7 +250,8 @@ def check_linear(ops, epi=api.EPI_STORE, bias=None, residual=None, ot=BF, **kw):
 
 LINEAR_SHAPES = [(1, 1, 1), (3, 130, 5), (1, 128, 128), (2, 16, 8), (7, 144, 200), (16, 1024, 384), (17, 272, 136),
                  (33, 512, 1000), (64, 80, 64), (65, 640, 257), (128, 1280, 256), (130, 128, 520), (200, 1264, 1286),
-                 (257, 384, 640), (300, 192, 129), (513, 2048, 256), (1000, 256, 2048), (1731, 1280, 1280)]
+                 (257, 384, 640), (300, 192, 129), (513, 2048, 256), (1000, 256, 2048), (1731, 1280, 1280),
+                 (1300, 272, 4104), (1290, 144, 4112)]
 
 
 @pytest.mark.parametrize("M,K,N", LINEAR_SHAPES)

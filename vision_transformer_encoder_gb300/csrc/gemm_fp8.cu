@@ -991,10 +991,14 @@ cudaError_t launch_gemm_fp8(const Fp8GemmDesc& d, const DeviceInfo& dev, cudaStr
         // 200 x 1024 x 4096 10.4 / 6.7; 1000 x 1280 x 1280 16.9 / 7.8.
         if (d.M <= 16) return launch_rows<16>(d, dev, s);
         if (d.M <= 32 || ((d.M + 31) / 32) * ((d.N + 127) / 128) <= dev.num_sms) return launch_rows<32>(d, dev, s);
-        // 256-wide tiles halve the operand traffic per product; 128-wide ones when the wide tiles
-        // leave CTA pairs without work
-        const int64_t wide = ((d.M + FP_TILE_M - 1) / FP_TILE_M) * ((d.N + 255) / 256);
-        return wide >= dev.num_sms / 2 ? launch_pair<256>(d, dev, s) : launch_pair<128>(d, dev, s);
+        // A 256-wide tile takes 1.4 times a 128-wide one (0.55 to 0.60 us and 0.40 to 0.45 per block along K), so what
+        // counts is in how many rounds the pairs get through them. Measured, 128 / 256 wide, us (rows x K x N):
+        // 2308 x 4096 x 1024 27.3 / 20.7 (2 rounds / 1), 577 x 5120 x 5120 33.9 / 24.7 (2 / 1), 1154 x 4096 x 1024
+        // 15.8 / 20.4 (1 / 1), 2308 x 1024 x 4096 20.7 / 18.4 (5 / 3), 9232 x 4096 x 1024 55.9 / 39.9 (4 / 2).
+        const int64_t pairs = dev.num_sms / 2, high = (d.M + FP_TILE_M - 1) / FP_TILE_M;
+        const int64_t wide = (high * ((d.N + 255) / 256) + pairs - 1) / pairs;
+        const int64_t narrow = (high * ((d.N + 127) / 128) + pairs - 1) / pairs;
+        return narrow * 5 <= wide * 7 ? launch_pair<128>(d, dev, s) : launch_pair<256>(d, dev, s);
     }
     int64_t grid = ((d.M + GG_ROWS - 1) / GG_ROWS) * ((d.N + GG_COLS - 1) / GG_COLS);
     if (grid > 8 * (int64_t)dev.num_sms) grid = 8 * (int64_t)dev.num_sms;
