@@ -394,15 +394,17 @@ def test_cross_attention_of_few_queries_over_many_keys(dh, Tq):
         assert torch.equal(api.cross_attention(q, k, v), got)
 
 
+@pytest.mark.parametrize("dt", [BF, F32], ids=str)
 @pytest.mark.parametrize("B", [2, 37, 128, 130])
-def test_cross_attention_of_many_ragged_sequences(B):
+def test_cross_attention_of_many_ragged_sequences(B, dt):
     """More work than one round of CTAs, sequences in any order of length, equal and empty ones among them."""
     Tq, H, Tk = (1300, 16, 200) if B == 2 else (140, 6, 200)
-    q, k, v = make_cross(B, Tq, Tk, H, H, 64)
+    q, k, v = make_cross(B, Tq, Tk, H, H, 64, dt=dt)
     lens = torch.randint(0, Tk + 1, (B,), generator=torch.Generator().manual_seed(B)).to(torch.int32).to(DEV)
     lens[B // 3] = 0
     lens[1::5] = 77
-    check_cross(q, k, v, lens)
+    for t in (Tq, Tq - 30, 30):
+        check_cross(q[:, :t], k, v, lens)
 
 
 @pytest.mark.parametrize("dh", [1, 8, 17, 32, 48, 72, 160, 256, 512])

@@ -11,11 +11,14 @@
 // A CTA of four warps walks the keys of one (sequence, key head) 64 at a time, K and V tiles by TMA in
 // a ring that all warps read. Query rows are the n side of the products, S^T = K Q^T and
 // O^T = V^T P^T, eight or sixteen to a warp (packed row = token * G + head of the group):
-//   64 rows per CTA, sixteen to each warp; warps without rows skip the work;
-//   a CTA with at most sixteen rows (decoding, or the last of a head) is split along the keys: the
-//   same rows in every warp, which takes 16 of the 64 keys, joined at the end through shared
-//   memory. The last five of 197 rows took three quarters of a full CTA's time before. The last tiles
-//   of all heads come last in the grid, where they fill the end of it: 32 x 197 queries 177 -> 166 us.
+//   64 rows per CTA, sixteen to each warp;
+//   a CTA with at most 32 or 16 rows (decoding, or the last of a head) is split along the keys: two or four
+//   warps share the rows and take every second or fourth group of 16 keys, joined at the end through
+//   shared memory. The last five of 197 rows took three quarters of a full CTA's time before, and 100 x
+//   20 queries over 577 keys 149 us instead of 108. (Two warps for full CTAs too, of 32 rows, fetch K and V
+//   twice as often: 32 x 197 queries 223 us instead of 165.)
+// CTAs that are not split come first, of each kind the longest sequences: 16 x 100 queries over 1025 keys of
+// 16 heads of 80 221 -> 185 us, 4 x 500 over 577 of 12 heads of 64 75 -> 63.
 // Operands are read 16 bytes at a time from the 128-byte swizzled tiles without bank conflicts:
 // the order of the columns in a dot product is free, so thread c takes four consecutive columns
 // of its key for two k-steps; so is which column a row of V^T means; and P^T comes out of S^T by
@@ -33,6 +36,8 @@ namespace vit {
 namespace {
 
 constexpr int CF_KEYS = 64, CF_WARPS = 4, CF_ROWS = 64, CF_BOX = CF_KEYS * 128;   // a box: 32 columns of 64 keys
+constexpr int CF_SORT = 128;   // sequences that are put in order of their lengths, at most
+static_assert(CF_SORT <= CF_WARPS * 32, "a sequence per thread");
 
 template <int DHT> struct CfLayout {
     static constexpr int NB = DHT / 32;                 // boxes of a K or V tile
@@ -73,21 +78,18 @@ __device__ __forceinline__ void transpose_8x8_f32(float& x, float& y) {
 template <int DHT, int NR>
 __global__ void __launch_bounds__(CF_WARPS * 32, DHT <= 64 ? 2 : 1)
 cross_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                 const __grid_constant__ CrossDesc d, float scale_log2, uint32_t* err) {
+                 const __grid_constant__ CrossDesc d, float scale_log2, int sms, uint32_t* err) {
     using L = CfLayout<DHT>;
     constexpr int NB = L::NB, STAGES = L::STAGES;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[STAGES], empty[STAGES];
     __shared__ int abort_word;
+    __shared__ uint8_t order[CF_SORT];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     volatile int* abort_flag = &abort_word;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c4 = lane & 3, r8 = lane >> 2;
-    const int G = (int)(d.H / d.Hkv), dh = (int)d.dh, heads = (int)(d.B * d.Hkv);
-    const int qt = blockIdx.x / heads, bh = blockIdx.x - qt * heads;
-    const int b = bh / (int)d.Hkv, h = bh % (int)d.Hkv;
-    const int64_t rows = d.Tq * G, tile0 = (int64_t)qt * CF_ROWS;
-    const bool split = rows - tile0 <= NR * 8;
-    const int64_t first = tile0 + (split ? 0 : warp * NR * 8);
+    const int G = (int)(d.H / d.Hkv), dh = (int)d.dh;
+    const int64_t rows = d.Tq * G;
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
             ptx::mbar_init(full + i, 1);
@@ -101,6 +103,37 @@ cross_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     __syncthreads();
     griddep_wait();
     griddep_launch_dependents();
+
+    // Work in order: whole tiles of 64 rows, then the ragged last ones of all heads; of each, the longest sequences
+    // first. The CTAs that come to sit beside the first on each SM go backwards through theirs.
+    const bool sorted = sms > 0;
+    if (sorted) {
+        int* lens = reinterpret_cast<int*>(smem);   // before anything is copied there
+        const int i = threadIdx.x, n = (int)d.B;
+        if (i < n) lens[i] = min(max(__ldg(d.kv_lens + i), 0), (int)d.Tk);
+        __syncthreads();
+        int before = 0;
+        if (i < n)
+            for (int j = 0; j < n; ++j) before += lens[j] > lens[i] || (lens[j] == lens[i] && j < i);
+        if (i < n) order[before] = (uint8_t)i;
+        ptx::fence_proxy_async_smem();
+        __syncthreads();
+    }
+    int at = blockIdx.x;
+    if (sorted && DHT <= 64 && at >= sms && at < 2 * sms) at = sms + min(2 * sms, (int)gridDim.x) - 1 - at;
+    const int heads = (int)(d.B * d.Hkv), whole = (int)((rows - NR * 8 + CF_ROWS - 1) / CF_ROWS);   // tiles that are not split
+    int qt, bh;
+    if (at < whole * heads) {
+        bh = at / whole;
+        qt = at - bh * whole;
+    } else {
+        bh = at - whole * heads;
+        qt = whole;
+    }
+    const int b = sorted ? order[bh / (int)d.Hkv] : bh / (int)d.Hkv, h = bh % (int)d.Hkv;
+    const int64_t tile0 = (int64_t)qt * CF_ROWS;
+    const int W = rows - tile0 <= NR * 8 ? 4 : rows - tile0 <= NR * 16 ? 2 : 1;   // warps that share rows
+    const int64_t first = tile0 + warp / W * (NR * 8);
 
     int len = (int)d.Tk;
     if (d.kv_lens) len = min(max(__ldg(d.kv_lens + b), 0), (int)d.Tk);
@@ -152,7 +185,7 @@ cross_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         const uint8_t* sk = smem + st * L::STAGE;
         const uint8_t* sv = sk + NB * CF_BOX;
         // 16 keys at a time; the key groups of a warp
-        const int g0 = split ? warp : 0, g1 = split ? warp + 1 : CF_KEYS / 16;
+        const int share = CF_KEYS / 16 / W, g0 = warp % W * share, g1 = g0 + share;
 #pragma unroll 1
         for (int g = g0; g < g1; ++g) {
             const int valid = len - t * CF_KEYS - g * 16;
@@ -277,7 +310,7 @@ cross_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     };
     // [0] and [2] of m-tile j are columns 16 j' ..: 32 x + 4 r8 + 2 (j % 2) and the next, row 2 c4; [1] and [3]
     // the same of row 2 c4 + 1
-    if (!split) {
+    if (W == 1) {
 #pragma unroll
         for (int i = 0; i < NR; ++i)
 #pragma unroll
@@ -296,7 +329,7 @@ cross_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                 }
             }
     } else {
-        // join the warps: O, m and l of each over the ring, which nobody reads any more
+        // join the warps that share rows: O, m and l of each over the ring, which nobody reads any more
         constexpr int PIECE = NR * 8 * (DHT + 2);
         float* sm = reinterpret_cast<float*>(smem);
         static_assert(CF_WARPS * PIECE * 4 <= L::STAGES * L::STAGE, "join");
@@ -322,22 +355,24 @@ cross_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             }
         __syncthreads();
         for (int x = threadIdx.x; x < (int)(rows - tile0) * dh; x += CF_WARPS * 32) {
-            const int r = x / dh, c = x - r * dh;
+            const int rt = x / dh, c = x - rt * dh, r = rt % (NR * 8);
+            const float* sg = sm + rt / (NR * 8) * W * PIECE;
             float mw[CF_WARPS], mx = -INFINITY;
 #pragma unroll
             for (int w = 0; w < CF_WARPS; ++w) {
-                mw[w] = sm[w * PIECE + NR * 8 * DHT + r];
+                mw[w] = w < W ? sg[w * PIECE + NR * 8 * DHT + r] : -INFINITY;
                 mx = fmaxf(mx, mw[w]);
             }
             const float base = mx == -INFINITY ? 0.f : mx;
             float acc = 0.f, sum = 0.f;
 #pragma unroll
             for (int w = 0; w < CF_WARPS; ++w) {
+                if (w >= W) break;
                 const float f = exp2_approx(mw[w] - base);
-                acc = fmaf(f, sm[w * PIECE + r * DHT + c], acc);
-                sum = fmaf(f, sm[w * PIECE + NR * 8 * DHT + NR * 8 + r], sum);
+                acc = fmaf(f, sg[w * PIECE + r * DHT + c], acc);
+                sum = fmaf(f, sg[w * PIECE + NR * 8 * DHT + NR * 8 + r], sum);
             }
-            out(tile0 + r)[c] = tiles > 0 ? acc / sum : 0.f;
+            out(tile0 + rt)[c] = tiles > 0 ? acc / sum : 0.f;
         }
     }
 }
@@ -353,8 +388,10 @@ template <int DHT, int NR> cudaError_t launch_cf_inst(const CrossDesc& d, const 
         !ct_map_f32(&mv, d.v, d.vs, d.B, d.Tk, d.Hkv, d.dh, CF_KEYS))
         return cudaErrorInvalidValue;
     const int64_t qtiles = (d.Tq * (d.H / d.Hkv) + CF_ROWS - 1) / CF_ROWS;
+    const bool sorted = d.kv_lens && d.B > 1 && d.B <= CF_SORT && d.B * d.Hkv * qtiles > dev.num_sms;
     return launch_dependent(k, dim3((unsigned)(d.B * d.Hkv * qtiles)), dim3(CF_WARPS * 32), L::SMEM, s, mk, mv, d,
-                            (float)(d.scale * 1.4426950408889634), dev.err_word);
+                            (float)(d.scale * 1.4426950408889634),
+                            sorted ? dev.num_sms : 0, dev.err_word);
 }
 
 template <int DHT> cudaError_t launch_cf(const CrossDesc& d, const DeviceInfo& dev, cudaStream_t s) {
