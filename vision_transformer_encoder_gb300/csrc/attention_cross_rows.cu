@@ -7,6 +7,8 @@
 // and output rows, joined at the end through shared memory and, between the CTAs of a cluster,
 // distributed shared memory: no workspace, one launch, the same order of additions every time.
 //
+// 32 sequences of 288 to 577 keys, 16 heads of 64: 13.0 us (4.3 TB/s); 64 of 577 keys: 27 us (5.5 TB/s).
+//
 // Each warp streams its tiles through a ring of its own in shared memory: its lane 0 asks for the
 // tile two or three ahead by TMA as soon as the warp has used up a stage.
 //

