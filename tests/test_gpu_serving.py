@@ -478,6 +478,39 @@ def test_cross_attention_special_scores(Tq, dt):
     assert torch.equal(got[1], keep[1]) and torch.equal(got[0, :, 0], keep[0, :, 0])
 
 
+# Scores of 2^31 and more are farther apart in fp32 than the exponential's range is wide, so the largest
+# one has to come out as exactly zero behind the maximum. Forms: split and whole tensor-core items, few
+# queries on one CTA and on a cluster, fp32 with and without shared rows, CUDA cores.
+LARGE_SCORES = [(BF, 2, 150, 400, 4, 2, 64), (BF, 1, 64, 2500, 2, 2, 128), (BF, 40, 1, 300, 16, 16, 64),
+                (BF, 1, 2, 3000, 4, 2, 80), (F32, 2, 150, 400, 4, 2, 64), (F32, 2, 3, 400, 4, 2, 80),
+                (F32, 2, 20, 70, 4, 2, 128), (BF, 2, 40, 70, 4, 2, 72), (F64, 2, 3, 70, 4, 2, 64)]
+
+
+@pytest.mark.parametrize("scale", [1e9, 7e17, 1e30])
+@pytest.mark.parametrize("form", LARGE_SCORES, ids=str)
+def test_cross_attention_of_large_scores(form, scale):
+    """Queries and keys of small whole numbers have exact scores, and differences of 1 leave no weight: the mean
+    of the values under the largest score, the weights all exactly 1. Then numbers without structure, whose
+    scores are too coarse for more than this: every output lies between the values."""
+    dt, B, Tq, Tk, H, Hkv, dh = form
+    q, k, v = make_cross(B, Tq, Tk, H, Hkv, dh, dt=dt)
+    lens = torch.full((B,), Tk, dtype=torch.int32, device=DEV)
+    lens[0] = Tk - 45
+    qi, ki = (t.float().round().clamp(-2, 2).to(dt) for t in (q, k))
+    # the kernels that take the maximum of scaled scores also have negative scales
+    for sc in (scale, -scale):
+        o, w, _ = cross_ref(qi, ki, v, lens, sc)
+        got = api.cross_attention(qi, ki, v, kv_lens=lens, scale=sc)
+        # sums of up to Tk values and a division, the low parts of a 3xTF32 product, half a step
+        tol = (2 * U * (Tk + 8) + (2.0 ** -20 if dt == F32 else 0)) * w + HALF[dt] * o.abs() * 1.01
+        close(got, o, tol)
+        got = api.cross_attention(q, k, v, kv_lens=lens, scale=sc).double()
+        vd = v.double().repeat_interleave(H // Hkv, 2)
+        lo, hi = vd.amin(1, keepdim=True), vd.amax(1, keepdim=True)
+        room = 2.0 ** -7 * torch.maximum(lo.abs(), hi.abs())
+        assert ((got >= lo - room) & (got <= hi + room)).all()
+
+
 # ----------------------------------------------------------------------- limits of outputs, offsets
 def inside(shape, dt, lead, fn):
     """fn(out) with out a contiguous tensor between two margins (the first of `lead` bytes); nothing outside it changes."""

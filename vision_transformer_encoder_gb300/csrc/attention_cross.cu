@@ -44,7 +44,7 @@ cross_generic_kernel(const CrossDesc d) {
         if (d.kv_lens) len = min((int64_t)max(d.kv_lens[b], 0), d.Tk);
         __syncwarp();
         for (int c = lane; c < dh; c += 32) {
-            sq[c] = to_acc<A>(q[c]) * scale;
+            sq[c] = to_acc<A>(q[c]);
             so[c] = 0;
         }
         __syncwarp();
@@ -56,6 +56,9 @@ cross_generic_kernel(const CrossDesc d) {
                 const T* kr = k + (u0 + lane) * d.ks[1];
                 x = 0;
                 for (int c = 0; c < dh; ++c) x = sq[c] * to_acc<A>(kr[c]) + x;
+                // rounded here: the maximum and what it is taken off are the same numbers
+                if constexpr (std::is_same<A, double>::value) x = __dmul_rn(x, scale);
+                else x = __fmul_rn(x, scale);
             }
             A mn = x;
 #pragma unroll

@@ -220,7 +220,10 @@ cross_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                 for (int e = 0; e < 4; ++e) {   // key r8 + 8 (e / 2), row 2 c4 + e % 2
                     // an infinite hi hi stands as it is: the low part of an infinity is NaN
                     if (fabsf(s[i][e]) < INFINITY) s[i][e] += s2[i][e] + s3[i][e];
-                    if (r8 + 8 * (e >> 1) < valid) mx[e & 1] = fmaxf(mx[e & 1], s[i][e] * scale_log2);
+                    // rounded like the maximum that is taken off below: behind an exact product a maximum of 2^31
+                    // and more is off by more than the exponential's range
+                    s[i][e] = __fmul_rn(s[i][e], scale_log2);
+                    if (r8 + 8 * (e >> 1) < valid) mx[e & 1] = fmaxf(mx[e & 1], s[i][e]);
                 }
 #pragma unroll
                 for (int w = 4; w < 32; w *= 2) {
@@ -235,7 +238,7 @@ cross_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    s[i][e] = r8 + 8 * (e >> 1) < valid ? exp2_approx(fmaf(s[i][e], scale_log2, -mx[e & 1])) : 0.f;
+                    s[i][e] = r8 + 8 * (e >> 1) < valid ? exp2_approx(s[i][e] - mx[e & 1]) : 0.f;
                 l[i][0] = l[i][0] * alpha[i][0] + (s[i][0] + s[i][2]);
                 l[i][1] = l[i][1] * alpha[i][1] + (s[i][1] + s[i][3]);
                 transpose_8x8_f32(s[i][0], s[i][1]);   // now row r8, keys 2 c4 and 2 c4 + 1

@@ -159,7 +159,7 @@ cross_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 #pragma unroll
             for (int i = 0; i < NR; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[i][t][e] = (sp[i][0][e] + sp[i][1][e]) * scale_log2;
+                for (int e = 0; e < 4; ++e) s[i][t][e] = __fmul_rn(sp[i][0][e] + sp[i][1][e], scale_log2);   // rounded like the maximum
         }
         if (valid < KEYS) {
 #pragma unroll

@@ -48,6 +48,10 @@ constexpr int CT_BOX = CT_ROWS * 128;      // 64 columns x 128 rows: 16 KB
 constexpr int CT_MAXZ = 8;
 constexpr int CT_SORT = 128;               // sequences that are put in order of their lengths, at most
 constexpr float CT_SLACK = 8.f;            // log2 of the weights that are carried before a rescale
+// Weights are exp2(fma(s, scale, -m)): the product exact, m the rounded product of the largest score, so that the
+// largest weight is 2 to the power of up to half of m's last place. From here on that may be more than 2, and past 2^31 it
+// overflows: such rows round their products as m was rounded. (One vote with the rescaling, 0 to 1 % of the time.)
+constexpr float CT_COARSE = 16777216.f;
 
 template <int DH> struct CtLayout {
     static_assert(DH % 16 == 0 && DH >= 64 && DH <= 128, "head width");
@@ -397,22 +401,29 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                         if (m_new > -INFINITY) alpha = exp2_approx(m - m_new);
                         m = m_new;
                     }
-                    if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                        // P V of the half tile before writes O
-                        if (!(ok = wait(&bars->o_done[g][(tt - 1) & 1], ((tt - 1) >> 1) & 1))) break;
-                        ptx::tc_fence_after();
-#pragma unroll
-                        for (int c = 0; c < DH / 16; ++c) {
-                            uint32_t ov[16];
-                            ptx::tmem_ld_32x32b_x16(tO + c * 16, ov);
-                            ptx::tmem_ld_wait();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                            ptx::tmem_st_32x32b_x16(tO + c * 16, ov);
-                        }
-                    }
                     const float base = m == -INFINITY ? 0.f : m;   // only infinite scores so far: weights of zero
-                    const unsigned long long s2 = f2_pack(sl2, sl2), nm = f2_pack(-base, -base);
+                    const bool coarse = fabsf(base) > CT_COARSE;
+                    if (__any_sync(0xffffffffu, (j > 0 && alpha != 1.f) || coarse)) {
+                        if (j > 0) {
+                            // P V of the half tile before writes O
+                            if (!(ok = wait(&bars->o_done[g][(tt - 1) & 1], ((tt - 1) >> 1) & 1))) break;
+                            ptx::tc_fence_after();
+#pragma unroll
+                            for (int c = 0; c < DH / 16; ++c) {
+                                uint32_t ov[16];
+                                ptx::tmem_ld_32x32b_x16(tO + c * 16, ov);
+                                ptx::tmem_ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                                ptx::tmem_st_32x32b_x16(tO + c * 16, ov);
+                            }
+                        }
+                        const float f = coarse ? sl2 : 1.f;
+#pragma unroll
+                        for (int e = 0; e < CT_SUB; ++e) sv[e] = __float_as_uint(__fmul_rn(__uint_as_float(sv[e]), f));
+                    }
+                    const float mul = coarse ? 1.f : sl2;
+                    const unsigned long long s2 = f2_pack(mul, mul), nm = f2_pack(-base, -base);
                     unsigned long long ls[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
                     for (int e = 0; e < CT_SUB; e += 2) {
