@@ -420,8 +420,8 @@ int vit_attention(const void* qkv, int64_t N, int64_t T, int64_t D, int64_t H, i
  *             input or sum
  *   scales    (rows, ceil(D / 128)) fp32 with E4M3, else NULL
  * s is formed and normalised in fp32 (fp64 for F64); out comes from s before it is rounded to
- * sum. Any finite row of that type is normalised; squares below the fp32 range count as 0, so
- * eps should be positive.
+ * sum. Any finite row of that type is normalised; squares below its range count as 0, so eps should
+ * be positive.
  * Errors: VIT_ERR_ARG, VIT_ERR_DTYPE, VIT_ERR_CUDA.
  */
 int vit_rmsnorm(const void* x, int x_dtype, const void* residual, int residual_dtype, int64_t rows,

@@ -161,6 +161,24 @@ def test_rmsnorm_large_rows_and_eps(rows, D):
         close(api.rmsnorm(x, eps), y, 2.0 ** -19 * y.abs())
 
 
+@pytest.mark.parametrize("eps", [1e-6, 1e300])
+@pytest.mark.parametrize("value", [1e19, 1e150, 1e200, 1e300])
+@pytest.mark.parametrize("D", [5, 264, 3000])
+def test_rmsnorm_large_rows_in_fp64(D, value, eps):
+    """fp64 rows have fp64's range: squares past it are summed from scaled values, eps beside them."""
+    x = rand(3, D, seed=2, dtype=F64) * value
+    x[1] = 1.7e308
+    s, y = norm_ref(x * 2.0 ** -520, None, None, eps * 2.0 ** -1040)
+    # y of the scaled rows; a chain of ceil(D / 256) + 8 additions per thread, 10 in the tree, 8 more operations
+    close(api.rmsnorm(x, eps), y, 2 * (math.ceil(D / 256) + 26) * 2.0 ** -53 * y.abs())
+    r = rand(3, D, seed=3, dtype=F64) * value
+    r[1] = -1e308
+    out, total = api.rmsnorm(x, eps, residual=r)
+    s, y = norm_ref((x + r) * 2.0 ** -520, None, None, eps * 2.0 ** -1040)
+    assert torch.equal(total, x + r)
+    close(out, y, 2 * (math.ceil(D / 256) + 26) * 2.0 ** -53 * y.abs())
+
+
 def test_rmsnorm_leading_dimensions_and_no_gain():
     x = rand(2, 3, 5, 64, seed=5, dtype=BF)
     out = api.rmsnorm(x, 1e-5)

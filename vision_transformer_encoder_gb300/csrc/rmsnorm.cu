@@ -2,8 +2,8 @@
 // stream's type or in e4m3 with one scale for each 128 columns:
 //   s = x + residual,  y = s / sqrt(mean(s^2) + eps) * gamma
 // s is formed and normalised in fp32 (fp64 for fp64) and rounded only where it is stored as the
-// new residual stream; sums of squares are fp32 over at most a few hundred terms per thread and
-// then a tree, so their relative error stays far below one bf16 step.
+// new residual stream. Sums of squares stay in that type: at most 32 terms in turn per thread, and in the
+// generic kernel ceil(D / 256), then a tree, so that their relative error is below 2^-24 (max(32, D / 256) + 10).
 //
 // Fast kernel (D % 8 == 0, 16-byte aligned, D up to 16384): a row is read once, by the threads of a
 // group of 1 to 16 warps, 8 elements per thread and step, and stays in registers as fp32 sums until
@@ -34,10 +34,16 @@ namespace {
 
 constexpr int RN_THREADS = 256;
 
-// A row whose squares sum past kSquaresLimit (values of about 1e19 and more) is summed again from
-// values scaled by 2^-80, whose squares stay in the fp32 range for every finite row.
+// A row whose squares sum past the arithmetic's range (values of about 1e19 and more, fp64 1e154) is summed again
+// from values scaled by 2^-80 (fp64 2^-600), whose squares stay in the range for every finite row.
 constexpr float kSquaresLimit = 3.4028234e38f;
 constexpr float kPreScale = 8.271806125530277e-25f;
+template <typename A> struct LargeRows {
+    static constexpr A limit = kSquaresLimit, pre = kPreScale;
+};
+template <> struct LargeRows<double> {
+    static constexpr double limit = 1.7976931348623157e308, pre = 0x1p-600;
+};
 
 template <typename T> __device__ __forceinline__ T block_sum(T v, T* part) {
     v = warp_sum(v);
@@ -82,8 +88,8 @@ rmsnorm_generic_kernel(const TX* x, const TR* residual, int64_t rows, int64_t D,
         }
         ss = block_sum(ss, part);
         A pre = 1;
-        if (ss > (A)kSquaresLimit) {   // squares past the fp32 range: again from scaled values
-            pre = (A)kPreScale;
+        if (ss > LargeRows<A>::limit) {   // squares past the range: again from scaled values
+            pre = LargeRows<A>::pre;
             ss = 0;
             for (int64_t c = threadIdx.x; c < D; c += blockDim.x) {
                 const A v = value(c) * pre;
