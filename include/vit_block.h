@@ -413,6 +413,7 @@ int vit_attention(const void* qkv, int64_t N, int64_t T, int64_t D, int64_t H, i
  *   x         (rows, D) of x_dtype: BF16, F32 or F64
  *   residual  (rows, D) of residual_dtype, nullable (then 0): x_dtype, or F32 with a BF16 x
  *             (a residual stream kept in 32 bits)
+ *   eps       any finite number that fp32 holds (not 0 after rounding unless 0; fp64 for F64)
  *   gamma     (D) of gamma_dtype BF16 or F32 (F64 for F64), nullable (then 1)
  *   sum       (rows, D) of residual_dtype, nullable; only with a residual. It may be the
  *             residual itself (updated in place) or x itself where the types agree.

@@ -45,6 +45,21 @@ def test_rmsnorm_refuses(lib, kw, code):
     assert norm(lib, **kw) == code
 
 
+@pytest.mark.parametrize("eps,types", [(float("nan"), (BF16, BF16)), (float("inf"), (F32, F32)), (1e39, (BF16, F32)),
+                                       (1e-50, (BF16, BF16)), (-1e300, (F32, F32)), (float("inf"), (F64, F64))])
+def test_rmsnorm_refuses_eps_that_its_arithmetic_does_not_hold(lib, eps, types):
+    xd, rd = types
+    od = F64 if xd == F64 else F32
+    assert lib.vit_rmsnorm(at(0), xd, at(1), rd, 4, 256, eps, None, xd, None, at(4), od, None, None) == ARG
+
+
+@pytest.mark.parametrize("eps,xd", [(0.0, BF16), (1e-44, F32), (3e38, BF16), (1e300, F64), (1e-300, F64), (-1e-6, F32)])
+def test_rmsnorm_takes_every_other_eps(lib, eps, xd):
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses: a CUDA device is present")
+    assert lib.vit_rmsnorm(at(0), xd, None, xd, 4, 256, eps, None, xd, None, at(4), xd, None, None) == -3
+
+
 @pytest.mark.parametrize("kw,code", [
     (dict(x=None), ARG), (dict(q=None), ARG), (dict(s=None), ARG), (dict(rows=0), ARG), (dict(K=0), ARG),
     (dict(d=F64), DTYPE), (dict(d=E4M3), DTYPE), (dict(q=at(0)), ARG), (dict(s=at(1)), ARG), (dict(x=at(0, 1)), ARG),

@@ -1763,6 +1763,9 @@ int vit_rmsnorm(const void* x, int x_dtype, const void* residual, int residual_d
         if (gamma_dtype != DT_F32 && gamma_dtype != DT_BF16) return VIT_ERR_DTYPE;
         if (out_dtype != DT_F32 && out_dtype != DT_BF16 && out_dtype != DT_E4M3) return VIT_ERR_DTYPE;
     }
+    if (!(eps - eps == 0.0)) return VIT_ERR_ARG;   // not finite
+    // nor, in fp32, past it or rounded to nothing: rows of zeros would be divided by zero
+    if (x_dtype != DT_F64 && (std::fabs(eps) > 3.4028234e38 || ((float)eps == 0.f && eps != 0.0))) return VIT_ERR_ARG;
     if ((out_dtype == DT_E4M3) != (scales != nullptr)) return VIT_ERR_ARG;
     const size_t n = (size_t)(rows * D), xb = n * dt_size(x_dtype), rb = n * dt_size(residual_dtype);
     const size_t gb = (size_t)D * dt_size(gamma_dtype), ob = n * dt_size(out_dtype);
