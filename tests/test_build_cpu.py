@@ -3,10 +3,11 @@ that write their output files, so that nothing is compiled here."""
 import os
 import stat
 import sys
+import sysconfig
 
 import pytest
 
-from vision_transformer_encoder_gb300 import build
+from vision_transformer_encoder_gb300 import api, build
 
 
 def script(path, body):
@@ -30,8 +31,6 @@ def tree(tmp_path, monkeypatch):
     monkeypatch.setattr(build, "BUILD_DIR", str(tmp_path / "_build"))
     monkeypatch.setattr(build, "LIB_PATH", str(tmp_path / "libvit_block.so"))
     monkeypatch.setattr(build, "BINDING_SRC", str(csrc / "binding.cpp"))
-    if hasattr(build, "BINDING_PATH"):
-        monkeypatch.setattr(build, "BINDING_PATH", str(tmp_path / "_serving.so"))
     monkeypatch.setenv("NVCC", script(tmp_path / "nvcc", WRITE_OUTPUT))
     monkeypatch.setenv("CXX", script(tmp_path / "cxx", WRITE_OUTPUT))
     return tmp_path
@@ -81,3 +80,46 @@ def test_a_binding_that_does_not_compile_is_an_error_and_leaves_the_library(tree
     with pytest.raises(RuntimeError, match="binding.cpp"):
         build.build()
     assert os.path.exists(build.LIB_PATH) and not bindings(tree) and not build.up_to_date()
+
+
+def fake_torch(site, version, git):
+    torch = site / "torch"
+    for part in ("include/torch/csrc/Dtype.h", "include/c10/cuda/CUDAGuard.h", "lib/libtorch_cuda.so", "__init__.py"):
+        (torch / part).parent.mkdir(parents=True, exist_ok=True)
+        (torch / part).write_text("")
+    (torch / "version.py").write_text("from typing import Optional\n__version__ = '%s'\ncuda: Optional[str] = '13.0'\n"
+                                      "git_version = '%s'\n" % (version, git))
+
+
+def test_another_torch_gets_a_binding_of_its_own(tree, monkeypatch):
+    monkeypatch.delitem(sys.modules, "torch", raising=False)
+    monkeypatch.syspath_prepend(str(tree / "site"))
+    made = []
+    for i, (version, git) in enumerate((("2.9.1+cu130", "5811a8d"), ("2.11.0+cu130", "5811a8d"), ("2.11.0+cu130", "70d99e9"))):
+        fake_torch(tree / "site", version, git)
+        assert not build.up_to_date() and not os.path.exists(build.binding_path())
+        build.build()
+        made.append(build.binding_path())
+        assert build.up_to_date() and os.path.exists(made[-1])
+        assert len(calls(tree, "cxx")) == i + 1 and len(calls(tree, "nvcc")) == 3   # the library is not made again
+    assert len(set(made)) == 3 and all(m.endswith(sysconfig.get_config_var("EXT_SUFFIX")) for m in made)
+    # and back: what was built for it is still good
+    fake_torch(tree / "site", "2.9.1+cu130", "5811a8d")
+    assert build.up_to_date() and build.binding_path() == made[0]
+
+
+def test_an_untagged_binding_is_not_taken(tree, monkeypatch):
+    """A module without a tag in its name, as an earlier build left it, is neither up to date nor loaded."""
+    (tree / "_serving.so").write_text("")
+    assert not build.up_to_date()
+    build.build()
+    assert len(calls(tree, "cxx")) == 1
+    monkeypatch.setattr(api, "_native", None)
+    monkeypatch.setattr(api, "load_library", lambda: None)
+    os.remove(build.binding_path())
+    with pytest.raises(RuntimeError, match="is not built; run python -m vision_transformer_encoder_gb300.build$"):
+        api.quantize(None)
+    with open(build.binding_path(), "w"):   # no ELF file
+        pass
+    with pytest.raises(RuntimeError, match="cannot be loaded .*--force$"):
+        api.quantize(None)

@@ -8,6 +8,7 @@ passes raw pointers and the current CUDA stream, and turns a non-zero status int
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -450,15 +451,30 @@ def attention(qkv, H, out=None, stream=None):
 _native = None
 
 
+def _load_binding():
+    # by its path: the name says which build of torch and which interpreter it was compiled for
+    from . import build
+    path = build.binding_path()
+    if not os.path.exists(path):
+        missing = build.binding_toolchain()
+        raise RuntimeError("the serving binding for this torch and interpreter, %s, is not built%s; run "
+                           "python -m vision_transformer_encoder_gb300.build" % (
+                               os.path.basename(path), " (%s)" % missing if isinstance(missing, str) else ""))
+    spec = importlib.util.spec_from_file_location(__package__ + "._serving", path)
+    try:
+        native = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(native)
+    except ImportError as e:
+        raise RuntimeError("the serving binding cannot be loaded (%s); run "
+                           "python -m vision_transformer_encoder_gb300.build --force" % e)
+    return native
+
+
 def _serving():
     global _native
     if _native is None:
         lib = load_library()
-        try:
-            from . import _serving as native
-        except ImportError as e:
-            raise RuntimeError("the serving binding is not built (%s); run "
-                               "python -m vision_transformer_encoder_gb300.build" % e)
+        native = _load_binding()
 
         def on_error(status, what):
             raise VitError(status, what)
