@@ -179,6 +179,41 @@ def test_rmsnorm_large_rows_in_fp64(D, value, eps):
     close(out, y, 2 * (math.ceil(D / 256) + 26) * 2.0 ** -53 * y.abs())
 
 
+@pytest.mark.parametrize("types", [(BF, BF, F8), (BF, F32, BF), (F32, F32, F32)], ids=str)
+@pytest.mark.parametrize("rows,D", [(2500, 1024), (1501, 5120), (700, 10240), (5, 8200), (3, 1001)])   # rows to a warp, to 2 to 8 warps, few, generic
+def test_rmsnorm_in_place_in_every_form(rows, D, types):
+    xt, rt, ot = types
+    x, r, g = rand(rows, D, seed=1, dtype=xt), rand(rows, D, seed=2, dtype=rt), rand(D, seed=3)
+    ref = check_norm(x, r, g, ot)
+    for over in (["residual", "x"] if xt == rt else ["residual"]):
+        x2, r2 = x.clone(), r.clone()
+        got = api.rmsnorm(x2, 1e-6, gamma=g, residual=r2, out_dtype=ot, sum_out=r2 if over == "residual" else x2)
+        for a, b in zip(got, ref):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+        assert torch.equal(r2 if over == "x" else x2, r if over == "x" else x)
+    # x as its own residual: a sum of 2 x
+    got = api.rmsnorm(x, 1e-6, gamma=g, residual=x)
+    assert torch.equal(got[1], (x.double() * 2).to(xt))
+
+
+@pytest.mark.parametrize("rows,D", [(2500, 1024), (1501, 5120), (6, 1001)])
+def test_rmsnorm_special_rows_in_every_form(rows, D):
+    x = rand(rows, D, seed=4, dtype=BF)
+    plain, (pq, ps) = api.rmsnorm(x, 1e-6), api.rmsnorm(x, 1e-6, out_dtype=F8)
+    x[0], x[1, 7], x[2, 300], x[4] = 0, math.nan, math.inf, 2.0 ** 60
+    out, (q, s) = api.rmsnorm(x, 1e-6), api.rmsnorm(x, 1e-6, out_dtype=F8)
+    v = q.float() * spread(s, D).float()
+    assert (out[0] == 0).all() and (v[0] == 0).all() and (s[0] == TINY).all()
+    assert torch.isnan(out[1]).all() and torch.isnan(v[1]).all()
+    for t in (out, v):
+        assert torch.isnan(t[2, 300]) and (t[2, :300] == 0).all() and (t[2, 301:] == 0).all()
+    y = norm_ref(x[4:5], None, None, 1e-6)[1]
+    close(out[4:5], y, 2.0 ** -7 * y.abs())
+    keep = torch.tensor([i for i in range(rows) if i not in (0, 1, 2, 4)], device=DEV)
+    assert torch.equal(out[keep], plain[keep]) and torch.equal(s[keep], ps[keep])
+    assert torch.equal(q.view(torch.uint8)[keep], pq.view(torch.uint8)[keep])
+
+
 def test_rmsnorm_leading_dimensions_and_no_gain():
     x = rand(2, 3, 5, 64, seed=5, dtype=BF)
     out = api.rmsnorm(x, 1e-5)
@@ -225,6 +260,26 @@ def test_quantize_special_values():
     assert torch.isnan(v[0, 3]) and (v[0, 4:] == 0).all()
     assert torch.isnan(v[1, 128:]).all() and (v[1, :128] == 0).all()
     assert (s[2] == TINY).all() and (v[2].abs() <= 2.0 ** -135).all()
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=str)
+@pytest.mark.parametrize("K,N", [(256, 264), (255, 131)])   # by 8, generic
+def test_quantize_special_values_in_every_form(K, N, dt):
+    x = rand(K, N, seed=6, dtype=dt)
+    q0, s0 = api.quantize(x)
+    w0, t0 = api.quantize_weight(x)
+    x[1, 3], x[2, 130], x[3, 130] = math.nan, math.inf, -math.inf
+    q, s = api.quantize(x)
+    v = q.double() * spread(s, N)
+    # a NaN is one; the block of an infinity is NaN throughout; the rest is as before
+    assert torch.isnan(v[1, 3]) and not torch.isnan(v[1, 4:]).any() and not torch.isnan(v[2:4, :128]).any()
+    assert torch.isnan(v[2:4, 128:256]).all() and not torch.isnan(v[2:4, 256:]).any() and torch.isinf(s[2:4, 1]).all()
+    assert torch.equal(q.view(torch.uint8)[4:], q0.view(torch.uint8)[4:]) and torch.equal(s[4:], s0[4:])
+    w, t = api.quantize_weight(x)   # the infinities are in the block of rows 128.. of the transpose, columns ..127
+    v = w.double() * spread(t, K, N)
+    assert torch.isnan(v[128:256, :128]).all() and torch.isinf(t[1, 0]) and torch.isnan(v[3, 1])
+    assert torch.isnan(v).sum() == 1 + (min(N, 256) - 128) * 128 and torch.equal(t[:, 1], t0[:, 1])
+    assert torch.equal(w.view(torch.uint8)[:, 128:], w0.view(torch.uint8)[:, 128:])
 
 
 # -------------------------------------------------------------------------------- product
@@ -335,6 +390,72 @@ def test_linear_fp8_gelu_of_large_values(M, K, ot):
     # e4m3: half a step of the block's scale, at most 448 of which are the largest value
     tol = (2.0 ** -4 if ot == F8 else 2.0 ** -7) * z[above].abs() + (2.0 ** -17 * z.abs().max() if ot == F8 else 0)
     close(v[above], z[above], tol)
+
+
+# 16 and 32 rows to a tile, CTA pairs with tiles of 128 and of 256 columns, CUDA cores (on 152 SMs: 32-row tiles up to
+# one wave of CTAs, then pairs)
+GEMM_FORMS = [(4, 256, 384), (600, 256, 384), (2400, 256, 384), (2400, 256, 4096), (4, 255, 384)]
+PAIR_SHAPES = [(2405, 272, 392), (2405, 272, 4104), (2405, 272, 389)]
+
+
+@pytest.mark.parametrize("M,K,N", GEMM_FORMS)
+def test_linear_fp8_gelu_to_bf16_is_rounded_once(M, K, N):
+    """No more than the fp32 GELU's own error beside the output's half step: no 8-bit kernel takes the hardware tangent."""
+    ops = make_product(M, K, N)
+    z, mag = linear_ref(*ops)
+    err = 1.13 * 2 * U * (128 + ops[1].shape[1] + 8) * mag + 2.0 ** -19 * z.abs()
+    y = gelu64(z)
+    close(api.linear_fp8(*ops, epilogue=api.EPI_GELU, out_dtype=BF), y, HALF[BF] * y.abs() * (1 + 2.0 ** -8) + err)
+
+
+@pytest.mark.parametrize("ot", [BF, F32, F8], ids=str)
+@pytest.mark.parametrize("M,K,N", GEMM_FORMS)
+def test_linear_fp8_values_of_any_size(M, K, N, ot):
+    """GELU of -1e25 is zero and of 1e25 itself; NaN and infinities stay in their rows."""
+    a, sa, w, sw = make_product(M, K, N)
+    sa = sa.clone()
+    sa[1::2] *= 1e25
+    z = linear_ref(a, sa, w, sw)[0]
+    got = api.linear_fp8(a, sa, w, sw, epilogue=api.EPI_GELU, out_dtype=ot)
+    v = got[0].double() * spread(got[1], N) if ot == F8 else got.double()
+    below, above = z < -1e23, z > 1e23
+    assert below.any() and above.any() and (v[below] == 0).all()
+    # e4m3: half a step of the block's scale, at most 448 of which are the largest value
+    tol = (2.0 ** -4 if ot == F8 else 2.0 ** -7) * z[above].abs() + (2.0 ** -17 * z.abs().max() if ot == F8 else 0)
+    close(v[above], z[above], tol)
+    a, sa, w, sw = make_product(M, K, N)
+    ref = api.linear_fp8(a, sa, w, sw, out_dtype=ot)
+    a.view(torch.uint8)[M - 2, 200] = 0x7F          # NaN
+    sa[0, 1] = math.inf
+    got = api.linear_fp8(a, sa, w, sw, out_dtype=ot)
+    if ot == F8:
+        assert torch.equal(got[1][1:M - 2], ref[1][1:M - 2]) and torch.equal(got[1][M - 1], ref[1][M - 1])
+        got, ref = got[0], ref[0]
+    assert torch.isnan(got[M - 2].float()).all() and not torch.isfinite(got[0].float()).any()
+    same = got.view(torch.uint8) == ref.view(torch.uint8)
+    assert same[1:M - 2].all() and same[M - 1].all()
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=str)
+@pytest.mark.parametrize("M,K,N", PAIR_SHAPES)
+def test_linear_fp8_of_pairs_in_place_and_unaligned(M, K, N, dt):
+    ops = make_product(M, K, N)
+    r = rand(M, N, seed=2, dtype=dt)
+    ref = check_linear(ops, api.EPI_RESIDUAL, residual=r, ot=dt)
+    apart = unaligned(r)
+    assert torch.equal(api.linear_fp8(*ops, residual=apart, epilogue=api.EPI_RESIDUAL, out_dtype=dt), ref)
+    assert torch.equal(api.linear_fp8(*ops, residual=apart, epilogue=api.EPI_RESIDUAL, out=apart), ref)
+    got = api.linear_fp8(*ops, residual=r, epilogue=api.EPI_RESIDUAL, out=r)
+    assert got is r and torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("lead", [4096, 4104])
+@pytest.mark.parametrize("M,K,N", PAIR_SHAPES)
+def test_nothing_outside_the_outputs_of_pairs_is_written(M, K, N, lead):
+    ops = make_product(M, K, N)
+    for dt in (BF, F32, F8):
+        inside((M, N), dt, lead, lambda t: api.linear_fp8(*ops, out=t))
+    inside((M, (N + 127) // 128), F32, lead, lambda t: api.linear_fp8(*ops, out_dtype=F8, out_scales=t))
 
 
 # -------------------------------------------------------------------------- cross attention
@@ -527,6 +648,37 @@ def test_cross_attention_of_large_scores(form, scale):
         lo, hi = vd.amin(1, keepdim=True), vd.amax(1, keepdim=True)
         room = 2.0 ** -7 * torch.maximum(lo.abs(), hi.abs())
         assert ((got >= lo - room) & (got <= hi + room)).all()
+
+
+@pytest.mark.parametrize("dh,Hkv", [(64, 2), (128, 2), (80, 1), (72, 2)])
+@pytest.mark.parametrize("Tq", [1, 3, 20, 130])
+def test_cross_attention_special_values_where_keys_are_dealt_out(Tq, dh, Hkv):
+    """Parts of a long sequence on different CTAs: what lies past the length, keys and whole parts without weight, NaN."""
+    B, Tk = 2, 2500
+    q, k, v = make_cross(B, Tq, Tk, 2 * Hkv, Hkv, dh)
+    lens = torch.tensor([1290, 129], dtype=torch.int32, device=DEV)
+    ref = check_cross(q, k, v, lens)
+    k2, v2 = k.clone(), v.clone()
+    for b, n in enumerate(lens.tolist()):
+        k2[b, n:], v2[b, n:] = math.nan, math.nan
+        k2[b, n + 1:], v2[b, n + 1:] = math.inf, -math.inf
+    assert torch.equal(api.cross_attention(q, k2, v2, kv_lens=lens), ref)
+    # scores of minus infinity for all keys but the last ones, or but the first
+    q2 = q.abs() + 0.01
+    for live in (slice(2300, 2500), slice(0, 100), slice(1200, 1201)):
+        k2 = torch.full_like(k, -math.inf)
+        k2[:, live] = k[:, live]
+        o, w, _ = cross_ref(q2, k[:, live], v[:, live], None, dh ** -0.5)
+        close(api.cross_attention(q2, k2, v), o, 2.0 ** -7 * w)
+    k2 = torch.full_like(k, -math.inf)
+    assert torch.isnan(api.cross_attention(q2, k2, v)).all()
+    k2 = k.clone()
+    k2[0, 1700, 0] = math.nan
+    got, keep = api.cross_attention(q, k2, v), api.cross_attention(q, k, v)
+    assert torch.isnan(got[0, :, :2]).all() and torch.equal(got[1], keep[1]) and torch.equal(got[0, :, 2:], keep[0, :, 2:])
+    # scores that grow through the parts
+    grow = torch.linspace(0, 6, Tk, device=DEV)[None, :, None, None]
+    check_cross(q, (k[:, :1].float().expand(-1, Tk, -1, -1) * grow).to(BF), v)
 
 
 # ----------------------------------------------------------------------- limits of outputs, offsets
