@@ -477,8 +477,11 @@ int vit_linear_fp8(const void* a, const float* a_scales, const void* w, const fl
  *             clamped to [0, Tk]. With none its outputs are zero. Keys past the length may hold
  *             anything, NaN included.
  *   scale     any finite number, of magnitude up to 1e30 unless F64; 1 / sqrt(dh) is usual
- * Softmax in fp32 (fp64 for F64); F32 products as three TF32 products per step for dh <= 128
- * (an infinite value, or one above 3.4e38, then gives NaN). dh up to 512.
+ * Softmax in fp32 (fp64 for F64), where scaled scores past its range, as infinite ones, give NaN, and so does a
+ * row whose scores are all minus infinity. On tensor cores, BF16 weights meet V rounded to bf16 (their sum is
+ * not), and F32 products are three TF32 products per step (an infinite value, or one above 3.4e38, then
+ * gives NaN). Tensor cores take 16-byte aligned rows: BF16 with dh 64, 80, 96 or 128, or a multiple of 8 up to 128 where
+ * a key head has at most 16 query rows (Tq G); F32 with dh a multiple of 4 up to 128. dh up to 512.
  * Errors: VIT_ERR_ARG, VIT_ERR_DTYPE, VIT_ERR_UNSUPPORTED (dh), VIT_ERR_CUDA.
  */
 int vit_cross_attention(const void* q, const int64_t* q_strides, const void* k,

@@ -3,7 +3,8 @@
 Every computation runs in the CUDA library ``libvit_block.so``; this module checks
 that tensors are contiguous and on the right device, picks the element-type code,
 passes raw pointers and the current CUDA stream, and turns a non-zero status into
-``VitError``. There is no fallback: if the library is missing, calls raise.
+``VitError``. There is no fallback: if the library is missing, calls raise. Forward only: a
+result carries no gradient, whether or not its inputs require one.
 """
 from __future__ import annotations
 

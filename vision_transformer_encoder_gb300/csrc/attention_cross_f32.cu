@@ -3,10 +3,12 @@
 //
 // Products are 3xTF32 (hi hi + hi lo + lo hi, hi rounded to the 11 bits that the tensor cores read,
 // lo the rest) on mma.m16n8k8, and sums longer than 16 keys are fp32 additions: the outputs of 8 x 197
-// queries over 288 to 577 keys are off by 3.6e-7 in the 2-norm, and by 3.3e-6 when O is summed on the
-// tensor cores, which cut sums off instead of rounding them. Bound by the tensor pipe (50 %
-// active); 53 us at 12 heads of 64 (36 TFLOP/s). A CUDA-core kernel took 103 us: one warp per
-// scheduler issues a product every other cycle.
+// queries over 288 to 577 keys are off by 3.7e-7 in the 2-norm, and by 3.3e-6 when O is summed on the
+// tensor cores, which cut sums off instead of rounding them. 53 us at 12 heads of 64 (36 TFLOP/s): bound by each
+// warp's own chain of dependent steps, with one or two warps to a scheduler and the tensor pipe of mma.sync 50 % active. It
+// is the simple form; attention_tf32.cu, on tcgen05, reaches twice that rate in self attention. A CUDA-core kernel
+// took 103 us. Heads wider than 64 and 96 columns spill with sixteen rows to a warp (20 and 196 bytes a thread written, 76
+// and 344 read back).
 //
 // A CTA of four warps walks the keys of one (sequence, key head) 64 at a time, K and V tiles by TMA in
 // a ring that all warps read. Query rows are the n side of the products, S^T = K Q^T and
@@ -15,10 +17,11 @@
 //   a CTA with at most 32 or 16 rows (decoding, or the last of a head) is split along the keys: two or four
 //   warps share the rows and take every second or fourth group of 16 keys, joined at the end through
 //   shared memory. The last five of 197 rows took three quarters of a full CTA's time before, and 100 x
-//   20 queries over 577 keys 149 us instead of 108. (Two warps for full CTAs too, of 32 rows, fetch K and V
-//   twice as often: 32 x 197 queries 223 us instead of 165.)
-// CTAs that are not split come first, of each kind the longest sequences: 16 x 100 queries over 1025 keys of
-// 16 heads of 80 221 -> 185 us, 4 x 500 over 577 of 12 heads of 64 75 -> 63.
+//   20 queries over 577 keys 149 us instead of 107. (Two warps for full CTAs too, of 32 rows, fetch K and V
+//   twice as often: 32 x 197 queries 223 us instead of 163.)
+// CTAs whose rows four warps share come last, before them all others, of each kind the longest sequences first: 16 x 100
+// queries over 1025 keys of 16 heads of 80 221 -> 186 us, 4 x 500 over 577 of 12 heads of 64 75 -> 62. All keys of a
+// (sequence, key head) are walked by one CTA: one query over 1100 keys of 12 heads of 64, on 12 SMs, takes 18 us.
 // Operands are read 16 bytes at a time from the 128-byte swizzled tiles without bank conflicts:
 // the order of the columns in a dot product is free, so thread c takes four consecutive columns
 // of its key for two k-steps; so is which column a row of V^T means; and P^T comes out of S^T by
@@ -104,8 +107,8 @@ cross_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     griddep_wait();
     griddep_launch_dependents();
 
-    // Work in order: whole tiles of 64 rows, then the ragged last ones of all heads; of each, the longest sequences
-    // first. The CTAs that come to sit beside the first on each SM go backwards through theirs.
+    // Work in order: tiles of more than NR * 8 rows, then the last ones of all heads that have fewer and that four warps
+    // share; of each, the longest sequences first. The CTAs that come to sit beside the first on each SM go backwards through theirs.
     const bool sorted = sms > 0;
     if (sorted) {
         int* lens = reinterpret_cast<int*>(smem);   // before anything is copied there
@@ -121,7 +124,7 @@ cross_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     }
     int at = blockIdx.x;
     if (sorted && DHT <= 64 && at >= sms && at < 2 * sms) at = sms + min(2 * sms, (int)gridDim.x) - 1 - at;
-    const int heads = (int)(d.B * d.Hkv), whole = (int)((rows - NR * 8 + CF_ROWS - 1) / CF_ROWS);   // tiles that are not split
+    const int heads = (int)(d.B * d.Hkv), whole = (int)((rows - NR * 8 + CF_ROWS - 1) / CF_ROWS);   // tiles before the last kind
     int qt, bh;
     if (at < whole * heads) {
         bh = at / whole;

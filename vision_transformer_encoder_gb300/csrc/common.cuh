@@ -132,8 +132,10 @@ __device__ __forceinline__ void gelu_tanh_fast2(float& a, float& b) {
     f2_unpack(f2_fma(hz, f2_pack(tanh_approx(u0), tanh_approx(u1)), hz), a, b);
 }
 
-// tanh-approximation GELU of a pair to fp32 accuracy (about 2^-20 relative, 2^-59 absolute in the
-// factor of z): with u = sqrt(2/pi) (z + 0.044715 z^3), 0.5 z (1 + tanh u) = z / (1 + exp(-2u)). The
+// tanh-approximation GELU of a pair: with u = sqrt(2/pi) (z + 0.044715 z^3),
+// 0.5 z (1 + tanh u) = z / (1 + exp(-2u)). With t = -2u log2(e), off by up to four roundings, the factor of z is off
+// by |t| ln(2) 2^-22 of itself where z is negative (2^-20 at -2, 2^-18.5 at -4), and by 2^-21 for the exponential and
+// the reciprocal; by less where z is positive and exp adds less than 1; and by 2^-59 absolutely. The
 // two quotients share one hardware reciprocal, 1/a = b / (a b) and 1/b = a / (a b); exp is cut off
 // at 2^60, which keeps the product of the denominators in range. Taking 2^-59 off, at zero at the
 // least, makes the factor of what was cut off 0: large negative z give 0, and -infinity NaN as

@@ -44,9 +44,5 @@ __device__ __forceinline__ uint8_t fp8_pack1(float a) {
 __device__ __forceinline__ float fp8_value(uint8_t q) {
     return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)q, __NV_E4M3)));
 }
-__device__ __forceinline__ float2 fp8_value2(uint16_t q) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)q, __NV_E4M3);
-    return __half22float2(__half2(h));
-}
 
 }  // namespace vit

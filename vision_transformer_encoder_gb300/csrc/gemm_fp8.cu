@@ -11,10 +11,12 @@
 // stay in one accumulator with the others': each block gets an accumulator of its own in TMEM
 // (512 / BN, in turn), and the epilogue warps add scale * block sum to fp32 registers while the
 // tensor cores make the next ones. With four in turn instead of two 577 x 5120 -> 5120 (BN 128) takes
-// 34.1 us instead of 34.7. At BN 256 that addition is what bounds it, some 1160 cycles per block of which the products
-// need 512 (36928 x 4096 -> 4096: 563 us, 2.20 PFLOP/s, near the power limit). Measured and slower: loads of 64
+// 34.1 us instead of 34.7. At BN 256 a block takes some 1160 cycles of which the products
+// need 512 (36928 x 4096 -> 4096: 564 us, 2.20 PFLOP/s, near the power limit). No one part of it bounds that: without the
+// additions 546 us, without the loads from TMEM too 473, with every tile's operands in L2 559 (BN 128: 803, 703, 684 and
+// 798); what is left is the handing over between ring, products and sums, block by block. Measured and slower: loads of 64
 // columns, 642 us; sixteen epilogue warps of 64 columns each with loads of 16, 780 us; products of 128 columns with
-// accumulators handed over by halves, 573 us.
+// accumulators handed over by halves, 573 us. The BN 128 instances spill 28 bytes a thread (100 read back).
 //   warp 0       MMA issue (one lane of the leader CTA's)
 //   warps 1-3    TMA: a stage is four boxes, A and B rows in halves, dealt out to the three warps in
 //                turn (one thread's copies run one after another: with A's 16 KB on one warp the
@@ -28,7 +30,7 @@
 // cluster of CTAs shares the blocks along K, so that a decoding step's product streams its weight
 // with most of the SMs. The CTAs' fp32 sums meet in distributed shared memory and are added in
 // rank order: no workspace, one launch, the same result every time. 8 x 1024 -> 4096 with GELU to
-// e4m3 takes 5.0 us, 8 x 5120 -> 5120 7.6 (the pair kernel 7.2 and 19.5).
+// e4m3 takes 5.0 us, 8 x 5120 -> 5120 7.4 (the pair kernel 7.2 and 20.2).
 //
 // Generic kernel: CUDA cores, any size and alignment; a CTA makes 16 rows x 128 columns (one
 // output block per row), a thread eight columns of one row.
@@ -897,8 +899,8 @@ template <int TN, int EPI> cudaError_t launch_rows_out(const Fp8GemmDesc& d, con
 
 template <int TN> cudaError_t launch_rows(const Fp8GemmDesc& d, const DeviceInfo& dev, cudaStream_t s) {
     // One block along K at least for each CTA; a second CTA on an SM only for eight or more (us with
-    // one / two per SM: 8 x 5120 x 5120 10.1 / 7.9, 256 x 4096 x 1024 11.0 / 9.1, but 512 x 1024 x 1024,
-    // four blocks each, 5.5 / 8.3).
+    // one / two per SM: 8 x 5120 x 5120 9.7 / 7.4, 256 x 4096 x 1024 10.8 / 8.8, but 512 x 1024 x 1024,
+    // four blocks each, 5.3 / 8.0).
     const int64_t tiles = ((d.M + TN - 1) / TN) * ((d.N + 127) / 128), kblocks = (d.K + kFp8Block - 1) / kFp8Block;
     int Z = 1;
     while (Z < FR_MAXZ && tiles * Z * 2 <= 2 * (int64_t)dev.num_sms &&
@@ -987,15 +989,15 @@ cudaError_t launch_gemm_fp8(const Fp8GemmDesc& d, const DeviceInfo& dev, cudaStr
     if (f8_tc_ok(d, dev)) {
         // Up to 32 rows the rows kernel reads the weight once, with every SM. Beyond, 32 rows at a time,
         // while its tiles are one wave of CTAs: it then has more CTAs than the pair kernel has pairs
-        // with work. Measured, rows / pair kernel, us (rows x K x N): 8 x 5120 x 5120 10.0 / 19.5;
-        // 100 x 4096 x 1024 7.2 / 15.7; 512 x 1024 x 1024 5.5 / 6.7; and past one wave
-        // 200 x 1024 x 4096 10.4 / 6.7; 1000 x 1280 x 1280 16.9 / 7.8.
+        // with work. Measured, rows / pair kernel, us (rows x K x N): 8 x 5120 x 5120 7.4 / 20.2;
+        // 100 x 4096 x 1024 6.9 / 15.1; 512 x 1024 x 1024 5.3 / 6.5; and past one wave
+        // 200 x 1024 x 4096 6.5 / 6.5; 1000 x 1280 x 1280 12.2 / 7.6.
         if (d.M <= 16) return launch_rows<16>(d, dev, s);
         if (d.M <= 32 || ((d.M + 31) / 32) * ((d.N + 127) / 128) <= dev.num_sms) return launch_rows<32>(d, dev, s);
         // A 256-wide tile takes 1.4 times a 128-wide one (0.55 to 0.60 us and 0.40 to 0.45 per block along K), so what
         // counts is in how many rounds the pairs get through them. Measured, 128 / 256 wide, us (rows x K x N):
-        // 2308 x 4096 x 1024 27.3 / 20.7 (2 rounds / 1), 577 x 5120 x 5120 33.9 / 24.7 (2 / 1), 1154 x 4096 x 1024
-        // 15.8 / 20.4 (1 / 1), 2308 x 1024 x 4096 20.7 / 18.4 (5 / 3), 9232 x 4096 x 1024 55.9 / 39.9 (4 / 2).
+        // 2308 x 4096 x 1024 27.1 / 20.7 (2 rounds / 1), 577 x 5120 x 5120 33.7 / 24.4 (2 / 1), 1154 x 4096 x 1024
+        // 15.7 / 20.5 (1 / 1), 2308 x 1024 x 4096 20.6 / 18.1 (5 / 3), 9232 x 4096 x 1024 55.9 / 40.0 (4 / 2).
         const int64_t pairs = dev.num_sms / 2, high = (d.M + FP_TILE_M - 1) / FP_TILE_M;
         const int64_t wide = (high * ((d.N + 255) / 256) + pairs - 1) / pairs;
         const int64_t narrow = (high * ((d.N + 127) / 128) + pairs - 1) / pairs;
