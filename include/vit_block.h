@@ -490,6 +490,98 @@ int vit_cross_attention(const void* q, const int64_t* q_strides, const void* k,
                         int64_t Hkv, int64_t dh, double scale, int dtype, void* o, void* stream);
 
 /* ------------------------------------------------------------------------------
+ * A decoder's self attention: rotary positions, a paged cache of keys and values, and attention
+ * over it in which a batch may share a prefix.
+ * ------------------------------------------------------------------------------ */
+
+/* Which columns of a head make pair i of n. */
+typedef enum {
+    VIT_ROTARY_HALF = 0,         /* i and i + n     */
+    VIT_ROTARY_INTERLEAVED = 1   /* 2 i and 2 i + 1 */
+} vit_rotary_layout;
+
+/*
+ * Rotary positions: at position p, pair i (u, v) of the first 2 n columns of a head becomes
+ *   scale (u cos a - v sin a, u sin a + v cos a),   a = p frequencies[i]
+ * and the other columns stay. The angle is reduced to a turn exactly (64-bit fixed point), however far the
+ * position; arithmetic in fp32 (fp64 for F64), rounded once.
+ */
+typedef struct {
+    const double* frequencies;   /* (n) on the device, radians per position; finite */
+    int64_t n;                   /* 2 n <= dh */
+    int layout;                  /* a vit_rotary_layout */
+    double scale;                /* finite, of magnitude up to 1e30 unless F64; 1 is usual */
+} vit_rope;
+
+/*
+ * vit_rotary -- rotates x (B, T, H, dh) of dtype BF16, F32 or F64 into out.
+ *   x_strides  host array of three element strides (sequence, token, head), all >= 0; NULL:
+ *              contiguous. The dh elements of a head are contiguous.
+ *   positions  (B, T) device array, nullable (then t). Any int32, negative ones too.
+ *   out        (B, T, H, dh) contiguous, apart from x; or x itself, rotated where it lies (its strides
+ *              must then keep its elements apart)
+ * Errors: VIT_ERR_ARG, VIT_ERR_DTYPE, VIT_ERR_CUDA.
+ */
+int vit_rotary(const void* x, const int64_t* x_strides, const int32_t* positions, const vit_rope* rope,
+               int64_t B, int64_t T, int64_t H, int64_t dh, int dtype, void* out, void* stream);
+
+/*
+ * A pool of pages of `page` tokens each: keys k and values v (pages, page, heads, dh), all of dtype. A sequence's
+ * page table (one row of a (sequences, table_pages) int32 device array) says which page holds its keys
+ * [i page, (i + 1) page). Entries outside [0, pages) are absent: nothing is written there, and attention does not see
+ * their keys. Entries that no key falls on are not read.
+ */
+typedef struct {
+    void* k;
+    void* v;
+    int64_t k_strides[3], v_strides[3];   /* elements: page, token, head; > 0 where there are several */
+    int64_t pages, page, heads, dh;
+    int dtype;                            /* BF16, F32 or F64 */
+} vit_paged_cache;
+
+/*
+ * vit_cache_append -- token t of sequence b goes to slot u = starts[b] + t of the sequence, for t < lens[b]:
+ * its key, rotated, and its value. A query, when given, is rotated alongside into q_out, for every t.
+ *   k, v       (B, T, heads, dh) with strides as vit_rotary's, apart from the pool
+ *   q          (B, T, H, dh), nullable; q_out then contiguous, or q itself
+ *   table      (B, table_pages); slots outside [0, table_pages page) and on absent pages are not written
+ *   starts     (B); lens (B), nullable (then T; clamped to [0, T])
+ *   rope       nullable: no rotation. positions (B, T), nullable (then starts[b] + t)
+ * No two tokens of a call may have the same slot of the same page, as sequences that share it would. Only those
+ * slots are written.
+ * Errors: VIT_ERR_ARG, VIT_ERR_DTYPE, VIT_ERR_CUDA.
+ */
+int vit_cache_append(const void* k, const int64_t* k_strides, const void* v, const int64_t* v_strides,
+                     const void* q, const int64_t* q_strides, const vit_paged_cache* cache, const int32_t* table,
+                     int64_t table_pages, const int32_t* starts, const int32_t* lens, const vit_rope* rope,
+                     const int32_t* positions, int64_t B, int64_t T, int64_t H, void* q_out, void* stream);
+
+/*
+ * vit_paged_attention -- causal attention of the newest tokens of each sequence over its cached keys:
+ *   o[b, t, h] = sum_u softmax_u(scale q[b, t, h] . k[u, h / G]) v[u, h / G],   G = H / heads
+ * over the keys u of the sequence with u < kv_lens[b] - (q_lens[b] - 1 - t), so that the last query sees them all, and,
+ * in front of them, over the prefix of its group. The sequences fall into `groups` groups of B / groups in turn, each
+ * with a prefix of its own, whose keys are read and scored for the whole group at once.
+ *   q             (B, Tq, H, dh) with strides as vit_rotary's; H % heads == 0
+ *   table         (B, table_pages); kv_lens (B), clamped to [0, table_pages page], the new tokens counted in
+ *   q_lens        (B), nullable (then Tq; clamped to [0, Tq]): rows t >= q_lens[b] of o are zeros
+ *   prefix_table  (groups, prefix_pages), nullable (then no prefix, prefix_pages 0 and groups 1);
+ *                 prefix_lens (groups), clamped to [0, prefix_pages page]
+ *   scale         finite, of magnitude up to 1e30 unless F64
+ *   o             (B, Tq, H, dh) contiguous, apart from every input
+ * A row that sees no key, or whose scores are all minus infinity, is zeros. What lies past the lengths and on absent
+ * pages may be anything, NaN included. Softmax in fp32 (fp64 for F64). On tensor cores weights meet V
+ * rounded to bf16 (their sum is not). They take BF16, dh a multiple of 8 up to 128 where a key head has at most 16
+ * query rows (Tq G) and no prefix, else 64, 80, 96 or 128; pages of a multiple of 16 tokens; 16-byte aligned
+ * rows; positive scales. dh up to 512.
+ * Errors: VIT_ERR_ARG, VIT_ERR_DTYPE, VIT_ERR_UNSUPPORTED (dh), VIT_ERR_NOMEM, VIT_ERR_CUDA.
+ */
+int vit_paged_attention(const void* q, const int64_t* q_strides, const vit_paged_cache* cache, const int32_t* table,
+                        int64_t table_pages, const int32_t* kv_lens, const int32_t* q_lens,
+                        const int32_t* prefix_table, int64_t prefix_pages, const int32_t* prefix_lens,
+                        int64_t groups, int64_t B, int64_t Tq, int64_t H, double scale, void* o, void* stream);
+
+/* ------------------------------------------------------------------------------
  * Status, diagnostics and measurement
  * ------------------------------------------------------------------------------ */
 

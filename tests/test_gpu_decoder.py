@@ -1,0 +1,762 @@
+"""A decoder's self attention against plain 64-bit implementations: rotary positions, appending to a paged cache,
+attention over it behind a shared prefix, and a run of them together.
+
+Tolerances, from the arithmetic (u = 2^-24, one fp32 rounding):
+  results         half a step: bf16 2^-8 |y|, fp32 2^-24 |y|
+  rotation        sine and cosine of the reduced angle are off by pi u for its rounding and, fp32, two units in the last place
+                  (2^-22 at most together); bf16, 2^-21.19 of the hardware's and pi u: 16 u covers either. The
+                  factor, two products and an addition: 4 u more. All of it times |u| + |v| and the factor.
+                  fp64: the angle p f is off by 2^-51 of itself and by p 2^-63, here and in the reference
+  attention       a score is off by 2 u (dh + 4) scale sum|q||k|, and its weight by twice that, relatively; bf16 weights
+                  by 2^-8 more; sums of n fp32 terms by 2 u (n + 8); the exponential of a rounded argument by 2^-20;
+                  the joining factors of parts by 2^-20 again
+"""
+import math
+
+import pytest
+import torch
+
+from vision_transformer_encoder_gb300 import api
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+BF, F32, F64 = torch.bfloat16, torch.float32, torch.float64
+HALF = {BF: 2.0 ** -8, F32: U, F64: 2.0 ** -53}
+DEV = "cuda:0"
+LAYOUTS = [api.ROTARY_HALF, api.ROTARY_INTERLEAVED]
+
+
+@pytest.fixture(autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    yield
+    assert api.device_error() == 0
+
+
+def rand(*shape, seed=0, std=1.0, dtype=F32):
+    g = torch.Generator().manual_seed(seed * 7919 + sum(shape))
+    return (torch.randn(*shape, generator=g) * std).to(dtype).to(DEV)
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+def close(got, ref, tol):
+    got = got.double()
+    assert torch.equal(torch.isnan(got), torch.isnan(ref))
+    bad = ~((got - ref).abs() <= tol) & ~torch.isnan(ref) & ~(got == ref)
+    if bad.any():
+        i = int(torch.argmax(((got - ref).abs() / tol.clamp_min(1e-300)).nan_to_num(0).reshape(-1)))
+        raise AssertionError("%d of %d outside: worst got %g ref %g tol %g" % (
+            int(bad.sum()), bad.numel(), got.reshape(-1)[i], ref.reshape(-1)[i], tol.expand_as(ref).reshape(-1)[i]))
+
+
+def same(a, b):
+    return torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+# --------------------------------------------------------------------------------- rotary
+def rotary_ref(x, f, pos, layout, scale=1.0):
+    """(rotated x, what its errors go by) in 64 bits."""
+    x, n = x.double(), f.numel()
+    a = pos.double()[:, :, None, None] * f.double()
+    c, s = torch.cos(a) * scale, torch.sin(a) * scale
+    i = torch.arange(n, device=x.device)
+    i, j = (i, i + n) if layout == api.ROTARY_HALF else (2 * i, 2 * i + 1)
+    y, w = x.clone(), torch.zeros_like(x)
+    y[..., i], y[..., j] = x[..., i] * c - x[..., j] * s, x[..., i] * s + x[..., j] * c
+    w[..., i] = w[..., j] = (x[..., i].abs() + x[..., j].abs()) * abs(scale)
+    return y, w
+
+
+def rotary_tol(y, w, dt, f, pos):
+    if dt == F64:
+        a = pos.double().abs()[:, :, None, None] * f.abs().max()
+        return w * (a * 2.0 ** -50 + pos.double().abs()[:, :, None, None] * 2.0 ** -60 + 2.0 ** -49) + HALF[dt] * y.abs()
+    return w * 20 * U + HALF[dt] * y.abs() * 1.01
+
+
+def check_rotary(x, f, pos=None, layout=api.ROTARY_HALF, scale=1.0, **kw):
+    got = api.rotary(x, f, positions=pos, layout=layout, scale=scale, **kw)
+    if pos is None:
+        pos = torch.arange(x.shape[1], device=DEV).expand(x.shape[0], -1)
+    y, w = rotary_ref(x, f, pos, layout, scale)
+    close(got, y, rotary_tol(y, w, x.dtype, f, pos))
+    return got
+
+
+ROTARY_SHAPES = [(1, 1, 1, 2, 2), (1, 1, 1, 64, 64), (3, 5, 3, 64, 32), (2, 7, 4, 80, 80), (1, 300, 16, 128, 128), (2, 33, 5, 96, 6),
+                 (5, 1, 12, 64, 64), (1, 3, 2, 17, 10), (2, 2, 3, 512, 512), (1, 2, 7, 40, 8), (700, 1, 20, 64, 48),
+                 (1, 2600, 12, 64, 16)]
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("dt", [BF, F32, F64], ids=str)
+@pytest.mark.parametrize("shape", ROTARY_SHAPES, ids=str)
+def test_rotary(shape, dt, layout):
+    B, T, H, dh, width = shape
+    x = rand(B, T, H, dh, seed=1, dtype=dt)
+    f = api.rotary_frequencies(width, device=DEV)
+    check_rotary(x, f, layout=layout)
+    pos = torch.randint(-1000, 5000, (B, T), generator=torch.Generator().manual_seed(3), dtype=torch.int32).to(DEV)
+    check_rotary(x, f, pos, layout, 1.25)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("dt", [BF, F32], ids=str)
+def test_rotary_at_far_positions(dt, layout):
+    x = rand(1, 6, 3, 64, seed=2, dtype=dt)
+    for f in (api.rotary_frequencies(64, device=DEV), api.rotary_frequencies(64, 500000.0, factor=8, trained=8192, device=DEV),
+              torch.tensor([7.0, -3.0, 6.283185307179586, 0.0, 1e3, -1e-3], dtype=F64, device=DEV)):
+        pos = ints([[0, -1, 1 << 20, -(1 << 24) + 1, (1 << 31) - 1, -(1 << 31)]])
+        # the reference's own angle: p f 2^-53, and as much for f / 2 pi
+        y, w = rotary_ref(x, f, pos, layout)
+        a = pos.double().abs()[:, :, None, None] * f.abs().max() * 2.0 ** -51
+        close(api.rotary(x, f, positions=pos, layout=layout), y, rotary_tol(y, w, dt, f, pos) + w * a)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("dt", [BF, F32, F64], ids=str)
+def test_rotary_layouts_in_place_and_unaligned(dt, layout):
+    B, T, H, dh = 3, 10, 4, 64
+    f = api.rotary_frequencies(48, device=DEV)
+    qkv = rand(B, T, H + 4, dh, seed=4, dtype=dt)
+    for x in (qkv[:, :, 1:1 + H], rand(B, H, T, dh, seed=5, dtype=dt).transpose(1, 2), qkv[:, :, :1].expand(-1, -1, H, -1),
+              rand(T, B, H, dh, seed=6, dtype=dt).transpose(0, 1), rand(B * T * H * dh + 1, seed=7, dtype=dt)[1:].view(B, T, H, dh),
+              rand(B, T, H, dh + 3, seed=8, dtype=dt)[..., :dh]):
+        got = check_rotary(x, f, layout=layout)
+        assert got.is_contiguous()
+        shifted = torch.empty(x.numel() + 1, dtype=dt, device=DEV)[1:].view(x.shape)
+        assert same(check_rotary(x, f, layout=layout, out=shifted), got) and same(shifted, got)
+    ref = check_rotary(qkv[:, :, 1:1 + H], f, layout=layout)
+    whole = qkv.clone()
+    view = qkv[:, :, 1:1 + H]
+    assert api.rotary(view, f, layout=layout, out=view) is view
+    assert same(view, ref) and same(qkv[:, :, 0], whole[:, :, 0]) and same(qkv[:, :, 1 + H:], whole[:, :, 1 + H:])
+
+
+def test_rotary_frequencies():
+    """By parts: pairs that turn often within the trained length keep their frequency, slow ones are stretched."""
+    f = api.rotary_frequencies(64)
+    assert f.dtype == F64 and f.shape == (32,) and f[0] == 1
+    assert torch.allclose(f, torch.tensor([10000.0 ** (-2 * i / 64) for i in range(32)], dtype=F64), rtol=1e-14)
+    assert torch.allclose(api.rotary_frequencies(64, factor=4), f / 4, rtol=1e-14)
+    g = api.rotary_frequencies(64, factor=4, trained=4096)
+    turns = 4096 * f / (2 * math.pi)
+    assert torch.equal(g[turns > 32], f[turns > 32]) and torch.allclose(g[turns < 1], f[turns < 1] / 4, rtol=1e-14)
+    mid = (turns > 1) & (turns < 32)
+    assert mid.any() and ((g[mid] < f[mid]) & (g[mid] > f[mid] / 4)).all()
+    for bad in (dict(width=0), dict(width=3), dict(width=8, factor=0), dict(width=8, slow=2, fast=1)):
+        with pytest.raises(ValueError):
+            api.rotary_frequencies(**bad)
+
+
+# ------------------------------------------------------------------------------ the cache
+def pool(pages, page, Hkv, dh, dt, fill=math.nan):
+    """(keys, values), contiguous pools with `fill` everywhere."""
+    return [torch.full((pages, page, Hkv, dh), fill, dtype=dt, device=DEV) for _ in range(2)]
+
+
+def tables(held, page, spare=1, seed=0, width=None):
+    """A page table for sequences with `held` keys each, pages in no order; entries behind them are rubbish. And the pages
+    that the pool needs."""
+    need = [-(-n // page) for n in held]
+    total = sum(need) + spare
+    order = torch.randperm(total, generator=torch.Generator().manual_seed(seed)).tolist()
+    width = max(max(need), 1) + 1 if width is None else width
+    t = torch.full((len(held), width), 1 << 30, dtype=torch.int32)
+    t[:, 1::2] = -5
+    at = 0
+    for b, n in enumerate(need):
+        t[b, :n] = torch.tensor(order[at:at + n], dtype=torch.int32)
+        at += n
+    return t.to(DEV), total
+
+
+def slots(table, b, u, page):
+    return int(table[b, u // page]), u % page
+
+
+def append_ref(k, v, kp, vp, table, starts, lens, f, pos, layout, scale):
+    """(keys, values) pools in 64 bits, and what the keys' errors go by."""
+    k64, w = (k.double(), torch.zeros_like(k, dtype=F64)) if f is None else rotary_ref(k, f, pos, layout, scale)
+    kp, vp, wp = kp.double(), vp.double(), torch.zeros_like(kp, dtype=F64)
+    P, page = kp.shape[:2]
+    t = table.cpu()
+    for b in range(k.shape[0]):
+        for i in range(k.shape[1] if lens is None else max(0, min(int(lens[b]), k.shape[1]))):
+            u = int(starts[b]) + i
+            if u < 0 or u >= t.shape[1] * page:
+                continue
+            pg, s = slots(t, b, u, page)
+            if 0 <= pg < P:
+                kp[pg, s], vp[pg, s], wp[pg, s] = k64[b, i], v[b, i].double(), w[b, i]
+    return kp, vp, wp
+
+
+def check_append(k, v, q, page, starts, lens=None, f=None, pos=None, layout=0, scale=1.0, table=None, pages=None, pools=None, **kw):
+    B, T, Hkv, dh = k.shape
+    dt = k.dtype
+    if table is None:
+        table, pages = tables([s + T for s in starts], page)
+    kp, vp = pools or pool(pages, page, Hkv, dh, dt)
+    starts = ints(starts)
+    p = starts.long()[:, None] + torch.arange(T, device=DEV) if pos is None else pos   # past 32 bits too
+    rk, rv, w = append_ref(k, v, kp, vp, table, starts, lens, f, p, layout, scale)
+    got = api.cache_append(k, v, kp, vp, table, starts, lens=lens, q=q, frequencies=f, positions=pos, layout=layout, scale=scale, **kw)
+    pp = torch.zeros((1, 1), dtype=torch.int32, device=DEV) if f is None else p.abs().max()[None, None]
+    close(kp, rk, rotary_tol(rk, w, dt, f if f is not None else torch.zeros(1, dtype=F64, device=DEV), pp))
+    assert torch.equal(vp.double().nan_to_num(7.0), rv.nan_to_num(7.0))
+    if q is None:
+        assert got is None
+    elif f is None:
+        assert same(got, q)
+    else:
+        y, w = rotary_ref(q, f, p, layout, scale)
+        close(got, y, rotary_tol(y, w, dt, f, p))
+    return got, kp, vp
+
+
+APPEND_SHAPES = [(1, 1, 1, 1, 2, 2, 1), (3, 1, 16, 16, 64, 64, 16), (2, 5, 16, 2, 128, 128, 64), (2, 37, 12, 4, 80, 40, 16),
+                 (4, 3, 6, 3, 17, 10, 5), (1, 300, 4, 4, 64, 64, 32), (64, 1, 12, 3, 96, 96, 128), (2, 9, 0, 2, 64, 32, 7)]
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("dt", [BF, F32, F64], ids=str)
+@pytest.mark.parametrize("shape", APPEND_SHAPES, ids=str)
+def test_cache_append(shape, dt, layout):
+    B, T, H, Hkv, dh, width, page = shape
+    k, v = rand(B, T, Hkv, dh, seed=1, dtype=dt), rand(B, T, Hkv, dh, seed=2, dtype=dt)
+    q = rand(B, T, H, dh, seed=3, dtype=dt) if H else None
+    f = api.rotary_frequencies(width, device=DEV)
+    starts = [(7 * b) % 40 for b in range(B)]
+    check_append(k, v, q, page, starts, f=f, layout=layout)
+    lens = ints([(T * (b + 1)) // B - (b == 1) for b in range(B)])
+    pos = torch.randint(0, 900, (B, T), generator=torch.Generator().manual_seed(3), dtype=torch.int32).to(DEV)
+    check_append(k, v, q, page, starts, lens=lens, f=f, pos=pos, layout=layout, scale=0.9)
+    check_append(k, v, q, page, starts)   # nothing turned
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=str)
+def test_cache_append_keeps_to_its_slots(dt):
+    """Absent pages, slots outside the table, lengths outside [0, T]: nothing of those is written."""
+    B, T, Hkv, dh, page = 6, 9, 2, 64, 4
+    k, v, q = (rand(B, T, h, dh, seed=i, dtype=dt) for i, h in ((1, Hkv), (2, Hkv), (3, 4)))
+    f = api.rotary_frequencies(64, device=DEV)
+    table, pages = tables([24] * B, page, spare=3, width=6)
+    table[0, 1], table[0, 2], table[1, 0], table[2, 5] = -1, pages, -(1 << 31), (1 << 31) - 1
+    lens = ints([9, 9, 20, -3, 0, 9])
+    check_append(k, v, q, page, [2, 0, 18, 3, 1, 22], lens=lens, f=f, table=table, pages=pages)
+    check_append(k, v, q, page, [-4, 23, 24, 1 << 30, (1 << 31) - 1, -(1 << 31)], f=f, table=table, pages=pages)
+
+
+@pytest.mark.parametrize("dt", [BF, F32, F64], ids=str)
+def test_cache_append_layouts(dt):
+    """A fused projection's parts, pools side by side in a page and heads before tokens, queries turned where they lie."""
+    B, T, H, Hkv, dh, page = 2, 11, 4, 2, 64, 16
+    qkv = rand(B, T, H + 2 * Hkv, dh, seed=1, dtype=dt)
+    q, k, v = qkv[:, :, :H], qkv[:, :, H:H + Hkv], qkv[:, :, H + Hkv:]
+    f = api.rotary_frequencies(64, device=DEV)
+    table, pages = tables([30, 30], page)
+    ref, kp, vp = check_append(k, v, q, page, [19, 3], f=f, table=table, pages=pages)
+    side = torch.full((pages, 2, page, Hkv, dh), math.nan, dtype=dt, device=DEV)
+    heads = torch.full((2, pages, Hkv, page, dh), math.nan, dtype=dt, device=DEV).transpose(2, 3)
+    odd = torch.full((2, pages, page, Hkv, dh + 1), math.nan, dtype=dt, device=DEV)[..., :dh]
+    for pools in ((side[:, 0], side[:, 1]), (heads[0], heads[1]), (odd[0], odd[1])):
+        got, a, b = check_append(k, v, q, page, [19, 3], f=f, table=table, pages=pages, pools=pools)
+        assert same(got, ref) and same(a, kp) and same(b, vp)
+    keep = qkv.clone()
+    pools = pool(pages, page, Hkv, dh, dt)
+    assert api.cache_append(k, v, *pools, table, ints([19, 3]), q=q, frequencies=f, q_out=q) is q
+    assert same(q, ref) and same(pools[0], kp) and same(qkv[:, :, H:], keep[:, :, H:])
+    api.cache_append(k[:, :, :1], v[:, :, :1], kp[:, :, :1], vp[:, :, :1], table, ints([19, 3]), frequencies=f)
+    assert same(kp, pools[0])
+
+
+# --------------------------------------------------------------------------- paged attention
+class Held:
+    """Sequences in a paged cache: own[b] keys each (the new ones last), behind prefix[g] keys of their group. Pools hold NaN
+    wherever there is no key."""
+
+    def __init__(self, Tq, H, Hkv, dh, page, own, prefix=(), dt=BF, seed=0, q_lens=None):
+        self.B, self.page, self.own, self.prefix, self.dt = len(own), page, list(own), list(prefix), dt
+        self.q = rand(self.B, Tq, H, dh, seed=seed + 1, dtype=dt)
+        held = self.own + self.prefix
+        table, pages = tables(held, page, seed=seed)
+        self.kp, self.vp = pool(pages, page, Hkv, dh, dt)
+        kv = rand(sum(held) + 1, 2, Hkv, dh, seed=seed + 2, dtype=dt)
+        at, where = 0, []
+        for b, n in enumerate(held):
+            for u in range(0, n, page):
+                m = min(page, n - u)
+                pg = int(table[b, u // page])
+                self.kp[pg, :m], self.vp[pg, :m] = kv[at + u:at + u + m, 0], kv[at + u:at + u + m, 1]
+            where.append((at, n))
+            at += n
+        self.k, self.v, self.where = kv[:, 0], kv[:, 1], where
+        self.table = table[:self.B].contiguous()
+        self.prefix_table = table[self.B:].contiguous() if prefix else None
+        self.kv_lens, self.prefix_lens = ints(self.own), ints(self.prefix) if prefix else None
+        self.q_lens = None if q_lens is None else ints(q_lens)
+
+    def keys(self, b):
+        """Rows of k and v that sequence b holds: (prefix, own)."""
+        g = b // (self.B // len(self.prefix)) if self.prefix else None
+        r = [torch.arange(a, a + n) for a, n in ([self.where[self.B + g]] if self.prefix else [(0, 0)]) + [self.where[b]]]
+        return r
+
+    def ref(self, scale, gone=()):
+        """(o, sums of w |v|, largest sum |q||k| times |scale|, keys seen) in 64 bits; gone: (sequence, first, last) of own
+        keys that are absent."""
+        B, Tq, H, dh = self.q.shape
+        Hkv = self.k.shape[1]
+        G = H // Hkv
+        out = [torch.zeros(B, Tq, H, n, dtype=F64, device=DEV) for n in (dh, dh, 1, 1)]
+        for b in range(B):
+            pre, mine = self.keys(b)
+            idx = torch.cat([pre, mine]).to(DEV)
+            new = Tq if self.q_lens is None else max(0, min(Tq, int(self.q_lens[b])))
+            if not new or not len(idx):
+                continue
+            k, v = self.k[idx].double(), self.v[idx].double()
+            u = torch.arange(len(idx), device=DEV) - len(pre)
+            see = u < (self.own[b] - new + 1 + torch.arange(new, device=DEV))[:, None]
+            see = see | (u < 0)
+            for s, a, e in gone:
+                if s == b:
+                    see &= ~((u >= a) & (u < e))
+            q = self.q[b, :new].double().reshape(new, Hkv, G, dh)
+            x = torch.einsum("thgd,khd->thgk", q, k) * scale
+            live = see[:, None, None, :]
+            p = torch.softmax(x.masked_fill(~live, -math.inf), 3).masked_fill(~live.any(3, keepdim=True), 0.0)
+            mag = (torch.einsum("thgd,khd->thgk", q.abs(), k.abs()) * abs(scale)).masked_fill(~live, 0).amax(3)
+            out[0][b, :new] = torch.einsum("thgk,khd->thgd", p, v).reshape(new, H, dh)
+            out[1][b, :new] = torch.einsum("thgk,khd->thgd", p, v.abs()).reshape(new, H, dh)
+            out[2][b, :new] = mag.reshape(new, H, 1)
+            out[3][b, :new] = live.sum(3).expand(-1, Hkv, G).reshape(new, H, 1).double()
+        return out
+
+    def call(self, scale=None, **kw):
+        a = dict(q=self.q, k_pages=self.kp, v_pages=self.vp, page_table=self.table, kv_lens=self.kv_lens, q_lens=self.q_lens,
+                 prefix_table=self.prefix_table, prefix_lens=self.prefix_lens, scale=scale)
+        return api.paged_attention(**(a | kw))
+
+
+def paged_tol(h, o, w, mag, n, dh):
+    dt = h.dt
+    u = 2.0 ** -53 if dt == F64 else U
+    es = 2 * u * (dh + 4) * mag
+    tol = (2 * es + 2 * u * (n + 8) + (0 if dt == F64 else 2.0 ** -19)) * w + HALF[dt] * o.abs() * 1.01
+    return tol + 2.0 ** -8 * w if dt == BF else tol
+
+
+def check_paged(h, scale=None, gone=(), **kw):
+    dh = h.q.shape[3]
+    o, w, mag, n = h.ref(dh ** -0.5 if scale is None else scale, gone)
+    got = h.call(scale, **kw)
+    close(got, o, paged_tol(h, o, w, mag, n, dh))
+    return got
+
+
+# Tq, H, Hkv, dh, page, own, prefix
+PAGED_SHAPES = [
+    (1, 1, 1, 64, 16, [1], []), (1, 3, 3, 64, 16, [5, 17], []), (1, 4, 2, 64, 32, [127, 1, 300], []),
+    (1, 16, 16, 64, 16, [128, 577, 3, 290], []), (1, 16, 2, 128, 64, [1000, 63], []), (1, 2, 1, 96, 128, [4000], []),
+    (3, 6, 3, 64, 16, [63, 3, 100], []), (2, 8, 4, 72, 16, [200, 2], []), (4, 12, 3, 80, 64, [300, 64], []),
+    (17, 4, 1, 64, 16, [17, 90], []), (33, 3, 3, 64, 32, [577, 33], []), (100, 15, 5, 96, 16, [100, 140], []),
+    (128, 4, 4, 128, 64, [128, 500], []), (129, 8, 2, 64, 128, [385, 129], []), (300, 4, 4, 80, 16, [300], []),
+    (260, 2, 1, 128, 256, [1025, 260], []), (513, 6, 2, 96, 32, [700], []), (150, 6, 2, 64, 48, [3000], []),
+    (1, 4, 4, 64, 16, [1, 9, 30, 17], [100]), (1, 16, 2, 128, 64, [70, 1, 33, 5, 129, 64], [257, 1000]),
+    (1, 16, 16, 64, 16, [20] * 32, [1025]), (3, 16, 2, 128, 64, [30, 3, 577, 70], [700, 200]),
+    (2, 12, 4, 80, 32, [5, 2, 60], [33, 1, 500]), (5, 8, 2, 64, 16, [5] * 16, [2000]), (40, 3, 3, 64, 16, [40, 77, 41], [130]),
+    (16, 4, 2, 96, 16, [16] * 9, [385]), (150, 4, 4, 80, 32, [150, 200], [600]), (260, 6, 2, 128, 64, [260, 300], [1000, 64]),
+    (1, 6, 2, 64, 16, [0, 4, 0], [50]), (3, 5, 5, 64, 16, [3, 3], [1]),
+    # what the fast forms do not take: pages, widths
+    (1, 4, 2, 64, 1, [5, 30], [7]), (2, 4, 2, 64, 20, [45, 2], [30]), (9, 4, 4, 40, 16, [40, 9], [20]), (3, 2, 1, 33, 8, [50], []),
+    (2, 4, 1, 160, 16, [40, 2], [50]), (2, 2, 2, 300, 16, [40, 2], []), (20, 2, 1, 512, 16, [70], [33]),
+]
+
+
+@pytest.mark.parametrize("dt", [BF, F32, F64], ids=str)
+@pytest.mark.parametrize("shape", PAGED_SHAPES, ids=str)
+def test_paged_attention(shape, dt):
+    Tq, H, Hkv, dh, page, own, prefix = shape
+    h = Held(Tq, H, Hkv, dh, page, own, prefix, dt=dt)
+    got = check_paged(h)
+    assert same(h.call(), got)
+
+
+@pytest.mark.parametrize("prefix", [[], [90], [90, 5], [600], [1300, 64]])
+@pytest.mark.parametrize("Tq,H,Hkv,dh", [(3, 4, 2, 64), (4, 16, 4, 128), (40, 4, 4, 64), (70, 6, 2, 80), (300, 2, 1, 64)])
+def test_paged_attention_of_ragged_queries(Tq, H, Hkv, dh, prefix):
+    """Lengths of zero and one, more new tokens than keys, lengths outside their range; rows behind are zeros."""
+    own = [Tq, 1, 0, 400, Tq + 1, 2, 77, 130]
+    lens = [Tq, 1, 0, Tq // 2, 1, min(Tq, 3), Tq // 3, 0]
+    for dt in (BF, F32):
+        h = Held(Tq, H, Hkv, dh, 16, own, prefix, dt=dt, q_lens=lens)
+        got = check_paged(h)
+        for b, n in enumerate(lens):
+            assert (got[b, n:] == 0).all()
+        more = ints([n + 9 if n == Tq else n or -4 for n in lens])
+        assert same(h.call(q_lens=more), got)
+        many = h.kv_lens.clone()
+        many[2] = -7
+        assert same(h.call(kv_lens=many), got)
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=str)
+@pytest.mark.parametrize("Tq,H,Hkv,dh,page", [(1, 4, 2, 64, 16), (2, 8, 2, 128, 64), (40, 4, 4, 64, 16), (200, 4, 2, 80, 32), (3, 2, 2, 64, 12)])
+def test_paged_attention_lengths_past_the_table(Tq, H, Hkv, dh, page, dt):
+    own = [page * 9, page * 9]
+    h = Held(Tq, H, Hkv, dh, page, own, [page * 5], dt=dt)
+    h.table, h.prefix_table = h.table[:, :9].contiguous(), h.prefix_table[:, :5].contiguous()
+    got = check_paged(h)
+    assert same(h.call(kv_lens=ints([1 << 30, (1 << 31) - 1]), prefix_lens=ints([page * 5 + 1])), got)
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=str)
+@pytest.mark.parametrize("Tq,H,Hkv,dh,page", [(1, 4, 2, 64, 16), (2, 8, 2, 128, 64), (4, 16, 4, 96, 32), (40, 4, 4, 64, 16),
+                                              (200, 4, 2, 80, 32), (130, 2, 2, 128, 128), (300, 2, 2, 64, 16), (3, 2, 2, 64, 12)])
+def test_paged_attention_does_not_see_absent_pages(Tq, H, Hkv, dh, page, dt):
+    """Pages dropped from the front, the middle and the whole of a sequence, and all of a prefix."""
+    own = [800, 500, 300]
+    for prefix in ([], [400]):
+        h = Held(Tq, H, Hkv, dh, page, own, prefix, dt=dt)
+        P = h.kp.shape[0]
+        last = 300 // page   # pages of the last sequence, all of them
+        h.table[0, 0], h.table[0, 3], h.table[0, 4] = -1, P, -(1 << 31)
+        h.table[1, 500 // page - 1] = (1 << 31) - 1
+        h.table[2, :last + 1] = -1
+        gone = [(0, 0, page), (0, 3 * page, 5 * page), (1, (500 // page - 1) * page, 500 // page * page), (2, 0, 300)]
+        check_paged(h, gone=gone)
+        if prefix:
+            h.prefix_table[:] = -1
+            h.prefix = []
+            o, w, mag, n = h.ref(dh ** -0.5, gone)
+            got = h.call()
+            close(got, o, paged_tol(h, o, w, mag, n, dh))
+            assert (got[2] == 0).all()
+
+
+@pytest.mark.parametrize("dt", [BF, F32, F64], ids=str)
+@pytest.mark.parametrize("Tq,H,Hkv,dh,page", [(1, 4, 2, 64, 16), (3, 8, 2, 128, 64), (40, 4, 4, 64, 16), (200, 4, 2, 80, 32)])
+def test_paged_attention_layouts(Tq, H, Hkv, dh, page, dt):
+    """Queries in a fused projection, tokens or heads first; pools side by side in a page, heads before tokens, unaligned."""
+    B = 4
+    h = Held(Tq, H, Hkv, dh, page, [Tq + 70 * b for b in range(B)], [300, 33], dt=dt)
+    ref = check_paged(h)
+    P = h.kp.shape[0]
+    wide = torch.full((B, Tq, H + 3, dh), math.nan, dtype=dt, device=DEV)
+    wide[:, :, 1:1 + H] = h.q
+    early = torch.empty(Tq, B, H, dh, dtype=dt, device=DEV).transpose(0, 1).copy_(h.q)
+    heads = torch.empty(B, H, Tq, dh, dtype=dt, device=DEV).transpose(1, 2).copy_(h.q)
+    off = torch.empty(h.q.numel() + 1, dtype=dt, device=DEV)[1:].view(h.q.shape).copy_(h.q)
+    tol = 2.0 ** -7 if dt == BF else 2.0 ** -16
+    for q in (wide[:, :, 1:1 + H], early, heads, off):
+        close(h.call(q=q), ref.double(), tol * (ref.double().abs() + 0.1))
+    side = torch.empty(P, 2, page, Hkv, dh, dtype=dt, device=DEV)
+    inner = torch.empty(2, P, Hkv, page, dh, dtype=dt, device=DEV).transpose(2, 3)
+    odd = torch.empty(2, P, page, Hkv, dh + 1, dtype=dt, device=DEV)[..., :dh]
+    for kp, vp in ((side[:, 0], side[:, 1]), (inner[0], inner[1]), (odd[0], odd[1])):
+        kp.copy_(h.kp)
+        vp.copy_(h.vp)
+        close(h.call(k_pages=kp, v_pages=vp), ref.double(), tol * (ref.double().abs() + 0.1))
+    out = torch.full((ref.numel() + 1,), math.nan, dtype=dt, device=DEV)[1:].view(ref.shape)
+    assert h.call(out=out) is out
+    close(out, ref.double(), tol * (ref.double().abs() + 0.1))
+
+
+SPECIAL = [(1, 4, 2, 64, [300, 70], []), (3, 8, 2, 128, [400, 9], [500]), (1, 16, 16, 64, [30] * 20, [700]), (40, 4, 4, 64, [300, 70], [200]),
+           (200, 4, 2, 80, [400, 250], []), (200, 2, 2, 128, [250, 200], [400])]
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=str)
+@pytest.mark.parametrize("Tq,H,Hkv,dh,own,prefix", SPECIAL)
+def test_paged_attention_special_scores(Tq, H, Hkv, dh, own, prefix, dt):
+    h = Held(Tq, H, Hkv, dh, 16, own, prefix, dt=dt)
+    check_paged(h, scale=0.0)
+    check_paged(h, scale=-0.3)
+    check_paged(h, scale=3.0)
+    # one key's scores of minus infinity carry no weight
+    pg, s = slots(h.table, 0, 2, 16)
+    h.q = h.q.abs() + 0.01
+    keep = h.kp.clone()
+    h.kp[pg, s] = -math.inf
+    o, w, mag, n = h.ref(dh ** -0.5, [(0, 2, 3)])
+    close(h.call(), o, (2.0 ** -7 if dt == BF else 2.0 ** -16) * w)
+    # nothing else: zeros
+    if not prefix:
+        h.kp.copy_(torch.where(torch.isnan(keep), keep, -math.inf))
+        assert (h.call() == 0).all()
+    # a key that is not a number spoils the rows of its sequence and head that see it, no others
+    h.kp.copy_(keep)
+    ref = h.call()
+    h.kp[pg, s, 0] = math.nan
+    got = h.call()
+    G = H // Hkv
+    sees = torch.arange(Tq, device=DEV) + own[0] - Tq >= 2
+    assert torch.isnan(got[0, sees, :G]).all() and same(got[1:], ref[1:]) and same(got[0, :, G:], ref[0, :, G:])
+    assert same(got[0, ~sees], ref[0, ~sees])
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=str)
+@pytest.mark.parametrize("Tq,H,Hkv,dh,own,prefix", [(4, 4, 2, 64, [90, 4], []), (3, 8, 2, 128, [400, 9], [500]), (40, 4, 4, 64, [300, 40], [200]),
+                                                    (200, 4, 2, 80, [400, 250], []), (200, 2, 2, 128, [250, 200], [400])])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_paged_attention_later_tokens_do_not_reach_earlier_ones(Tq, H, Hkv, dh, own, prefix, dt, value):
+    """The key and value of a sequence's newest token are seen by its last query alone, whatever they hold."""
+    h = Held(Tq, H, Hkv, dh, 16, own, prefix, dt=dt)
+    ref = h.call()
+    for b, n in enumerate(own):
+        pg, s = slots(h.table, b, n - 1, 16)
+        h.vp[pg, s] = value
+    got = h.call()
+    assert same(got[:, :-1], ref[:, :-1]) and not torch.isfinite(got[:, -1]).any()
+    for b, n in enumerate(own):
+        pg, s = slots(h.table, b, n - 1, 16)
+        h.kp[pg, s] = value
+    got = h.call()
+    assert same(got[:, :-1], ref[:, :-1]) and not torch.isfinite(got[:, -1]).any()
+
+
+@pytest.mark.parametrize("scale", [1e9, 7e17, 1e30])
+@pytest.mark.parametrize("dt", [BF, F32, F64], ids=str)
+@pytest.mark.parametrize("Tq,H,Hkv,dh,own,prefix", SPECIAL)
+def test_paged_attention_of_large_scores(Tq, H, Hkv, dh, own, prefix, dt, scale):
+    """Queries and keys of small whole numbers have exact scores, and differences of 1 leave no weight: the mean of the
+    values under the largest score, the weights all exactly 1."""
+    h = Held(Tq, H, Hkv, dh, 16, own, prefix, dt=dt)
+    whole = [t.float().round().clamp(-2, 2).to(dt) for t in (h.q, h.kp, h.k)]
+    h.q, h.kp, h.k = whole
+    for sc in (scale, -scale):
+        o, w, _, n = h.ref(sc)
+        tol = (2 * U * (n + 8) + (2.0 ** -20 if dt == F32 else 0)) * w + HALF[dt] * o.abs() * 1.01
+        close(h.call(sc), o, tol)
+
+
+def inside(shape, dt, lead, fn):
+    """fn(out) with out a contiguous tensor between two margins; nothing outside it changes."""
+    n = math.prod(shape) * torch.empty(0, dtype=dt).element_size()
+    buf = torch.full((lead + n + 4096,), 0x5A, dtype=torch.uint8, device=DEV)
+    fn(buf[lead:lead + n].view(dt).view(shape))
+    assert (buf[:lead] == 0x5A).all() and (buf[lead + n:] == 0x5A).all()
+
+
+@pytest.mark.parametrize("lead", [4096, 4104])
+def test_nothing_outside_the_outputs_is_written(lead):
+    for dt in (BF, F32):
+        x, f = rand(3, 7, 5, 80, dtype=dt), api.rotary_frequencies(64, device=DEV)
+        inside(tuple(x.shape), dt, lead, lambda t: api.rotary(x, f, out=t))
+        for Tq, H, Hkv, dh, own, prefix in SPECIAL + [(131, 6, 2, 64, [140, 131], []), (37, 5, 1, 128, [37, 90], [64]), (7, 3, 3, 40, [9], [])]:
+            h = Held(Tq, H, Hkv, dh, 16, own, prefix, dt=dt)
+            inside(tuple(h.q.shape), dt, lead, lambda t: h.call(out=t))
+
+
+@pytest.mark.parametrize("dt,Tq,dh", [(BF, 1, 64), (BF, 150, 128), (F32, 1, 64), (BF, 4, 64), (BF, 20, 72)], ids=str)
+def test_pools_past_32_bit_offsets(dt, Tq, dh):
+    """Pages, or tokens, that lie more than 2^32 elements apart: appended to, and read."""
+    Hkv, page = 2, 16
+    for strides in (((1 << 32) + 64, Hkv * dh, dh), (Hkv * dh, 1 << 29, dh)):
+        span = 2 * strides[0] + 15 * strides[1] + Hkv * dh
+        buf = torch.empty(span, dtype=dt, device=DEV)
+        far = buf.as_strided((3, page, Hkv, dh), strides + (1,))
+        far.fill_(math.nan)
+        h = Held(Tq, 4, Hkv, dh, page, [40], dt=dt) if Tq < 40 else Held(Tq, 4, Hkv, dh, page, [160], dt=dt)
+        P = h.kp.shape[0]
+        near = [pool(3, page, Hkv, dh, dt)[0] for _ in range(2)]
+        k, v = rand(1, 40, Hkv, dh, seed=1, dtype=dt), rand(1, 40, Hkv, dh, seed=2, dtype=dt)
+        f, table = api.rotary_frequencies(dh, device=DEV), ints([[2, 0, 1]])
+        q = rand(1, min(Tq, 40), 4, dh, seed=3, dtype=dt)
+        for i in range(2):   # the far pool as keys, as values
+            far.fill_(math.nan)
+            other = near[1].clone()
+            a = (far, other) if i == 0 else (other, far)
+            b = (near[0].clone(), near[1].clone())
+            for pools in (a, b):
+                api.cache_append(k, v, *pools, table, ints([0]), frequencies=f)
+            assert same(a[0], b[0]) and same(a[1], b[1])
+            got = [api.paged_attention(q, *pools, table, ints([40])) for pools in (a, b)]
+            assert same(*got) and torch.isfinite(got[0]).all()
+        del buf, far
+
+
+def test_outputs_past_32_bit_offsets():
+    T, n = 1 << 20, 4096
+    x = torch.empty(1, T + 600, 16, 256, dtype=BF, device=DEV).normal_()
+    f = api.rotary_frequencies(256, device=DEV)
+    pos = torch.arange(T + 600, dtype=torch.int32, device=DEV)[None]
+    got = api.rotary(x, f)
+    assert same(got[:, -n:], api.rotary(x[:, -n:], f, positions=pos[:, -n:].contiguous()))
+    del got
+    x = x.view(1, -1, 32, 128)[:, :T + 600]
+    # rows that see 600 keys at most; the last ones alone, with the same keys, see the same
+    h = Held(1, 32, 2, 128, 64, [600])
+    got = h.call(q=x)
+    assert same(got[:, -600:], h.call(q=x[:, -600:])) and (got[:, :-600] == 0).all()
+
+
+@pytest.mark.parametrize("B", [37, 200])
+def test_paged_attention_of_many_ragged_sequences(B):
+    """More work than one round of CTAs, sequences in any order of length, empty ones among them."""
+    g = torch.Generator().manual_seed(B)
+    own = torch.randint(0, 400, (B,), generator=g).tolist()
+    for Tq, prefix in ((1, []), (140, []), (140, [200]), (20, [300]), (2, [300])):
+        lens = [min(n, Tq, 1 + i % Tq) for i, n in enumerate(own)]
+        check_paged(Held(Tq, 6, 3, 64, 16, own, prefix, q_lens=lens))
+
+
+@pytest.mark.parametrize("Tq,H,Hkv,dh", [(1, 4, 2, 64), (2, 16, 2, 128), (100, 4, 2, 64), (260, 2, 2, 96)])
+def test_paged_attention_where_keys_are_dealt_out(Tq, H, Hkv, dh):
+    """Few rows over many keys: parts go to different CTAs, some of them, or all but one key, without any."""
+    for own, prefix in (([5000], []), ([Tq, 4000], []), ([Tq, Tq, Tq], [6000]), ([300, Tq, 2000], [1, 129, 3000])):
+        h = Held(Tq, H, Hkv, dh, 64, own, prefix)
+        got = check_paged(h)
+        for _ in range(3):
+            assert same(h.call(), got)
+
+
+# ------------------------------------------------------------------------------- together
+def step(p, x, kp, vp, table, starts, kv_lens, f, H, Hkv, lens=None, positions=None, before=None, out=None):
+    """The self attention of a decoder's layer on new tokens x (B, T, D): projection, rotation and append, attention."""
+    B, T, D = x.shape
+    dh = D // H
+    q8, qs = api.rmsnorm(x, 1e-6, gamma=p["g"], out_dtype=torch.float8_e4m3fn)
+    qkv = api.linear_fp8(q8, qs, *p["wqkv"]).view(B, T, H + 2 * Hkv, dh)
+    q = api.cache_append(qkv[:, :, H:H + Hkv], qkv[:, :, H + Hkv:], kp, vp, table, starts, lens=lens, q=qkv[:, :, :H],
+                         frequencies=f, positions=positions)
+    table_, lens_ = before if before else (None, None)
+    return api.paged_attention(q, kp, vp, table, kv_lens, q_lens=lens, prefix_table=table_, prefix_lens=lens_, out=out)
+
+
+def make_step(D, H, Hkv, seed=0):
+    dh = D // H
+    w = rand(D, (H + 2 * Hkv) * dh, seed=seed + 1, std=D ** -0.5, dtype=BF)
+    return dict(g=1 + rand(D, seed=seed, std=0.1), wqkv=api.quantize_weight(w))
+
+
+@pytest.mark.parametrize("H,Hkv", [(4, 4), (8, 2)])
+def test_tokens_one_by_one_and_in_parts_see_what_the_whole_text_sees(H, Hkv):
+    """A text of 150 tokens at once, in parts of 64, token by token from the 140th, and behind a shared prefix of its
+    first 100 tokens that another page table holds: the same rows, up to what rounding weights and joining parts differ by."""
+    D, page, n = 64 * H, 16, 150
+    p, f, x = make_step(D, H, Hkv), api.rotary_frequencies(64, device=DEV), rand(2, n, D, seed=9, dtype=BF)
+    table, pages = tables([n, n], page)
+
+    def fresh():
+        return pool(pages, page, Hkv, 64, BF)
+
+    kp, vp = fresh()
+    whole = step(p, x, kp, vp, table, ints([0, 0]), ints([n, n]), f, H, Hkv)
+    kp2, vp2 = fresh()
+    got = []
+    for a, b in [(0, 64), (64, 128), (128, 140)] + [(i, i + 1) for i in range(140, n)]:
+        got.append(step(p, x[:, a:b].contiguous(), kp2, vp2, table, ints([a, a]), ints([b, b]), f, H, Hkv))
+    # the same products in another kernel's order of additions can round a key to its neighbour in bf16
+    tol = 2.0 ** -6 * (whole.double().abs() + 0.25)
+    close(torch.cat(got, 1), whole.double(), tol)
+    # one text as a prefix for three continuations
+    kp3, vp3 = fresh()
+    t1 = table[:1].contiguous()
+    step(p, x[:1, :100].contiguous(), kp3, vp3, t1, ints([0]), ints([100]), f, H, Hkv)
+    own, more = tables([50] * 3, page, seed=4)
+    kp3, vp3 = (torch.cat([t, torch.full((more,) + t.shape[1:], math.nan, dtype=BF, device=DEV)]) for t in (kp3, vp3))
+    own = torch.where(own < more, own + pages, own)
+    tail = x[:1, 100:].expand(3, -1, -1).contiguous()
+    pos = torch.arange(100, n, dtype=torch.int32, device=DEV).expand(3, -1).contiguous()
+    got = step(p, tail, kp3, vp3, own, ints([0] * 3), ints([50] * 3), f, H, Hkv, positions=pos, before=(t1, ints([100])))
+    close(got, whole[:1, 100:].double().expand(3, -1, -1, -1), tol[:1, 100:])
+    assert same(got[0], got[1]) and same(got[0], got[2])
+
+
+def test_a_captured_step_replays_on_new_inputs_and_streams_agree():
+    """Two graphs of one decoding step behind a shared prefix, each with a cache of its own, replayed at once."""
+    B, H, Hkv, D, page = 6, 8, 2, 512, 16
+    p, f = make_step(D, H, Hkv), api.rotary_frequencies(64, device=DEV)
+    h = Held(1, H, Hkv, 64, page, [40, 3, 17, 90, 1, 64], [300, 700])
+    x = rand(B, 1, D, seed=30, dtype=BF)
+    starts, lens = h.kv_lens - 1, h.kv_lens.clone()
+    pos = (starts + 700)[:, None].contiguous()
+    args = lambda kp, vp: (p, x, kp, vp, h.table, starts, lens, f, H, Hkv, None, pos, (h.prefix_table, h.prefix_lens))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(*args(h.kp.clone(), h.vp.clone()))
+    torch.cuda.current_stream().wait_stream(side)
+    graphs = []
+    for _ in range(2):
+        kp, vp = h.kp.clone(), h.vp.clone()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            y = step(*args(kp, vp))
+        graphs.append((g, y, kp, vp))
+    for seed in (40, 41):
+        x.copy_(rand(B, 1, D, seed=seed, dtype=BF))
+        kp, vp = graphs[0][2].clone(), graphs[0][3].clone()
+        eager = step(*args(kp, vp))
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in graphs]
+        for _ in range(3):
+            for (g, *_), st in zip(graphs, streams):
+                with torch.cuda.stream(st):
+                    g.replay()
+        torch.cuda.synchronize()
+        for _, y, a, b in graphs:
+            assert same(y, eager) and same(a, kp) and same(b, vp)
+
+
+def test_calls_on_explicit_streams_and_at_once():
+    """Calls that need scratch memory, on three streams in turn without waiting."""
+    hs = [Held(t, 16, 2, 128, 64, [70 + t] * 4, [900], seed=t) for t in (1, 2, 30)]
+    ref = [h.call() for h in hs]
+    x, f = rand(3, 5, 4, 64, dtype=BF), api.rotary_frequencies(64, device=DEV)
+    r = api.rotary(x, f)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in hs]
+    for _ in range(5):
+        got = [h.call(stream=s) for h, s in zip(hs, streams)]
+        z = api.rotary(x, f, stream=streams[0].cuda_stream)
+        torch.cuda.synchronize()
+        assert all(same(a, b) for a, b in zip(got, ref)) and same(z, r)
+    kp, vp = hs[0].kp.clone(), hs[0].vp.clone()
+    k = rand(4, 1, 2, 128, dtype=BF)
+    api.cache_append(k, k, kp, vp, hs[0].table, ints([3] * 4), stream=streams[1])
+    streams[1].synchronize()
+    api.cache_append(k, k, hs[0].kp, hs[0].vp, hs[0].table, ints([3] * 4))
+    assert same(kp, hs[0].kp) and same(vp, hs[0].vp)
+
+
+def test_the_binding_refuses_what_does_not_fit():
+    h = Held(2, 4, 2, 64, 16, [5, 7], [20])
+    x, f = h.q, api.rotary_frequencies(64, device=DEV)
+    k = rand(2, 3, 2, 64, dtype=BF)
+    s, P = ints([0, 0]), h.kp
+    append = lambda **kw: api.cache_append(**(dict(k=k, v=k, k_pages=P, v_pages=h.vp, page_table=h.table, starts=s) | kw))
+    bad = [
+        lambda: api.rotary(x[0], f), lambda: api.rotary(x.half(), f), lambda: api.rotary(x, f.float()), lambda: api.rotary(x, f.cpu()),
+        lambda: api.rotary(x, f, positions=s), lambda: api.rotary(x, f, layout=2), lambda: api.rotary(x, f[:0]), lambda: api.rotary(x, None),
+        lambda: api.rotary(x.transpose(2, 3), f), lambda: api.rotary(x[:0], f), lambda: api.rotary(x, f, out=x[:, :, :2]),
+        lambda: api.rotary(x, f, positions=s[:, None].expand(2, 2)), lambda: api.rotary(x, f[None]),
+        lambda: append(k=k.float()), lambda: append(v=k[:, :2]), lambda: append(k=k[..., :32]), lambda: append(page_table=h.table[:1]),
+        lambda: append(starts=None), lambda: append(starts=s.long()), lambda: append(lens=s[:1]), lambda: append(q_out=x),
+        lambda: append(q=x), lambda: append(v_pages=P[:1]), lambda: append(page_table=h.table.t()), lambda: append(frequencies=f.float()),
+        lambda: append(positions=s), lambda: append(k_pages=P[0]),
+        lambda: h.call(q=x.float()), lambda: h.call(q=x[..., :32]), lambda: h.call(kv_lens=None), lambda: h.call(kv_lens=s.long()),
+        lambda: h.call(prefix_lens=None), lambda: h.call(prefix_table=None), lambda: h.call(prefix_table=h.table.repeat(2, 1)[:3], prefix_lens=ints([1] * 3)),
+        lambda: h.call(q_lens=s[:1]), lambda: h.call(page_table=h.table[0]), lambda: h.call(out=x.float()), lambda: h.call(v_pages=h.vp.float()),
+        lambda: h.call(q=x.cpu()), lambda: h.call(page_table=h.table[:, ::2]),
+    ]
+    for i, fn in enumerate(bad):
+        with pytest.raises(ValueError):
+            fn()
+            raise AssertionError("call %d was taken" % i)
+    for fn in (lambda: api.rotary(x, api.rotary_frequencies(128, device=DEV)),          # wider than the heads
+               lambda: api.rotary(x[:, :, :1].expand(-1, -1, 4, -1), f, out=x[:, :, :1].expand(-1, -1, 4, -1)),   # rows upon each other
+               lambda: api.rotary(x, f, scale=math.nan), lambda: append(v_pages=P),     # one pool for both
+               lambda: append(k=P[:1, :3].expand(2, -1, -1, -1)),                       # out of the pool
+               lambda: append(k_pages=P[:1].expand(P.shape)), lambda: h.call(scale=math.inf), lambda: h.call(out=x),
+               lambda: h.call(q=rand(2, 2, 3, 64, dtype=BF))):                          # 3 heads on 2
+        with pytest.raises(api.VitError):
+            fn()

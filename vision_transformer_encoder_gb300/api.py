@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(_HERE, "libvit_block.so")
 
 VIT_F32, VIT_BF16, VIT_F64, VIT_E4M3 = 0, 1, 2, 3
 EPI_STORE, EPI_GELU, EPI_RESIDUAL = 0, 1, 2
+ROTARY_HALF, ROTARY_INTERLEAVED = 0, 1
 
 _DT = {torch.float32: VIT_F32, torch.bfloat16: VIT_BF16, torch.float64: VIT_F64}
 
@@ -61,6 +62,9 @@ SIGNATURES = {
     "vit_quantize_weight": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _vp]),
     "vit_linear_fp8": (_int, [_vp] * 5 + [_int, _vp, _int] + [_i64] * 3 + [_int, _vp, _int, _vp, _vp]),
     "vit_cross_attention": (_int, [_vp] * 7 + [_i64] * 6 + [_dbl, _int, _vp, _vp]),
+    "vit_rotary": (_int, [_vp] * 4 + [_i64] * 4 + [_int, _vp, _vp]),
+    "vit_cache_append": (_int, [_vp] * 8 + [_i64] + [_vp] * 4 + [_i64] * 3 + [_vp, _vp]),
+    "vit_paged_attention": (_int, [_vp] * 4 + [_i64] + [_vp] * 3 + [_i64, _vp] + [_i64] * 4 + [_dbl, _vp, _vp]),
     "vit_status_string": (ctypes.c_char_p, [_int]),
     "vit_device_error": (_int, [ctypes.POINTER(ctypes.c_uint32)]),
     "vit_launch_count": (_i64, []),
@@ -445,7 +449,7 @@ def attention(qkv, H, out=None, stream=None):
     return out
 
 
-# ---- serving stages: rms norm, 8-bit products, cross attention -------------------------
+# ---- serving stages: rms norm, 8-bit products, cross attention; self attention over a paged cache ----
 # Called once per layer and token, where marshalling in Python costs several times what the
 # kernels take: csrc/binding.cpp checks the tensors, makes the outputs and calls the library.
 
@@ -481,7 +485,8 @@ def _serving():
             raise VitError(status, what)
 
         native.set_entry(on_error, *[ctypes.cast(getattr(lib, name), _vp).value for name in (
-            "vit_rmsnorm", "vit_quantize", "vit_quantize_weight", "vit_linear_fp8", "vit_cross_attention")])
+            "vit_rmsnorm", "vit_quantize", "vit_quantize_weight", "vit_linear_fp8", "vit_cross_attention", "vit_rotary",
+            "vit_cache_append", "vit_paged_attention")])
         _native = native
     return _native
 
@@ -568,6 +573,76 @@ def cross_attention(q, k, v, kv_lens=None, scale=None, out=None, stream=None):
     if stream is None:
         return fn(q, k, v, kv_lens, scale, out)
     return _on(stream, (q, k, v, kv_lens, out), fn, q, k, v, kv_lens, scale, out)
+
+
+def rotary_frequencies(width, base=10000.0, factor=1.0, trained=None, slow=1.0, fast=32.0, device=None):
+    """Frequencies (width / 2) in fp64 for rotary positions of the first `width` columns of a head:
+    base^(-2 i / width) radians per position.
+
+    factor: positions stretched by so much. With `trained`, the length that a model was trained on, by parts: a pair
+    that turns `fast` times within it or more keeps its frequency, one that turns `slow` times or less is divided by
+    factor, those between are mixed linearly in their turns. Without, all are divided."""
+    if width <= 0 or width % 2 != 0:
+        raise ValueError("width must be positive and even, got %r" % (width,))
+    if not factor > 0 or not base > 0 or not fast > slow:
+        raise ValueError("base and factor must be positive, fast above slow")
+    f = torch.pow(torch.tensor(float(base), dtype=torch.float64), -torch.arange(0, width, 2, dtype=torch.float64) / width)
+    keep = torch.zeros_like(f)
+    if trained is not None:
+        keep = ((trained * f / (2 * torch.pi) - slow) / (fast - slow)).clamp(0, 1)
+    return (f * (keep + (1 - keep) / factor)).to(device)
+
+
+def rotary(x, frequencies, positions=None, layout=ROTARY_HALF, scale=1.0, out=None, stream=None):
+    """x (B, T, H, dh) with rotary positions: pair i of the first 2 n columns of each head turned by the
+    angle positions[b, t] * frequencies[i] and multiplied by scale; the other columns as they are.
+
+    frequencies: (n) fp64 on the device (rotary_frequencies). positions: (B, T) int32 on the device; t when not
+    given. layout: ROTARY_HALF pairs columns i and i + n, ROTARY_INTERLEAVED 2 i and 2 i + 1. x may be a view
+    with any strides over sequences, tokens and heads. out: contiguous, or x itself. Returns out."""
+    fn = (_native or _serving()).rotary
+    if stream is None:
+        return fn(x, frequencies, positions, layout, scale, out)
+    return _on(stream, (x, frequencies, positions, out), fn, x, frequencies, positions, layout, scale, out)
+
+
+def cache_append(k, v, k_pages, v_pages, page_table, starts, lens=None, q=None, frequencies=None, positions=None,
+                 layout=ROTARY_HALF, scale=1.0, q_out=None, stream=None):
+    """Puts keys and values k, v (B, T, Hkv, dh) into a paged cache, rotating the keys, and the queries q
+    (B, T, H, dh) alongside. Token t < lens[b] of sequence b becomes key u = starts[b] + t of it, slot u % page of
+    page page_table[b, u // page].
+
+    k_pages, v_pages: (pages, page, Hkv, dh), written in place; views with any strides over pages, tokens and heads.
+    page_table: (B, table_pages) int32; entries outside [0, pages) are absent, and their tokens not kept. starts, lens:
+    (B) int32; all T tokens without lens. frequencies, positions, layout, scale: as rotary; positions are
+    starts[b] + t when not given (behind a prefix, give them), and without frequencies nothing is turned. No two
+    tokens of a call may have the same slot of the same page.
+    Returns the rotated queries, in q_out (contiguous, or q itself) or a new tensor; None without q."""
+    fn = (_native or _serving()).cache_append
+    a = (k, v, k_pages, v_pages, page_table, starts, lens, q, frequencies, positions, layout, scale, q_out)
+    if stream is None:
+        return fn(*a)
+    return _on(stream, (k_pages,) + a[:2] + a[3:10] + (q_out,), fn, *a)
+
+
+def paged_attention(q, k_pages, v_pages, page_table, kv_lens, q_lens=None, prefix_table=None, prefix_lens=None,
+                    scale=None, out=None, stream=None):
+    """Causal attention of the newest tokens q (B, Tq, H, dh) of each sequence over its keys and values in pages, as
+    cache_append leaves them; H / Hkv query heads share a key head. Returns (B, Tq, H, dh).
+
+    Query t of sequence b sees the keys u < kv_lens[b] - (q_lens[b] - 1 - t) of the sequence: kv_lens (B) int32 counts
+    the new tokens in; q_lens (B) int32 says how many those are, Tq when not given. Rows behind them are zeros.
+    page_table: (B, table_pages) int32; keys on absent pages (entries outside [0, pages)) are not seen.
+    prefix_table (groups, prefix_pages) and prefix_lens (groups), int32: keys in front of all those, the same for the
+    B / groups sequences of a group (the first B / groups sequences are the first group), read once for all of
+    them. A row that sees nothing is zeros. scale: 1 / sqrt(dh) by default."""
+    fn = (_native or _serving()).paged_attention
+    if scale is None:
+        scale = (q.shape[-1] or 1) ** -0.5
+    a = (q, k_pages, v_pages, page_table, kv_lens, q_lens, prefix_table, prefix_lens)
+    if stream is None:
+        return fn(*a, scale, out)
+    return _on(stream, a + (out,), fn, *a, scale, out)
 
 
 def device_error() -> int:

@@ -29,6 +29,9 @@ decltype(&vit_quantize) p_quantize;
 decltype(&vit_quantize_weight) p_quantize_weight;
 decltype(&vit_linear_fp8) p_linear_fp8;
 decltype(&vit_cross_attention) p_cross_attention;
+decltype(&vit_rotary) p_rotary;
+decltype(&vit_cache_append) p_cache_append;
+decltype(&vit_paged_attention) p_paged_attention;
 PyObject* g_on_error;   // called with (status, name)
 
 struct Refused : std::exception {
@@ -308,6 +311,157 @@ PyObject* cross_attention(PyObject* const* a) {
     return keep.result(1);
 }
 
+// A tensor (B, T, heads, dh) with elements; its first dimensions as given where those are set (>= 0).
+const void* rows_of(const at::Tensor& t, const char* name, at::ScalarType dt, int64_t dev, int64_t B, int64_t T, int64_t heads,
+                    int64_t dh, int64_t (&st)[3]) {
+    if (t.dim() != 4 || t.numel() == 0) refuse(name, " must have four dimensions and at least one element");
+    const int64_t want[4] = {B, T, heads, dh};
+    for (int i = 0; i < 4; ++i)
+        if (want[i] >= 0 && t.size(i) != want[i])
+            refuse(name, " has shape " + dims(t.sizes()) + ", expected " + std::to_string(want[i]) + " in dimension " + std::to_string(i));
+    return strided(t, name, dt, dev, st);
+}
+
+// A contiguous int32 CUDA tensor of this shape, or none.
+const int32_t* ints(PyObject* o, const char* name, at::IntArrayRef shape, int64_t dev) {
+    return o == Py_None ? nullptr : static_cast<const int32_t*>(fits(tensor(o, name), name, at::kInt, shape, dev));
+}
+
+// (frequencies, layout, scale); null where there are no frequencies
+const vit_rope* rope_of(PyObject* f, PyObject* layout, PyObject* scale, int64_t dev, vit_rope* r) {
+    const int64_t l = integer(layout);
+    if (l != VIT_ROTARY_HALF && l != VIT_ROTARY_INTERLEAVED) refuse("layout", " must be ROTARY_HALF or ROTARY_INTERLEAVED");
+    const double s = number(scale);
+    if (f == Py_None) return nullptr;
+    const at::Tensor& t = tensor(f, "frequencies");
+    if (t.dim() != 1 || t.numel() == 0) refuse("frequencies", " must have one dimension and at least one element");
+    r->frequencies = static_cast<const double*>(fits(t, "frequencies", at::kDouble, t.sizes(), dev));
+    r->n = t.numel();
+    r->layout = (int)l;
+    r->scale = s;
+    return r;
+}
+
+// Where x (B, T, H, dh) goes rotated: into a new tensor, a contiguous one that is given, or x itself.
+void* turned_output(PyObject* given, const char* name, const at::Tensor& x, PyObject** keep) {
+    if (given != Py_None) {
+        const at::Tensor& o = tensor(given, name);
+        if (o.is_cuda() && o.data_ptr() == x.data_ptr() && o.sizes() == x.sizes() && o.strides() == x.strides() &&
+            o.scalar_type() == x.scalar_type()) {
+            Py_INCREF(given);
+            *keep = given;
+            return o.data_ptr();
+        }
+    }
+    return output(given, name, x.scalar_type(), x.sizes(), x, keep);
+}
+
+// ---- (x, frequencies, positions, layout, scale, out)
+PyObject* rotary(PyObject* const* a) {
+    const at::Tensor& x = tensor(a[0], "x");
+    const int code = code_of(x.scalar_type(), false, "x");
+    on_device(x, "x", -1);
+    const int64_t dev = x.get_device();
+    int64_t st[3];
+    const void* xp = rows_of(x, "x", x.scalar_type(), dev, -1, -1, -1, -1, st);
+    vit_rope r;
+    if (!rope_of(a[1], a[3], a[4], dev, &r)) refuse("frequencies", " must be a tensor");
+    const int32_t* pos = ints(a[2], "positions", {x.size(0), x.size(1)}, dev);
+    Kept keep;
+    void* op = turned_output(a[5], "out", x, &keep.o[0]);
+    call("vit_rotary", dev, [&](void* s) {
+        return p_rotary(xp, st, pos, &r, x.size(0), x.size(1), x.size(2), x.size(3), code, op, s);
+    });
+    return keep.result(1);
+}
+
+// The pools k_pages and v_pages (pages, page, heads, dh).
+vit_paged_cache cache_of(const at::Tensor& k, const at::Tensor& v) {
+    vit_paged_cache c;
+    const int code = code_of(k.scalar_type(), false, "k_pages");
+    on_device(k, "k_pages", -1);
+    const int64_t dev = k.get_device();
+    c.k = const_cast<void*>(rows_of(k, "k_pages", k.scalar_type(), dev, -1, -1, -1, -1, c.k_strides));
+    c.v = const_cast<void*>(rows_of(v, "v_pages", k.scalar_type(), dev, k.size(0), k.size(1), k.size(2), k.size(3), c.v_strides));
+    c.pages = k.size(0);
+    c.page = k.size(1);
+    c.heads = k.size(2);
+    c.dh = k.size(3);
+    c.dtype = code;
+    return c;
+}
+
+// A page table (rows, pages per row).
+const int32_t* table_of(PyObject* o, const char* name, int64_t rows, int64_t dev, int64_t* pages) {
+    const at::Tensor& t = tensor(o, name);
+    if (t.dim() != 2 || t.numel() == 0 || (rows >= 0 && t.size(0) != rows))
+        refuse(name, " has shape " + dims(t.sizes()) + ", expected a row of pages for each of " + std::to_string(rows));
+    *pages = t.size(1);
+    return static_cast<const int32_t*>(fits(t, name, at::kInt, t.sizes(), dev));
+}
+
+// ---- (k, v, k_pages, v_pages, table, starts, lens, q, frequencies, positions, layout, scale, q_out)
+PyObject* cache_append(PyObject* const* a) {
+    const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v"), &kp = tensor(a[2], "k_pages"), &vp = tensor(a[3], "v_pages");
+    const vit_paged_cache c = cache_of(kp, vp);
+    const at::ScalarType dt = kp.scalar_type();
+    const int64_t dev = kp.get_device();
+    int64_t ks[3], vs[3], qs[3], pages;
+    const void* k_ = rows_of(k, "k", dt, dev, -1, -1, c.heads, c.dh, ks);
+    const int64_t B = k.size(0), T = k.size(1);
+    const void *v_ = rows_of(v, "v", dt, dev, B, T, c.heads, c.dh, vs), *q_ = nullptr;
+    const int32_t* table = table_of(a[4], "page_table", B, dev, &pages);
+    if (a[5] == Py_None) refuse("starts", " must be a tensor");
+    const int32_t *starts = ints(a[5], "starts", {B}, dev), *lens = ints(a[6], "lens", {B}, dev);
+    vit_rope r;
+    const vit_rope* rope = rope_of(a[8], a[10], a[11], dev, &r);
+    const int32_t* pos = ints(a[9], "positions", {B, T}, dev);
+    Kept keep;
+    void* op = nullptr;
+    int64_t H = 0;
+    if (a[7] != Py_None) {
+        const at::Tensor& q = tensor(a[7], "q");
+        q_ = rows_of(q, "q", dt, dev, B, T, -1, c.dh, qs);
+        H = q.size(2);
+        op = turned_output(a[12], "q_out", q, &keep.o[0]);
+    } else if (a[12] != Py_None) {
+        refuse("q_out", " needs a q");
+    }
+    call("vit_cache_append", dev, [&](void* s) {
+        return p_cache_append(k_, ks, v_, vs, q_, qs, &c, table, pages, starts, lens, rope, pos, B, T, H, op, s);
+    });
+    if (!op) Py_RETURN_NONE;
+    return keep.result(1);
+}
+
+// ---- (q, k_pages, v_pages, table, kv_lens, q_lens, prefix_table, prefix_lens, scale, out)
+PyObject* paged_attention(PyObject* const* a) {
+    const at::Tensor &q = tensor(a[0], "q"), &kp = tensor(a[1], "k_pages"), &vp = tensor(a[2], "v_pages");
+    const vit_paged_cache c = cache_of(kp, vp);
+    const at::ScalarType dt = kp.scalar_type();
+    const int64_t dev = kp.get_device();
+    int64_t qs[3], pages, prefix_pages = 0, groups = 1;
+    const void* q_ = rows_of(q, "q", dt, dev, -1, -1, -1, c.dh, qs);
+    const int64_t B = q.size(0), T = q.size(1), H = q.size(2);
+    const int32_t *table = table_of(a[3], "page_table", B, dev, &pages), *before = nullptr;
+    if (a[4] == Py_None) refuse("kv_lens", " must be a tensor");
+    const int32_t *kv = ints(a[4], "kv_lens", {B}, dev), *ql = ints(a[5], "q_lens", {B}, dev);
+    if ((a[6] == Py_None) != (a[7] == Py_None)) refuse("prefix_table", " and prefix_lens go together");
+    if (a[6] != Py_None) {
+        before = table_of(a[6], "prefix_table", -1, dev, &prefix_pages);
+        groups = tensor(a[6], "prefix_table").size(0);
+        if (B % groups != 0) refuse("prefix_table", " has " + std::to_string(groups) + " rows, which do not divide " + std::to_string(B) + " sequences");
+    }
+    const int32_t* pl = ints(a[7], "prefix_lens", {groups}, dev);
+    const double scale = number(a[8]);
+    Kept keep;
+    void* op = output(a[9], "out", dt, q.sizes(), q, &keep.o[0]);
+    call("vit_paged_attention", dev, [&](void* s) {
+        return p_paged_attention(q_, qs, &c, table, pages, kv, ql, before, prefix_pages, pl, groups, B, T, H, scale, op, s);
+    });
+    return keep.result(1);
+}
+
 template <PyObject* (*F)(PyObject* const*), int N> PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     if (n != N) {
@@ -323,14 +477,14 @@ template <PyObject* (*F)(PyObject* const*), int N> PyObject* entry(PyObject*, Py
     END_HANDLE_TH_ERRORS
 }
 
-// set_entry(on_error, addresses of the five entry points)
+// set_entry(on_error, addresses of the eight entry points)
 PyObject* set_entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
-    if (n != 6) {
-        PyErr_SetString(PyExc_TypeError, "set_entry takes a callable and five addresses");
+    if (n != 9) {
+        PyErr_SetString(PyExc_TypeError, "set_entry takes a callable and eight addresses");
         return nullptr;
     }
-    void* p[5];
-    for (int i = 0; i < 5; ++i) {
+    void* p[8];
+    for (int i = 0; i < 8; ++i) {
         p[i] = PyLong_AsVoidPtr(args[i + 1]);
         if (PyErr_Occurred()) return nullptr;
     }
@@ -341,6 +495,9 @@ PyObject* set_entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     p_quantize_weight = reinterpret_cast<decltype(p_quantize_weight)>(p[2]);
     p_linear_fp8 = reinterpret_cast<decltype(p_linear_fp8)>(p[3]);
     p_cross_attention = reinterpret_cast<decltype(p_cross_attention)>(p[4]);
+    p_rotary = reinterpret_cast<decltype(p_rotary)>(p[5]);
+    p_cache_append = reinterpret_cast<decltype(p_cache_append)>(p[6]);
+    p_paged_attention = reinterpret_cast<decltype(p_paged_attention)>(p[7]);
     Py_RETURN_NONE;
 }
 
@@ -350,6 +507,9 @@ PyMethodDef methods[] = {ENTRY("rmsnorm", rmsnorm, 8),
                          ENTRY("quantize_weight", quantize_weight, 3),
                          ENTRY("linear_fp8", linear_fp8, 10),
                          ENTRY("cross_attention", cross_attention, 6),
+                         ENTRY("rotary", rotary, 6),
+                         ENTRY("cache_append", cache_append, 13),
+                         ENTRY("paged_attention", paged_attention, 10),
                          {"set_entry", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&set_entry)), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serving", "Marshalling of the serving stages.", -1, methods,

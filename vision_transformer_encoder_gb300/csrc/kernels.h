@@ -263,4 +263,67 @@ bool cross_tc_supported(const CrossDesc& d);
 cudaError_t launch_cross_tc(const CrossDesc& d, const DeviceInfo& dev, cudaStream_t s);
 cudaError_t launch_cross_attention(const CrossDesc& d, const DeviceInfo& dev, cudaStream_t s);
 
+// ---- Rotary positions and the paged cache (rotary.cu) ---------------------------
+// One launch turns the heads of q into q_out (strides qo) and, with cache set, appends k and v.
+struct RotaryDesc {
+    const double* frequencies; int64_t n;      // n pairs; 0: no rotation
+    int layout;
+    double scale;
+    const int32_t* positions;                  // (B, T), nullable: starts[b] + t, or t
+    int64_t B, T, H, Hkv, dh;                  // H 0: no queries; Hkv 0: nothing appended
+    const void* q; int64_t qs[3];
+    void* q_out; int64_t qo[3];
+    const void* k; int64_t ks[3];
+    const void* v; int64_t vs[3];
+    void* k_pages; int64_t kp[3];              // page, token, head
+    void* v_pages; int64_t vp[3];
+    const int32_t* table; int64_t table_pages, pages, page;
+    const int32_t* starts;
+    const int32_t* lens;                       // nullable
+    int dt;
+};
+cudaError_t launch_rotary(const RotaryDesc& d, const DeviceInfo& dev, cudaStream_t s);
+
+// ---- Paged attention (attention_paged.cu) ---------------------------------------
+struct PagedDesc {
+    const void* q; int64_t qs[3];              // sequence, token, head
+    const void* k; int64_t ks[3];              // page, token, head
+    const void* v; int64_t vs[3];
+    const int32_t* table; int64_t table_pages;
+    const int32_t* kv_lens;
+    const int32_t* q_lens;                     // nullable
+    const int32_t* prefix_table;               // nullable: no prefix
+    int64_t prefix_pages;
+    const int32_t* prefix_lens;
+    int64_t groups, B, Tq, H, Hkv, dh, pages, page;
+    double scale;
+    int dt;
+    void* o;                                   // (B, Tq, H, dh) contiguous
+};
+constexpr int64_t kPagedMaxHead = 512;
+
+// Partial results: part p of output row r (of B Tq H), over a share of the keys, is an unnormalised row
+// acc[p][r][dh], the maximum of its scores in log2 and the sum of its weights, ml[p][r] = {m, l} (m = -inf, l = 0
+// where it has no keys; acc is not read then).
+struct PagedParts {
+    void* acc;
+    void* ml;
+    int64_t rows;
+    int n;                                     // parts in all
+};
+
+// How a call is worked off, from sizes and pointers alone.
+struct PagedPlan {
+    int form;                                  // PagedForm
+    int own_parts, prefix_parts;               // parts along the keys; prefix_parts 0: no prefix, or in the own ones
+    bool partial;                              // results go through workspace
+    size_t workspace;                          // bytes
+    int launches;
+};
+enum PagedForm : int { PAGED_GENERIC = 0 };
+PagedPlan plan_paged(const PagedDesc& d, const DeviceInfo& dev);
+// workspace: plan.workspace bytes, 16-byte aligned.
+cudaError_t launch_paged_attention(const PagedDesc& d, const PagedPlan& plan, void* workspace, const DeviceInfo& dev,
+                                   cudaStream_t s);
+
 }  // namespace vit

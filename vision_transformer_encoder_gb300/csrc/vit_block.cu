@@ -27,6 +27,7 @@
 #include <cstring>
 #include <mutex>
 #include <new>
+#include <utility>
 #include <vector>
 
 #include "common.cuh"
@@ -155,9 +156,79 @@ bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
 
 // Element counts are kept below this, so that no byte count or offset overflows.
 constexpr int64_t kMaxElements = (int64_t)1 << 46;
+// Keys of one sequence, and heads, of the paged cache: positions and head counts stay far inside 32 bits.
+constexpr int64_t kMaxKeys = (int64_t)1 << 30, kMaxHeads = 65536;
 
 // A null pointer, or one aligned to its elements.
 bool aligned_to(const void* p, int dt) { return reinterpret_cast<uintptr_t>(p) % dt_size(dt) == 0; }
+
+// Element strides of n[0] x n[1] x n[2] rows of dh contiguous elements: those given, or contiguous ones; dimensions of
+// one are never stepped along. last: offset of the last element. False where they cannot be used.
+bool row_strides(const int64_t* given, const int64_t (&n)[3], int64_t dh, int64_t (&st)[3], int64_t* last) {
+    const int64_t own[3] = {n[1] * n[2] * dh, n[2] * dh, dh};
+    *last = dh - 1;
+    for (int j = 0; j < 3; ++j) {
+        st[j] = given && n[j] > 1 ? given[j] : own[j];
+        if (st[j] < 0) return false;
+        if (n[j] > 1 && st[j] > (kMaxElements - *last) / (n[j] - 1)) return false;
+        *last += (n[j] - 1) * st[j];
+    }
+    return true;
+}
+
+// Whether no two elements of such rows share an address: each stride steps over all that lies within.
+bool keeps_apart(const int64_t (&n)[3], const int64_t (&st)[3], int64_t dh) {
+    int order[3] = {0, 1, 2};
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2 - i; ++j)
+            if (st[order[j]] > st[order[j + 1]]) std::swap(order[j], order[j + 1]);
+    int64_t span = dh;
+    for (int i : order) {
+        if (n[i] == 1) continue;
+        if (st[i] < span) return false;
+        span += (n[i] - 1) * st[i];
+    }
+    return true;
+}
+
+// Whether some element of b lies `delta` elements behind one of a, for rows in dimensions dim.. that keep apart with these
+// strides.
+bool meets(int64_t delta, const int64_t (&na)[3], const int64_t (&nb)[3], const int64_t (&st)[3], int64_t dh, const int (&order)[3],
+           int i) {
+    if (i == 3) return delta > -dh && delta < dh;
+    const int d = order[i];
+    if (na[d] == 1 && nb[d] == 1) return meets(delta, na, nb, st, dh, order, i + 1);
+    // what lies within spans less than a stride, so two multiples of it can be left
+    int64_t q = delta / st[d];
+    if (q * st[d] > delta) --q;
+    for (int64_t s = q; s <= q + 1; ++s)
+        if (s > -nb[d] && s < na[d] && meets(delta - s * st[d], na, nb, st, dh, order, i + 1)) return true;
+    return false;
+}
+
+// Whether two sets of rows in one buffer may share an element; true where their strides differ. a and b: first elements.
+bool rows_meet(const void* a, const int64_t (&na)[3], const int64_t (&sa)[3], const void* b, const int64_t (&nb)[3],
+               const int64_t (&sb)[3], int64_t dh, size_t es) {
+    int64_t last_a = dh - 1, last_b = dh - 1, st[3], n[3];
+    for (int j = 0; j < 3; ++j) {
+        last_a += (na[j] - 1) * sa[j];
+        last_b += (nb[j] - 1) * sb[j];
+    }
+    if (!overlaps(a, (size_t)(last_a + 1) * es, b, (size_t)(last_b + 1) * es)) return false;
+    for (int j = 0; j < 3; ++j) {
+        if (na[j] > 1 && nb[j] > 1 && sa[j] != sb[j]) return true;
+        st[j] = na[j] > 1 ? sa[j] : sb[j];
+        n[j] = na[j] > nb[j] ? na[j] : nb[j];
+    }
+    const int64_t bytes = static_cast<const uint8_t*>(a) - static_cast<const uint8_t*>(b);
+    if (bytes % (int64_t)es != 0 || !keeps_apart(n, st, dh)) return true;
+    int order[3] = {0, 1, 2};   // the widest first
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2 - i; ++j)
+            if (st[order[j]] < st[order[j + 1]]) std::swap(order[j], order[j + 1]);
+    // an element of a at index i and one of b at index j: a + i st = b + j st, so (j - i) st = a - b
+    return meets(bytes / (int64_t)es, nb, na, st, dh, order, 0);
+}
 
 // Runs launch(device info, stream) for a single-stage call on the current device, counts it
 // and turns its outcome into a status; with VIT_DEBUG_SYNC=1 it waits for the stream and
@@ -1873,6 +1944,178 @@ int vit_cross_attention(const void* q, const int64_t* q_strides, const void* k, 
     if (overlaps(o, ob, kv_lens, (size_t)B * 4) || !aligned_to(o, dtype) || !aligned_to(kv_lens, DT_F32))
         return VIT_ERR_ARG;
     return enqueue(stream, [&](const DeviceInfo& dev, cudaStream_t s) { return launch_cross_attention(d, dev, s); });
+}
+
+// The rotation's part of a descriptor; a status.
+static int take_rope(const vit_rope* rope, int64_t dh, int dtype, RotaryDesc* d) {
+    if (!rope->frequencies || rope->n <= 0 || rope->n > dh / 2) return VIT_ERR_ARG;
+    if (rope->layout != VIT_ROTARY_HALF && rope->layout != VIT_ROTARY_INTERLEAVED) return VIT_ERR_ARG;
+    if (!(rope->scale - rope->scale == 0.0) || (dtype != DT_F64 && std::fabs(rope->scale) > 1e30)) return VIT_ERR_ARG;
+    if (!aligned_to(rope->frequencies, DT_F64)) return VIT_ERR_ARG;
+    d->frequencies = rope->frequencies;
+    d->n = rope->n;
+    d->layout = rope->layout;
+    d->scale = rope->scale;
+    return VIT_OK;
+}
+
+// The queries' part: q (B, T, H, dh), turned into q_out, which is contiguous or q itself; a status.
+static int take_turned(const void* q, const int64_t* strides, void* q_out, RotaryDesc* d, int64_t* last) {
+    const int64_t n[3] = {d->B, d->T, d->H};
+    int64_t end;
+    if (!row_strides(strides, n, d->dh, d->qs, last) || !row_strides(nullptr, n, d->dh, d->qo, &end)) return VIT_ERR_ARG;
+    if (!aligned_to(q, d->dt) || !aligned_to(q_out, d->dt)) return VIT_ERR_ARG;
+    const size_t es = dt_size(d->dt);
+    if (q == q_out) {
+        if (!keeps_apart(n, d->qs, d->dh)) return VIT_ERR_ARG;
+        std::memcpy(d->qo, d->qs, sizeof(d->qo));
+    } else if (overlaps(q_out, (size_t)(end + 1) * es, q, (size_t)(*last + 1) * es)) {
+        return VIT_ERR_ARG;
+    }
+    d->q = q;
+    d->q_out = q_out;
+    return VIT_OK;
+}
+
+static bool elements_fit(int64_t a, int64_t b, int64_t c, int64_t dh) {
+    return c <= kMaxElements / dh && b <= kMaxElements / (c * dh) && a <= kMaxElements / (b * c * dh);
+}
+
+// Sizes of a cache and the strides of its pools; a status.
+static int take_cache(const vit_paged_cache* c, int64_t (&ks)[3], int64_t (&vs)[3], int64_t* k_last, int64_t* v_last) {
+    if (!c || !c->k || !c->v || c->pages <= 0 || c->page <= 0 || c->heads <= 0 || c->dh <= 0) return VIT_ERR_ARG;
+    if (c->dtype != DT_F32 && c->dtype != DT_BF16 && c->dtype != DT_F64) return VIT_ERR_DTYPE;
+    if (c->dh > kPagedMaxHead) return VIT_ERR_UNSUPPORTED;
+    if (c->pages > 0x7fffffff || c->page > kMaxKeys || c->heads > kMaxHeads) return VIT_ERR_ARG;
+    if (!elements_fit(c->pages, c->page, c->heads, c->dh)) return VIT_ERR_ARG;
+    const int64_t n[3] = {c->pages, c->page, c->heads};
+    for (int j = 0; j < 3; ++j)
+        if (n[j] > 1 && (c->k_strides[j] <= 0 || c->v_strides[j] <= 0)) return VIT_ERR_ARG;
+    if (!row_strides(c->k_strides, n, c->dh, ks, k_last) || !row_strides(c->v_strides, n, c->dh, vs, v_last)) return VIT_ERR_ARG;
+    if (!aligned_to(c->k, c->dtype) || !aligned_to(c->v, c->dtype)) return VIT_ERR_ARG;
+    return VIT_OK;
+}
+
+int vit_rotary(const void* x, const int64_t* x_strides, const int32_t* positions, const vit_rope* rope, int64_t B, int64_t T,
+               int64_t H, int64_t dh, int dtype, void* out, void* stream) {
+    if (!x || !rope || !out || B <= 0 || T <= 0 || H <= 0 || dh <= 0 || H > kMaxHeads) return VIT_ERR_ARG;
+    if (dtype != DT_F32 && dtype != DT_BF16 && dtype != DT_F64) return VIT_ERR_DTYPE;
+    if (dh > kPagedMaxHead) return VIT_ERR_UNSUPPORTED;
+    if (!elements_fit(B, T, H, dh)) return VIT_ERR_ARG;
+    RotaryDesc d{};
+    d.B = B; d.T = T; d.H = H; d.dh = dh; d.dt = dtype; d.positions = positions;
+    int rc = take_rope(rope, dh, dtype, &d);
+    if (rc != VIT_OK) return rc;
+    int64_t last;
+    rc = take_turned(x, x_strides, out, &d, &last);
+    if (rc != VIT_OK) return rc;
+    const size_t ob = (size_t)(x == out ? last + 1 : B * T * H * dh) * dt_size(dtype);
+    if (overlaps(out, ob, positions, (size_t)(B * T) * 4) || overlaps(out, ob, rope->frequencies, (size_t)rope->n * 8) ||
+        !aligned_to(positions, DT_F32))
+        return VIT_ERR_ARG;
+    return enqueue(stream, [&](const DeviceInfo& dev, cudaStream_t s) { return launch_rotary(d, dev, s); });
+}
+
+int vit_cache_append(const void* k, const int64_t* k_strides, const void* v, const int64_t* v_strides, const void* q,
+                     const int64_t* q_strides, const vit_paged_cache* cache, const int32_t* table, int64_t table_pages,
+                     const int32_t* starts, const int32_t* lens, const vit_rope* rope, const int32_t* positions, int64_t B,
+                     int64_t T, int64_t H, void* q_out, void* stream) {
+    if (!k || !v || !cache || !table || !starts || B <= 0 || T <= 0 || table_pages <= 0) return VIT_ERR_ARG;
+    if (!q != !q_out || (q && (H <= 0 || H > kMaxHeads))) return VIT_ERR_ARG;
+    RotaryDesc d{};
+    int64_t k_last, v_last, pool_k, pool_v, q_last = 0;
+    int rc = take_cache(cache, d.kp, d.vp, &pool_k, &pool_v);
+    if (rc != VIT_OK) return rc;
+    const int64_t Hkv = cache->heads, dh = cache->dh;
+    if (!elements_fit(B, T, Hkv, dh) || (q && !elements_fit(B, T, H, dh)) || B > kMaxElements / table_pages) return VIT_ERR_ARG;
+    d.B = B; d.T = T; d.H = q ? H : 0; d.Hkv = Hkv; d.dh = dh; d.dt = cache->dtype; d.positions = positions;
+    d.k = k; d.v = v; d.k_pages = cache->k; d.v_pages = cache->v; d.table = table; d.table_pages = table_pages;
+    d.pages = cache->pages; d.page = cache->page; d.starts = starts; d.lens = lens;
+    d.scale = 1.0;
+    if (rope && (rc = take_rope(rope, dh, d.dt, &d)) != VIT_OK) return rc;
+    const int64_t nk[3] = {B, T, Hkv}, np[3] = {d.pages, d.page, Hkv};
+    if (!row_strides(k_strides, nk, dh, d.ks, &k_last) || !row_strides(v_strides, nk, dh, d.vs, &v_last)) return VIT_ERR_ARG;
+    if (q && (rc = take_turned(q, q_strides, q_out, &d, &q_last)) != VIT_OK) return rc;
+    const size_t es = dt_size(d.dt), qb = q ? (size_t)(q == q_out ? q_last + 1 : B * T * H * dh) * es : 0;
+    // what is written: the pools, each slot apart from every other, and q_out
+    if (!keeps_apart(np, d.kp, dh) || !keeps_apart(np, d.vp, dh) || rows_meet(cache->k, np, d.kp, cache->v, np, d.vp, dh, es))
+        return VIT_ERR_ARG;
+    const struct { void* p; size_t n; } out[] = {{cache->k, (size_t)(pool_k + 1) * es}, {cache->v, (size_t)(pool_v + 1) * es}, {q_out, qb}};
+    const struct { const void* p; size_t n; } in[] = {
+        {table, (size_t)(B * table_pages) * 4}, {starts, (size_t)B * 4}, {lens, (size_t)B * 4},
+        {positions, (size_t)(B * T) * 4}, {d.frequencies, (size_t)d.n * 8}};
+    for (const auto& o : out)
+        for (const auto& i : in)
+            if (overlaps(o.p, o.n, i.p, i.n)) return VIT_ERR_ARG;
+    for (int i = 0; i < 2; ++i)
+        if (overlaps(out[i].p, out[i].n, k, (size_t)(k_last + 1) * es) || overlaps(out[i].p, out[i].n, v, (size_t)(v_last + 1) * es) ||
+            (q && (overlaps(out[i].p, out[i].n, q, (size_t)(q_last + 1) * es) || overlaps(out[i].p, out[i].n, q_out, qb))))
+            return VIT_ERR_ARG;
+    if (q) {   // q may be turned where it lies, between the k and v of one projection
+        const int64_t nq[3] = {B, T, H};
+        if (rows_meet(q_out, nq, d.qo, k, nk, d.ks, dh, es) || rows_meet(q_out, nq, d.qo, v, nk, d.vs, dh, es)) return VIT_ERR_ARG;
+    }
+    if (!aligned_to(k, d.dt) || !aligned_to(v, d.dt) || !aligned_to(table, DT_F32) || !aligned_to(starts, DT_F32) ||
+        !aligned_to(lens, DT_F32) || !aligned_to(positions, DT_F32))
+        return VIT_ERR_ARG;
+    return enqueue(stream, [&](const DeviceInfo& dev, cudaStream_t s) { return launch_rotary(d, dev, s); });
+}
+
+int vit_paged_attention(const void* q, const int64_t* q_strides, const vit_paged_cache* cache, const int32_t* table,
+                        int64_t table_pages, const int32_t* kv_lens, const int32_t* q_lens, const int32_t* prefix_table,
+                        int64_t prefix_pages, const int32_t* prefix_lens, int64_t groups, int64_t B, int64_t Tq, int64_t H,
+                        double scale, void* o, void* stream) {
+    if (!q || !cache || !table || !kv_lens || !o || B <= 0 || Tq <= 0 || H <= 0 || table_pages <= 0) return VIT_ERR_ARG;
+    if (!prefix_table != !prefix_lens || (prefix_table ? prefix_pages <= 0 : prefix_pages != 0)) return VIT_ERR_ARG;
+    if (groups <= 0 || B % groups != 0 || (!prefix_table && groups != 1)) return VIT_ERR_ARG;
+    PagedDesc d{};
+    int64_t k_last, v_last, q_last;
+    const int rc = take_cache(cache, d.ks, d.vs, &k_last, &v_last);
+    if (rc != VIT_OK) return rc;
+    const int64_t Hkv = cache->heads, dh = cache->dh;
+    if (H % Hkv != 0 || H > kMaxHeads || !elements_fit(B, Tq, H, dh)) return VIT_ERR_ARG;
+    if (!(scale - scale == 0.0) || (cache->dtype != DT_F64 && std::fabs(scale) > 1e30)) return VIT_ERR_ARG;
+    if (table_pages > kMaxKeys / cache->page || prefix_pages > kMaxKeys / cache->page || B > kMaxElements / table_pages ||
+        (prefix_pages && groups > kMaxElements / prefix_pages))
+        return VIT_ERR_ARG;
+    d.q = q; d.k = cache->k; d.v = cache->v; d.table = table; d.table_pages = table_pages; d.kv_lens = kv_lens;
+    d.q_lens = q_lens; d.prefix_table = prefix_table; d.prefix_pages = prefix_pages; d.prefix_lens = prefix_lens;
+    d.groups = groups; d.B = B; d.Tq = Tq; d.H = H; d.Hkv = Hkv; d.dh = dh; d.pages = cache->pages; d.page = cache->page;
+    d.scale = scale; d.dt = cache->dtype; d.o = o;
+    const int64_t nq[3] = {B, Tq, H};
+    if (!row_strides(q_strides, nq, dh, d.qs, &q_last)) return VIT_ERR_ARG;
+    const size_t es = dt_size(d.dt), ob = (size_t)(B * Tq * H * dh) * es;
+    const struct { const void* p; size_t n; } in[] = {
+        {q, (size_t)(q_last + 1) * es}, {cache->k, (size_t)(k_last + 1) * es}, {cache->v, (size_t)(v_last + 1) * es},
+        {table, (size_t)(B * table_pages) * 4}, {kv_lens, (size_t)B * 4}, {q_lens, (size_t)B * 4},
+        {prefix_table, (size_t)(groups * prefix_pages) * 4}, {prefix_lens, (size_t)groups * 4}};
+    for (const auto& i : in)
+        if (overlaps(o, ob, i.p, i.n)) return VIT_ERR_ARG;
+    if (!aligned_to(q, d.dt) || !aligned_to(o, d.dt) || !aligned_to(table, DT_F32) || !aligned_to(kv_lens, DT_F32) ||
+        !aligned_to(q_lens, DT_F32) || !aligned_to(prefix_table, DT_F32) || !aligned_to(prefix_lens, DT_F32))
+        return VIT_ERR_ARG;
+    DeviceState* st = nullptr;
+    const int on = current_device(&st);
+    if (on != VIT_OK) return on;
+    const PagedPlan plan = plan_paged(d, st->info);
+    void* ws = nullptr;
+    if (plan.workspace) {
+        const cudaError_t e = cudaMallocFromPoolAsync(&ws, plan.workspace, st->pool, static_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return status_from(e);
+        }
+    }
+    const int ran = enqueue(stream, [&](const DeviceInfo& dev, cudaStream_t s) {
+        const cudaError_t e = launch_paged_attention(d, plan, ws, dev, s);
+        if (e == cudaSuccess) g_launches.fetch_add(plan.launches - 1, std::memory_order_relaxed);
+        return e;
+    });
+    if (ws && cudaFreeAsync(ws, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+        cudaGetLastError();
+        return ran != VIT_OK ? ran : VIT_ERR_CUDA;
+    }
+    return ran;
 }
 
 int vit_block_noalloc(const void* x, const void* w_q, const void* w_k, const void* w_v,
