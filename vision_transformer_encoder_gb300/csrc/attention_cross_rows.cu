@@ -33,28 +33,13 @@
 #include "cross_maps.cuh"
 #include "kernels.h"
 #include "launch.cuh"
+#include "mma_rows.cuh"
 #include "ptx.cuh"
 
 namespace vit {
 namespace {
 
 constexpr int CR_ROWS = 16, CR_MAXZ = 8;
-
-__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Lane (r, c) of an 8 x 8 matrix of 16-bit elements holds row r, columns 2c and 2c + 1: the same of
-// the transpose.
-__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
-    uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-    return r;
-}
 
 // DHT: the head width rounded up to 64 or 128; columns past dh are zeros.
 template <int DHT, int NR, int NW, int KEYS, int CR_STAGES, int MINB>

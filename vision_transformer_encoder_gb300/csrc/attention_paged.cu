@@ -275,7 +275,7 @@ template <typename T, typename A, int RT> cudaError_t run_generic_of(const Gener
 int generic_rows(const PagedDesc& d) { return d.Tq * (d.H / d.Hkv) <= 4 ? 4 : 16; }
 
 template <typename T, typename A>
-cudaError_t generic(const PagedDesc& d, const PagedPlan& plan, const PagedParts& parts, const DeviceInfo& dev, cudaStream_t s) {
+cudaError_t generic(const PagedDesc& d, const PagedPlan& plan, const PagedParts& parts, const DeviceInfo& dev, cudaStream_t s, bool own = true) {
     const int RT = generic_rows(d);
     const int64_t G = d.H / d.Hkv, tokens = d.B / d.groups * d.Tq;
     GenericParams p{};
@@ -286,7 +286,7 @@ cudaError_t generic(const PagedDesc& d, const PagedPlan& plan, const PagedParts&
     p.own_rb = (d.Tq * G + RT - 1) / RT;
     p.prefix_rb = (tokens * G + RT - 1) / RT;
     p.prefix_blocks = d.groups * d.Hkv * p.prefix_rb * plan.prefix_parts;
-    p.blocks = p.prefix_blocks + d.B * d.Hkv * p.own_rb * plan.own_parts;
+    p.blocks = p.prefix_blocks + (own ? d.B * d.Hkv * p.own_rb * plan.own_parts : 0);
     p.scale_log2 = d.scale * 1.4426950408889634;
     return RT == 4 ? run_generic_of<T, A, 4>(p, dev, s) : run_generic_of<T, A, 16>(p, dev, s);
 }
@@ -295,7 +295,7 @@ cudaError_t generic(const PagedDesc& d, const PagedPlan& plan, const PagedParts&
 
 PagedPlan plan_paged(const PagedDesc& d, const DeviceInfo& dev) {
     PagedPlan plan{};
-    plan.form = PAGED_GENERIC;
+    plan.form = paged_rows_supported(d) ? PAGED_ROWS : PAGED_GENERIC;
     // CTAs of four warps, some eight of them to an SM: cut the keys where there are fewer, in parts of 128 at least
     const int RT = generic_rows(d);
     const int64_t G = d.H / d.Hkv, want = 8 * (int64_t)dev.num_sms;
@@ -304,10 +304,14 @@ PagedPlan plan_paged(const PagedDesc& d, const DeviceInfo& dev) {
         z = z < most ? z : most;
         return (int)(z < 1 ? 1 : z > 32 ? 32 : z);
     };
-    plan.own_parts = parts(d.B * d.Hkv * ((d.Tq * G + RT - 1) / RT), d.table_pages * d.page);
     if (d.prefix_table)
         plan.prefix_parts = parts(d.groups * d.Hkv * ((d.B / d.groups * d.Tq * G + RT - 1) / RT), d.prefix_pages * d.page);
-    plan.partial = plan.prefix_parts + plan.own_parts > 1;
+    if (plan.form == PAGED_GENERIC) {
+        plan.own_parts = parts(d.B * d.Hkv * ((d.Tq * G + RT - 1) / RT), d.table_pages * d.page);
+        plan.partial = plan.prefix_parts + plan.own_parts > 1;
+    } else {
+        plan.partial = plan.prefix_parts > 0;
+    }
     plan.launches = plan.partial ? 2 : 1;
     if (plan.partial)
         plan.workspace = (size_t)(plan.prefix_parts + plan.own_parts) * (size_t)(d.B * d.Tq * d.H) * (size_t)(d.dh + 2) *
@@ -325,6 +329,10 @@ cudaError_t launch_paged_attention(const PagedDesc& d, const PagedPlan& plan, vo
         parts.ml = static_cast<uint8_t*>(workspace) + (size_t)parts.n * parts.rows * d.dh * (d.dt == DT_F64 ? 8 : 4);
     }
     cudaError_t e;
+    if (plan.form == PAGED_ROWS) {
+        e = plan.partial ? generic<__nv_bfloat16, float>(d, plan, parts, dev, s, false) : cudaSuccess;
+        return e != cudaSuccess ? e : launch_paged_rows(d, parts, dev, s);
+    }
     if (d.dt == DT_F64) e = generic<double, double>(d, plan, parts, dev, s);
     else if (d.dt == DT_F32) e = generic<float, float>(d, plan, parts, dev, s);
     else e = generic<__nv_bfloat16, float>(d, plan, parts, dev, s);

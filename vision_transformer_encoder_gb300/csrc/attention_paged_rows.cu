@@ -1,0 +1,451 @@
+// attention_paged_rows.cu -- paged attention of few queries (decoding): the mathematics of attention_paged.cu where one key
+// head serves at most 16 query rows (Tq * G <= 16), bf16, head width up to 128 in steps of 8, pages of a multiple of
+// 16 tokens.
+//
+// Bound by reading the sequence's own keys and values once. They are dealt out in tiles of 16, which lie in one page each, to the
+// warps of one CTA or of a cluster of CTAs; every warp looks its pages up one tile ahead of asking for them, keeps its own
+// running maximum, sum and output rows, joined at the end through shared memory and, between the CTAs of a cluster, distributed
+// shared memory. The rows of the prefix, where there is one, were worked off by the kernel launched before this
+// one: its parts are joined here. This kernel starts beside that one and waits for it only then: its own keys, queries
+// and tables were there before that one began (it lets this one start behind its own wait).
+//
+// Tiles, rings and products are those of attention_cross_rows.cu: mma.m16n8k16 with the query rows as the n side,
+// S^T = K Q^T and O^T = V^T P^T, K and V by TMA into a ring of each warp's own. Weights are rounded to bf16 for the second
+// product (their sum is not).
+//
+// A query does not see later tokens, but the product adds their values times weights of zero. Where such a value is
+// not finite, the tile is multiplied once per token with what that token does not see cleared.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "cross_maps.cuh"
+#include "kernels.h"
+#include "launch.cuh"
+#include "mma_rows.cuh"
+#include "ptx.cuh"
+
+namespace vit {
+namespace {
+
+constexpr int PR_ROWS = 16, PR_MAXZ = 8, PR_KEYS = 16;
+
+struct PagedRowsParams {
+    PagedDesc d;
+    PagedParts parts;    // the prefix's; n 0: none
+    float scale_log2;
+    int Z;
+    uint32_t* err;
+};
+
+__device__ __forceinline__ bool not_finite(uint32_t pair) {
+    return (pair & 0x7f80u) == 0x7f80u || (pair & 0x7f800000u) == 0x7f800000u;
+}
+
+// DHT: the head width rounded up to 64 or 128; columns past dh are zeros. NR: eight rows or sixteen.
+template <int DHT, int NR, int NW, int STAGES, int MINB>
+__global__ void __launch_bounds__(NW * 32, MINB)
+paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                  const __grid_constant__ PagedRowsParams p) {
+    constexpr int NCH = DHT / 64, STAGE = PR_KEYS * NCH * 256;
+    constexpr int BOX = PR_KEYS * 128;   // 64 columns of one tile
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t bars[NW][STAGES];
+    const PagedDesc& d = p.d;
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c4 = lane & 3, r8 = lane >> 2;
+    const int Z = p.Z, z = Z > 1 ? (int)ptx::cluster_ctarank() : 0;
+    const int bh = blockIdx.x / Z, b = bh / (int)d.Hkv, h = bh % (int)d.Hkv;
+    const int Tq = (int)d.Tq, G = (int)(d.H / d.Hkv), R = Tq * G, dh = (int)d.dh;
+    uint64_t* bar = bars[warp];
+    uint8_t* ring = smem + warp * STAGES * STAGE;
+    // once a warp's keys are done, over its ring: O (R x dh), m and l (R each); behind the rings
+    // this CTA's joined O, m and l
+    constexpr int piece = STAGES * STAGE / 4;
+    float* sm = reinterpret_cast<float*>(smem);
+    float* wO = sm + warp * piece;
+    float* jO = sm + NW * piece;
+    static_assert(NR * 8 * (DHT + 2) <= piece, "output rows in a ring");
+    if (lane == 0) {
+        for (int i = 0; i < STAGES; ++i) ptx::mbar_init(bar + i, 1);
+        ptx::fence_mbar_init();
+        ptx::prefetch_tensormap(&tmK);
+        ptx::prefetch_tensormap(&tmV);
+    }
+    __syncwarp();
+    if (!p.parts.n) {
+        griddep_wait();
+        griddep_launch_dependents();
+    }
+
+    const int held = (int)(d.table_pages * d.page), tpp = (int)d.page / PR_KEYS;
+    const int len = min(max(__ldg(d.kv_lens + b), 0), held);
+    const int new_ = d.q_lens ? min(max(__ldg(d.q_lens + b), 0), Tq) : Tq;
+    // tiles of this warp: first, first + stride, ...; a sequence without new tokens needs none
+    const int tiles = new_ > 0 ? (len + PR_KEYS - 1) / PR_KEYS : 0, first = z * NW + warp, stride = Z * NW;
+    const int32_t* table = d.table + (int64_t)b * d.table_pages;
+    auto entry = [&](int tile) -> int { return tile < tiles ? __ldg(table + tile / tpp) : -1; };
+    uint32_t there = 0;   // stages with a tile on its way or landed
+    auto request = [&](int tile, int pg, int st) {   // converged
+        if (pg < 0 || pg >= d.pages) return;
+        there |= 1u << st;
+        if (lane != 0) return;
+        uint8_t* dst = ring + st * STAGE;
+        const int token = tile % tpp * PR_KEYS;
+        ptx::mbar_arrive_expect_tx(bar + st, STAGE);
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) ptx::tma_load_4d(dst + c * BOX, &tmK, bar + st, c * 64, h, token, pg);
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) ptx::tma_load_4d(dst + STAGE / 2 + c * BOX, &tmV, bar + st, c * 64, h, token, pg);
+    };
+    {
+        int pg[STAGES];
+#pragma unroll
+        for (int i = 0; i < STAGES; ++i) pg[i] = entry(first + i * stride);
+#pragma unroll
+        for (int i = 0; i < STAGES; ++i) request(first + i * stride, pg[i], i);
+    }
+    int ahead = entry(first + STAGES * stride);
+
+    // query rows 8 i + r8; packed row = token * G + head of the group
+    uint4 q[NR][2 * NCH];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        const int r = r8 + 8 * i;
+        const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(d.q) + b * d.qs[0] + (r / G) * d.qs[1] +
+                                  (int64_t)(h * G + r % G) * d.qs[2];
+#pragma unroll
+        for (int c = 0; c < 2 * NCH; ++c) {
+            const int col = (c >> 1) * 64 + (2 * c4 + (c & 1)) * 8;
+            q[i][c] = r < R && col < dh ? *reinterpret_cast<const uint4*>(qr + col) : make_uint4(0, 0, 0, 0);
+        }
+    }
+    // Row 8 i + 2 c4 + e sees the keys before lim; all live rows those before `low`. Rows of no token see what there
+    // is: they are zeroed at the end.
+    const int low = len - (new_ - 1);
+    int lim[NR][2];
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int t = (8 * i + 2 * c4 + e) / G;
+            lim[i][e] = t < new_ ? low + t : len;
+        }
+
+    // rows 8 i + 2 c4 + e: maximum, this thread's part of the sum; O^T of m-tile t of piece c
+    float o[NR][NCH * 4][4], m[NR][2], l[NR][2];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        m[i][0] = m[i][1] = -INFINITY;
+        l[i][0] = l[i][1] = 0.f;
+#pragma unroll
+        for (int j = 0; j < NCH * 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][j][e] = 0.f;
+    }
+
+    uint32_t it = 0, phases = 0;
+    bool ok = true;
+    for (int tile = first; tile < tiles; tile += stride, ++it) {
+        const uint32_t st = it % STAGES;
+        const int next = tile + STAGES * stride;
+        if (there >> st & 1) {   // else its page is absent
+            ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar + st, phases >> st & 1, nullptr));
+            if (!ok) break;
+            phases ^= 1u << st;
+            there &= ~(1u << st);
+            const uint8_t* sk = ring + st * STAGE;
+            const uint8_t* sv = sk + STAGE / 2;
+            const int u0 = tile * PR_KEYS;
+            // s[i]: keys r8 (0, 1) and 8 + r8 (2, 3), rows 8 i + 2 c4 + {0, 1}
+            float s[NR][4];
+            {
+                float sp[NR][2][4] = {};   // even and odd k-steps: shorter chains of dependent products
+#pragma unroll
+                for (int c = 0; c < 2 * NCH; ++c) {
+                    // 16-byte unit i of key u at i ^ (u % 8)
+                    const uint8_t* at = sk + (c >> 1) * BOX + r8 * 128 + (((2 * c4 + (c & 1)) ^ r8) << 4);
+                    const uint4 k0 = *reinterpret_cast<const uint4*>(at), k1 = *reinterpret_cast<const uint4*>(at + 1024);
+                    const uint32_t a0[4] = {k0.x, k1.x, k0.y, k1.y}, a1[4] = {k0.z, k1.z, k0.w, k1.w};
+#pragma unroll
+                    for (int i = 0; i < NR; ++i) {
+                        mma_16816(sp[i][0], a0, q[i][c].x, q[i][c].y);
+                        mma_16816(sp[i][1], a1, q[i][c].z, q[i][c].w);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < NR; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[i][e] = __fmul_rn(sp[i][0][e] + sp[i][1][e], p.scale_log2);   // rounded like the maximum
+            }
+            const bool edge = u0 + PR_KEYS > low;   // some row does not see all of it
+            if (edge) {
+#pragma unroll
+                for (int i = 0; i < NR; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (u0 + (e >> 1) * 8 + r8 >= lim[i][e & 1]) s[i][e] = -INFINITY;
+            }
+            uint32_t pt[NR][2];   // P^T: row 8 i + r8, keys 2 c4 + {0, 1} and + 8
+            bool grew = false;
+            float alpha[NR][2];
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                float mx[2] = {fmaxf(m[i][0], fmaxf(s[i][0], s[i][2])), fmaxf(m[i][1], fmaxf(s[i][1], s[i][3]))};
+#pragma unroll
+                for (int w = 4; w < 32; w *= 2) {
+                    mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], w));
+                    mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], w));
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    alpha[i][e] = mx[e] > m[i][e] ? exp2_approx(m[i][e] - mx[e]) : 1.f;
+                    grew = grew || mx[e] > m[i][e];
+                    m[i][e] = mx[e];
+                    if (mx[e] == -INFINITY) mx[e] = 0.f;   // only infinite scores so far: weights of zero
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[i][e] = exp2_approx(s[i][e] - mx[e & 1]);
+                pt[i][0] = transpose_8x8(pack_bf16x2(s[i][0], s[i][1]));
+                pt[i][1] = transpose_8x8(pack_bf16x2(s[i][2], s[i][3]));
+                l[i][0] = l[i][0] * alpha[i][0] + (s[i][0] + s[i][2]);
+                l[i][1] = l[i][1] * alpha[i][1] + (s[i][1] + s[i][3]);
+            }
+            if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                for (int i = 0; i < NR; ++i)
+#pragma unroll
+                    for (int j = 0; j < NCH * 4; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[i][j][e] *= alpha[i][e & 1];
+            }
+#pragma unroll
+            for (int c = 0; c < NCH; ++c) {
+                uint32_t w[4][4];
+                bool odd = false;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {   // keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9
+                    const int u = 2 * c4 + (k & 1) + 8 * (k >> 1);
+                    *reinterpret_cast<uint4*>(w[k]) = *reinterpret_cast<const uint4*>(sv + c * BOX + u * 128 + ((r8 ^ (u & 7)) << 4));
+                    if (edge && u0 + u >= low) {
+                        // past the length there may be anything, and 0 * NaN is NaN
+                        if (u0 + u >= len) w[k][0] = w[k][1] = w[k][2] = w[k][3] = 0u;
+                        odd = odd || not_finite(w[k][0]) || not_finite(w[k][1]) || not_finite(w[k][2]) || not_finite(w[k][3]);
+                    }
+                }
+                if (__builtin_expect(!__any_sync(0xffffffffu, odd), 1)) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t a[4] = {__byte_perm(w[0][e], w[1][e], 0x5410), __byte_perm(w[0][e], w[1][e], 0x7632),
+                                               __byte_perm(w[2][e], w[3][e], 0x5410), __byte_perm(w[2][e], w[3][e], 0x7632)};
+#pragma unroll
+                        for (int i = 0; i < NR; ++i) mma_16816(o[i][c * 4 + e], a, pt[i][0], pt[i][1]);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int t = 0; t < new_; ++t) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t x[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) x[k] = u0 + 2 * c4 + (k & 1) + 8 * (k >> 1) < low + t ? w[k][e] : 0u;
+                            const uint32_t a[4] = {__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[0], x[1], 0x7632),
+                                                   __byte_perm(x[2], x[3], 0x5410), __byte_perm(x[2], x[3], 0x7632)};
+#pragma unroll
+                            for (int i = 0; i < NR; ++i) {
+                                float one[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma_16816(one, a, pt[i][0], pt[i][1]);
+#pragma unroll
+                                for (int y = 0; y < 4; ++y)
+                                    if ((8 * i + 2 * c4 + (y & 1)) / G == t) o[i][c * 4 + e][y] += one[y];
+                            }
+                        }
+                    }
+                }
+            }
+            __syncwarp();   // the stage has been read
+        }
+        request(next, ahead, st);
+        ahead = entry(next + stride);
+    }
+    if (!ok) {
+        if (lane == 0 && p.err) atomicOr(p.err, ERRBIT_TIMEOUT_ATTENTION);
+        // copies in flight land before the CTA can exit
+        for (int i = 0; i < STAGES; ++i)
+            if (there >> i & 1) ptx::mbar_wait_bounded(bar + i, phases >> i & 1, nullptr);
+    }
+    __syncwarp();
+
+    // this warp's rows: [0], [2] are columns 8 r8 + 2 t, + 1 of row 8 i + 2 c4; [1], [3] of the next row
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int w = 4; w < 32; w *= 2) l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], w);
+            const int r = 8 * i + 2 * c4 + e;
+            if (r >= R) continue;
+#pragma unroll
+            for (int c = 0; c < NCH; ++c)
+                if (c * 64 + r8 * 8 < dh) {
+                    float* at = wO + r * dh + c * 64 + r8 * 8;
+                    *reinterpret_cast<float2*>(at) = make_float2(o[i][c * 4][e], o[i][c * 4][2 + e]);
+                    *reinterpret_cast<float2*>(at + 2) = make_float2(o[i][c * 4 + 1][e], o[i][c * 4 + 1][2 + e]);
+                    *reinterpret_cast<float2*>(at + 4) = make_float2(o[i][c * 4 + 2][e], o[i][c * 4 + 2][2 + e]);
+                    *reinterpret_cast<float2*>(at + 6) = make_float2(o[i][c * 4 + 3][e], o[i][c * 4 + 3][2 + e]);
+                }
+            if (r8 == 0) {
+                wO[R * dh + r] = m[i][e];
+                wO[R * dh + R + r] = l[i][e];
+            }
+        }
+    __syncthreads();
+    if (p.parts.n) {   // the prefix's rows are there
+        griddep_wait();
+        griddep_launch_dependents();
+    }
+
+    // Columns col, col + 1 of row r, joined from own keys (x, y, weights' sum and maximum) and the prefix's parts, stored.
+    auto finish = [&](int r, int col, float x, float y, float sum, float mx) {
+        const int t = r / G;
+        const int64_t row = ((int64_t)b * Tq + t) * d.H + h * G + r % G;
+        if (p.parts.n) {
+            const float2* ml = static_cast<const float2*>(p.parts.ml) + row;
+            float top = mx;
+            for (int i = 0; i < p.parts.n; ++i) top = fmaxf(top, __ldcg(ml + i * p.parts.rows).x);
+            const float base = top == -INFINITY ? 0.f : top;
+            const float f = exp2_approx(mx - base);
+            x *= f;
+            y *= f;
+            sum *= f;
+            for (int i = 0; i < p.parts.n; ++i) {
+                const float2 w = __ldcg(ml + i * p.parts.rows);
+                if (w.y == 0.f) continue;   // no keys: its row is not there
+                const float g = exp2_approx(w.x - base);
+                const float2 v = __ldcg(reinterpret_cast<const float2*>(static_cast<const float*>(p.parts.acc) + (i * p.parts.rows + row) * dh + col));
+                x = fmaf(g, v.x, x);
+                y = fmaf(g, v.y, y);
+                sum = fmaf(g, w.y, sum);
+            }
+        }
+        const bool none = sum == 0.f || t >= new_;
+        const float inv = 1.f / sum;
+        x = none ? 0.f : x * inv;
+        y = none ? 0.f : y * inv;
+        __nv_bfloat16* at = static_cast<__nv_bfloat16*>(d.o) + row * dh + col;
+        if ((reinterpret_cast<uintptr_t>(at) & 3) == 0) {
+            *reinterpret_cast<uint32_t*>(at) = pack_bf16x2(x, y);
+        } else {
+            at[0] = __float2bfloat16_rn(x);
+            at[1] = __float2bfloat16_rn(y);
+        }
+    };
+    // join the warps' rows, two columns per thread and step, every operand asked for at once
+    for (int i = threadIdx.x * 2; i < R * dh; i += NW * 64) {
+        const int r = i / dh;
+        float mw[NW], mx = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            mw[w] = sm[w * piece + R * dh + r];
+            mx = fmaxf(mx, mw[w]);
+        }
+        const float base = mx == -INFINITY ? 0.f : mx;
+        float2 acc = make_float2(0.f, 0.f);
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const float f = exp2_approx(mw[w] - base);
+            const float2 v = *reinterpret_cast<const float2*>(sm + w * piece + i);
+            acc.x = fmaf(f, v.x, acc.x);
+            acc.y = fmaf(f, v.y, acc.y);
+            sum = fmaf(f, sm[w * piece + R * dh + R + r], sum);
+        }
+        if (Z == 1) {
+            finish(r, i - r * dh, acc.x, acc.y, sum, mx);
+        } else {
+            *reinterpret_cast<float2*>(jO + i) = acc;
+            if (i == r * dh) {
+                jO[R * dh + r] = mx;
+                jO[R * dh + R + r] = sum;
+            }
+        }
+    }
+    if (Z > 1) {
+        ptx::cluster_sync();   // every CTA's joined rows are in place
+        const uint32_t own = ptx::smem_addr(jO);
+        for (int i = (z * NW * 32 + threadIdx.x) * 2; i < R * dh; i += Z * NW * 64) {
+            const int r = i / dh;
+            float mz[PR_MAXZ], lz[PR_MAXZ];
+            float2 oz[PR_MAXZ];
+#pragma unroll
+            for (int y = 0; y < PR_MAXZ; ++y) {
+                const uint32_t at = ptx::mapa_shared(own, y < Z ? y : 0);
+                mz[y] = ptx::ld_cluster_f32(at + (R * dh + r) * 4);
+                lz[y] = ptx::ld_cluster_f32(at + (R * dh + R + r) * 4);
+                oz[y].x = ptx::ld_cluster_f32(at + i * 4);
+                oz[y].y = ptx::ld_cluster_f32(at + i * 4 + 4);
+                if (y >= Z) mz[y] = -INFINITY;
+            }
+            float mx = -INFINITY;
+#pragma unroll
+            for (int y = 0; y < PR_MAXZ; ++y) mx = fmaxf(mx, mz[y]);
+            const float base = mx == -INFINITY ? 0.f : mx;
+            float ax = 0.f, ay = 0.f, sum = 0.f;
+#pragma unroll
+            for (int y = 0; y < PR_MAXZ; ++y) {
+                if (y >= Z) break;
+                const float f = exp2_approx(mz[y] - base);
+                ax = fmaf(f, oz[y].x, ax);
+                ay = fmaf(f, oz[y].y, ay);
+                sum = fmaf(f, lz[y], sum);
+            }
+            finish(r, i - r * dh, ax, ay, sum, mx);
+        }
+        __syncwarp();
+        ptx::cluster_sync();   // no CTA leaves while another reads its shared memory
+    }
+}
+
+template <int DHT, int NR, int NW, int STAGES, int MINB>
+cudaError_t launch_rows(const PagedRowsParams& p, cudaStream_t s) {
+    constexpr int STAGE = PR_KEYS * (DHT / 64) * 256;
+    auto k = paged_rows_kernel<DHT, NR, NW, STAGES, MINB>;
+    static std::atomic<uint64_t> attr{0};
+    constexpr int smem = NW * STAGES * STAGE + NR * 8 * (DHT + 2) * 4 + 1024;
+    const cudaError_t e = set_smem_limit_once(k, smem, attr);
+    if (e != cudaSuccess) return e;
+    const PagedDesc& d = p.d;
+    alignas(64) CUtensorMap mk, mv;
+    if (!ct_map(&mk, d.k, d.ks, d.pages, d.page, d.Hkv, d.dh, 1, PR_KEYS, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
+        !ct_map(&mv, d.v, d.vs, d.pages, d.page, d.Hkv, d.dh, 1, PR_KEYS, CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+        return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)(d.B * d.Hkv * p.Z)), block(NW * 32);
+    if (p.Z == 1) return launch_dependent(k, grid, block, smem, s, mk, mv, p);
+    return launch_dependent_cluster(k, grid, block, p.Z, smem, s, mk, mv, p);
+}
+
+}  // namespace
+
+bool paged_rows_supported(const PagedDesc& d) {
+    if (d.dt != DT_BF16 || d.dh % 8 != 0 || d.dh > 128 || d.Tq * (d.H / d.Hkv) > PR_ROWS || d.page % PR_KEYS != 0) return false;
+    if (d.B > 0x7fffffff / 8 / d.Hkv) return false;
+    if ((reinterpret_cast<uintptr_t>(d.q) & 15) || d.qs[0] % 8 || d.qs[1] % 8 || d.qs[2] % 8) return false;
+    return ct_strides_ok(d.k, d.ks, d.page) && ct_strides_ok(d.v, d.vs, d.page) && ct_encode_fn() != nullptr;
+}
+
+cudaError_t launch_paged_rows(const PagedDesc& d, const PagedParts& prefix, const DeviceInfo& dev, cudaStream_t s) {
+    // CTAs and warps to a key head as in attention_cross_rows.cu, by the keys that the table has room for.
+    const int64_t heads = d.B * d.Hkv, sms = dev.num_sms, keys = d.table_pages * d.page;
+    const bool narrow = d.dh <= 64;
+    const int warps = narrow || heads > sms / 2 ? 4 : 8;
+    const int64_t ctas = narrow || warps == 4 ? 2 * sms : sms;   // aimed at; more CTAs only add joins
+    int Z = 1;
+    while (Z < PR_MAXZ && heads * Z * 2 <= ctas && keys >= (int64_t)Z * 2 * warps * 16 * 2) Z *= 2;
+    if (warps == 8 && Z == 8 && heads * 8 > sms / 2) Z = 4;
+    const PagedRowsParams p{d, prefix, (float)(d.scale * 1.4426950408889634), Z, dev.err_word};
+    if (d.Tq * (d.H / d.Hkv) > 8)
+        return narrow ? launch_rows<64, 2, 4, 3, 3>(p, s) : warps == 8 ? launch_rows<128, 2, 8, 2, 1>(p, s) : launch_rows<128, 2, 4, 3, 2>(p, s);
+    return narrow ? launch_rows<64, 1, 4, 3, 4>(p, s) : warps == 8 ? launch_rows<128, 1, 8, 2, 1>(p, s) : launch_rows<128, 1, 4, 3, 2>(p, s);
+}
+
+}  // namespace vit

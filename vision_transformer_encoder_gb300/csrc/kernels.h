@@ -320,7 +320,12 @@ struct PagedPlan {
     size_t workspace;                          // bytes
     int launches;
 };
-enum PagedForm : int { PAGED_GENERIC = 0 };
+// GENERIC: CUDA cores throughout. ROWS: the kernel of few queries for the own keys, joining the prefix's parts.
+enum PagedForm : int { PAGED_GENERIC = 0, PAGED_ROWS = 1 };
+// Few queries (attention_paged_rows.cu): bf16, at most 16 query rows per key head; joins the parts of the prefix that the
+// kernel launched before it leaves (n 0: there is none).
+bool paged_rows_supported(const PagedDesc& d);
+cudaError_t launch_paged_rows(const PagedDesc& d, const PagedParts& prefix, const DeviceInfo& dev, cudaStream_t s);
 PagedPlan plan_paged(const PagedDesc& d, const DeviceInfo& dev);
 // workspace: plan.workspace bytes, 16-byte aligned.
 cudaError_t launch_paged_attention(const PagedDesc& d, const PagedPlan& plan, void* workspace, const DeviceInfo& dev,
