@@ -447,26 +447,28 @@ def test_paged_attention_layouts(Tq, H, Hkv, dh, page, dt):
     """Queries in a fused projection, tokens or heads first; pools side by side in a page, heads before tokens, unaligned."""
     B = 4
     h = Held(Tq, H, Hkv, dh, page, [Tq + 70 * b for b in range(B)], [300, 33], dt=dt)
-    ref = check_paged(h)
+    check_paged(h)
     P = h.kp.shape[0]
     wide = torch.full((B, Tq, H + 3, dh), math.nan, dtype=dt, device=DEV)
     wide[:, :, 1:1 + H] = h.q
     early = torch.empty(Tq, B, H, dh, dtype=dt, device=DEV).transpose(0, 1).copy_(h.q)
     heads = torch.empty(B, H, Tq, dh, dtype=dt, device=DEV).transpose(1, 2).copy_(h.q)
     off = torch.empty(h.q.numel() + 1, dtype=dt, device=DEV)[1:].view(h.q.shape).copy_(h.q)
-    tol = 2.0 ** -7 if dt == BF else 2.0 ** -16
+    # other layouts may take another kernel, whose weights are rounded elsewhere: each is held to the reference
+    o, w, mag, n = h.ref(dh ** -0.5)
+    tol = paged_tol(h, o, w, mag, n, dh)
     for q in (wide[:, :, 1:1 + H], early, heads, off):
-        close(h.call(q=q), ref.double(), tol * (ref.double().abs() + 0.1))
+        close(h.call(q=q), o, tol)
     side = torch.empty(P, 2, page, Hkv, dh, dtype=dt, device=DEV)
     inner = torch.empty(2, P, Hkv, page, dh, dtype=dt, device=DEV).transpose(2, 3)
     odd = torch.empty(2, P, page, Hkv, dh + 1, dtype=dt, device=DEV)[..., :dh]
     for kp, vp in ((side[:, 0], side[:, 1]), (inner[0], inner[1]), (odd[0], odd[1])):
         kp.copy_(h.kp)
         vp.copy_(h.vp)
-        close(h.call(k_pages=kp, v_pages=vp), ref.double(), tol * (ref.double().abs() + 0.1))
-    out = torch.full((ref.numel() + 1,), math.nan, dtype=dt, device=DEV)[1:].view(ref.shape)
+        close(h.call(k_pages=kp, v_pages=vp), o, tol)
+    out = torch.full((h.q.numel() + 1,), math.nan, dtype=dt, device=DEV)[1:].view(h.q.shape)
     assert h.call(out=out) is out
-    close(out, ref.double(), tol * (ref.double().abs() + 0.1))
+    close(out, o, tol)
 
 
 SPECIAL = [(1, 4, 2, 64, [300, 70], []), (3, 8, 2, 128, [400, 9], [500]), (1, 16, 16, 64, [30] * 20, [700]), (40, 4, 4, 64, [300, 70], [200]),
@@ -507,19 +509,23 @@ def test_paged_attention_special_scores(Tq, H, Hkv, dh, own, prefix, dt):
                                                     (200, 4, 2, 80, [400, 250], []), (200, 2, 2, 128, [250, 200], [400])])
 @pytest.mark.parametrize("value", [math.nan, math.inf])
 def test_paged_attention_later_tokens_do_not_reach_earlier_ones(Tq, H, Hkv, dh, own, prefix, dt, value):
-    """The key and value of a sequence's newest token are seen by its last query alone, whatever they hold."""
+    """The key and value of a sequence's newest token are seen by its last query alone, whatever they hold. (Rows on
+    tensor cores that meet such a value are made again with weights that are not rounded: held to the reference, not to the bits.)"""
     h = Held(Tq, H, Hkv, dh, 16, own, prefix, dt=dt)
-    ref = h.call()
+    o, w, mag, n = h.ref(dh ** -0.5)
+    tol = paged_tol(h, o, w, mag, n, dh)
     for b, n in enumerate(own):
         pg, s = slots(h.table, b, n - 1, 16)
         h.vp[pg, s] = value
     got = h.call()
-    assert same(got[:, :-1], ref[:, :-1]) and not torch.isfinite(got[:, -1]).any()
+    close(got[:, :-1], o[:, :-1], tol[:, :-1])
+    assert not torch.isfinite(got[:, -1]).any()
     for b, n in enumerate(own):
         pg, s = slots(h.table, b, n - 1, 16)
         h.kp[pg, s] = value
     got = h.call()
-    assert same(got[:, :-1], ref[:, :-1]) and not torch.isfinite(got[:, -1]).any()
+    close(got[:, :-1], o[:, :-1], tol[:, :-1])
+    assert not torch.isfinite(got[:, -1]).any()
 
 
 @pytest.mark.parametrize("scale", [1e9, 7e17, 1e30])

@@ -295,22 +295,34 @@ cudaError_t generic(const PagedDesc& d, const PagedPlan& plan, const PagedParts&
 
 PagedPlan plan_paged(const PagedDesc& d, const DeviceInfo& dev) {
     PagedPlan plan{};
-    plan.form = paged_rows_supported(d) ? PAGED_ROWS : PAGED_GENERIC;
-    // CTAs of four warps, some eight of them to an SM: cut the keys where there are fewer, in parts of 128 at least
+    const int64_t keys = d.table_pages * d.page, before = d.prefix_pages * d.page;
+    plan.form = paged_rows_supported(d) ? PAGED_ROWS : paged_tc_supported(d, true) ? PAGED_TC : PAGED_GENERIC;
+    plan.prefix_tc = plan.form != PAGED_GENERIC && d.prefix_table && paged_tc_supported(d, false);
+    // Generic: CTAs of four warps, some eight of them to an SM: cut the keys where there are fewer, in parts of 128 at least
     const int RT = generic_rows(d);
-    const int64_t G = d.H / d.Hkv, want = 8 * (int64_t)dev.num_sms;
-    auto parts = [&](int64_t blocks, int64_t keys) {
-        int64_t z = want / blocks, most = keys / 128;
+    const int64_t G = d.H / d.Hkv;
+    auto cut = [&](int64_t blocks, int64_t n) {
+        int64_t z = 8 * (int64_t)dev.num_sms / blocks, most = n / 128;
         z = z < most ? z : most;
         return (int)(z < 1 ? 1 : z > 32 ? 32 : z);
     };
-    if (d.prefix_table)
-        plan.prefix_parts = parts(d.groups * d.Hkv * ((d.B / d.groups * d.Tq * G + RT - 1) / RT), d.prefix_pages * d.page);
-    if (plan.form == PAGED_GENERIC) {
-        plan.own_parts = parts(d.B * d.Hkv * ((d.Tq * G + RT - 1) / RT), d.table_pages * d.page);
+    // Tensor cores: a CTA to an SM, parts of four key tiles at least
+    auto cut_tc = [&](int64_t items, int64_t n) {
+        int64_t z = dev.num_sms / items, most = n / 512;
+        z = z < most ? z : most;
+        return (int)(z < 1 ? 1 : z > 32 ? 32 : z);
+    };
+    if (plan.form == PAGED_TC) {
+        const bool apart = plan.prefix_tc && paged_tc_apart(d);
+        if (apart) plan.prefix_parts = cut_tc(paged_tc_items(d, false), before);
+        plan.own_parts = cut_tc(paged_tc_items(d, true), keys + (apart ? 0 : before));
         plan.partial = plan.prefix_parts + plan.own_parts > 1;
     } else {
-        plan.partial = plan.prefix_parts > 0;
+        if (d.prefix_table)
+            plan.prefix_parts = plan.prefix_tc ? cut_tc(paged_tc_items(d, false), before)
+                                               : cut(d.groups * d.Hkv * ((d.B / d.groups * d.Tq * G + RT - 1) / RT), before);
+        if (plan.form == PAGED_GENERIC) plan.own_parts = cut(d.B * d.Hkv * ((d.Tq * G + RT - 1) / RT), keys);
+        plan.partial = plan.form == PAGED_GENERIC ? plan.prefix_parts + plan.own_parts > 1 : plan.prefix_parts > 0;
     }
     plan.launches = plan.partial ? 2 : 1;
     if (plan.partial)
@@ -330,10 +342,14 @@ cudaError_t launch_paged_attention(const PagedDesc& d, const PagedPlan& plan, vo
     }
     cudaError_t e;
     if (plan.form == PAGED_ROWS) {
-        e = plan.partial ? generic<__nv_bfloat16, float>(d, plan, parts, dev, s, false) : cudaSuccess;
-        return e != cudaSuccess ? e : launch_paged_rows(d, parts, dev, s);
+        if (plan.partial) {
+            e = plan.prefix_tc ? launch_paged_tc(d, plan, parts, false, dev, s) : generic<__nv_bfloat16, float>(d, plan, parts, dev, s, false);
+            if (e != cudaSuccess) return e;
+        }
+        return launch_paged_rows(d, parts, dev, s);
     }
-    if (d.dt == DT_F64) e = generic<double, double>(d, plan, parts, dev, s);
+    if (plan.form == PAGED_TC) e = launch_paged_tc(d, plan, parts, true, dev, s);
+    else if (d.dt == DT_F64) e = generic<double, double>(d, plan, parts, dev, s);
     else if (d.dt == DT_F32) e = generic<float, float>(d, plan, parts, dev, s);
     else e = generic<__nv_bfloat16, float>(d, plan, parts, dev, s);
     if (e != cudaSuccess || !plan.partial) return e;

@@ -317,15 +317,24 @@ struct PagedPlan {
     int form;                                  // PagedForm
     int own_parts, prefix_parts;               // parts along the keys; prefix_parts 0: no prefix, or in the own ones
     bool partial;                              // results go through workspace
+    bool prefix_tc;                            // ROWS: the prefix on tensor cores (tcgen05)
     size_t workspace;                          // bytes
     int launches;
 };
-// GENERIC: CUDA cores throughout. ROWS: the kernel of few queries for the own keys, joining the prefix's parts.
-enum PagedForm : int { PAGED_GENERIC = 0, PAGED_ROWS = 1 };
+// GENERIC: CUDA cores throughout. ROWS: the kernel of few queries for the own keys, joining the prefix's parts. TC: tensor
+// cores (tcgen05) throughout.
+enum PagedForm : int { PAGED_GENERIC = 0, PAGED_ROWS = 1, PAGED_TC = 2 };
 // Few queries (attention_paged_rows.cu): bf16, at most 16 query rows per key head; joins the parts of the prefix that the
 // kernel launched before it leaves (n 0: there is none).
 bool paged_rows_supported(const PagedDesc& d);
 cudaError_t launch_paged_rows(const PagedDesc& d, const PagedParts& prefix, const DeviceInfo& dev, cudaStream_t s);
+// Tensor cores (attention_paged_tc.cu): bf16, head widths 64, 80, 96 and 128. own: items of a sequence's own keys (with
+// the prefix in front where plan.prefix_parts is 0), beside those of the prefixes.
+bool paged_tc_supported(const PagedDesc& d, bool own);
+int64_t paged_tc_items(const PagedDesc& d, bool own);   // of one part each
+bool paged_tc_apart(const PagedDesc& d);                // whether the prefix is better worked off apart
+cudaError_t launch_paged_tc(const PagedDesc& d, const PagedPlan& plan, const PagedParts& parts, bool own, const DeviceInfo& dev,
+                            cudaStream_t s);
 PagedPlan plan_paged(const PagedDesc& d, const DeviceInfo& dev);
 // workspace: plan.workspace bytes, 16-byte aligned.
 cudaError_t launch_paged_attention(const PagedDesc& d, const PagedPlan& plan, void* workspace, const DeviceInfo& dev,
