@@ -32,6 +32,12 @@ __device__ __forceinline__ void griddep_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// A load that stays behind griddep_wait: the compiler may take those of __ldg for constant and move them in front.
+template <typename T> __device__ __forceinline__ T load(const T* p) { return *p; }
+
+// Fetches a line into L2 and goes on: a hint, for memory that may still be written.
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 __device__ __forceinline__ uint64_t global_timer_ns() {
     uint64_t t;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));

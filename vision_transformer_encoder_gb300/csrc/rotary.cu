@@ -8,9 +8,10 @@
 // (2^-52 of it): no range reduction, and far positions lose nothing. Sine and cosine are the hardware's on [-pi, pi] for
 // bf16 (off by 2^-20, where a result is rounded at 2^-9), sincospi for fp32 and fp64.
 //
-// Bound by reading and writing each head once. A thread owns a 16-byte unit of a head (both halves of its pairs) of
-// one token: it makes their sines once and walks over the token's heads, four in flight. With few tokens the heads go to
-// threads of their own.
+// Bound by reading and writing each head once. A block takes a few tokens: it makes their sines and cosines once, in shared
+// memory, and streams 16-byte units of all their heads past them (both halves of a pair where they lie apart). Sines of its
+// own for each thread, which then walked over the heads with eight units in flight, kept 70 to 118 registers and ran at
+// 4.4 TB/s instead. With few tokens the heads go to blocks of their own.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -23,7 +24,7 @@
 namespace vit {
 namespace {
 
-constexpr int RO_THREADS = 256, RO_MAXPAIRS = 256, RO_AHEAD = 4;
+constexpr int RO_THREADS = 256, RO_MAXPAIRS = 256, RO_TOKENS = 32, RO_SINES = 1024;
 
 // f / 2 pi as a fraction of a turn in units of 2^-64
 __device__ __forceinline__ uint64_t turn_of(double f) {
@@ -63,15 +64,15 @@ __device__ __forceinline__ Token token_of(const RotaryDesc& d, int64_t tok) {
         x.b = tok / d.T;
         x.t = tok % d.T;
     }
-    const int64_t start = d.starts ? (int64_t)__ldg(d.starts + x.b) : 0;
+    const int64_t start = d.starts ? (int64_t)load(d.starts + x.b) : 0;
     const int64_t u = start + x.t;
-    x.pos = d.positions ? (int64_t)__ldg(d.positions + tok) : u;
+    x.pos = d.positions ? (int64_t)load(d.positions + tok) : u;
     x.live = false;
     x.page = x.slot = 0;
-    if (d.Hkv > 0 && u >= 0 && x.t < (d.lens ? (int64_t)__ldg(d.lens + x.b) : d.T)) {
+    if (d.Hkv > 0 && u >= 0 && x.t < (d.lens ? (int64_t)load(d.lens + x.b) : d.T)) {
         const int64_t i = u <= 0x7fffffff && d.page <= 0x7fffffff ? (int64_t)((uint32_t)u / (uint32_t)d.page) : u / d.page;
         if (i < d.table_pages) {
-            x.page = __ldg(d.table + x.b * d.table_pages + i);
+            x.page = load(d.table + x.b * d.table_pages + i);
             x.slot = u - i * d.page;
             x.live = x.page >= 0 && x.page < d.pages;
         }
@@ -129,85 +130,125 @@ template <typename T> struct Unit {
     }
 };
 
-// groups: threads that share a token's heads; each takes every groups-th.
+// tile: tokens of a block; groups: blocks that share a token's heads, `span` each.
 template <typename T, bool HALF>
-__global__ void __launch_bounds__(RO_THREADS) rotary_units_kernel(const __grid_constant__ RotaryDesc d, int groups) {
-    constexpr int N = Unit<T>::N, PAIRS = HALF ? N : N / 2;
+__global__ void __launch_bounds__(RO_THREADS) rotary_units_kernel(const __grid_constant__ RotaryDesc d, int tile, int groups, int span) {
+    constexpr int N = Unit<T>::N, PAIRS = HALF ? N : N / 2, AHEAD = 2;
     __shared__ uint64_t turns[RO_MAXPAIRS];
+    __shared__ __align__(16) float sines[2 * RO_SINES];   // token by token: cosines, sines
+    // offsets of a token's rows: queries, keys and values, where they come from and go to
+    __shared__ int64_t from[RO_TOKENS][3], to[RO_TOKENS][3], place[RO_TOKENS];
+    __shared__ bool live[RO_TOKENS];
     griddep_wait();
     griddep_launch_dependents();
-    for (int i = threadIdx.x; i < d.n; i += RO_THREADS) turns[i] = turn_of(d.frequencies[i]);
+    const int n = (int)d.n, half = HALF ? n / N : 0;   // units whose partner is half units on
+    const int items = (int)d.dh / N - half, heads = (int)d.H, Hkv = (int)d.Hkv, HH = heads + 2 * Hkv;
+    const int64_t tokens = d.B * d.T, first = (int64_t)(blockIdx.x / groups) * tile;
+    const int h0 = (int)(blockIdx.x % groups) * span, h1 = min(HH, h0 + span), width = h1 - h0;
+    const int count = (int)min((int64_t)tile, tokens - first);
+    for (int i = threadIdx.x; i < n; i += RO_THREADS) turns[i] = turn_of(d.frequencies[i]);
+    for (int i = threadIdx.x; i < count; i += RO_THREADS) {
+        const Token x = token_of(d, first + i);
+        from[i][0] = x.b * d.qs[0] + x.t * d.qs[1];
+        from[i][1] = x.b * d.ks[0] + x.t * d.ks[1];
+        from[i][2] = x.b * d.vs[0] + x.t * d.vs[1];
+        to[i][0] = x.b * d.qo[0] + x.t * d.qo[1];
+        to[i][1] = x.page * d.kp[0] + x.slot * d.kp[1];
+        to[i][2] = x.page * d.vp[0] + x.slot * d.vp[1];
+        place[i] = x.pos;
+        live[i] = x.live;
+    }
     __syncthreads();
-    const int half = HALF ? (int)d.n / N : 0;   // units whose partner is half units on
-    const int items = (int)d.dh / N - half, HH = (int)(d.H + 2 * d.Hkv), per = groups * items;
-    const int64_t tokens = d.B * d.T;
-    const int64_t total = tokens * per;
     const float scale = (float)d.scale;
-    for (int64_t i = (int64_t)blockIdx.x * RO_THREADS + threadIdx.x; i < total; i += (int64_t)gridDim.x * RO_THREADS) {
-        int64_t tok;
-        int rest;
-        if (total <= 0x7fffffff) {
-            tok = (uint32_t)i / (uint32_t)per;
-            rest = (uint32_t)i % (uint32_t)per;
-        } else {
-            tok = i / per;
-            rest = (int)(i % per);
-        }
-        const int group = rest / items, item = rest % items;
-        const Token x = token_of(d, tok);
-        const bool pair = HALF ? item < half : item * N < 2 * d.n;
-        // with a partner: units item and item + half; the others stand behind them
-        const int at = (HALF && !pair ? item + half : item) * N, to = at + (HALF ? (int)d.n : 0);
-        float c[PAIRS], s[PAIRS];
-        if (pair) {
-            const uint64_t p = (uint64_t)x.pos;
-            const int first = HALF ? at : at / 2;
+    for (int i = threadIdx.x; i < count * n; i += RO_THREADS) {
+        const int t = i / n, j = i - t * n;
+        cos_sin<T, float>(turns[j] * (uint64_t)place[t], scale, sines[2 * t * n + j], sines[(2 * t + 1) * n + j]);
+    }
+    __syncthreads();
+    // rows of the block, a head of a token each: this thread's unit of every step-th
+    const int item = threadIdx.x % items, step = RO_THREADS / items;
+    int row = threadIdx.x / items;
+    if (row >= step) return;
+    const bool pair = HALF ? item < half : item * N < 2 * n;
+    // with a partner: units item and item + half; the others stand behind them
+    const int at = (HALF && !pair ? item + half : item) * N, partner = at + (HALF ? n : 0), sine = HALF ? at : at / 2;
+    int t = row / width, h = row % width;
+    const int dt = step / width, dh = step % width;
+    while (t < count) {
+        Unit<T> a[AHEAD], b[HALF ? AHEAD : 1];
+        T* dst[AHEAD];
+        int tt[AHEAD];
+        bool on[AHEAD], turned[AHEAD];
 #pragma unroll
-            for (int j = 0; j < PAIRS; ++j) cos_sin<T, float>(turns[first + j] * p, scale, c[j], s[j]);
-        }
-        for (int h0 = group; h0 < HH; h0 += RO_AHEAD * groups) {
-            Unit<T> a[RO_AHEAD], b[HALF ? RO_AHEAD : 1];
-            T* dst[RO_AHEAD];
-            bool on[RO_AHEAD], turned[RO_AHEAD];
-#pragma unroll
-            for (int j = 0; j < RO_AHEAD; ++j) {
+        for (int j = 0; j < AHEAD; ++j) {
+            on[j] = false;
+            tt[j] = t;
+            if (t < count) {
+                const int hh = h0 + h;
                 const T* src;
-                on[j] = h0 + j * groups < HH && row_of<T>(d, x, h0 + j * groups, src, dst[j], turned[j]);
-                if (!on[j]) continue;
-                a[j].raw = *reinterpret_cast<const uint4*>(src + at);
-                if constexpr (HALF)
-                    if (pair) b[j].raw = *reinterpret_cast<const uint4*>(src + to);
-            }
-#pragma unroll
-            for (int j = 0; j < RO_AHEAD; ++j) {
-                if (!on[j]) continue;
-                if (pair && turned[j]) {
-                    float u[N];
-                    a[j].get(u);
-                    if constexpr (HALF) {
-                        float v[N];
-                        b[j].get(v);
-#pragma unroll
-                        for (int e = 0; e < N; ++e) {
-                            const float r = fmaf(u[e], c[e], -v[e] * s[e]);
-                            v[e] = fmaf(u[e], s[e], v[e] * c[e]);
-                            u[e] = r;
-                        }
-                        b[j].put(v);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < N / 2; ++e) {
-                            const float r = fmaf(u[2 * e], c[e], -u[2 * e + 1] * s[e]);
-                            u[2 * e + 1] = fmaf(u[2 * e], s[e], u[2 * e + 1] * c[e]);
-                            u[2 * e] = r;
-                        }
-                    }
-                    a[j].put(u);
+                if (hh < heads) {
+                    src = static_cast<const T*>(d.q) + from[t][0] + hh * d.qs[2];
+                    dst[j] = static_cast<T*>(d.q_out) + to[t][0] + hh * d.qo[2];
+                    on[j] = turned[j] = true;
+                } else if (hh < heads + Hkv) {
+                    src = static_cast<const T*>(d.k) + from[t][1] + (hh - heads) * d.ks[2];
+                    dst[j] = static_cast<T*>(d.k_pages) + to[t][1] + (hh - heads) * d.kp[2];
+                    on[j] = live[t];
+                    turned[j] = true;
+                } else {
+                    src = static_cast<const T*>(d.v) + from[t][2] + (hh - heads - Hkv) * d.vs[2];
+                    dst[j] = static_cast<T*>(d.v_pages) + to[t][2] + (hh - heads - Hkv) * d.vp[2];
+                    on[j] = live[t];
+                    turned[j] = false;
                 }
-                *reinterpret_cast<uint4*>(dst[j] + at) = a[j].raw;
-                if constexpr (HALF)
-                    if (pair) *reinterpret_cast<uint4*>(dst[j] + to) = b[j].raw;
+                if (on[j]) {
+                    a[j].raw = *reinterpret_cast<const uint4*>(src + at);
+                    if constexpr (HALF)
+                        if (pair) b[j].raw = *reinterpret_cast<const uint4*>(src + partner);
+                }
+                t += dt;
+                h += dh;
+                if (h >= width) {
+                    h -= width;
+                    ++t;
+                }
             }
+        }
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            if (!on[j]) continue;
+            if (pair && turned[j]) {
+                float c[PAIRS], s[PAIRS], u[N];
+                const float* cs = sines + 2 * tt[j] * n + sine;
+#pragma unroll
+                for (int e = 0; e < PAIRS; ++e) {
+                    c[e] = cs[e];
+                    s[e] = cs[n + e];
+                }
+                a[j].get(u);
+                if constexpr (HALF) {
+                    float v[N];
+                    b[j].get(v);
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        const float r = fmaf(u[e], c[e], -v[e] * s[e]);
+                        v[e] = fmaf(u[e], s[e], v[e] * c[e]);
+                        u[e] = r;
+                    }
+                    b[j].put(v);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < N / 2; ++e) {
+                        const float r = fmaf(u[2 * e], c[e], -u[2 * e + 1] * s[e]);
+                        u[2 * e + 1] = fmaf(u[2 * e], s[e], u[2 * e + 1] * c[e]);
+                        u[2 * e] = r;
+                    }
+                }
+                a[j].put(u);
+            }
+            *reinterpret_cast<uint4*>(dst[j] + at) = a[j].raw;
+            if constexpr (HALF)
+                if (pair) *reinterpret_cast<uint4*>(dst[j] + partner) = b[j].raw;
         }
     }
 }
@@ -264,20 +305,37 @@ cudaError_t launch_rotary(const RotaryDesc& d, const DeviceInfo& dev, cudaStream
     if (d.Hkv)
         units = units && units_fit(d.k, d.ks, N) && units_fit(d.v, d.vs, N) && units_fit(d.k_pages, d.kp, N) &&
                 units_fit(d.v_pages, d.vp, N);
-    const int64_t items = units ? d.dh / N - (half ? d.n / N : 0) : d.dh - d.n;
+    const dim3 block(RO_THREADS);
+    if (units) {
+        const int64_t items = d.dh / N - (half ? d.n / N : 0), tokens = d.B * d.T;
+        // Tokens to a block: as many as leave four blocks to an SM, up to RO_SINES pairs of sines; where one leaves fewer
+        // its heads are dealt out too, as rows enough for the block's threads.
+        int64_t tile = tokens / (4 * (int64_t)dev.num_sms);
+        const int64_t most = d.n ? RO_SINES / d.n : RO_TOKENS;
+        tile = tile > most ? most : tile;
+        tile = tile > RO_TOKENS ? RO_TOKENS : tile < 1 ? 1 : tile;
+        int64_t groups = 4 * (int64_t)dev.num_sms / ((tokens + tile - 1) / tile);
+        const int64_t rows = RO_THREADS / items, apart = (HH + rows - 1) / rows;
+        groups = groups < 1 ? 1 : groups > apart ? apart : groups;
+        const int64_t span = (HH + groups - 1) / groups;
+        groups = (HH + span - 1) / span;
+        const int64_t blocks = (tokens + tile - 1) / tile * groups;
+        if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+        const dim3 grid((unsigned)blocks);
+        if (d.dt == DT_BF16)
+            return half ? launch_dependent(rotary_units_kernel<__nv_bfloat16, true>, grid, block, 0, s, d, (int)tile, (int)groups, (int)span)
+                        : launch_dependent(rotary_units_kernel<__nv_bfloat16, false>, grid, block, 0, s, d, (int)tile, (int)groups, (int)span);
+        return half ? launch_dependent(rotary_units_kernel<float, true>, grid, block, 0, s, d, (int)tile, (int)groups, (int)span)
+                    : launch_dependent(rotary_units_kernel<float, false>, grid, block, 0, s, d, (int)tile, (int)groups, (int)span);
+    }
+    const int64_t items = d.dh - d.n;
     // heads of a token that one thread walks over: all of them where there are threads enough
     const double threads = (double)d.B * d.T * HH * items;
     int64_t walk = (int64_t)(threads / (1024.0 * dev.num_sms));
     walk = walk < 1 ? 1 : walk > HH ? HH : walk;
     const int groups = (int)((HH + walk - 1) / walk);
     const double want = ((double)d.B * d.T * groups * items + RO_THREADS - 1) / RO_THREADS;
-    const dim3 grid((unsigned)(want < 8.0 * dev.num_sms ? want : 8.0 * dev.num_sms)), block(RO_THREADS);
-    if (units && d.dt == DT_BF16)
-        return half ? launch_dependent(rotary_units_kernel<__nv_bfloat16, true>, grid, block, 0, s, d, groups)
-                    : launch_dependent(rotary_units_kernel<__nv_bfloat16, false>, grid, block, 0, s, d, groups);
-    if (units)
-        return half ? launch_dependent(rotary_units_kernel<float, true>, grid, block, 0, s, d, groups)
-                    : launch_dependent(rotary_units_kernel<float, false>, grid, block, 0, s, d, groups);
+    const dim3 grid((unsigned)(want < 8.0 * dev.num_sms ? want : 8.0 * dev.num_sms));
     if (d.dt == DT_F64) return launch_dependent(rotary_generic_kernel<double, double>, grid, block, 0, s, d, groups);
     if (d.dt == DT_F32) return launch_dependent(rotary_generic_kernel<float, float>, grid, block, 0, s, d, groups);
     return launch_dependent(rotary_generic_kernel<__nv_bfloat16, float>, grid, block, 0, s, d, groups);
