@@ -72,13 +72,13 @@ __global__ void __launch_bounds__(PG_THREADS) paged_generic_kernel(const __grid_
         const int64_t tokens = prefix ? S * d.Tq : d.Tq, first = at * tokens;
         const int32_t* table = prefix ? d.prefix_table + at * d.prefix_pages : d.table + at * d.table_pages;
         const int64_t held = (prefix ? d.prefix_pages : d.table_pages) * d.page;
-        const int len = (int)min((int64_t)max(__ldg((prefix ? d.prefix_lens : d.kv_lens) + at), 0), held);
+        const int len = (int)min((int64_t)max(load((prefix ? d.prefix_lens : d.kv_lens) + at), 0), held);
         __syncthreads();   // the last block's rows have been stored
         for (int r = warp; r < RT; r += PG_THREADS / 32) {
             const int64_t n = rb * RT + r, token = first + n / G, h = hk * G + n % G;
             const bool there = n < tokens * G;
             const int64_t b = there ? token / d.Tq : 0, t = token - b * d.Tq;
-            const int64_t qlen = there ? (d.q_lens ? min((int64_t)max(__ldg(d.q_lens + b), 0), d.Tq) : d.Tq) : 0;
+            const int64_t qlen = there ? (d.q_lens ? min((int64_t)max(load(d.q_lens + b), 0), d.Tq) : d.Tq) : 0;
             if (lane == 0) {
                 srow[r] = there ? token * d.H + h : -1;
                 slim[r] = there && t < qlen ? (prefix ? len : (int)max((int64_t)0, len - (qlen - 1 - t))) : 0;
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(PG_THREADS) paged_generic_kernel(const __grid_
             const int u0 = tile * PG_KEYS, n = min(PG_KEYS, most - u0);
             int* spage = spages[tile & 1];   // the last tile's may still be read
             if (tid < PG_KEYS) {
-                int pg = tid < n ? __ldg(table + (int64_t)(u0 + tid) / d.page) : -1;
+                int pg = tid < n ? load(table + (int64_t)(u0 + tid) / d.page) : -1;
                 spage[tid] = pg >= 0 && pg < d.pages ? pg : -1;
             }
             __syncthreads();   // the last tile's values have been read
@@ -295,34 +295,39 @@ cudaError_t generic(const PagedDesc& d, const PagedPlan& plan, const PagedParts&
 
 PagedPlan plan_paged(const PagedDesc& d, const DeviceInfo& dev) {
     PagedPlan plan{};
-    const int64_t keys = d.table_pages * d.page, before = d.prefix_pages * d.page;
-    plan.form = paged_rows_supported(d) ? PAGED_ROWS : paged_tc_supported(d, true) ? PAGED_TC : PAGED_GENERIC;
-    plan.prefix_tc = plan.form != PAGED_GENERIC && d.prefix_table && paged_tc_supported(d, false);
-    // Generic: CTAs of four warps, some eight of them to an SM: cut the keys where there are fewer, in parts of 128 at least
+    const int64_t keys = d.table_pages * d.page, before = d.prefix_pages * d.page, sms = dev.num_sms;
+    plan.form = paged_rows_supported(d) ? PAGED_ROWS : paged_tc_supported(d, true) ? PAGED_TC : paged_f32_supported(d) ? PAGED_F32 : PAGED_GENERIC;
+    plan.prefix_tc = (plan.form == PAGED_ROWS || plan.form == PAGED_TC) && d.prefix_table && paged_tc_supported(d, false);
+    // `blocks` CTAs over n keys, cut into parts of `least` keys or more until there are `want` of them
+    auto cut = [](int64_t want, int64_t blocks, int64_t n, int64_t least) {
+        int64_t z = want / blocks;
+        z = z < n / least ? z : n / least;
+        return (int)(z < 1 ? 1 : z > 32 ? 32 : z);
+    };
     const int RT = generic_rows(d);
-    const int64_t G = d.H / d.Hkv;
-    auto cut = [&](int64_t blocks, int64_t n) {
-        int64_t z = 8 * (int64_t)dev.num_sms / blocks, most = n / 128;
-        z = z < most ? z : most;
-        return (int)(z < 1 ? 1 : z > 32 ? 32 : z);
-    };
-    // Tensor cores: a CTA to an SM, parts of four key tiles at least
-    auto cut_tc = [&](int64_t items, int64_t n) {
-        int64_t z = dev.num_sms / items, most = n / 512;
-        z = z < most ? z : most;
-        return (int)(z < 1 ? 1 : z > 32 ? 32 : z);
-    };
+    const int64_t G = d.H / d.Hkv, own_rb = (d.Tq * G + RT - 1) / RT, prefix_rb = (d.B / d.groups * d.Tq * G + RT - 1) / RT;
     if (plan.form == PAGED_TC) {
+        // A CTA to an SM. Parts cost a write and a read of fp32 rows: items that fill the SMs once are not cut (2 x 1025
+        // queries over 4100 keys, 120 items: 60 us, in two parts 72, in three 64).
         const bool apart = plan.prefix_tc && paged_tc_apart(d);
-        if (apart) plan.prefix_parts = cut_tc(paged_tc_items(d, false), before);
-        plan.own_parts = cut_tc(paged_tc_items(d, true), keys + (apart ? 0 : before));
+        if (apart) plan.prefix_parts = cut(sms, paged_tc_items(d, false), before, 512);
+        plan.own_parts = cut(sms, paged_tc_items(d, true), keys + (apart ? 0 : before), 512);
+        plan.partial = plan.prefix_parts + plan.own_parts > 1;
+    } else if (plan.form == PAGED_F32) {
+        // CTAs of four warps, four of them to an SM (8: 14.7 us, 16: 14.7, 4: 13.1 for 8 x 12 heads over 577 keys
+        // behind 197), parts of two steps to each warp at least
+        plan.own_parts = cut(4 * sms, paged_f32_blocks(d, true), keys, 64);
+        if (d.prefix_table) plan.prefix_parts = cut(4 * sms, paged_f32_blocks(d, false), before, 64);
         plan.partial = plan.prefix_parts + plan.own_parts > 1;
     } else {
+        // the prefix of few queries: two key tiles to a part at least, one for each softmax group (32 x 16 heads behind
+        // 1025 keys: 12.7 us, with four 13.8)
         if (d.prefix_table)
-            plan.prefix_parts = plan.prefix_tc ? cut_tc(paged_tc_items(d, false), before)
-                                               : cut(d.groups * d.Hkv * ((d.B / d.groups * d.Tq * G + RT - 1) / RT), before);
-        if (plan.form == PAGED_GENERIC) plan.own_parts = cut(d.B * d.Hkv * ((d.Tq * G + RT - 1) / RT), keys);
-        plan.partial = plan.form == PAGED_GENERIC ? plan.prefix_parts + plan.own_parts > 1 : plan.prefix_parts > 0;
+            plan.prefix_parts = plan.prefix_tc ? cut(sms, paged_tc_items(d, false), before, 256)
+                                               : cut(8 * sms, d.groups * d.Hkv * prefix_rb, before, 128);
+        // CTAs of four warps, some eight of them to an SM
+        if (plan.form == PAGED_GENERIC) plan.own_parts = cut(8 * sms, d.B * d.Hkv * own_rb, keys, 128);
+        plan.partial = plan.prefix_parts > 0 || plan.own_parts > 1;
     }
     plan.launches = plan.partial ? 2 : 1;
     if (plan.partial)
@@ -342,13 +347,14 @@ cudaError_t launch_paged_attention(const PagedDesc& d, const PagedPlan& plan, vo
     }
     cudaError_t e;
     if (plan.form == PAGED_ROWS) {
-        if (plan.partial) {
+        if (plan.prefix_parts) {
             e = plan.prefix_tc ? launch_paged_tc(d, plan, parts, false, dev, s) : generic<__nv_bfloat16, float>(d, plan, parts, dev, s, false);
             if (e != cudaSuccess) return e;
         }
         return launch_paged_rows(d, parts, dev, s);
     }
-    if (plan.form == PAGED_TC) e = launch_paged_tc(d, plan, parts, true, dev, s);
+    if (plan.form == PAGED_F32) e = launch_paged_f32(d, plan, parts, s);
+    else if (plan.form == PAGED_TC) e = launch_paged_tc(d, plan, parts, true, dev, s);
     else if (d.dt == DT_F64) e = generic<double, double>(d, plan, parts, dev, s);
     else if (d.dt == DT_F32) e = generic<float, float>(d, plan, parts, dev, s);
     else e = generic<__nv_bfloat16, float>(d, plan, parts, dev, s);

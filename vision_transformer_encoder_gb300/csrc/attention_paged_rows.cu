@@ -28,13 +28,14 @@
 namespace vit {
 namespace {
 
-constexpr int PR_ROWS = 16, PR_MAXZ = 8, PR_KEYS = 16;
+constexpr int PR_ROWS = 16, PR_MAXZ = 8, PR_KEYS = 32, PR_HALF = 16;   // a tile is two halves, each within one page
+constexpr float PR_SLACK = 8.f;   // log2 of the weights that are carried before a rescale
 
 struct PagedRowsParams {
     PagedDesc d;
     PagedParts parts;    // the prefix's; n 0: none
     float scale_log2;
-    int Z;
+    int Z;               // CTAs of a cluster
     uint32_t* err;
 };
 
@@ -49,6 +50,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                   const __grid_constant__ PagedRowsParams p) {
     constexpr int NCH = DHT / 64, STAGE = PR_KEYS * NCH * 256;
     constexpr int BOX = PR_KEYS * 128;   // 64 columns of one tile
+    constexpr int NT = PR_KEYS / 16;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bars[NW][STAGES];
     const PagedDesc& d = p.d;
@@ -73,39 +75,71 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         ptx::prefetch_tensormap(&tmV);
     }
     __syncwarp();
+    // tiles of this warp: first, first + stride, ...
+    const int first = z * NW + warp, stride = Z * NW;
     if (!p.parts.n) {
+        // While the kernel in front ends: what is read first goes to L2, by lengths and pages as they stand, which may
+        // still change. They are read again behind the wait.
+        if (lane < 2) {
+            const int len = __ldcg(d.kv_lens + b), hpp = (int)d.page / PR_HALF;
+#pragma unroll
+            for (int i = 0; i < STAGES; ++i) {
+                const int half = 2 * (first + i * stride) + lane;
+                const int pg = half / hpp < d.table_pages && half < len / PR_HALF ? __ldcg(d.table + (int64_t)b * d.table_pages + half / hpp) : -1;
+                if (pg < 0 || pg >= d.pages) continue;
+#pragma unroll
+                for (int c = 0; c < NCH; ++c) {
+                    ptx::tma_prefetch_4d(&tmK, c * 64, h, half % hpp * PR_HALF, pg);
+                    ptx::tma_prefetch_4d(&tmV, c * 64, h, half % hpp * PR_HALF, pg);
+                }
+            }
+        }
         griddep_wait();
         griddep_launch_dependents();
     }
 
-    const int held = (int)(d.table_pages * d.page), tpp = (int)d.page / PR_KEYS;
-    const int len = min(max(__ldg(d.kv_lens + b), 0), held);
-    const int new_ = d.q_lens ? min(max(__ldg(d.q_lens + b), 0), Tq) : Tq;
-    // tiles of this warp: first, first + stride, ...; a sequence without new tokens needs none
-    const int tiles = new_ > 0 ? (len + PR_KEYS - 1) / PR_KEYS : 0, first = z * NW + warp, stride = Z * NW;
+    const int held = (int)(d.table_pages * d.page), hpp = (int)d.page / PR_HALF;
     const int32_t* table = d.table + (int64_t)b * d.table_pages;
-    auto entry = [&](int tile) -> int { return tile < tiles ? __ldg(table + tile / tpp) : -1; };
-    uint32_t there = 0;   // stages with a tile on its way or landed
-    auto request = [&](int tile, int pg, int st) {   // converged
-        if (pg < 0 || pg >= d.pages) return;
-        there |= 1u << st;
-        if (lane != 0) return;
-        uint8_t* dst = ring + st * STAGE;
-        const int token = tile % tpp * PR_KEYS;
-        ptx::mbar_arrive_expect_tx(bar + st, STAGE);
-#pragma unroll
-        for (int c = 0; c < NCH; ++c) ptx::tma_load_4d(dst + c * BOX, &tmK, bar + st, c * 64, h, token, pg);
-#pragma unroll
-        for (int c = 0; c < NCH; ++c) ptx::tma_load_4d(dst + STAGE / 2 + c * BOX, &tmV, bar + st, c * 64, h, token, pg);
+    // Lanes 0 and 1 look the pages of a tile's halves up: entry and half in the page, of the tile that comes next. Entries
+    // behind the last key are read with the others, so that the first ones are asked for together with the length.
+    int place = (2 * first + (lane & 1)) / hpp, part_of = (2 * first + (lane & 1)) % hpp;
+    const int place_step = 2 * stride / hpp, part_step = 2 * stride % hpp;
+    struct Page { int pg, half; };
+    auto look_up = [&]() -> Page {   // in turn: first, first + stride, ...
+        const Page x{place < d.table_pages ? load(table + place) : -1, part_of};
+        place += place_step;
+        part_of += part_step;
+        if (part_of >= hpp) {
+            part_of -= hpp;
+            ++place;
+        }
+        return x;
     };
-    {
-        int pg[STAGES];
+    Page ahead, early[STAGES];
 #pragma unroll
-        for (int i = 0; i < STAGES; ++i) pg[i] = entry(first + i * stride);
+    for (int i = 0; i < STAGES; ++i) early[i] = look_up();
+    ahead = look_up();
+    const int len = min(max(load(d.kv_lens + b), 0), held);
+    const int new_ = d.q_lens ? min(max(load(d.q_lens + b), 0), Tq) : Tq;
+    const int tiles = new_ > 0 ? (len + PR_KEYS - 1) / PR_KEYS : 0;   // a sequence without new tokens needs none
+    uint32_t absent = 0;   // two bits of each stage: its halves' pages are
+    auto request = [&](int tile, const Page& x, int st) {   // converged
+        if (tile >= tiles) return;
+        const bool on = lane < 2 && (tile * 2 + lane) * PR_HALF < len, there = x.pg >= 0 && x.pg < d.pages;
+        absent = (absent & ~(3u << (2 * st))) | __ballot_sync(0xffffffffu, on && !there) << (2 * st);
+        if (lane == 0) ptx::mbar_arrive_expect_tx(bar + st, (tile * 2 + 1) * PR_HALF < len ? STAGE : STAGE / 2);
+        __syncwarp();
+        if (on) {
+            uint8_t* dst = ring + st * STAGE + lane * (PR_HALF * 128);
+            const int token = x.half * PR_HALF, pg = there ? x.pg : -1;   // an absent page: outside the tensor, zeros
 #pragma unroll
-        for (int i = 0; i < STAGES; ++i) request(first + i * stride, pg[i], i);
-    }
-    int ahead = entry(first + STAGES * stride);
+            for (int c = 0; c < NCH; ++c) ptx::tma_load_4d(dst + c * BOX, &tmK, bar + st, c * 64, h, token, pg);
+#pragma unroll
+            for (int c = 0; c < NCH; ++c) ptx::tma_load_4d(dst + STAGE / 2 + c * BOX, &tmV, bar + st, c * 64, h, token, pg);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i) request(first + i * stride, early[i], i);
 
     // query rows 8 i + r8; packed row = token * G + head of the group
     uint4 q[NR][2 * NCH];
@@ -144,135 +178,194 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             for (int e = 0; e < 4; ++e) o[i][j][e] = 0.f;
     }
 
-    uint32_t it = 0, phases = 0;
+    uint32_t it = 0;
     bool ok = true;
     for (int tile = first; tile < tiles; tile += stride, ++it) {
         const uint32_t st = it % STAGES;
         const int next = tile + STAGES * stride;
-        if (there >> st & 1) {   // else its page is absent
-            ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar + st, phases >> st & 1, nullptr));
-            if (!ok) break;
-            phases ^= 1u << st;
-            there &= ~(1u << st);
-            const uint8_t* sk = ring + st * STAGE;
-            const uint8_t* sv = sk + STAGE / 2;
-            const int u0 = tile * PR_KEYS;
-            // s[i]: keys r8 (0, 1) and 8 + r8 (2, 3), rows 8 i + 2 c4 + {0, 1}
-            float s[NR][4];
-            {
-                float sp[NR][2][4] = {};   // even and odd k-steps: shorter chains of dependent products
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar + st, (it / STAGES) & 1, nullptr));
+        if (!ok) break;
+        const uint8_t* sk = ring + st * STAGE;
+        const uint8_t* sv = sk + STAGE / 2;
+        const int u0 = tile * PR_KEYS;
+        // s[i][t]: keys 16 t + r8 (0, 1) and 16 t + 8 + r8 (2, 3), rows 8 i + 2 c4 + {0, 1}
+        float s[NR][NT][4];
+        {
+            float sp[NR][NT][2][4] = {};   // even and odd k-steps: shorter chains of dependent products
 #pragma unroll
-                for (int c = 0; c < 2 * NCH; ++c) {
+            for (int c = 0; c < 2 * NCH; ++c) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
                     // 16-byte unit i of key u at i ^ (u % 8)
-                    const uint8_t* at = sk + (c >> 1) * BOX + r8 * 128 + (((2 * c4 + (c & 1)) ^ r8) << 4);
+                    const uint8_t* at = sk + (c >> 1) * BOX + (t * 16 + r8) * 128 + (((2 * c4 + (c & 1)) ^ r8) << 4);
                     const uint4 k0 = *reinterpret_cast<const uint4*>(at), k1 = *reinterpret_cast<const uint4*>(at + 1024);
                     const uint32_t a0[4] = {k0.x, k1.x, k0.y, k1.y}, a1[4] = {k0.z, k1.z, k0.w, k1.w};
 #pragma unroll
                     for (int i = 0; i < NR; ++i) {
-                        mma_16816(sp[i][0], a0, q[i][c].x, q[i][c].y);
-                        mma_16816(sp[i][1], a1, q[i][c].z, q[i][c].w);
+                        mma_16816(sp[i][t][0], a0, q[i][c].x, q[i][c].y);
+                        mma_16816(sp[i][t][1], a1, q[i][c].z, q[i][c].w);
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < NR; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[i][e] = __fmul_rn(sp[i][0][e] + sp[i][1][e], p.scale_log2);   // rounded like the maximum
             }
-            const bool edge = u0 + PR_KEYS > low;   // some row does not see all of it
-            if (edge) {
 #pragma unroll
-                for (int i = 0; i < NR; ++i)
+            for (int i = 0; i < NR; ++i)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (u0 + (e >> 1) * 8 + r8 >= lim[i][e & 1]) s[i][e] = -INFINITY;
+                        s[i][t][e] = __fmul_rn(sp[i][t][0][e] + sp[i][t][1][e], p.scale_log2);   // rounded like the maximum
+        }
+        const bool edge = u0 + PR_KEYS > low;   // some row does not see all of it
+        if (edge) {
+#pragma unroll
+            for (int i = 0; i < NR; ++i)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (u0 + t * 16 + (e >> 1) * 8 + r8 >= lim[i][e & 1]) s[i][t][e] = -INFINITY;
+        }
+        const uint32_t gone = absent >> (2 * st) & 3u;
+        if (__builtin_expect(gone != 0, 0)) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                if (gone >> t & 1)
+#pragma unroll
+                    for (int i = 0; i < NR; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[i][t][e] = -INFINITY;
+        }
+        // A row's maximum is raised when a score exceeds it by more than PR_SLACK: one vote a tile, and weights of up to
+        // 2^PR_SLACK, exactly as good in bf16.
+        bool over = false;
+        float top[NR][2];
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                top[i][e] = fmaxf(fmaxf(s[i][0][e], s[i][0][e + 2]), fmaxf(s[i][1][e], s[i][1][e + 2]));
+                over = over || top[i][e] > m[i][e] + PR_SLACK;   // from -inf: any score
             }
-            uint32_t pt[NR][2];   // P^T: row 8 i + r8, keys 2 c4 + {0, 1} and + 8
-            bool grew = false;
-            float alpha[NR][2];
+        if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
-                float mx[2] = {fmaxf(m[i][0], fmaxf(s[i][0], s[i][2])), fmaxf(m[i][1], fmaxf(s[i][1], s[i][3]))};
-#pragma unroll
-                for (int w = 4; w < 32; w *= 2) {
-                    mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], w));
-                    mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], w));
-                }
+                float alpha[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    alpha[i][e] = mx[e] > m[i][e] ? exp2_approx(m[i][e] - mx[e]) : 1.f;
-                    grew = grew || mx[e] > m[i][e];
-                    m[i][e] = mx[e];
-                    if (mx[e] == -INFINITY) mx[e] = 0.f;   // only infinite scores so far: weights of zero
+                    float mx = fmaxf(m[i][e], top[i][e]);
+#pragma unroll
+                    for (int w = 4; w < 32; w *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+                    alpha[e] = mx > m[i][e] ? exp2_approx(m[i][e] - mx) : 1.f;
+                    m[i][e] = mx;
+                    l[i][e] *= alpha[e];
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[i][e] = exp2_approx(s[i][e] - mx[e & 1]);
-                pt[i][0] = transpose_8x8(pack_bf16x2(s[i][0], s[i][1]));
-                pt[i][1] = transpose_8x8(pack_bf16x2(s[i][2], s[i][3]));
-                l[i][0] = l[i][0] * alpha[i][0] + (s[i][0] + s[i][2]);
-                l[i][1] = l[i][1] * alpha[i][1] + (s[i][1] + s[i][3]);
+                for (int j = 0; j < NCH * 4; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[i][j][e] *= alpha[e & 1];
             }
-            if (__any_sync(0xffffffffu, grew)) {
+        }
+        uint32_t pt[NR][NT][2];   // P^T: row 8 i + r8, keys 16 t + 2 c4 + {0, 1} and + 8
 #pragma unroll
-                for (int i = 0; i < NR; ++i)
+        for (int i = 0; i < NR; ++i) {
+            const float base[2] = {m[i][0] == -INFINITY ? 0.f : m[i][0], m[i][1] == -INFINITY ? 0.f : m[i][1]};   // no scores so far: weights of zero
 #pragma unroll
-                    for (int j = 0; j < NCH * 4; ++j)
+            for (int t = 0; t < NT; ++t) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) o[i][j][e] *= alpha[i][e & 1];
+                for (int e = 0; e < 4; ++e) s[i][t][e] = exp2_approx(s[i][t][e] - base[e & 1]);
+                pt[i][t][0] = transpose_8x8(pack_bf16x2(s[i][t][0], s[i][t][1]));
+                pt[i][t][1] = transpose_8x8(pack_bf16x2(s[i][t][2], s[i][t][3]));
             }
 #pragma unroll
-            for (int c = 0; c < NCH; ++c) {
-                uint32_t w[4][4];
-                bool odd = false;
+            for (int e = 0; e < 2; ++e) l[i][e] += (s[i][0][e] + s[i][0][e + 2]) + (s[i][1][e] + s[i][1][e + 2]);
+        }
+        // V rows of keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9 of 16, columns 8 r8 on
+        auto key_of = [&](int t, int k) { return t * 16 + 2 * c4 + (k & 1) + 8 * (k >> 1); };
+        auto values = [&](int t, int c, int k) {
+            const int u = key_of(t, k);
+            return *reinterpret_cast<const uint4*>(sv + c * BOX + u * 128 + ((r8 ^ (u & 7)) << 4));
+        };
+        auto pairs = [&](const uint32_t (&w)[4][4], int e, uint32_t (&a)[4]) {   // m-tile e
+            a[0] = __byte_perm(w[0][e], w[1][e], 0x5410);
+            a[1] = __byte_perm(w[0][e], w[1][e], 0x7632);
+            a[2] = __byte_perm(w[2][e], w[3][e], 0x5410);
+            a[3] = __byte_perm(w[2][e], w[3][e], 0x7632);
+        };
+        if (!edge) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {   // keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9
-                    const int u = 2 * c4 + (k & 1) + 8 * (k >> 1);
-                    *reinterpret_cast<uint4*>(w[k]) = *reinterpret_cast<const uint4*>(sv + c * BOX + u * 128 + ((r8 ^ (u & 7)) << 4));
-                    if (edge && u0 + u >= low) {
-                        // past the length there may be anything, and 0 * NaN is NaN
-                        if (u0 + u >= len) w[k][0] = w[k][1] = w[k][2] = w[k][3] = 0u;
-                        odd = odd || not_finite(w[k][0]) || not_finite(w[k][1]) || not_finite(w[k][2]) || not_finite(w[k][3]);
-                    }
-                }
-                if (__builtin_expect(!__any_sync(0xffffffffu, odd), 1)) {
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int c = 0; c < NCH; ++c) {
+                    uint32_t w[4][4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(w[k]) = values(t, c, k);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const uint32_t a[4] = {__byte_perm(w[0][e], w[1][e], 0x5410), __byte_perm(w[0][e], w[1][e], 0x7632),
-                                               __byte_perm(w[2][e], w[3][e], 0x5410), __byte_perm(w[2][e], w[3][e], 0x7632)};
+                        uint32_t a[4];
+                        pairs(w, e, a);
 #pragma unroll
-                        for (int i = 0; i < NR; ++i) mma_16816(o[i][c * 4 + e], a, pt[i][0], pt[i][1]);
+                        for (int i = 0; i < NR; ++i) mma_16816(o[i][c * 4 + e], a, pt[i][t][0], pt[i][t][1]);
                     }
-                } else {
+                }
+        } else {
 #pragma unroll 1
-                    for (int t = 0; t < new_; ++t) {
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int c = 0; c < NCH; ++c) {
+                    uint32_t w[4][4], p0[NR], p1[NR];
+                    bool odd = false;
+#pragma unroll
+                    for (int i = 0; i < NR; ++i) {
+                        p0[i] = t ? pt[i][1][0] : pt[i][0][0];
+                        p1[i] = t ? pt[i][1][1] : pt[i][0][1];
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        *reinterpret_cast<uint4*>(w[k]) = values(t, c, k);
+                        // past the length there may be anything, and 0 * NaN is NaN
+                        if (u0 + key_of(t, k) >= len) w[k][0] = w[k][1] = w[k][2] = w[k][3] = 0u;
+                        odd = odd || (u0 + key_of(t, k) >= low &&
+                                      (not_finite(w[k][0]) || not_finite(w[k][1]) || not_finite(w[k][2]) || not_finite(w[k][3])));
+                    }
+                    if (!__any_sync(0xffffffffu, odd)) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            uint32_t x[4];
+                            uint32_t a[4];
+                            pairs(w, e, a);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) x[k] = u0 + 2 * c4 + (k & 1) + 8 * (k >> 1) < low + t ? w[k][e] : 0u;
-                            const uint32_t a[4] = {__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[0], x[1], 0x7632),
-                                                   __byte_perm(x[2], x[3], 0x5410), __byte_perm(x[2], x[3], 0x7632)};
+                            for (int i = 0; i < NR; ++i) mma_16816(o[i][c * 4 + e], a, p0[i], p1[i]);
+                        }
+                        continue;
+                    }
+#pragma unroll 1
+                    for (int tok = 0; tok < new_; ++tok) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t x[4][4], a[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) x[k][e] = u0 + key_of(t, k) < low + tok ? w[k][e] : 0u;
+                            pairs(x, e, a);
 #pragma unroll
                             for (int i = 0; i < NR; ++i) {
                                 float one[4] = {0.f, 0.f, 0.f, 0.f};
-                                mma_16816(one, a, pt[i][0], pt[i][1]);
+                                mma_16816(one, a, p0[i], p1[i]);
 #pragma unroll
                                 for (int y = 0; y < 4; ++y)
-                                    if ((8 * i + 2 * c4 + (y & 1)) / G == t) o[i][c * 4 + e][y] += one[y];
+                                    if ((8 * i + 2 * c4 + (y & 1)) / G == tok) o[i][c * 4 + e][y] += one[y];
                             }
                         }
                     }
                 }
-            }
-            __syncwarp();   // the stage has been read
         }
+        __syncwarp();   // the stage has been read
         request(next, ahead, st);
-        ahead = entry(next + stride);
+        ahead = look_up();
     }
     if (!ok) {
         if (lane == 0 && p.err) atomicOr(p.err, ERRBIT_TIMEOUT_ATTENTION);
         // copies in flight land before the CTA can exit
-        for (int i = 0; i < STAGES; ++i)
-            if (there >> i & 1) ptx::mbar_wait_bounded(bar + i, phases >> i & 1, nullptr);
+        for (uint32_t i = it; i < it + STAGES; ++i)
+            if (first + (int)i * stride < tiles) ptx::mbar_wait_bounded(bar + i % STAGES, (i / STAGES) & 1, nullptr);
     }
     __syncwarp();
 
@@ -416,8 +509,8 @@ cudaError_t launch_rows(const PagedRowsParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const PagedDesc& d = p.d;
     alignas(64) CUtensorMap mk, mv;
-    if (!ct_map(&mk, d.k, d.ks, d.pages, d.page, d.Hkv, d.dh, 1, PR_KEYS, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
-        !ct_map(&mv, d.v, d.vs, d.pages, d.page, d.Hkv, d.dh, 1, PR_KEYS, CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+    if (!ct_map(&mk, d.k, d.ks, d.pages, d.page, d.Hkv, d.dh, 1, PR_HALF, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
+        !ct_map(&mv, d.v, d.vs, d.pages, d.page, d.Hkv, d.dh, 1, PR_HALF, CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
         return cudaErrorInvalidValue;
     const dim3 grid((unsigned)(d.B * d.Hkv * p.Z)), block(NW * 32);
     if (p.Z == 1) return launch_dependent(k, grid, block, smem, s, mk, mv, p);
@@ -427,25 +520,30 @@ cudaError_t launch_rows(const PagedRowsParams& p, cudaStream_t s) {
 }  // namespace
 
 bool paged_rows_supported(const PagedDesc& d) {
-    if (d.dt != DT_BF16 || d.dh % 8 != 0 || d.dh > 128 || d.Tq * (d.H / d.Hkv) > PR_ROWS || d.page % PR_KEYS != 0) return false;
+    if (d.dt != DT_BF16 || d.dh % 8 != 0 || d.dh > 128 || d.Tq * (d.H / d.Hkv) > PR_ROWS || d.page % PR_HALF != 0) return false;
     if (d.B > 0x7fffffff / 8 / d.Hkv) return false;
     if ((reinterpret_cast<uintptr_t>(d.q) & 15) || d.qs[0] % 8 || d.qs[1] % 8 || d.qs[2] % 8) return false;
     return ct_strides_ok(d.k, d.ks, d.page) && ct_strides_ok(d.v, d.vs, d.page) && ct_encode_fn() != nullptr;
 }
 
 cudaError_t launch_paged_rows(const PagedDesc& d, const PagedParts& prefix, const DeviceInfo& dev, cudaStream_t s) {
-    // CTAs and warps to a key head as in attention_cross_rows.cu, by the keys that the table has room for.
+    // A warp takes 1.1 us for a tile, half of it the matrix instructions' own time, so what counts is to have many of them, each
+    // with two tiles at least, in one round of CTAs. Widths up to 64: three warps, four CTAs to an SM (32 heads x 16, 577
+    // keys: 13.0 us; with four warps, of which three CTAs fit and the rest are a second round, 15.3). Wider: six warps
+    // with an SM of their own where key heads are few, else three and two CTAs. Clusters, us at 1 / 2 / 4 / 8 CTAs per key
+    // head for 16 heads of 128 over 8200 keys, six warps: 54 / 30 / 18.8 / 23 (clusters of eight CTAs that fill an SM
+    // each do not pack into the GPU's SM groups). Parts joined by another kernel, on all SMs, were no faster: 18.4.
     const int64_t heads = d.B * d.Hkv, sms = dev.num_sms, keys = d.table_pages * d.page;
-    const bool narrow = d.dh <= 64;
-    const int warps = narrow || heads > sms / 2 ? 4 : 8;
-    const int64_t ctas = narrow || warps == 4 ? 2 * sms : sms;   // aimed at; more CTAs only add joins
+    const bool narrow = d.dh <= 64, many = d.Tq * (d.H / d.Hkv) > 8;
+    const int warps = narrow || heads > sms / 2 ? 3 : 6;
+    const int64_t ctas = warps == 3 ? 2 * sms : sms;   // aimed at; more CTAs only add joins
     int Z = 1;
-    while (Z < PR_MAXZ && heads * Z * 2 <= ctas && keys >= (int64_t)Z * 2 * warps * 16 * 2) Z *= 2;
-    if (warps == 8 && Z == 8 && heads * 8 > sms / 2) Z = 4;
+    while (Z < PR_MAXZ && heads * Z * 2 <= ctas && keys >= (int64_t)Z * 2 * warps * PR_KEYS * 2) Z *= 2;
+    if (warps == 6 && Z == 8 && heads * 8 > sms / 2) Z = 4;
     const PagedRowsParams p{d, prefix, (float)(d.scale * 1.4426950408889634), Z, dev.err_word};
-    if (d.Tq * (d.H / d.Hkv) > 8)
-        return narrow ? launch_rows<64, 2, 4, 3, 3>(p, s) : warps == 8 ? launch_rows<128, 2, 8, 2, 1>(p, s) : launch_rows<128, 2, 4, 3, 2>(p, s);
-    return narrow ? launch_rows<64, 1, 4, 3, 4>(p, s) : warps == 8 ? launch_rows<128, 1, 8, 2, 1>(p, s) : launch_rows<128, 1, 4, 3, 2>(p, s);
+    if (narrow) return many ? launch_rows<64, 2, 3, 2, 3>(p, s) : launch_rows<64, 1, 3, 2, 4>(p, s);
+    if (warps == 3) return many ? launch_rows<128, 2, 3, 2, 2>(p, s) : launch_rows<128, 1, 3, 2, 2>(p, s);
+    return many ? launch_rows<128, 2, 6, 2, 1>(p, s) : launch_rows<128, 1, 6, 2, 1>(p, s);
 }
 
 }  // namespace vit

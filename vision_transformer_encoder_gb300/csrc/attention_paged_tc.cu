@@ -41,17 +41,19 @@ constexpr int PT_SORT = 128;               // sequences that are put in order of
 constexpr float PT_SLACK = 8.f;            // log2 of the weights that are carried before a rescale
 constexpr float PT_COARSE = 16777216.f;    // maxima from which products are rounded before the maximum is taken off
 
-template <int DH> struct PtLayout {
+// NARROW: items of one tile only, which leave room for deeper rings.
+template <int DH, bool NARROW> struct PtLayout {
     static_assert(DH % 16 == 0 && DH >= 64 && DH <= 128, "head width");
     static constexpr int NCH = (DH + 63) / 64;           // 64-column boxes per tile
     static constexpr int TILE = NCH * PT_BOX;
-    static constexpr int QBUF = NCH == 2 ? 1 : 2;        // buffers of two query tiles
-    static constexpr int KVS = NCH == 2 ? 2 : 4;         // stages of each ring
-    static constexpr int OFF_K = QBUF * 2 * TILE;
-    static constexpr int OFF_V = OFF_K + KVS * TILE;
-    static constexpr int OFF_O = OFF_V + KVS * TILE;     // per group: one 64-column box of O on its way out
-    static constexpr int OFF_BAR = OFF_O + 2 * PT_BOX;
-    static constexpr int OFF_ML = OFF_BAR + 512;         // group 1's maxima and sums for group 0; lengths while sorting
+    static constexpr int QT = NARROW ? 1 : 2;            // query tiles of a buffer
+    static constexpr int QBUF = NCH == 2 ? 1 : 2;
+    static constexpr int KS = NCH == 2 ? 2 : NARROW ? 5 : 4;               // stages of the rings
+    static constexpr int VS = NCH == 2 ? (NARROW ? 3 : 2) : NARROW ? 6 : 4;
+    static constexpr int OFF_K = QBUF * QT * TILE;
+    static constexpr int OFF_V = OFF_K + KS * TILE;
+    static constexpr int OFF_BAR = OFF_V + VS * TILE;
+    static constexpr int OFF_ML = OFF_BAR + 768;         // group 1's maxima and sums for group 0; lengths while sorting
     static constexpr int SMEM = OFF_ML + 1024 + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
@@ -72,16 +74,16 @@ struct PtParams {
 
 struct PtBars {
     uint64_t q_full[2], q_empty[2];
-    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+    uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
     // two of each for the half tiles in turn: a waiter may be one phase behind, never two
-    uint64_t s_full[2][2], p_full[2][2], o_done[2][2], o_free[2], ost_full[2], ost_free[2];
+    uint64_t s_full[2][2], p_full[2][2], o_done[2][2], o_free[2];
     uint64_t ml_full;            // group 1's part of a shared tile is there
     uint64_t done;
     uint32_t tmem_slot;
     int abort_flag;
     uint8_t order[PT_SORT];      // sequences, the longest first
 };
-static_assert(sizeof(PtBars) <= 512, "barriers");
+static_assert(sizeof(PtBars) <= 768, "barriers");
 
 struct PtItem {
     bool prefix;                 // kind
@@ -149,8 +151,8 @@ __device__ __forceinline__ PtItem pt_item(const PtParams& p, int item, const uin
         x.t0 = (p.own_pairs - 1 - i / (int)d.B) * 2 * p.TT;
         if (p.sorted) x.at = order[x.at];
         x.tokens = Tq;
-        x.new_ = d.q_lens ? min(max(__ldg(d.q_lens + x.at), 0), Tq) : Tq;
-        const int len = min(max(__ldg(d.kv_lens + x.at), 0), (int)(d.table_pages * d.page));
+        x.new_ = d.q_lens ? min(max(load(d.q_lens + x.at), 0), Tq) : Tq;
+        const int len = min(max(load(d.kv_lens + x.at), 0), (int)(d.table_pages * d.page));
         x.low = len - (x.new_ - 1);
         x.table1 = d.table + (int64_t)x.at * d.table_pages;
     }
@@ -159,7 +161,7 @@ __device__ __forceinline__ PtItem pt_item(const PtParams& p, int item, const uin
     x.table0 = nullptr;
     if (ahead) {
         const int g = x.prefix ? x.at : x.at / p.S;
-        x.len0 = min(max(__ldg(d.prefix_lens + g), 0), (int)(d.prefix_pages * d.page));
+        x.len0 = min(max(load(d.prefix_lens + g), 0), (int)(d.prefix_pages * d.page));
         x.table0 = d.prefix_table + (int64_t)g * d.prefix_pages;
     }
     x.n0 = (x.len0 + PT_KEYS - 1) / PT_KEYS;
@@ -174,51 +176,55 @@ __device__ __forceinline__ PtItem pt_item(const PtParams& p, int item, const uin
     return x;
 }
 
-// One row from its definition, over the key tiles of the item's range; only where a product with a weight of zero was not
-// a number. acc: dh sums. The maximum and the sum of weights come back in m and l.
-__device__ __noinline__ void pt_row(const PtParams& p, const PtItem& x, int t, int head, int lim, float* acc, float* m_, float* l_) {
+// One row from the definition, over the key tiles of the item's range, with its maximum m: only where a product with a weight
+// of zero was not a number. False where no value that the row does not see is to blame. acc: dh sums.
+__device__ __noinline__ bool pt_row(const PtParams& p, const PtItem& x, int t, int head, int lim, float m, float* acc) {
     const PagedDesc& d = p.d;
-    const int dh = (int)d.dh, page = (int)d.page;
-    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(d.q) + head * d.qs[2] +
-                             (x.prefix ? (x.at * (int64_t)p.S + t / (int)d.Tq) * d.qs[0] + t % (int)d.Tq * d.qs[1]
-                                       : x.at * d.qs[0] + t * d.qs[1]);
-    float m = -INFINITY, l = 0.f;
+    const int dh = (int)d.dh, page = (int)d.page, tiles = x.tiles();
+    auto row = [&](const void* pool, const int64_t (&st)[3], bool ahead, int u) -> const __nv_bfloat16* {
+        const int pg = load((ahead ? x.table0 : x.table1) + u / page);
+        if (pg < 0 || pg >= d.pages) return nullptr;
+        return static_cast<const __nv_bfloat16*>(pool) + pg * st[0] + u % page * st[1] + x.h * st[2];
+    };
+    bool blame = false;
+    for (int u = max(lim, 0); u < x.len1 && !blame; ++u) {
+        const __nv_bfloat16* v = row(d.v, d.vs, false, u);
+        for (int c = 0; v && c < dh; ++c) blame = blame || !isfinite(__bfloat162float(v[c]));
+    }
+    if (!blame) return false;
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(d.q) + head * d.qs[2] + x.at * d.qs[0] + t * d.qs[1];
+    const float base = m == -INFINITY ? 0.f : m;
     for (int c = 0; c < dh; ++c) acc[c] = 0.f;
-    const int n = x.tiles();
-    for (int j = 0; j < n; ++j) {
+    for (int j = 0; j < tiles; ++j) {
         const bool ahead = x.kt0 + j < x.n0;
-        const int base = (ahead ? x.kt0 + j : x.kt0 + j - x.n0) * PT_KEYS, last = min(PT_KEYS, x.keys(j, lim));
+        const int first = (ahead ? x.kt0 + j : x.kt0 + j - x.n0) * PT_KEYS, last = min(PT_KEYS, x.keys(j, lim));
         for (int u = 0; u < last; ++u) {
-            const int pg = __ldg((ahead ? x.table0 : x.table1) + (base + u) / page);
-            if (pg < 0 || pg >= d.pages) continue;
-            const int64_t at = (base + u) % page;
-            const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(d.k) + pg * d.ks[0] + at * d.ks[1] + x.h * d.ks[2];
-            const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(d.v) + pg * d.vs[0] + at * d.vs[1] + x.h * d.vs[2];
+            const __nv_bfloat16 *k = row(d.k, d.ks, ahead, first + u), *v = row(d.v, d.vs, ahead, first + u);
+            if (!k) continue;
             float s = 0.f;
             for (int c = 0; c < dh; ++c) s = fmaf(__bfloat162float(q[c]), __bfloat162float(k[c]), s);
-            s = __fmul_rn(s, p.scale_log2);
-            const float mn = fmaxf(m, s), off = mn == -INFINITY ? 0.f : mn;
-            const float alpha = exp2_approx(m - off), w = exp2_approx(s - off);
-            l = l * alpha + w;
-            for (int c = 0; c < dh; ++c) acc[c] = fmaf(w, __bfloat162float(v[c]), acc[c] * alpha);
-            m = mn;
+            const float w = exp2_approx(__fmul_rn(s, p.scale_log2) - base);
+            bool over = true;   // nothing can change any more
+            for (int c = 0; c < dh; ++c) {
+                acc[c] = fmaf(w, __bfloat162float(v[c]), acc[c]);
+                over = over && acc[c] != acc[c];
+            }
+            if (over) return true;
         }
     }
-    *m_ = m;
-    *l_ = l;
+    return true;
 }
 
 __device__ __forceinline__ void pt_error(uint32_t* err, uint32_t bit) {
     if (err) atomicOr(err, bit);
 }
 
-template <int DH>
+template <int DH, bool NARROW>
 __global__ void __launch_bounds__(PT_THREADS, 1)
 paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQP,
-                const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                const __grid_constant__ CUtensorMap tmO, const __grid_constant__ PtParams p) {
-    using L = PtLayout<DH>;
-    constexpr int KVS = L::KVS, QB = L::QBUF, NCH = L::NCH;
+                const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PtParams p) {
+    using L = PtLayout<DH, NARROW>;
+    constexpr int KS = L::KS, VS = L::VS, QB = L::QBUF, QT = L::QT, NCH = L::NCH;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t* sQ = smem;
@@ -239,10 +245,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 ptx::mbar_init(&bars->o_done[i][b], 1);
             }
             ptx::mbar_init(&bars->o_free[i], 4);
-            ptx::mbar_init(&bars->ost_full[i], 4);
-            ptx::mbar_init(&bars->ost_free[i], 1);
         }
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 6; ++i) {
             ptx::mbar_init(&bars->k_full[i], 1);
             ptx::mbar_init(&bars->k_empty[i], 2);     // both groups, or the producer for one that does not use the stage
             ptx::mbar_init(&bars->v_full[i], 1);
@@ -258,7 +262,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         ptx::prefetch_tensormap(&tmQP);
         ptx::prefetch_tensormap(&tmK);
         ptx::prefetch_tensormap(&tmV);
-        ptx::prefetch_tensormap(&tmO);
     }
     if (warp == 1) {
         ptx::tmem_alloc(&bars->tmem_slot, 512);
@@ -268,6 +271,19 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_slot, 0);
+    // While the kernel in front ends: lengths and page tables, of which the first item needs one after the other, go to L2.
+    // They may still change, and are read behind the wait. (Looking keys up by them, for L2 too, held the warp up for
+    // longer than it gained: 32 x 1 over 64 keys behind 1025, 13.5 -> 15.8 us.)
+    if (warp == 2) {
+        const int32_t* lens[3] = {p.d.kv_lens, p.d.q_lens, p.d.prefix_lens};
+        for (int i = 0; i < 3; ++i)
+            if (lens[i])
+                for (int b = lane * 32; b < (i < 2 ? p.d.B : p.d.groups) && b < 4096; b += 1024) prefetch_l2(lens[i] + b);
+        if (p.items > p.prefix_items)
+            for (int b = lane; b < p.d.B && b < 128; b += 32) prefetch_l2(p.d.table + b * p.d.table_pages);
+        if (p.d.prefix_table)
+            for (int b = lane; b < p.d.groups && b < 128; b += 32) prefetch_l2(p.d.prefix_table + b * p.d.prefix_pages);
+    }
     griddep_wait();
     griddep_launch_dependents();
     // item of round i: there and back over the CTAs, as the items fall in length
@@ -276,7 +292,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     if (p.sorted) {
         int* lens = reinterpret_cast<int*>(sml);
         const int b = threadIdx.x, B = (int)p.d.B;
-        if (b < B) lens[b] = max(__ldg(p.d.kv_lens + b), 0);
+        if (b < B) lens[b] = max(load(p.d.kv_lens + b), 0);
         __syncthreads();
         if (b < B) {
             int before = 0;
@@ -290,6 +306,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     if (warp >= 10) {
         // ---------------------------------------------------- TMA producers, a lane to a box
         const bool kq = warp == 10;
+        const uint32_t KVS = kq ? KS : VS;
         uint64_t* full = kq ? bars->k_full : bars->v_full;
         uint64_t* empty = kq ? bars->k_empty : bars->v_empty;
         uint8_t* ring = kq ? sK : sV;
@@ -313,7 +330,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     ptx::mbar_arrive_expect_tx(&bars->q_full[qb], x.live * NCH * p.G * p.TT * 128);
                     for (int g = 0; g < x.live; ++g)
                         for (int c = 0; c < NCH; ++c)
-                            ptx::tma_load_4d(sQ + (qb * 2 + g) * L::TILE + c * PT_BOX, tq, &bars->q_full[qb], c * 64, x.h * p.G,
+                            ptx::tma_load_4d(sQ + (qb * QT + g) * L::TILE + c * PT_BOX, tq, &bars->q_full[qb], c * 64, x.h * p.G,
                                              x.t0 + g * p.TT, b);
                 }
                 __syncwarp();
@@ -324,9 +341,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 const bool ahead = t < x.n0;
                 const int key = (ahead ? t : t - x.n0) * PT_KEYS + lane * unit;
                 const bool mine = lane * unit < PT_KEYS && key < (ahead ? x.len0 : x.len1);
-                int pg = mine ? __ldg((ahead ? x.table0 : x.table1) + key / page) : -1;
-                if (pg >= p.d.pages) pg = -1;   // an absent page: outside the tensor, zeros
-                if (pg < 0) pg = -1;
+                int pg = mine ? load((ahead ? x.table0 : x.table1) + key / page) : -1;
+                if (pg < 0 || pg >= p.d.pages) pg = -1;   // an absent page: outside the tensor, zeros
                 const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, mine));
                 const uint32_t st = it % KVS;
                 if (!(ok = wait(empty + st, ((it / KVS) & 1) ^ 1))) break;
@@ -353,7 +369,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 for (uint32_t i = 0; i < (uint32_t)QB; ++i)
                     if (ii > i && !ptx::mbar_wait_bounded(&bars->q_full[(ii - 1 - i) % QB], ((ii - 1 - i) / QB) & 1, nullptr))
                         pt_error(p.err, ERRBIT_TIMEOUT_TEARDOWN);
-            for (uint32_t i = 0; i < (uint32_t)KVS; ++i)
+            for (uint32_t i = 0; i < KVS; ++i)
                 if (it > i && !ptx::mbar_wait_bounded(full + (it - 1 - i) % KVS, ((it - 1 - i) / KVS) & 1, nullptr))
                     pt_error(p.err, ERRBIT_TIMEOUT_TEARDOWN);
         }
@@ -386,11 +402,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             }
             // S of half tile j of this item, and what its last user releases
             auto scores = [&](int j) -> bool {
-                const uint32_t it = base + x.tile(g, j >> 1), st = it % KVS, b = (pc + j) & 1;
-                if (!wait(&bars->k_full[st], (it / KVS) & 1)) return false;
+                const uint32_t it = base + x.tile(g, j >> 1), st = it % KS, b = (pc + j) & 1;
+                if (!wait(&bars->k_full[st], (it / KS) & 1)) return false;
                 ptx::tc_fence_after();
                 // descriptors count 16-byte units: those of later steps are sums
-                const uint64_t qd = ptx::smem_desc(ptx::smem_addr(sQ + (qb * 2 + qt) * L::TILE), 16, 1024, ptx::kLayoutSw128);
+                const uint64_t qd = ptx::smem_desc(ptx::smem_addr(sQ + (qb * QT + qt) * L::TILE), 16, 1024, ptx::kLayoutSw128);
                 const uint64_t kd = ptx::smem_desc(ptx::smem_addr(sK + st * L::TILE + (j & 1) * (PT_SUB * 128)), 16, 1024,
                                                    ptx::kLayoutSw128);
                 const uint32_t tD = tS + b * PT_SUB;
@@ -411,8 +427,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             ok = (pc == 0 || wait(&bars->o_done[g][(pc - 1) & 1], ((pc - 1) >> 1) & 1)) && scores(0) && (nst < 2 || scores(1));
             for (int j = 0; j < nst && ok; ++j) {
                 const int tile = x.tile(g, j >> 1);
-                const uint32_t it = base + tile, st = it % KVS, m = pc + j;
-                if (!(ok = wait(&bars->v_full[st], (it / KVS) & 1))) break;
+                const uint32_t it = base + tile, st = it % VS, m = pc + j;
+                if (!(ok = wait(&bars->v_full[st], (it / VS) & 1))) break;
                 const int valid = x.keys(tile, x.len1) - (j & 1) * PT_SUB;
                 uint8_t* v = sV + st * L::TILE + (j & 1) * (PT_SUB * 128);
                 if (valid < PT_SUB) {
@@ -458,16 +474,14 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             if (!ptx::mbar_wait_bounded(&bars->done, 0, nullptr)) pt_error(p.err, ERRBIT_TIMEOUT_TEARDOWN);
         }
     } else {
-        // ---------------------------------------------------- softmax groups
+        // ---------------------------------------------------- softmax groups, a thread to a row
         const int g = (warp - 2) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
         const uint32_t tO = tmem + 256 + g * 128 + lane_off;
-        uint8_t* stage = smem + L::OFF_O + g * PT_BOX;
-        const bool storer = quarter == 2 && lane == 0;
         const float sl2 = p.scale_log2;
         const int unit = p.unit < PT_SUB ? p.unit : PT_SUB, page = (int)p.d.page, G = p.G;
         const int tok = r / G;
-        uint32_t tt = 0, sc = 0, joins = 0;   // half tiles, staged boxes of this group, shared tiles so far
+        uint32_t tt = 0, joins = 0;   // half tiles, shared tiles of this group so far
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
             return __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, parity, abort_flag));
@@ -482,42 +496,54 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             const int most = x.limit(p, qt);
             const int lim = t < x.new_ ? x.low + t : most;   // own keys that this row sees
             float m = -INFINITY, l = 0.f;
+            // whether any page of the range is absent: half tiles are looked at one by one only then
+            bool gaps = false;
+            if (live && nst > 0) {
+                const int end = x.kt0 + x.tiles();
+                if (x.kt0 < x.n0)
+                    for (int e = x.kt0 * PT_KEYS / page + lane; e * page < min(x.len0, end * PT_KEYS); e += 32)
+                        gaps = gaps || (uint32_t)load(x.table0 + e) >= (uint32_t)p.d.pages;
+                for (int e = max(0, x.kt0 - x.n0) * PT_KEYS / page + lane; e * page < min(x.len1, (end - x.n0) * PT_KEYS); e += 32)
+                    gaps = gaps || (uint32_t)load(x.table1 + e) >= (uint32_t)p.d.pages;
+                gaps = __any_sync(0xffffffffu, gaps);
+            }
             for (int j = 0; j < nst; ++j, ++tt) {
                 const int kt = x.kt0 + x.tile(g, j >> 1);
                 const bool ahead = kt < x.n0;
                 const int key = (ahead ? kt : kt - x.n0) * PT_KEYS + (j & 1) * PT_SUB;
-                int pg = 0;   // of this lane's unit of the half tile
-                if (live && lane * unit < PT_SUB && key + lane * unit < (ahead ? x.len0 : x.len1))
-                    pg = __ldg((ahead ? x.table0 : x.table1) + (key + lane * unit) / page);
                 if (!(ok = wait(&bars->s_full[g][tt & 1], (tt >> 1) & 1))) break;
                 ptx::tc_fence_after();
                 const uint32_t tS = tmem + g * 128 + (tt & 1) * PT_SUB + lane_off;
                 if (live) {
-                    uint32_t sv[PT_SUB];   // S, then P packed in place
-                    ptx::tmem_ld_32x32b_x32(tS, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-                    ptx::tmem_ld_32x32b_x32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
-                    ptx::tmem_ld_wait();
+                    uint32_t sv[PT_SUB];   // S, then P packed in place; the largest of each half comes with the load
+                    uint32_t(&s0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sv[0]);
+                    uint32_t(&s1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sv[32]);
+                    float mrow = ptx::tmem_ld_red_max_32x32b_x32(tS, s0);
+                    float mx1 = ptx::tmem_ld_red_max_32x32b_x32(tS + 32, s1);
+                    ptx::tmem_ld_wait_for(s0, mrow);
+                    ptx::tmem_ld_wait_for(s1, mx1);
+                    mrow = fmaxf(mrow, mx1);
                     const int valid = (ahead ? x.len0 : lim) - key;
-                    if (__any_sync(0xffffffffu, valid < PT_SUB)) {
+                    if (gaps || __any_sync(0xffffffffu, valid < PT_SUB)) {
+                        uint32_t absent = 0;
+                        if (__builtin_expect(gaps, 0)) {
+                            int pg = 0;   // of this lane's unit of the half tile
+                            if (lane * unit < PT_SUB && key + lane * unit < (ahead ? x.len0 : x.len1))
+                                pg = load((ahead ? x.table0 : x.table1) + (key + lane * unit) / page);
+                            absent = __ballot_sync(0xffffffffu, pg < 0 || pg >= p.d.pages);
+                        }
+                        mrow = -INFINITY;
 #pragma unroll
-                        for (int e = 0; e < PT_SUB; ++e)
-                            if (e >= valid) sv[e] = __float_as_uint(-INFINITY);
+                        for (int e = 0; e < PT_SUB; e += 16) {
+                            const bool away = absent >> (e / unit) & 1;
+#pragma unroll
+                            for (int y = e; y < e + 16; ++y) {
+                                if (y >= valid || away) sv[y] = __float_as_uint(-INFINITY);
+                                mrow = fmaxf(mrow, __uint_as_float(sv[y]));
+                            }
+                        }
                     }
-                    const uint32_t absent = __ballot_sync(0xffffffffu, pg < 0 || pg >= p.d.pages);
-                    if (absent) {
-#pragma unroll
-                        for (int e = 0; e < PT_SUB; e += 16)
-                            if (absent >> (e / unit) & 1)
-#pragma unroll
-                                for (int y = 0; y < 16; ++y) sv[e + y] = __float_as_uint(-INFINITY);
-                    }
-                    float mx[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) mx[e] = __uint_as_float(sv[e]);
-#pragma unroll
-                    for (int e = 8; e < PT_SUB; ++e) mx[e & 7] = fmaxf(mx[e & 7], __uint_as_float(sv[e]));
-                    const float mrow = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                             fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * sl2;
+                    mrow *= sl2;
                     float alpha = 1.f;
                     if (mrow > m + PT_SLACK || m == -INFINITY) {   // raise the maximum
                         const float m_new = fmaxf(m, mrow);
@@ -532,13 +558,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                             if (!(ok = wait(&bars->o_done[g][(tt - 1) & 1], ((tt - 1) >> 1) & 1))) break;
                             ptx::tc_fence_after();
 #pragma unroll
-                            for (int c = 0; c < DH / 16; ++c) {
+                            for (int c = 0; c < DH; c += 16) {
                                 uint32_t ov[16];
-                                ptx::tmem_ld_32x32b_x16(tO + c * 16, ov);
+                                ptx::tmem_ld_32x32b_x16(tO + c, ov);
                                 ptx::tmem_ld_wait_for(ov);
 #pragma unroll
                                 for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                                ptx::tmem_st_32x32b_x16(tO + c * 16, ov);
+                                ptx::tmem_st_32x32b_x16(tO + c, ov);
                             }
                         }
                         const float f = coarse ? sl2 : 1.f;
@@ -556,7 +582,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                         ls[(e >> 1) & 3] = f2_add(ls[(e >> 1) & 3], f2_pack(p0, p1));
                         sv[e >> 1] = pack_bf16x2(p0, p1);
                     }
-                    ptx::tmem_st_32x32b_x32(tS, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+                    ptx::tmem_st_32x32b_x32(tS, s0);
                     float a0, a1, b0, b1;
                     f2_unpack(f2_add(ls[0], ls[1]), a0, a1);
                     f2_unpack(f2_add(ls[2], ls[3]), b0, b1);
@@ -602,140 +628,87 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 l = 0.f;
             }
             const int out_rows = min(p.TT, x.tokens - out_t0) * G;   // of this group's own query tile; none if it does not exist
-            auto column = [&](int c, uint32_t (&ov)[16]) {   // 16 columns of O from c on, all lanes of the warp
-                if (!have) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) ov[e] = 0u;
-                    return;
-                }
-                ptx::tmem_ld_32x32b_x16(tO + c, ov);
+            auto column = [&](int c, uint32_t (&ov)[8]) {   // 8 columns of O, all lanes of the warp
+                ptx::tmem_ld_32x32b_x8(tO + c, ov);
                 ptx::tmem_ld_wait_for(ov);
                 if (both) {
-                    uint32_t o1[16];
-                    ptx::tmem_ld_32x32b_x16(tO + 128 + c, o1);
+                    uint32_t o1[8];
+                    ptx::tmem_ld_32x32b_x8(tO + 128 + c, o1);
                     ptx::tmem_ld_wait_for(o1);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
+                    for (int e = 0; e < 8; ++e)
                         ov[e] = __float_as_uint(fmaf(f1, __uint_as_float(o1[e]), f0 * __uint_as_float(ov[e])));
                 }
             };
             bool row = r < out_rows && t < x.new_ && !(g == 1 && x.live < 2);
             if (x.prefix && row && p.d.q_lens)   // a token of its sequence
-                row = t % (int)p.d.Tq < __ldg(p.d.q_lens + (int64_t)x.at * p.S + t / (int)p.d.Tq);
+                row = t % (int)p.d.Tq < load(p.d.q_lens + (int64_t)x.at * p.S + t / (int)p.d.Tq);
+            if (!row) l = 0.f;
             bool again = false;
             float acc[DH];
             if (have && live && x.len1 > 0) {
                 // rows do not all see the same: values that this one does not see can make it a NaN
                 float odd = 0.f;
 #pragma unroll
-                for (int c = 0; c < DH; c += 16) {
-                    uint32_t ov[16];
+                for (int c = 0; c < DH; c += 8) {
+                    uint32_t ov[8];
                     column(c, ov);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) odd = fmaf(__uint_as_float(ov[e]), 0.f, odd);
+                    for (int e = 0; e < 8; ++e) odd = fmaf(__uint_as_float(ov[e]), 0.f, odd);
                 }
-                again = row && odd != 0.f;
-                if (__builtin_expect(again, 0)) {
+                if (__builtin_expect(row && odd != 0.f, 0)) {
                     const PtItem y = x;   // so that x itself keeps to registers
-                    float m2, l2;
-                    pt_row(p, y, t, x.h * G + r % G, lim, acc, &m2, &l2);
-                    m = m2;
-                    l = l2;
+                    again = pt_row(p, y, t, x.h * G + r % G, lim, m, acc);
                 }
                 __syncwarp();
+            }
+            const bool there = r < out_rows;
+            const int64_t at = ((int64_t)x.at * x.tokens + out_t0 + tok) * p.d.H + x.h * G + r % G;   // row of the output
+            if (quarter * 32 < out_rows) {
+                const int64_t to = (int64_t)(x.prefix ? x.z : p.prefix_parts + x.z) * p.parts.rows + at;
+                float* part = static_cast<float*>(p.parts.acc) + to * DH;
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.d.o) + at * DH;
+                const bool none = l == 0.f;
+                const float inv = none ? 0.f : 1.f / l;
+#pragma unroll
+                for (int c = 0; c < DH; c += 8) {
+                    uint32_t ov[8];
+                    if (have) {
+                        column(c, ov);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) ov[e] = 0u;
+                    }
+                    if (__builtin_expect(again, 0)) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) ov[e] = __float_as_uint(acc[c + e]);
+                    }
+                    if (!there) continue;
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(ov[e]);
+                    if (p.parts.n) {
+                        if (none) continue;
+                        *reinterpret_cast<float4*>(part + c) = make_float4(v[0], v[1], v[2], v[3]);
+                        *reinterpret_cast<float4*>(part + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = none ? 0.f : v[e] * inv;
+                        *reinterpret_cast<uint4*>(out + c) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                                        pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+                    }
+                }
+                if (p.parts.n && there)
+                    static_cast<float2*>(p.parts.ml)[to] = make_float2(none ? -INFINITY : m, l);
             }
             // O has been read: its group's next products may write it, and group 1's where it was read alongside
-            auto released = [&]() {
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (g == 0 ? nst > 0 : (nst > 0 && !both)) ptx::mbar_arrive(&bars->o_free[g]);
-                    if (g == 0 && both) ptx::mbar_arrive(&bars->o_free[1]);
-                }
-            };
-            if (p.parts.n) {
-                const bool there = r < out_rows;
-                const int64_t at = ((int64_t)x.at * x.tokens + out_t0 + tok) * p.d.H + x.h * G + r % G;
-                const int64_t part = x.prefix ? x.z : p.prefix_parts + x.z;
-                const int64_t to = part * p.parts.rows + at;
-                if (quarter * 32 < out_rows) {
-                    float* dst = static_cast<float*>(p.parts.acc) + to * DH;
-                    if (!row) l = 0.f;
-                    if (have) {
-#pragma unroll
-                        for (int c = 0; c < DH; c += 16) {
-                            uint32_t ov[16];
-                            column(c, ov);
-                            if (there && l != 0.f) {
-#pragma unroll
-                                for (int e = 0; e < 16; e += 4)
-                                    *reinterpret_cast<float4*>(dst + c + e) =
-                                        again ? make_float4(acc[c + e], acc[c + e + 1], acc[c + e + 2], acc[c + e + 3])
-                                              : make_float4(__uint_as_float(ov[e]), __uint_as_float(ov[e + 1]), __uint_as_float(ov[e + 2]),
-                                                            __uint_as_float(ov[e + 3]));
-                            }
-                        }
-                    }
-                    if (there) static_cast<float2*>(p.parts.ml)[to] = make_float2(l == 0.f ? -INFINITY : m, l);
-                }
-                released();
-                continue;
-            }
-            const bool none = !row || l == 0.f;
-            const float inv = 1.f / l;
-            if (out_rows <= 0) {   // no such tile
-                released();
-                continue;
-            }
-#pragma unroll 1
-            for (int c = 0; c < NCH; ++c, ++sc) {
-                // the previous store has read the staging box
-                if (sc > 0 && !(ok = wait(&bars->ost_free[g], (sc - 1) & 1))) break;
-                if (quarter * 32 < out_rows) {
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        uint32_t ov[16];
-                        if (c * 64 + u * 16 < DH) {
-                            column(c * 64 + u * 16, ov);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) ov[e] = 0u;
-                        }
-                        if (__builtin_expect(again, 0) && c * 64 + u * 16 < DH) {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(acc[c * 64 + u * 16 + e]);
-                        }
-                        uint32_t w[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float lo = __uint_as_float(ov[2 * e]), hi = __uint_as_float(ov[2 * e + 1]);
-                            w[e] = none ? 0u : pack_bf16x2(lo * inv, hi * inv);
-                        }
-                        // 16-byte unit i of row r at i ^ (r % 8)
-                        *reinterpret_cast<uint4*>(stage + r * 128 + (((2 * u) ^ (r & 7)) << 4)) =
-                            make_uint4(w[0], w[1], w[2], w[3]);
-                        *reinterpret_cast<uint4*>(stage + r * 128 + (((2 * u + 1) ^ (r & 7)) << 4)) =
-                            make_uint4(w[4], w[5], w[6], w[7]);
-                    }
-                }
-                ptx::fence_proxy_async_smem();
-                if (c == NCH - 1) released();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&bars->ost_full[g]);
-                bool sok = true;
-                if (storer) {
-                    sok = ptx::mbar_wait_bounded(&bars->ost_full[g], sc & 1, abort_flag);
-                    if (sok) {
-                        ptx::tma_store_4d(&tmO, stage, c * 64, x.h * G, out_t0, x.at);
-                        ptx::bulk_commit_group();
-                        ptx::bulk_wait_group_read<0>();
-                        ptx::mbar_arrive(&bars->ost_free[g]);
-                    }
-                }
-                if (!(ok = __all_sync(0xffffffffu, sok))) break;
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (g == 0 ? nst > 0 : (nst > 0 && !both)) ptx::mbar_arrive(&bars->o_free[g]);
+                if (g == 0 && both) ptx::mbar_arrive(&bars->o_free[1]);
             }
         }
-        if (storer) ptx::bulk_wait_group<0>();   // the group's last store has completed
         if (!ok) {
             if (lane == 0) pt_error(p.err, ERRBIT_TIMEOUT_ATTENTION);
             *abort_flag = 1;
@@ -760,32 +733,34 @@ bool merged(const PagedDesc& d, int64_t (&st)[3]) {
     return true;
 }
 
-template <int DH> cudaError_t launch_pt(const PtParams& given, const DeviceInfo& dev, cudaStream_t s) {
-    using L = PtLayout<DH>;
+template <int DH, bool NARROW> cudaError_t launch_pt(const PtParams& given, const DeviceInfo& dev, cudaStream_t s) {
+    using L = PtLayout<DH, NARROW>;
     PtParams p = given;
     const PagedDesc& d = p.d;
-    alignas(64) CUtensorMap mq, mqp, mk, mv, mo;
-    const int64_t os[3] = {d.Tq * d.H * d.dh, d.H * d.dh, d.dh};
+    alignas(64) CUtensorMap mq, mqp, mk, mv;
     int64_t qm[3];
     const auto l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
     if (!ct_map(&mk, d.k, d.ks, d.pages, d.page, d.Hkv, d.dh, 1, p.unit, l2) ||
         !ct_map(&mv, d.v, d.vs, d.pages, d.page, d.Hkv, d.dh, 1, p.unit, l2))
         return cudaErrorInvalidValue;
-    // maps that no item uses are copies of another
-    mq = mqp = mo = mk;
+    // a map that no item uses is a copy of another
+    mq = mqp = mk;
     if (p.items > p.prefix_items && !ct_map(&mq, d.q, d.qs, d.B, d.Tq, d.H, d.dh, p.G, p.TT, l2)) return cudaErrorInvalidValue;
     if (p.prefix_items && (!merged(d, qm) || !ct_map(&mqp, d.q, qm, d.groups, p.S * d.Tq, d.H, d.dh, p.G, p.TT, l2)))
-        return cudaErrorInvalidValue;
-    if (!p.parts.n && !ct_map(&mo, d.o, os, d.B, d.Tq, d.H, d.dh, p.G, p.TT, CU_TENSOR_MAP_L2_PROMOTION_NONE))
         return cudaErrorInvalidValue;
     p.qb = d.qs[0] != 0;
     p.qpb = p.prefix_items && qm[0] != 0;
     static std::atomic<uint64_t> attr{0};
-    const cudaError_t e = set_smem_limit_once(paged_tc_kernel<DH>, L::SMEM, attr);
+    const cudaError_t e = set_smem_limit_once(paged_tc_kernel<DH, NARROW>, L::SMEM, attr);
     if (e != cudaSuccess) return e;
     const int grid = p.items < dev.num_sms ? p.items : dev.num_sms;
     p.sorted = p.items - p.prefix_items > grid && d.B > 1 && d.B <= PT_SORT;
-    return launch_dependent(paged_tc_kernel<DH>, dim3(grid), dim3(PT_THREADS), L::SMEM, s, mq, mqp, mk, mv, mo, p);
+    return launch_dependent(paged_tc_kernel<DH, NARROW>, dim3(grid), dim3(PT_THREADS), L::SMEM, s, mq, mqp, mk, mv, p);
+}
+
+template <int DH> cudaError_t launch_pt(const PtParams& p, const DeviceInfo& dev, cudaStream_t s) {
+    const bool one = (p.items == p.prefix_items || p.d.Tq <= p.TT) && (!p.prefix_items || p.S * p.d.Tq <= p.TT);
+    return one ? launch_pt<DH, true>(p, dev, s) : launch_pt<DH, false>(p, dev, s);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }

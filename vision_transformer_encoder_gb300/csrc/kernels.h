@@ -316,14 +316,14 @@ struct PagedParts {
 struct PagedPlan {
     int form;                                  // PagedForm
     int own_parts, prefix_parts;               // parts along the keys; prefix_parts 0: no prefix, or in the own ones
-    bool partial;                              // results go through workspace
+    bool partial;                              // results go through workspace; ROWS: the prefix's do
     bool prefix_tc;                            // ROWS: the prefix on tensor cores (tcgen05)
     size_t workspace;                          // bytes
     int launches;
 };
 // GENERIC: CUDA cores throughout. ROWS: the kernel of few queries for the own keys, joining the prefix's parts. TC: tensor
-// cores (tcgen05) throughout.
-enum PagedForm : int { PAGED_GENERIC = 0, PAGED_ROWS = 1, PAGED_TC = 2 };
+// cores (tcgen05) throughout. F32: the kernel of few queries in fp32 throughout.
+enum PagedForm : int { PAGED_GENERIC = 0, PAGED_ROWS = 1, PAGED_TC = 2, PAGED_F32 = 3 };
 // Few queries (attention_paged_rows.cu): bf16, at most 16 query rows per key head; joins the parts of the prefix that the
 // kernel launched before it leaves (n 0: there is none).
 bool paged_rows_supported(const PagedDesc& d);
@@ -335,6 +335,10 @@ int64_t paged_tc_items(const PagedDesc& d, bool own);   // of one part each
 bool paged_tc_apart(const PagedDesc& d);                // whether the prefix is better worked off apart
 cudaError_t launch_paged_tc(const PagedDesc& d, const PagedPlan& plan, const PagedParts& parts, bool own, const DeviceInfo& dev,
                             cudaStream_t s);
+// Few queries in fp32 (attention_paged_f32.cu): at most 16 query rows per key head.
+bool paged_f32_supported(const PagedDesc& d);
+int64_t paged_f32_blocks(const PagedDesc& d, bool own);   // CTAs of one part each
+cudaError_t launch_paged_f32(const PagedDesc& d, const PagedPlan& plan, const PagedParts& parts, cudaStream_t s);
 PagedPlan plan_paged(const PagedDesc& d, const DeviceInfo& dev);
 // workspace: plan.workspace bytes, 16-byte aligned.
 cudaError_t launch_paged_attention(const PagedDesc& d, const PagedPlan& plan, void* workspace, const DeviceInfo& dev,

@@ -168,6 +168,13 @@ __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* tm, int32_t c
                  : "memory");
 }
 
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* tm, int32_t c0, int32_t c1, int32_t c2, int32_t c3) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                     reinterpret_cast<uint64_t>(tm)),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+                 : "memory");
+}
+
 // 3-D variant (c0 innermost).
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* tm, uint64_t* bar,
                                             int32_t c0, int32_t c1, int32_t c2) {
@@ -366,6 +373,17 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&a)[32]) {
                    "+r"(a[14]), "+r"(a[15]), "+r"(a[16]), "+r"(a[17]), "+r"(a[18]), "+r"(a[19]),
                    "+r"(a[20]), "+r"(a[21]), "+r"(a[22]), "+r"(a[23]), "+r"(a[24]), "+r"(a[25]),
                    "+r"(a[26]), "+r"(a[27]), "+r"(a[28]), "+r"(a[29]), "+r"(a[30]), "+r"(a[31])
+                 :
+                 : "memory");
+}
+// And of the maximum that came with it.
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&a)[32], float& top) {
+    tmem_ld_wait_for(a);
+    asm volatile("" : "+f"(top)::"memory");
+}
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
                  :
                  : "memory");
 }
