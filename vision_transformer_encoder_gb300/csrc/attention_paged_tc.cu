@@ -53,7 +53,7 @@ template <int DH, bool NARROW> struct PtLayout {
     static constexpr int OFF_K = QBUF * QT * TILE;
     static constexpr int OFF_V = OFF_K + KS * TILE;
     static constexpr int OFF_BAR = OFF_V + VS * TILE;
-    static constexpr int OFF_ML = OFF_BAR + 768;         // group 1's maxima and sums for group 0; lengths while sorting
+    static constexpr int OFF_ML = OFF_BAR + 1024;        // group 1's maxima and sums for group 0; lengths while sorting
     static constexpr int SMEM = OFF_ML + 1024 + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
@@ -78,14 +78,14 @@ struct PtBars {
     // two of each for the half tiles in turn: a waiter may be one phase behind, never two
     uint64_t s_full[2][2], p_full[2][2], o_done[2][2], o_free[2];
     uint64_t ml_full;            // group 1's part of a shared tile is there
+    uint64_t x_full[2], x_empty[2];   // items, as the producer of keys makes them out ahead of the others
     uint64_t done;
     uint32_t tmem_slot;
     int abort_flag;
     uint8_t order[PT_SORT];      // sequences, the longest first
 };
-static_assert(sizeof(PtBars) <= 768, "barriers");
 
-struct PtItem {
+struct alignas(16) PtItem {
     bool prefix;                 // kind
     int at, h, z;                // sequence or group, key head, part
     int t0, tokens;              // first token of the pair, tokens of the sequence (group)
@@ -95,6 +95,7 @@ struct PtItem {
     int low, new_;               // query t sees own keys before low + t; new tokens
     int kt0;                     // first key tile of the range
     int count0, count1;          // key tiles of it that tile 0, tile 1 see
+    bool gaps;                   // some page of the range is absent: half tiles are looked at one by one then
     const int32_t *table0, *table1;
 
     __device__ __forceinline__ int count(int g) const { return g ? count1 : count0; }
@@ -121,6 +122,12 @@ struct PtItem {
         return 2 * n - (j == count(q) - 1 && keys(j, limit(p, q)) <= PT_SUB);
     }
 };
+
+struct PtShared {
+    PtBars bars;
+    PtItem items[2];
+};
+static_assert(sizeof(PtShared) <= 1024, "barriers and items");
 
 __device__ __forceinline__ PtItem pt_item(const PtParams& p, int item, const uint8_t* order) {
     const PagedDesc& d = p.d;
@@ -230,7 +237,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     uint8_t* sQ = smem;
     uint8_t* sK = smem + L::OFF_K;
     uint8_t* sV = smem + L::OFF_V;
-    PtBars* bars = reinterpret_cast<PtBars*>(smem + L::OFF_BAR);
+    PtShared* shared = reinterpret_cast<PtShared*>(smem + L::OFF_BAR);
+    PtBars* bars = &shared->bars;
     float* sml = reinterpret_cast<float*>(smem + L::OFF_ML);
     volatile int* abort_flag = &bars->abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -245,6 +253,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 ptx::mbar_init(&bars->o_done[i][b], 1);
             }
             ptx::mbar_init(&bars->o_free[i], 4);
+            ptx::mbar_init(&bars->x_full[i], 1);
+            ptx::mbar_init(&bars->x_empty[i], 11);    // every other warp
         }
         for (int i = 0; i < 6; ++i) {
             ptx::mbar_init(&bars->k_full[i], 1);
@@ -301,6 +311,14 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         }
         __syncthreads();
     }
+    // The i-th item of this CTA, for every warp but the one that makes it out; false where the wait gave up.
+    auto take = [&](int i, PtItem& x) -> bool {
+        if (!__all_sync(0xffffffffu, ptx::mbar_wait_bounded(&bars->x_full[i & 1], (i >> 1) & 1, abort_flag))) return false;
+        x = shared->items[i & 1];
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bars->x_empty[i & 1]);
+        return true;
+    };
     // TMEM columns: S_g at 128 g, two buffers of 64 with P over each; O_g at 256 + 128 g
 
     if (warp >= 10) {
@@ -318,7 +336,26 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             return __all_sync(0xffffffffu, ptx::mbar_wait_bounded<true>(bar, parity, abort_flag));
         };
         for (int i = 0; item_of(i) < p.items && ok; ++i) {
-            const PtItem x = pt_item(p, (int)item_of(i), bars->order);
+            PtItem x;
+            if (kq) {
+                x = pt_item(p, (int)item_of(i), bars->order);
+                x.gaps = false;
+                const int end = x.kt0 + x.tiles();
+                if (x.kt0 < x.n0)
+                    for (int e = x.kt0 * PT_KEYS / page + lane; e * page < min(x.len0, end * PT_KEYS); e += 32)
+                        x.gaps = x.gaps || (uint32_t)load(x.table0 + e) >= (uint32_t)p.d.pages;
+                for (int e = max(0, x.kt0 - x.n0) * PT_KEYS / page + lane; e * page < min(x.len1, (end - x.n0) * PT_KEYS); e += 32)
+                    x.gaps = x.gaps || (uint32_t)load(x.table1 + e) >= (uint32_t)p.d.pages;
+                x.gaps = __any_sync(0xffffffffu, x.gaps);
+                if (!(ok = wait(&bars->x_empty[i & 1], ((i >> 1) & 1) ^ 1))) break;
+                if (lane == 0) {
+                    shared->items[i & 1] = x;
+                    ptx::mbar_arrive(&bars->x_full[i & 1]);
+                }
+                __syncwarp();
+            } else if (!(ok = take(i, x))) {
+                break;
+            }
             const int n = x.tiles();
             if (n == 0) continue;
             if (kq) {
@@ -387,7 +424,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             return __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, parity, abort_flag));
         };
         for (int i = 0; item_of(i) < p.items && ok; ++i) {
-            const PtItem x = pt_item(p, (int)item_of(i), bars->order);
+            PtItem x;
+            if (!(ok = take(i, x))) break;
             const int n = x.tiles();
             if (n == 0) continue;
             const uint32_t qb = ii % QB;
@@ -487,7 +525,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             return __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, parity, abort_flag));
         };
         for (int i = 0; item_of(i) < p.items && ok; ++i) {
-            const PtItem x = pt_item(p, (int)item_of(i), bars->order);
+            PtItem x;
+            if (!(ok = take(i, x))) break;
             const int nst = x.halves(p, g), qt = x.shared() ? 0 : g;   // query tile that it works on
             const int t = x.t0 + qt * p.TT + tok;
             // a warp whose 32 rows hold no query only keeps the barrier protocol
@@ -496,24 +535,20 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             const int most = x.limit(p, qt);
             const int lim = t < x.new_ ? x.low + t : most;   // own keys that this row sees
             float m = -INFINITY, l = 0.f;
-            // whether any page of the range is absent: half tiles are looked at one by one only then
-            bool gaps = false;
-            if (live && nst > 0) {
-                const int end = x.kt0 + x.tiles();
-                if (x.kt0 < x.n0)
-                    for (int e = x.kt0 * PT_KEYS / page + lane; e * page < min(x.len0, end * PT_KEYS); e += 32)
-                        gaps = gaps || (uint32_t)load(x.table0 + e) >= (uint32_t)p.d.pages;
-                for (int e = max(0, x.kt0 - x.n0) * PT_KEYS / page + lane; e * page < min(x.len1, (end - x.n0) * PT_KEYS); e += 32)
-                    gaps = gaps || (uint32_t)load(x.table1 + e) >= (uint32_t)p.d.pages;
-                gaps = __any_sync(0xffffffffu, gaps);
-            }
+            const bool gaps = x.gaps;
+            bool coarse = false;
             for (int j = 0; j < nst; ++j, ++tt) {
                 const int kt = x.kt0 + x.tile(g, j >> 1);
                 const bool ahead = kt < x.n0;
                 const int key = (ahead ? kt : kt - x.n0) * PT_KEYS + (j & 1) * PT_SUB;
+                const int valid = (ahead ? x.len0 : lim) - key;
+                // All rows of the warp see the whole half tile and have a maximum: no masks, and mostly none to raise. (At 128,
+                // where the products are what takes longest, this way round is slower: 563 us instead of 539 for 4 x 2048
+                // queries behind 8200 keys; below it is faster, 55.1 instead of 57.1 for 2 x 1025 over 4100.)
+                const bool plain = DH < 128 && !gaps && __all_sync(0xffffffffu, valid >= PT_SUB && m > -INFINITY && !coarse);
+                const uint32_t tS = tmem + g * 128 + (tt & 1) * PT_SUB + lane_off;
                 if (!(ok = wait(&bars->s_full[g][tt & 1], (tt >> 1) & 1))) break;
                 ptx::tc_fence_after();
-                const uint32_t tS = tmem + g * 128 + (tt & 1) * PT_SUB + lane_off;
                 if (live) {
                     uint32_t sv[PT_SUB];   // S, then P packed in place; the largest of each half comes with the load
                     uint32_t(&s0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sv[0]);
@@ -522,56 +557,57 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     float mx1 = ptx::tmem_ld_red_max_32x32b_x32(tS + 32, s1);
                     ptx::tmem_ld_wait_for(s0, mrow);
                     ptx::tmem_ld_wait_for(s1, mx1);
-                    mrow = fmaxf(mrow, mx1);
-                    const int valid = (ahead ? x.len0 : lim) - key;
-                    if (gaps || __any_sync(0xffffffffu, valid < PT_SUB)) {
-                        uint32_t absent = 0;
-                        if (__builtin_expect(gaps, 0)) {
-                            int pg = 0;   // of this lane's unit of the half tile
-                            if (lane * unit < PT_SUB && key + lane * unit < (ahead ? x.len0 : x.len1))
-                                pg = load((ahead ? x.table0 : x.table1) + (key + lane * unit) / page);
-                            absent = __ballot_sync(0xffffffffu, pg < 0 || pg >= p.d.pages);
-                        }
-                        mrow = -INFINITY;
-#pragma unroll
-                        for (int e = 0; e < PT_SUB; e += 16) {
-                            const bool away = absent >> (e / unit) & 1;
-#pragma unroll
-                            for (int y = e; y < e + 16; ++y) {
-                                if (y >= valid || away) sv[y] = __float_as_uint(-INFINITY);
-                                mrow = fmaxf(mrow, __uint_as_float(sv[y]));
+                    mrow = fmaxf(mrow, mx1) * sl2;
+                    float alpha = 1.f, mul = sl2;
+                    if (!plain || __any_sync(0xffffffffu, mrow > m + PT_SLACK)) {
+                        if (gaps || __any_sync(0xffffffffu, valid < PT_SUB)) {
+                            uint32_t absent = 0;
+                            if (__builtin_expect(gaps, 0)) {
+                                int pg = 0;   // of this lane's unit of the half tile
+                                if (lane * unit < PT_SUB && key + lane * unit < (ahead ? x.len0 : x.len1))
+                                    pg = load((ahead ? x.table0 : x.table1) + (key + lane * unit) / page);
+                                absent = __ballot_sync(0xffffffffu, pg < 0 || pg >= p.d.pages);
                             }
+                            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                            for (int e = 0; e < PT_SUB; e += 16) {
+                                const bool away = absent >> (e / unit) & 1;
+#pragma unroll
+                                for (int y = e; y < e + 16; ++y) {
+                                    if (y >= valid || away) sv[y] = __float_as_uint(-INFINITY);
+                                    mx[y & 3] = fmaxf(mx[y & 3], __uint_as_float(sv[y]));
+                                }
+                            }
+                            mrow = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
                         }
-                    }
-                    mrow *= sl2;
-                    float alpha = 1.f;
-                    if (mrow > m + PT_SLACK || m == -INFINITY) {   // raise the maximum
-                        const float m_new = fmaxf(m, mrow);
-                        if (m_new > -INFINITY) alpha = exp2_approx(m - m_new);
-                        m = m_new;
+                        if (mrow > m + PT_SLACK || m == -INFINITY) {   // raise the maximum
+                            const float m_new = fmaxf(m, mrow);
+                            if (m_new > -INFINITY) alpha = exp2_approx(m - m_new);
+                            m = m_new;
+                        }
+                        coarse = fabsf(m) > PT_COARSE && m > -INFINITY;
+                        if (__any_sync(0xffffffffu, (j > 0 && alpha != 1.f) || coarse)) {
+                            if (j > 0) {
+                                // P V of the half tile before writes O
+                                if (!(ok = wait(&bars->o_done[g][(tt - 1) & 1], ((tt - 1) >> 1) & 1))) break;
+                                ptx::tc_fence_after();
+#pragma unroll
+                                for (int c = 0; c < DH; c += 16) {
+                                    uint32_t ov[16];
+                                    ptx::tmem_ld_32x32b_x16(tO + c, ov);
+                                    ptx::tmem_ld_wait_for(ov);
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                                    ptx::tmem_st_32x32b_x16(tO + c, ov);
+                                }
+                            }
+                            const float f = coarse ? sl2 : 1.f;
+#pragma unroll
+                            for (int e = 0; e < PT_SUB; ++e) sv[e] = __float_as_uint(__fmul_rn(__uint_as_float(sv[e]), f));
+                        }
+                        mul = coarse ? 1.f : sl2;
                     }
                     const float base = m == -INFINITY ? 0.f : m;   // only infinite scores so far: weights of zero
-                    const bool coarse = fabsf(base) > PT_COARSE;
-                    if (__any_sync(0xffffffffu, (j > 0 && alpha != 1.f) || coarse)) {
-                        if (j > 0) {
-                            // P V of the half tile before writes O
-                            if (!(ok = wait(&bars->o_done[g][(tt - 1) & 1], ((tt - 1) >> 1) & 1))) break;
-                            ptx::tc_fence_after();
-#pragma unroll
-                            for (int c = 0; c < DH; c += 16) {
-                                uint32_t ov[16];
-                                ptx::tmem_ld_32x32b_x16(tO + c, ov);
-                                ptx::tmem_ld_wait_for(ov);
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                                ptx::tmem_st_32x32b_x16(tO + c, ov);
-                            }
-                        }
-                        const float f = coarse ? sl2 : 1.f;
-#pragma unroll
-                        for (int e = 0; e < PT_SUB; ++e) sv[e] = __float_as_uint(__fmul_rn(__uint_as_float(sv[e]), f));
-                    }
-                    const float mul = coarse ? 1.f : sl2;
                     const unsigned long long s2 = f2_pack(mul, mul), nm = f2_pack(-base, -base);
                     unsigned long long ls[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
@@ -628,40 +664,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 l = 0.f;
             }
             const int out_rows = min(p.TT, x.tokens - out_t0) * G;   // of this group's own query tile; none if it does not exist
-            auto column = [&](int c, uint32_t (&ov)[8]) {   // 8 columns of O, all lanes of the warp
-                ptx::tmem_ld_32x32b_x8(tO + c, ov);
-                ptx::tmem_ld_wait_for(ov);
-                if (both) {
-                    uint32_t o1[8];
-                    ptx::tmem_ld_32x32b_x8(tO + 128 + c, o1);
-                    ptx::tmem_ld_wait_for(o1);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        ov[e] = __float_as_uint(fmaf(f1, __uint_as_float(o1[e]), f0 * __uint_as_float(ov[e])));
-                }
-            };
             bool row = r < out_rows && t < x.new_ && !(g == 1 && x.live < 2);
             if (x.prefix && row && p.d.q_lens)   // a token of its sequence
                 row = t % (int)p.d.Tq < load(p.d.q_lens + (int64_t)x.at * p.S + t / (int)p.d.Tq);
             if (!row) l = 0.f;
-            bool again = false;
-            float acc[DH];
-            if (have && live && x.len1 > 0) {
-                // rows do not all see the same: values that this one does not see can make it a NaN
-                float odd = 0.f;
-#pragma unroll
-                for (int c = 0; c < DH; c += 8) {
-                    uint32_t ov[8];
-                    column(c, ov);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) odd = fmaf(__uint_as_float(ov[e]), 0.f, odd);
-                }
-                if (__builtin_expect(row && odd != 0.f, 0)) {
-                    const PtItem y = x;   // so that x itself keeps to registers
-                    again = pt_row(p, y, t, x.h * G + r % G, lim, m, acc);
-                }
-                __syncwarp();
-            }
             const bool there = r < out_rows;
             const int64_t at = ((int64_t)x.at * x.tokens + out_t0 + tok) * p.d.H + x.h * G + r % G;   // row of the output
             if (quarter * 32 < out_rows) {
@@ -670,36 +676,59 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.d.o) + at * DH;
                 const bool none = l == 0.f;
                 const float inv = none ? 0.f : 1.f / l;
-#pragma unroll
-                for (int c = 0; c < DH; c += 8) {
-                    uint32_t ov[8];
-                    if (have) {
-                        column(c, ov);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) ov[e] = 0u;
-                    }
-                    if (__builtin_expect(again, 0)) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) ov[e] = __float_as_uint(acc[c + e]);
-                    }
-                    if (!there) continue;
-                    float v[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(ov[e]);
+                // A thread stores its row. (Turned round in shared memory, so that neighbouring lanes store one row, an item's
+                // end takes as long: 5100 cycles for 128 x 128.)
+                auto put = [&](int c, const float (&v)[8]) {
+                    if (!there || (p.parts.n && none)) return;
                     if (p.parts.n) {
-                        if (none) continue;
                         *reinterpret_cast<float4*>(part + c) = make_float4(v[0], v[1], v[2], v[3]);
                         *reinterpret_cast<float4*>(part + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
                     } else {
+                        uint32_t w[4];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = none ? 0.f : v[e] * inv;
-                        *reinterpret_cast<uint4*>(out + c) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                                        pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+                        for (int e = 0; e < 4; ++e) w[e] = none ? 0u : pack_bf16x2(v[2 * e] * inv, v[2 * e + 1] * inv);
+                        *reinterpret_cast<uint4*>(out + c) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                };
+                float odd = 0.f;
+#pragma unroll
+                for (int c = 0; c < DH; c += 16) {
+                    uint32_t ov[16];
+                    if (have) {   // not group 1 behind a shared tile, which has nothing of its own, nor anything beyond its columns
+                        ptx::tmem_ld_32x32b_x16(tO + c, ov);
+                        ptx::tmem_ld_wait_for(ov);
+                        if (both) {
+                            uint32_t o1[16];
+                            ptx::tmem_ld_32x32b_x16(tO + 128 + c, o1);
+                            ptx::tmem_ld_wait_for(o1);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                ov[e] = __float_as_uint(fmaf(f1, __uint_as_float(o1[e]), f0 * __uint_as_float(ov[e])));
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) ov[e] = 0u;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; e += 8) {
+                        float v[8];
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) {
+                            v[y] = __uint_as_float(ov[e + y]);
+                            odd = fmaf(v[y], 0.f, odd);
+                        }
+                        put(c + e, v);
                     }
                 }
-                if (p.parts.n && there)
-                    static_cast<float2*>(p.parts.ml)[to] = make_float2(none ? -INFINITY : m, l);
+                // rows do not all see the same: values that this one does not see can make it a NaN
+                if (__builtin_expect(row && x.len1 > 0 && odd != 0.f, 0)) {
+                    const PtItem y = x;   // so that x itself keeps to registers
+                    float acc[DH];
+                    if (pt_row(p, y, t, x.h * G + r % G, lim, m, acc))
+                        for (int c = 0; c < DH; c += 8) put(c, *reinterpret_cast<float(*)[8]>(acc + c));
+                }
+                __syncwarp();
+                if (p.parts.n && there) static_cast<float2*>(p.parts.ml)[to] = make_float2(none ? -INFINITY : m, l);
             }
             // O has been read: its group's next products may write it, and group 1's where it was read alongside
             ptx::tc_fence_before();
