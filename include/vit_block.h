@@ -35,7 +35,9 @@
  *    lets the next one start its set-up early. Stream order is kept for every caller
  *    kernel launched normally. A caller kernel launched after a call with programmatic
  *    stream serialisation must wait on the grid dependency before reading the results,
- *    as CUDA requires of any such launch. VIT_PDL=0 turns it off.
+ *    as CUDA requires of any such launch. VIT_PDL=0 turns it off. (vit_paged_attention also reads
+ *    lengths and page tables ahead of that wait, to bring to L2 what they point at; it uses nothing of
+ *    that, and reads them again behind it. They have to be allocated by then.)
  *  - Every call returns a vit_status (0 = success). No call aborts, traps or throws.
  *  - Results are deterministic: the same inputs give bit-identical outputs.
  */
@@ -529,7 +531,7 @@ int vit_rotary(const void* x, const int64_t* x_strides, const int32_t* positions
  * A pool of pages of `page` tokens each: keys k and values v (pages, page, heads, dh), all of dtype. A sequence's
  * page table (one row of a (sequences, table_pages) int32 device array) says which page holds its keys
  * [i page, (i + 1) page). Entries outside [0, pages) are absent: nothing is written there, and attention does not see
- * their keys. Entries that no key falls on are not read.
+ * their keys. Entries that no key falls on may be anything.
  */
 typedef struct {
     void* k;
@@ -570,10 +572,12 @@ int vit_cache_append(const void* k, const int64_t* k_strides, const void* v, con
  *   scale         finite, of magnitude up to 1e30 unless F64
  *   o             (B, Tq, H, dh) contiguous, apart from every input
  * A row that sees no key, or whose scores are all minus infinity, is zeros. What lies past the lengths and on absent
- * pages may be anything, NaN included. Softmax in fp32 (fp64 for F64). On tensor cores weights meet V
- * rounded to bf16 (their sum is not). They take BF16, dh a multiple of 8 up to 128 where a key head has at most 16
- * query rows (Tq G) and no prefix, else 64, 80, 96 or 128; pages of a multiple of 16 tokens; 16-byte aligned
- * rows; positive scales. dh up to 512.
+ * pages may be anything, NaN included; what a later token holds does not reach the queries in front of it. Softmax in
+ * fp32 (fp64 for F64), where scaled scores past its range, as infinite ones, give NaN. BF16 runs on tensor cores, where weights meet V rounded to bf16
+ * (their sum is not), with pages of a multiple of 16 tokens and 16-byte aligned rows: own keys with dh a multiple of 8 up
+ * to 128 where a key head has at most 16 query rows (Tq G); more rows, and prefixes, with dh 64, 80, 96 or 128 and
+ * positive scales, up to 2^26 keys. F32 has a kernel for at most 16 query rows, dh a multiple of 4 up to 128, pages of a multiple of 8.
+ * Everything else runs on CUDA cores, some ten to a hundred times slower. dh up to 512.
  * Errors: VIT_ERR_ARG, VIT_ERR_DTYPE, VIT_ERR_UNSUPPORTED (dh), VIT_ERR_NOMEM, VIT_ERR_CUDA.
  */
 int vit_paged_attention(const void* q, const int64_t* q_strides, const vit_paged_cache* cache, const int32_t* table,

@@ -624,6 +624,42 @@ def test_paged_attention_where_keys_are_dealt_out(Tq, H, Hkv, dh):
             assert same(h.call(), got)
 
 
+@pytest.mark.parametrize("Tq,H,Hkv,dh,own,prefix", SPECIAL + [(40, 4, 4, 96, [300] * 3, [500])])
+def test_paged_attention_of_broadcast_queries(Tq, H, Hkv, dh, own, prefix):
+    """One set of queries for all sequences, one token's for all tokens, one head's for all heads (strides of zero)."""
+    h = Held(Tq, H, Hkv, dh, 16, own, prefix)
+    q = h.q
+    for wide in (q[:1].expand(q.shape), q[:, :1].expand(q.shape), q[:, :, :1].expand(q.shape)):
+        h.q = wide.contiguous()
+        o, w, mag, n = h.ref(dh ** -0.5)
+        close(h.call(q=wide), o, paged_tol(h, o, w, mag, n, dh))
+
+
+@pytest.mark.parametrize("Tq,H,Hkv,dh,own,prefix", SPECIAL + [(300, 4, 4, 64, [1500, 600], []), (130, 4, 2, 96, [800, 500], [700])])
+@pytest.mark.parametrize("dt", [BF, F32], ids=str)
+def test_paged_attention_of_values_that_are_no_numbers(Tq, H, Hkv, dh, own, prefix, dt):
+    """All values NaN, or one early one infinite: rows that see them are not finite, and the call ends in its time."""
+    h = Held(Tq, H, Hkv, dh, 16, own, prefix, dt=dt)
+    keep = h.vp.clone()
+    h.vp[:] = math.nan
+    assert torch.isnan(h.call()).all()
+    h.vp.copy_(keep)
+    ref = h.call()
+    pg, s = slots(h.table, 0, 0, 16)
+    h.vp[pg, s, 0] = math.inf
+    got, G = h.call(), H // Hkv
+    assert not torch.isfinite(got[0, :, :G]).any() and same(got[1:], ref[1:]) and same(got[0, :, G:], ref[0, :, G:])
+
+
+@pytest.mark.parametrize("page", [8, 16, 48, 80, 96, 112, 144, 160, 384])
+@pytest.mark.parametrize("Tq,H,Hkv,dh,dt", [(1, 4, 2, 64, BF), (3, 8, 2, 128, BF), (50, 4, 4, 80, BF), (200, 2, 2, 64, BF), (2, 4, 2, 80, F32)], ids=str)
+def test_paged_attention_page_sizes(Tq, H, Hkv, dh, dt, page):
+    """Pages that tiles straddle, and that end inside a tile."""
+    h = Held(Tq, H, Hkv, dh, page, [Tq, 3 * page + Tq, 500 + Tq], [2 * page + 5], dt=dt)
+    check_paged(h)
+    check_paged(Held(Tq, H, Hkv, dh, page, [Tq + page - 1, 1000 + Tq], [], dt=dt))
+
+
 # ------------------------------------------------------------------------------- together
 def step(p, x, kp, vp, table, starts, kv_lens, f, H, Hkv, lens=None, positions=None, before=None, out=None):
     """The self attention of a decoder's layer on new tokens x (B, T, D): projection, rotation and append, attention."""
@@ -677,14 +713,15 @@ def test_tokens_one_by_one_and_in_parts_see_what_the_whole_text_sees(H, Hkv):
     assert same(got[0], got[1]) and same(got[0], got[2])
 
 
-def test_a_captured_step_replays_on_new_inputs_and_streams_agree():
-    """Two graphs of one decoding step behind a shared prefix, each with a cache of its own, replayed at once."""
+@pytest.mark.parametrize("T", [1, 3, 40])
+def test_a_captured_step_replays_on_new_inputs_and_streams_agree(T):
+    """Two graphs of a step behind a shared prefix, each with a cache of its own, replayed at once."""
     B, H, Hkv, D, page = 6, 8, 2, 512, 16
     p, f = make_step(D, H, Hkv), api.rotary_frequencies(64, device=DEV)
-    h = Held(1, H, Hkv, 64, page, [40, 3, 17, 90, 1, 64], [300, 700])
-    x = rand(B, 1, D, seed=30, dtype=BF)
-    starts, lens = h.kv_lens - 1, h.kv_lens.clone()
-    pos = (starts + 700)[:, None].contiguous()
+    h = Held(T, H, Hkv, 64, page, [40, T, 47, 90, T + 1, 64], [300, 700])
+    x = rand(B, T, D, seed=30, dtype=BF)
+    starts, lens = h.kv_lens - T, h.kv_lens.clone()
+    pos = (starts[:, None] + 700 + torch.arange(T, device=DEV)).int().contiguous()
     args = lambda kp, vp: (p, x, kp, vp, h.table, starts, lens, f, H, Hkv, None, pos, (h.prefix_table, h.prefix_lens))
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -699,7 +736,7 @@ def test_a_captured_step_replays_on_new_inputs_and_streams_agree():
             y = step(*args(kp, vp))
         graphs.append((g, y, kp, vp))
     for seed in (40, 41):
-        x.copy_(rand(B, 1, D, seed=seed, dtype=BF))
+        x.copy_(rand(B, T, D, seed=seed, dtype=BF))
         kp, vp = graphs[0][2].clone(), graphs[0][3].clone()
         eager = step(*args(kp, vp))
         torch.cuda.synchronize()
