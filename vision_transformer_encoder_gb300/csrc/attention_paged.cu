@@ -107,13 +107,33 @@ __global__ void __launch_bounds__(PG_THREADS) paged_generic_kernel(const __grid_
                 int pg = tid < n ? load(table + (int64_t)(u0 + tid) / d.page) : -1;
                 spage[tid] = pg >= 0 && pg < d.pages ? pg : -1;
             }
+            // this tile of a pool to shared memory, AT keys of a warp's in flight
+            auto fetch = [&](const void* pool, const int64_t(&st)[3]) {
+                constexpr int COLS = DHT / 32, AT = DHT <= 128 ? 4 : 1, WARPS = PG_THREADS / 32;
+                const T* base = static_cast<const T*>(pool) + hk * st[2];
+                for (int u1 = warp; u1 < n; u1 += AT * WARPS) {
+                    T x[AT][COLS];
+#pragma unroll
+                    for (int y = 0; y < AT; ++y) {
+                        const int u = u1 + y * WARPS;
+                        if (u >= n || spage[u] < 0) continue;
+                        const T* row = base + spage[u] * st[0] + (int64_t)(u0 + u) % d.page * st[1];
+#pragma unroll
+                        for (int c = 0; c < COLS; ++c)
+                            if (lane + 32 * c < dh) x[y][c] = row[lane + 32 * c];
+                    }
+#pragma unroll
+                    for (int y = 0; y < AT; ++y) {
+                        const int u = u1 + y * WARPS;
+                        if (u >= n || spage[u] < 0) continue;
+#pragma unroll
+                        for (int c = 0; c < COLS; ++c)
+                            if (lane + 32 * c < dh) skv[u * (dh + 1) + lane + 32 * c] = to_acc<A>(x[y][c]);
+                    }
+                }
+            };
             __syncthreads();   // the last tile's values have been read
-            for (int u = warp; u < n; u += PG_THREADS / 32) {
-                const int pg = spage[u];
-                if (pg < 0) continue;
-                const T* k = static_cast<const T*>(d.k) + pg * d.ks[0] + (int64_t)(u0 + u) % d.page * d.ks[1] + hk * d.ks[2];
-                for (int c = lane; c < dh; c += 32) skv[u * (dh + 1) + c] = to_acc<A>(k[c]);
-            }
+            fetch(d.k, d.ks);
             __syncthreads();
             A x[KPT], mx = m;
 #pragma unroll
@@ -147,12 +167,7 @@ __global__ void __launch_bounds__(PG_THREADS) paged_generic_kernel(const __grid_
             m = mx;
             if (k0 == 0) salpha[r] = alpha;
             __syncthreads();   // scores made, weights there: values over the keys
-            for (int u = warp; u < n; u += PG_THREADS / 32) {
-                const int pg = spage[u];
-                if (pg < 0) continue;
-                const T* v = static_cast<const T*>(d.v) + pg * d.vs[0] + (int64_t)(u0 + u) % d.page * d.vs[1] + hk * d.vs[2];
-                for (int c = lane; c < dh; c += 32) skv[u * (dh + 1) + c] = to_acc<A>(v[c]);
-            }
+            fetch(d.v, d.vs);
             __syncthreads();
 #pragma unroll
             for (int e = 0; e < RPT; ++e)

@@ -1,5 +1,5 @@
-// attention_paged_f32.cu -- paged attention of few queries in fp32: the mathematics of attention_paged.cu where a key head serves
-// at most 16 query rows (Tq * G <= 16), head width up to 128 in steps of 4, pages of a multiple of 8 tokens.
+// attention_paged_f32.cu -- paged attention in fp32: the mathematics of attention_paged.cu for head widths up to 128 in steps
+// of 4 and pages of a multiple of 8 tokens.
 //
 // Bound by reading keys and values once. A warp takes up to four rows (NR) of one key head and 8 keys, which lie in one page, at
 // a time: its lanes hold VEC columns each, so that a key is one coalesced load, and all 16 loads of a step are in flight
@@ -253,9 +253,10 @@ int64_t paged_f32_blocks(const PagedDesc& d, bool own) {
 }
 
 bool paged_f32_supported(const PagedDesc& d) {
-    if (d.dt != DT_F32 || d.dh % 4 != 0 || d.dh > 128 || d.page % PF_KEYS != 0 || d.Tq * (d.H / d.Hkv) > 16) return false;
+    if (d.dt != DT_F32 || d.dh % 4 != 0 || d.dh > 128 || d.page % PF_KEYS != 0) return false;
     const int64_t unit = d.dh <= 64 ? 2 : 4;
-    if (d.B > 0x7fffffff / 256 / (d.Hkv * 16)) return false;
+    // CTAs: rows of a group's sequences and key head, 32 parts, own keys and prefix
+    if (d.Tq > 0x7fffffff / 64 / d.H || d.B > 0x7fffffff / 64 / (d.H * d.Tq)) return false;
     return columns_fit(d.q, d.qs, unit) && columns_fit(d.k, d.ks, unit) && columns_fit(d.v, d.vs, unit);
 }
 

@@ -322,7 +322,7 @@ struct PagedPlan {
     int launches;
 };
 // GENERIC: CUDA cores throughout. ROWS: the kernel of few queries for the own keys, joining the prefix's parts. TC: tensor
-// cores (tcgen05) throughout. F32: the kernel of few queries in fp32 throughout.
+// cores (tcgen05) throughout. F32: the fp32 kernel throughout.
 enum PagedForm : int { PAGED_GENERIC = 0, PAGED_ROWS = 1, PAGED_TC = 2, PAGED_F32 = 3 };
 // Few queries (attention_paged_rows.cu): bf16, at most 16 query rows per key head; joins the parts of the prefix that the
 // kernel launched before it leaves (n 0: there is none).
@@ -335,7 +335,7 @@ int64_t paged_tc_items(const PagedDesc& d, bool own);   // of one part each
 bool paged_tc_apart(const PagedDesc& d);                // whether the prefix is better worked off apart
 cudaError_t launch_paged_tc(const PagedDesc& d, const PagedPlan& plan, const PagedParts& parts, bool own, const DeviceInfo& dev,
                             cudaStream_t s);
-// Few queries in fp32 (attention_paged_f32.cu): at most 16 query rows per key head.
+// fp32 (attention_paged_f32.cu): head widths up to 128 in steps of 4, pages of a multiple of 8.
 bool paged_f32_supported(const PagedDesc& d);
 int64_t paged_f32_blocks(const PagedDesc& d, bool own);   // CTAs of one part each
 cudaError_t launch_paged_f32(const PagedDesc& d, const PagedPlan& plan, const PagedParts& parts, cudaStream_t s);
