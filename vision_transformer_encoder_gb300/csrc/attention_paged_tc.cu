@@ -690,7 +690,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                         *reinterpret_cast<uint4*>(out + c) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 };
-                float odd = 0.f;
+                unsigned long long sum = 0ull;   // of the row: not finite where an element is not
 #pragma unroll
                 for (int c = 0; c < DH; c += 16) {
                     uint32_t ov[16];
@@ -713,15 +713,15 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     for (int e = 0; e < 16; e += 8) {
                         float v[8];
 #pragma unroll
-                        for (int y = 0; y < 8; ++y) {
-                            v[y] = __uint_as_float(ov[e + y]);
-                            odd = fmaf(v[y], 0.f, odd);
-                        }
+                        for (int y = 0; y < 8; ++y) v[y] = __uint_as_float(ov[e + y]);
+                        sum = f2_add(sum, f2_add(f2_add(f2_pack(v[0], v[1]), f2_pack(v[2], v[3])), f2_add(f2_pack(v[4], v[5]), f2_pack(v[6], v[7]))));
                         put(c + e, v);
                     }
                 }
                 // rows do not all see the same: values that this one does not see can make it a NaN
-                if (__builtin_expect(row && x.len1 > 0 && odd != 0.f, 0)) {
+                float s0, s1;
+                f2_unpack(sum, s0, s1);
+                if (__builtin_expect(row && x.len1 > 0 && !isfinite(s0 + s1), 0)) {
                     const PtItem y = x;   // so that x itself keeps to registers
                     float acc[DH];
                     if (pt_row(p, y, t, x.h * G + r % G, lim, m, acc))
