@@ -9,9 +9,13 @@
 // bf16 (off by 2^-20, where a result is rounded at 2^-9), sincospi for fp32 and fp64.
 //
 // Bound by reading and writing each head once. A block takes a few tokens: it makes their sines and cosines once, in shared
-// memory, and streams 16-byte units of all their heads past them (both halves of a pair where they lie apart). Sines of its
-// own for each thread, which then walked over the heads with eight units in flight, kept 70 to 118 registers and ran at
-// 4.4 TB/s instead. With few tokens the heads go to blocks of their own.
+// memory. A thread has one 16-byte unit (both halves of its pairs where they lie apart) of one head and walks over the tokens,
+// RO_AHEAD in flight: what depends on the head stays in registers, and a unit costs little more than its load, products and
+// store. With few tokens the heads go to blocks of their own.
+//
+// 2 x 8200 tokens of 12 heads of 64 in fp32: 19.4 us (5.2 TB/s); 4 x 2048 tokens of 16 + 2 + 2 heads of 128 turned and
+// appended: 17.3 us (4.6 TB/s). Sines of a thread's own, which then walked over a token's heads: 22.9 and 22.0. Heads and
+// tokens in turn, with 105 instructions to a unit: 21.7 and 18.3.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -24,7 +28,7 @@
 namespace vit {
 namespace {
 
-constexpr int RO_THREADS = 256, RO_MAXPAIRS = 256, RO_TOKENS = 32, RO_SINES = 1024;
+constexpr int RO_THREADS = 256, RO_MAXPAIRS = 256, RO_TOKENS = 32, RO_SINES = 1024, RO_MOST = 512, RO_AHEAD = 4;
 
 // f / 2 pi as a fraction of a turn in units of 2^-64
 __device__ __forceinline__ uint64_t turn_of(double f) {
@@ -130,96 +134,68 @@ template <typename T> struct Unit {
     }
 };
 
-// tile: tokens of a block; groups: blocks that share a token's heads, `span` each.
+// tile: tokens of a block; groups: blocks that share a token's heads, `span` each; every rows-th token of the tile is a
+// thread's.
 template <typename T, bool HALF>
-__global__ void __launch_bounds__(RO_THREADS) rotary_units_kernel(const __grid_constant__ RotaryDesc d, int tile, int groups, int span) {
-    constexpr int N = Unit<T>::N, PAIRS = HALF ? N : N / 2, AHEAD = 2;
+__global__ void __launch_bounds__(RO_MOST) rotary_units_kernel(const __grid_constant__ RotaryDesc d, int tile, int groups, int span, int rows) {
+    constexpr int N = Unit<T>::N, PAIRS = HALF ? N : N / 2;
     __shared__ uint64_t turns[RO_MAXPAIRS];
     __shared__ __align__(16) float sines[2 * RO_SINES];   // token by token: cosines, sines
-    // offsets of a token's rows: queries, keys and values, where they come from and go to
+    // offsets of a token's rows: queries, keys and values, where they come from and go to (-1: nowhere)
     __shared__ int64_t from[RO_TOKENS][3], to[RO_TOKENS][3], place[RO_TOKENS];
-    __shared__ bool live[RO_TOKENS];
     griddep_wait();
     griddep_launch_dependents();
     const int n = (int)d.n, half = HALF ? n / N : 0;   // units whose partner is half units on
     const int items = (int)d.dh / N - half, heads = (int)d.H, Hkv = (int)d.Hkv, HH = heads + 2 * Hkv;
     const int64_t tokens = d.B * d.T, first = (int64_t)(blockIdx.x / groups) * tile;
-    const int h0 = (int)(blockIdx.x % groups) * span, h1 = min(HH, h0 + span), width = h1 - h0;
     const int count = (int)min((int64_t)tile, tokens - first);
-    for (int i = threadIdx.x; i < n; i += RO_THREADS) turns[i] = turn_of(d.frequencies[i]);
-    for (int i = threadIdx.x; i < count; i += RO_THREADS) {
+    for (int i = threadIdx.x; i < n; i += blockDim.x) turns[i] = turn_of(d.frequencies[i]);
+    for (int i = threadIdx.x; i < count; i += blockDim.x) {
         const Token x = token_of(d, first + i);
         from[i][0] = x.b * d.qs[0] + x.t * d.qs[1];
         from[i][1] = x.b * d.ks[0] + x.t * d.ks[1];
         from[i][2] = x.b * d.vs[0] + x.t * d.vs[1];
         to[i][0] = x.b * d.qo[0] + x.t * d.qo[1];
-        to[i][1] = x.page * d.kp[0] + x.slot * d.kp[1];
-        to[i][2] = x.page * d.vp[0] + x.slot * d.vp[1];
+        to[i][1] = x.live ? x.page * d.kp[0] + x.slot * d.kp[1] : -1;
+        to[i][2] = x.live ? x.page * d.vp[0] + x.slot * d.vp[1] : -1;
         place[i] = x.pos;
-        live[i] = x.live;
     }
     __syncthreads();
     const float scale = (float)d.scale;
-    for (int i = threadIdx.x; i < count * n; i += RO_THREADS) {
+    for (int i = threadIdx.x; i < count * n; i += blockDim.x) {
         const int t = i / n, j = i - t * n;
         cos_sin<T, float>(turns[j] * (uint64_t)place[t], scale, sines[2 * t * n + j], sines[(2 * t + 1) * n + j]);
     }
     __syncthreads();
-    // rows of the block, a head of a token each: this thread's unit of every step-th
-    const int item = threadIdx.x % items, step = RO_THREADS / items;
-    int row = threadIdx.x / items;
-    if (row >= step) return;
+    const int item = threadIdx.x % items, r = threadIdx.x / items, hh = (int)(blockIdx.x % groups) * span + r % span;
+    int t = r / span;
+    if (t >= rows || hh >= HH) return;
     const bool pair = HALF ? item < half : item * N < 2 * n;
     // with a partner: units item and item + half; the others stand behind them
-    const int at = (HALF && !pair ? item + half : item) * N, partner = at + (HALF ? n : 0), sine = HALF ? at : at / 2;
-    int t = row / width, h = row % width;
-    const int dt = step / width, dh = step % width;
-    while (t < count) {
-        Unit<T> a[AHEAD], b[HALF ? AHEAD : 1];
-        T* dst[AHEAD];
-        int tt[AHEAD];
-        bool on[AHEAD], turned[AHEAD];
+    const int at = (HALF && !pair ? item + half : item) * N, sine = HALF ? at : at / 2;
+    const int kind = hh < heads ? 0 : hh < heads + Hkv ? 1 : 2, h = hh - (kind > 0 ? heads : 0) - (kind > 1 ? Hkv : 0);
+    const T* src = static_cast<const T*>(kind == 0 ? d.q : kind == 1 ? d.k : d.v) + h * (kind == 0 ? d.qs[2] : kind == 1 ? d.ks[2] : d.vs[2]) + at;
+    T* dst = static_cast<T*>(kind == 0 ? d.q_out : kind == 1 ? d.k_pages : d.v_pages) + h * (kind == 0 ? d.qo[2] : kind == 1 ? d.kp[2] : d.vp[2]) + at;
+    const bool turned = pair && kind < 2;
+    for (; t < count; t += RO_AHEAD * rows) {
+        Unit<T> a[RO_AHEAD], b[HALF ? RO_AHEAD : 1];
+        int64_t where[RO_AHEAD];
 #pragma unroll
-        for (int j = 0; j < AHEAD; ++j) {
-            on[j] = false;
-            tt[j] = t;
-            if (t < count) {
-                const int hh = h0 + h;
-                const T* src;
-                if (hh < heads) {
-                    src = static_cast<const T*>(d.q) + from[t][0] + hh * d.qs[2];
-                    dst[j] = static_cast<T*>(d.q_out) + to[t][0] + hh * d.qo[2];
-                    on[j] = turned[j] = true;
-                } else if (hh < heads + Hkv) {
-                    src = static_cast<const T*>(d.k) + from[t][1] + (hh - heads) * d.ks[2];
-                    dst[j] = static_cast<T*>(d.k_pages) + to[t][1] + (hh - heads) * d.kp[2];
-                    on[j] = live[t];
-                    turned[j] = true;
-                } else {
-                    src = static_cast<const T*>(d.v) + from[t][2] + (hh - heads - Hkv) * d.vs[2];
-                    dst[j] = static_cast<T*>(d.v_pages) + to[t][2] + (hh - heads - Hkv) * d.vp[2];
-                    on[j] = live[t];
-                    turned[j] = false;
-                }
-                if (on[j]) {
-                    a[j].raw = *reinterpret_cast<const uint4*>(src + at);
-                    if constexpr (HALF)
-                        if (pair) b[j].raw = *reinterpret_cast<const uint4*>(src + partner);
-                }
-                t += dt;
-                h += dh;
-                if (h >= width) {
-                    h -= width;
-                    ++t;
-                }
-            }
+        for (int j = 0; j < RO_AHEAD; ++j) {
+            const int tt = t + j * rows;
+            where[j] = tt < count ? to[tt][kind] : -1;
+            if (where[j] < 0) continue;
+            const T* row = src + from[tt][kind];
+            a[j].raw = *reinterpret_cast<const uint4*>(row);
+            if constexpr (HALF)
+                if (pair) b[j].raw = *reinterpret_cast<const uint4*>(row + n);
         }
 #pragma unroll
-        for (int j = 0; j < AHEAD; ++j) {
-            if (!on[j]) continue;
-            if (pair && turned[j]) {
+        for (int j = 0; j < RO_AHEAD; ++j) {
+            if (where[j] < 0) continue;
+            if (turned) {
                 float c[PAIRS], s[PAIRS], u[N];
-                const float* cs = sines + 2 * tt[j] * n + sine;
+                const float* cs = sines + 2 * (t + j * rows) * n + sine;
 #pragma unroll
                 for (int e = 0; e < PAIRS; ++e) {
                     c[e] = cs[e];
@@ -231,24 +207,25 @@ __global__ void __launch_bounds__(RO_THREADS) rotary_units_kernel(const __grid_c
                     b[j].get(v);
 #pragma unroll
                     for (int e = 0; e < N; ++e) {
-                        const float r = fmaf(u[e], c[e], -v[e] * s[e]);
+                        const float x = fmaf(u[e], c[e], -v[e] * s[e]);
                         v[e] = fmaf(u[e], s[e], v[e] * c[e]);
-                        u[e] = r;
+                        u[e] = x;
                     }
                     b[j].put(v);
                 } else {
 #pragma unroll
                     for (int e = 0; e < N / 2; ++e) {
-                        const float r = fmaf(u[2 * e], c[e], -u[2 * e + 1] * s[e]);
+                        const float x = fmaf(u[2 * e], c[e], -u[2 * e + 1] * s[e]);
                         u[2 * e + 1] = fmaf(u[2 * e], s[e], u[2 * e + 1] * c[e]);
-                        u[2 * e] = r;
+                        u[2 * e] = x;
                     }
                 }
                 a[j].put(u);
             }
-            *reinterpret_cast<uint4*>(dst[j] + at) = a[j].raw;
+            T* row = dst + where[j];
+            *reinterpret_cast<uint4*>(row) = a[j].raw;
             if constexpr (HALF)
-                if (pair) *reinterpret_cast<uint4*>(dst[j] + partner) = b[j].raw;
+                if (pair) *reinterpret_cast<uint4*>(row + n) = b[j].raw;
         }
     }
 }
@@ -305,29 +282,40 @@ cudaError_t launch_rotary(const RotaryDesc& d, const DeviceInfo& dev, cudaStream
     if (d.Hkv)
         units = units && units_fit(d.k, d.ks, N) && units_fit(d.v, d.vs, N) && units_fit(d.k_pages, d.kp, N) &&
                 units_fit(d.v_pages, d.vp, N);
-    const dim3 block(RO_THREADS);
     if (units) {
-        const int64_t items = d.dh / N - (half ? d.n / N : 0), tokens = d.B * d.T;
-        // Tokens to a block: as many as leave four blocks to an SM, up to RO_SINES pairs of sines; where one leaves fewer
-        // its heads are dealt out too, as rows enough for the block's threads.
-        int64_t tile = tokens / (4 * (int64_t)dev.num_sms);
-        const int64_t most = d.n ? RO_SINES / d.n : RO_TOKENS;
-        tile = tile > most ? most : tile;
-        tile = tile > RO_TOKENS ? RO_TOKENS : tile < 1 ? 1 : tile;
-        int64_t groups = 4 * (int64_t)dev.num_sms / ((tokens + tile - 1) / tile);
-        const int64_t rows = RO_THREADS / items, apart = (HH + rows - 1) / rows;
-        groups = groups < 1 ? 1 : groups > apart ? apart : groups;
+        const int64_t items = d.dh / N - (half ? d.n / N : 0), tokens = d.B * d.T, sms = dev.num_sms;
+        // Heads to a block: all that fit it; with few tokens they are dealt out, while that gives each SM a block more.
+        int64_t groups = (HH * items + RO_MOST - 1) / RO_MOST;
+        while (groups < HH && tokens * groups * 2 <= sms) groups *= 2;
         const int64_t span = (HH + groups - 1) / groups;
         groups = (HH + span - 1) / span;
-        const int64_t blocks = (tokens + tile - 1) / tile * groups;
-        if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-        const dim3 grid((unsigned)blocks);
-        if (d.dt == DT_BF16)
-            return half ? launch_dependent(rotary_units_kernel<__nv_bfloat16, true>, grid, block, 0, s, d, (int)tile, (int)groups, (int)span)
-                        : launch_dependent(rotary_units_kernel<__nv_bfloat16, false>, grid, block, 0, s, d, (int)tile, (int)groups, (int)span);
-        return half ? launch_dependent(rotary_units_kernel<float, true>, grid, block, 0, s, d, (int)tile, (int)groups, (int)span)
-                    : launch_dependent(rotary_units_kernel<float, false>, grid, block, 0, s, d, (int)tile, (int)groups, (int)span);
+        const int64_t rows = RO_THREADS / (items * span) > 1 ? RO_THREADS / (items * span) : 1;
+        auto launch = [&](auto k, int which) -> cudaError_t {
+            // Tokens to a block: whole rounds of blocks, as few as RO_SINES pairs of sines and RO_TOKENS allow, and no rest
+            // of one (4 x 2048 tokens of 20 heads of 128 in 586 blocks, of which 608 fit: 17.3 us; in 631: 22).
+            static std::atomic<int> fits[4][RO_MOST / 32 + 1];   // blocks of so many warps to an SM
+            const int64_t warps = (items * span * rows + 31) / 32;
+            std::atomic<int>& fit = fits[which][warps];
+            int resident = fit.load(std::memory_order_relaxed);
+            if (!resident) {
+                const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, k, (int)warps * 32, 0);
+                if (e != cudaSuccess) return e;
+                resident = resident < 1 ? 1 : resident;
+                fit.store(resident, std::memory_order_relaxed);
+            }
+            int64_t most = d.n ? RO_SINES / d.n : RO_TOKENS;
+            most = most > RO_TOKENS ? RO_TOKENS : most;
+            const int64_t room = resident * sms, rounds = (tokens * groups + room * most - 1) / (room * most);
+            const int64_t tile = (tokens * groups + room * rounds - 1) / (room * rounds);
+            const int64_t blocks = (tokens + tile - 1) / tile * groups, used = rows < tile ? rows : tile;
+            if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+            const dim3 grid((unsigned)blocks), block((unsigned)((items * span * used + 31) / 32 * 32));
+            return launch_dependent(k, grid, block, 0, s, d, (int)tile, (int)groups, (int)span, (int)used);
+        };
+        if (d.dt == DT_BF16) return half ? launch(rotary_units_kernel<__nv_bfloat16, true>, 0) : launch(rotary_units_kernel<__nv_bfloat16, false>, 1);
+        return half ? launch(rotary_units_kernel<float, true>, 2) : launch(rotary_units_kernel<float, false>, 3);
     }
+    const dim3 block(RO_THREADS);
     const int64_t items = d.dh - d.n;
     // heads of a token that one thread walks over: all of them where there are threads enough
     const double threads = (double)d.B * d.T * HH * items;
