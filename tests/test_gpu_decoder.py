@@ -90,7 +90,7 @@ def check_rotary(x, f, pos=None, layout=api.ROTARY_HALF, scale=1.0, **kw):
 
 ROTARY_SHAPES = [(1, 1, 1, 2, 2), (1, 1, 1, 64, 64), (3, 5, 3, 64, 32), (2, 7, 4, 80, 80), (1, 300, 16, 128, 128), (2, 33, 5, 96, 6),
                  (5, 1, 12, 64, 64), (1, 3, 2, 17, 10), (2, 2, 3, 512, 512), (1, 2, 7, 40, 8), (700, 1, 20, 64, 48),
-                 (1, 2600, 12, 64, 16)]
+                 (1, 2600, 12, 64, 16), (1, 2, 256, 80, 80), (1, 9, 103, 80, 64), (1, 300, 70, 512, 512), (1, 3, 700, 64, 64)]
 
 
 @pytest.mark.parametrize("layout", LAYOUTS)
@@ -221,7 +221,8 @@ def check_append(k, v, q, page, starts, lens=None, f=None, pos=None, layout=0, s
 
 
 APPEND_SHAPES = [(1, 1, 1, 1, 2, 2, 1), (3, 1, 16, 16, 64, 64, 16), (2, 5, 16, 2, 128, 128, 64), (2, 37, 12, 4, 80, 40, 16),
-                 (4, 3, 6, 3, 17, 10, 5), (1, 300, 4, 4, 64, 64, 32), (64, 1, 12, 3, 96, 96, 128), (2, 9, 0, 2, 64, 32, 7)]
+                 (4, 3, 6, 3, 17, 10, 5), (1, 300, 4, 4, 64, 64, 32), (64, 1, 12, 3, 96, 96, 128), (2, 9, 0, 2, 64, 32, 7),
+                 (2, 40, 200, 28, 80, 80, 16), (1, 5, 0, 300, 64, 64, 16)]
 
 
 @pytest.mark.parametrize("layout", LAYOUTS)

@@ -285,10 +285,9 @@ cudaError_t launch_rotary(const RotaryDesc& d, const DeviceInfo& dev, cudaStream
     if (units) {
         const int64_t items = d.dh / N - (half ? d.n / N : 0), tokens = d.B * d.T, sms = dev.num_sms;
         // Heads to a block: all that fit it; with few tokens they are dealt out, while that gives each SM a block more.
-        int64_t groups = (HH * items + RO_MOST - 1) / RO_MOST;
-        while (groups < HH && tokens * groups * 2 <= sms) groups *= 2;
-        const int64_t span = (HH + groups - 1) / groups;
-        groups = (HH + span - 1) / span;
+        int64_t span = RO_MOST / items < HH ? RO_MOST / items : HH;
+        while (span > 1 && tokens * ((HH + span - 1) / span) * 2 <= sms) span = (span + 1) / 2;
+        const int64_t groups = (HH + span - 1) / span;
         const int64_t rows = RO_THREADS / (items * span) > 1 ? RO_THREADS / (items * span) : 1;
         auto launch = [&](auto k, int which) -> cudaError_t {
             // Tokens to a block: whole rounds of blocks, as few as RO_SINES pairs of sines and RO_TOKENS allow, and no rest
