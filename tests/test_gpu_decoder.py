@@ -652,6 +652,25 @@ def test_paged_attention_of_values_that_are_no_numbers(Tq, H, Hkv, dh, own, pref
     assert not torch.isfinite(got[0, :, :G]).any() and same(got[1:], ref[1:]) and same(got[0, :, G:], ref[0, :, G:])
 
 
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("dt", [BF, F32, F64], ids=str)
+@pytest.mark.parametrize("Tq,H,Hkv,dh,own,prefix", SPECIAL + [(1, 1, 1, 64, [300], []), (2, 2, 2, 128, [90], [70]), (5, 3, 1, 72, [90], []), (20, 2, 1, 40, [90], [70])])
+def test_paged_attention_of_seen_keys_without_weight(Tq, H, Hkv, dh, own, prefix, dt, value):
+    """A key that a row sees, so far below the others that its weight is zero: its value still counts as 0 times it."""
+    h = Held(Tq, H, Hkv, dh, 16, own, prefix, dt=dt)
+    h.q = h.q.abs() + 0.5
+    pg, s = slots(h.table, 0, 0, 16)
+    h.kp[pg, s], h.vp[pg, s] = -1e4, value
+    got = h.call()
+    assert torch.isnan(got[0]).all() and torch.isfinite(got[1:]).all()
+    if prefix:   # of the prefix: all sequences of the group
+        h = Held(Tq, H, Hkv, dh, 16, own, prefix, dt=dt)
+        h.q = h.q.abs() + 0.5
+        pg, s = slots(h.prefix_table, 0, 0, 16)
+        h.kp[pg, s], h.vp[pg, s] = -1e4, value
+        assert torch.isnan(h.call()).all()
+
+
 @pytest.mark.parametrize("page", [8, 16, 48, 80, 96, 112, 144, 160, 384])
 @pytest.mark.parametrize("Tq,H,Hkv,dh,dt", [(1, 4, 2, 64, BF), (3, 8, 2, 128, BF), (50, 4, 4, 80, BF), (200, 2, 2, 64, BF), (2, 4, 2, 80, F32)], ids=str)
 def test_paged_attention_page_sizes(Tq, H, Hkv, dh, dt, page):

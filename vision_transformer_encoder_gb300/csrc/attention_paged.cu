@@ -181,9 +181,9 @@ __global__ void __launch_bounds__(PG_THREADS) paged_generic_kernel(const __grid_
 #pragma unroll
                 for (int e = 0; e < RPT; ++e) {
                     // a key that the row does not see adds nothing, whatever its value
-                    const A w = u0 + u < slim[r0 + e] ? sp[r0 + e][u] : (A)0;
+                    const bool sees = u0 + u < slim[r0 + e];
 #pragma unroll
-                    for (int j = 0; j < NJ; ++j) acc[e][j] += w == (A)0 ? (A)0 : w * v[j];
+                    for (int j = 0; j < NJ; ++j) acc[e][j] += sees ? sp[r0 + e][u] * v[j] : (A)0;
                 }
             }
         }

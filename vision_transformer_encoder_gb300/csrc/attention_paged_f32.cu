@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(PF_WARPS * 32) paged_f32_kernel(const __grid_c
                     const float f = __shfl_sync(0xffffffffu, w, (u * NR + r) << (5 - BITS));
                     // a key that the row does not see adds nothing, whatever its value
 #pragma unroll
-                    for (int c = 0; c < VEC; ++c) o[r][c] += NR > 1 && f == 0.f ? 0.f : f * v[u].v[c];
+                    for (int c = 0; c < VEC; ++c) o[r][c] += NR == 1 || s * PF_KEYS + u < lim[r] ? f * v[u].v[c] : 0.f;
                 }
         }
         pg = next;
