@@ -576,8 +576,8 @@ int vit_cache_append(const void* k, const int64_t* k_strides, const void* v, con
  * fp32 (fp64 for F64), where scaled scores past its range, as infinite ones, give NaN. BF16 runs on tensor cores, where weights meet V rounded to bf16
  * (their sum is not), with pages of a multiple of 16 tokens and 16-byte aligned rows: own keys with dh a multiple of 8 up
  * to 128 where a key head has at most 16 query rows (Tq G); more rows, and prefixes, with dh 64, 80, 96 or 128 and
- * positive scales, up to 2^26 keys. F32 has a kernel for dh a multiple of 4 up to 128, pages of a multiple of 8 and
- * aligned rows. A generic one takes everything else, a few times slower. dh up to 512.
+ * positive scales, up to 2^22 keys (prefixes of few rows 2^26). F32 has a kernel for dh a multiple of 4 up to 128, pages of a
+ * multiple of 8 and aligned rows. A generic one takes everything else, a few times slower. dh up to 512.
  * Errors: VIT_ERR_ARG, VIT_ERR_DTYPE, VIT_ERR_UNSUPPORTED (dh), VIT_ERR_NOMEM, VIT_ERR_CUDA.
  */
 int vit_paged_attention(const void* q, const int64_t* q_strides, const vit_paged_cache* cache, const int32_t* table,

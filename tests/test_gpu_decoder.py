@@ -652,6 +652,59 @@ def test_paged_attention_of_values_that_are_no_numbers(Tq, H, Hkv, dh, own, pref
     assert not torch.isfinite(got[0, :, :G]).any() and same(got[1:], ref[1:]) and same(got[0, :, G:], ref[0, :, G:])
 
 
+@pytest.mark.parametrize("Tq,H,Hkv,dh,own,prefix", [(40, 4, 4, 64, [300, 140], [200]), (200, 4, 2, 80, [400, 250], []), (24, 4, 4, 96, [2900], []),
+                                                    (200, 6, 2, 128, [250, 3000], [400]), (3, 8, 2, 128, [400, 90], [])])
+def test_paged_attention_later_tokens_behind_absent_pages(Tq, H, Hkv, dh, own, prefix):
+    """Rows that are made again see what they see: not the pages that are absent, the prefix, parts of the keys."""
+    h = Held(Tq, H, Hkv, dh, 16, own, prefix)
+    pg, s = slots(h.table, 0, own[0] - 1, 16)
+    h.vp[pg, s, :, 1::2] = math.nan
+    gone = []
+    for b, page in ((0, 1), (len(own) - 1, 4)):
+        h.table[b, page] = -7 if b else 1 << 20
+        gone.append((b, 16 * page, 16 * page + 16))
+    o, w, mag, n = h.ref(dh ** -0.5, gone)
+    tol = paged_tol(h, o, w, mag, n, dh)
+    got = h.call()
+    last = torch.isnan(got[0, -1])
+    assert last[:, 1::2].all() and not last[:, 0::2].any()
+    got[0, -1] = o[0, -1].to(got.dtype)
+    close(got, o, tol)
+    assert same(h.call()[:, :-1], got[:, :-1])
+
+
+@pytest.mark.parametrize("n", [(1 << 17) + 1, (1 << 17) + (1 << 16) + 5])
+def test_paged_attention_of_keys_past_one_part(n):
+    """Enough sequences to fill the GPU, each longer than one part may be. Scores of zero and whole values: exact sums, one
+    division, one rounding. The pages are the same few in turn."""
+    B, Tq, page, P = 80, 20, 64, 8
+    kp, vp = rand(P, page, 1, 64, dtype=BF), rand(P, page, 1, 64, seed=1).round().to(BF)
+    table = (torch.arange((n + page - 1) // page) % P).int().to(DEV).repeat(B, 1)
+    got = api.paged_attention(torch.zeros(B, Tq, 1, 64, dtype=BF, device=DEV), kp, vp, table, ints([n] * B))
+    at = torch.cat([torch.zeros(1, 64, dtype=F64, device=DEV), vp.double().reshape(P * page, 64).cumsum(0)])
+    sees = torch.arange(n - Tq + 1, n + 1, device=DEV)
+    o = (at[-1] * (sees // (P * page))[:, None] + at[sees % (P * page)]) / sees[:, None]
+    close(got[:, :, 0], o.expand(B, Tq, 64), (HALF[BF] * 1.01 + 4 * U) * o.abs().expand(B, Tq, 64))
+
+
+@pytest.mark.parametrize("scale", [1.0, 1e5, 1e8, -1e7])
+@pytest.mark.parametrize("dt", [BF, F32], ids=str)
+@pytest.mark.parametrize("Tq,H,Hkv,dh,own,prefix", SPECIAL + [(40, 4, 2, 128, [900, 41], []), (300, 2, 1, 64, [1100], [300])])
+def test_paged_attention_weights_sum_to_one_behind_later_tokens(Tq, H, Hkv, dh, own, prefix, dt, scale):
+    """Values of 1 come out as 1, however far the scores are from zero (where the rounding of a score is a factor in its weight),
+    also where the newest token's value is not a number: a weight is off by its rounding to bf16, the sums by that of
+    each of their terms and of a rescale, the result by its own rounding."""
+    h = Held(Tq, H, Hkv, dh, 16, own, prefix, dt=dt)
+    h.vp.copy_(torch.where(torch.isnan(h.vp), h.vp, 1.0))
+    for b, n in enumerate(own):
+        pg, s = slots(h.table, b, n - 1, 16)
+        h.vp[pg, s] = math.nan
+    got, one = h.call(scale=scale), torch.ones((), dtype=F64, device=DEV)
+    terms = 4 * U * (max(own) + (max(prefix) if prefix else 0) + 64)
+    close(got[:, :-1], one.expand_as(got[:, :-1]), one * (terms + HALF[dt] * (2 if dt == BF else 1)) * 1.01)
+    assert torch.isnan(got[:, -1]).all()
+
+
 @pytest.mark.parametrize("value", [math.nan, math.inf])
 @pytest.mark.parametrize("dt", [BF, F32, F64], ids=str)
 @pytest.mark.parametrize("Tq,H,Hkv,dh,own,prefix", SPECIAL + [(1, 1, 1, 64, [300], []), (2, 2, 2, 128, [90], [70]), (5, 3, 1, 72, [90], []), (20, 2, 1, 40, [90], [70])])

@@ -323,10 +323,12 @@ PagedPlan plan_paged(const PagedDesc& d, const DeviceInfo& dev) {
     const int64_t G = d.H / d.Hkv, own_rb = (d.Tq * G + RT - 1) / RT, prefix_rb = (d.B / d.groups * d.Tq * G + RT - 1) / RT;
     if (plan.form == PAGED_TC) {
         // A CTA to an SM. Parts cost a write and a read of fp32 rows: items that fill the SMs once are not cut (2 x 1025
-        // queries over 4100 keys, 120 items: 60 us, in two parts 72, in three 64).
+        // queries over 4100 keys, 120 items: 56 us, in two parts 66, in three 57).
         const bool apart = plan.prefix_tc && paged_tc_apart(d);
         if (apart) plan.prefix_parts = cut(sms, paged_tc_items(d, false), before, 512);
         plan.own_parts = cut(sms, paged_tc_items(d, true), keys + (apart ? 0 : before), 512);
+        const int least = (int)((keys + (apart ? 0 : before) + PAGED_TC_PART - 1) / PAGED_TC_PART);
+        plan.own_parts = plan.own_parts < least ? least : plan.own_parts;
         plan.partial = plan.prefix_parts + plan.own_parts > 1;
     } else if (plan.form == PAGED_F32) {
         // CTAs of four warps, four of them to an SM (8: 14.7 us, 16: 14.7, 4: 13.1 for 8 x 12 heads over 577 keys

@@ -330,6 +330,7 @@ bool paged_rows_supported(const PagedDesc& d);
 cudaError_t launch_paged_rows(const PagedDesc& d, const PagedParts& prefix, const DeviceInfo& dev, cudaStream_t s);
 // Tensor cores (attention_paged_tc.cu): bf16, head widths 64, 80, 96 and 128. own: items of a sequence's own keys (with
 // the prefix in front where plan.prefix_parts is 0), beside those of the prefixes.
+constexpr int64_t PAGED_TC_PART = 1 << 17;              // own keys to a part, at most: made again key by key, a third of a wait's limit
 bool paged_tc_supported(const PagedDesc& d, bool own);
 int64_t paged_tc_items(const PagedDesc& d, bool own);   // of one part each
 bool paged_tc_apart(const PagedDesc& d);                // whether the prefix is better worked off apart
