@@ -2,14 +2,15 @@
 // head serves at most 16 query rows (Tq * G <= 16), bf16, head width up to 128 in steps of 8, pages of a multiple of
 // 16 tokens.
 //
-// Bound by reading the sequence's own keys and values once. They are dealt out in tiles of 16, which lie in one page each, to the
-// warps of one CTA or of a cluster of CTAs; every warp looks its pages up one tile ahead of asking for them, keeps its own
-// running maximum, sum and output rows, joined at the end through shared memory and, between the CTAs of a cluster, distributed
-// shared memory. The rows of the prefix, where there is one, were worked off by the kernel launched before this
+// Bound by reading the sequence's own keys and values once. They are dealt out in tiles of 32, two halves that lie in one page
+// each, to the warps of one CTA or of a cluster of CTAs; every warp looks its pages up one tile ahead of asking for them, keeps
+// its own running maximum, sum and output rows, joined at the end through shared memory and, between the CTAs of a cluster,
+// distributed shared memory. 32 sequences of up to 577 keys, 16 heads of 64: 12.2 us (4.6 TB/s), 4 us of it the latency of length,
+// page and first tile; 8 of up to 8200, 16 heads of 128 on 2 key heads: 19.2 us (2.6 TB/s), a warp's chain of products. The rows of the prefix, where there is one, were worked off by the kernel launched before this
 // one: its parts are joined here. This kernel starts beside that one and waits for it only then: its own keys, queries
 // and tables were there before that one began (it lets this one start behind its own wait).
 //
-// Tiles, rings and products are those of attention_cross_rows.cu: mma.m16n8k16 with the query rows as the n side,
+// Rings and products are those of attention_cross_rows.cu: mma.m16n8k16 with the query rows as the n side,
 // S^T = K Q^T and O^T = V^T P^T, K and V by TMA into a ring of each warp's own. Weights are rounded to bf16 for the second
 // product (their sum is not).
 //
@@ -529,9 +530,9 @@ bool paged_rows_supported(const PagedDesc& d) {
 cudaError_t launch_paged_rows(const PagedDesc& d, const PagedParts& prefix, const DeviceInfo& dev, cudaStream_t s) {
     // A warp takes 1.1 us for a tile, half of it the matrix instructions' own time, so what counts is to have many of them, each
     // with two tiles at least, in one round of CTAs. Widths up to 64: three warps, four CTAs to an SM (32 heads x 16, 577
-    // keys: 13.0 us; with four warps, of which three CTAs fit and the rest are a second round, 15.3). Wider: six warps
+    // keys: 10.2 us; with four warps, of which three CTAs fit and the rest are a second round, 15.2). Wider: six warps
     // with an SM of their own where key heads are few, else three and two CTAs. Clusters, us at 1 / 2 / 4 / 8 CTAs per key
-    // head for 16 heads of 128 over 8200 keys, six warps: 54 / 30 / 18.8 / 23 (clusters of eight CTAs that fill an SM
+    // head for 16 heads of 128 over 8200 keys, six warps: 52 / 30 / 18.3 / 26.5 (clusters of eight CTAs that fill an SM
     // each do not pack into the GPU's SM groups). Parts joined by another kernel, on all SMs, were no faster: 18.4.
     const int64_t heads = d.B * d.Hkv, sms = dev.num_sms, keys = d.table_pages * d.page;
     const bool narrow = d.dh <= 64, many = d.Tq * (d.H / d.Hkv) > 8;
