@@ -25,7 +25,7 @@
 namespace vit {
 namespace {
 
-constexpr int PG_THREADS = 128, PG_KEYS = 32;
+constexpr int PG_THREADS = 128, PG_KEYS = 32, PG_PARTS = 4;
 
 __device__ __forceinline__ float exp2_of(float x) { return exp2f(x); }
 __device__ __forceinline__ double exp2_of(double x) { return exp2(x); }
@@ -228,25 +228,46 @@ __global__ void __launch_bounds__(256) paged_join_kernel(PagedParts parts, int d
     const A* in = static_cast<const A*>(parts.acc);
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
         const int64_t row = i / per, c = i % per * V;
-        A top = -INFINITY;
-        for (int q = 0; q < parts.n; ++q) top = max_of(top, ml[2 * (q * parts.rows + row)]);
-        const A base = top == -INFINITY ? (A)0 : top;
-        A acc[V] = {}, sum = 0;
-        for (int q = 0; q < parts.n; ++q) {
-            const int64_t at = q * parts.rows + row;
-            const A l = ml[2 * at + 1];
-            if (l == (A)0) continue;   // no keys: its row is not there
-            const A f = exp2_of(ml[2 * at] - base);
-            sum += f * l;
-            if constexpr (V == 4 && sizeof(A) == 4) {
-                const float4 x = *reinterpret_cast<const float4*>(in + at * dh + c);
-                acc[0] += f * x.x;
-                acc[1] += f * x.y;
-                acc[2] += f * x.z;
-                acc[3] += f * x.w;
-            } else {
+        A acc[V] = {}, sum = 0, mx = -INFINITY;
+        for (int q = 0; q < parts.n; q += PG_PARTS) {   // parts asked for together
+            A m[PG_PARTS], l[PG_PARTS], x[PG_PARTS][V];
 #pragma unroll
-                for (int e = 0; e < V; ++e) acc[e] += f * in[at * dh + c + e];
+            for (int y = 0; y < PG_PARTS; ++y) {
+                const int64_t at = min(q + y, parts.n - 1) * parts.rows + row;
+                m[y] = ml[2 * at];
+                l[y] = ml[2 * at + 1];
+                if constexpr (V == 4 && sizeof(A) == 4) {
+                    const float4 z = *reinterpret_cast<const float4*>(in + at * dh + c);
+                    x[y][0] = z.x;
+                    x[y][1] = z.y;
+                    x[y][2] = z.z;
+                    x[y][3] = z.w;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) x[y][e] = in[at * dh + c + e];
+                }
+            }
+            A top = mx;
+#pragma unroll
+            for (int y = 0; y < PG_PARTS; ++y) {
+                if (q + y >= parts.n) {
+                    m[y] = -INFINITY;
+                    l[y] = 0;
+                }
+                top = max_of(top, m[y]);
+            }
+            const A base = top == -INFINITY ? (A)0 : top, f = exp2_of(mx - base);
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[e] *= f;
+            sum *= f;
+            mx = top;
+#pragma unroll
+            for (int y = 0; y < PG_PARTS; ++y) {
+                if (l[y] == (A)0) continue;   // no keys: its row is not there
+                const A g = exp2_of(m[y] - base);
+                sum += g * l[y];
+#pragma unroll
+                for (int e = 0; e < V; ++e) acc[e] += g * x[y][e];
             }
         }
 #pragma unroll
@@ -334,8 +355,9 @@ PagedPlan plan_paged(const PagedDesc& d, const DeviceInfo& dev) {
     } else if (plan.form == PAGED_F32) {
         // CTAs of four warps, four of them to an SM (8: 14.8 us, 16: 14.9, 4: 13.3 for 8 x 12 heads over 577 keys
         // behind 197), parts of two steps to each warp at least
-        plan.own_parts = cut(4 * sms, paged_f32_blocks(d, true), keys, 64);
-        if (d.prefix_table) plan.prefix_parts = cut(4 * sms, paged_f32_blocks(d, false), before, 64);
+        const int64_t ctas = sms * (d.dh > 64 && paged_f32_rows(d) == 4 ? 3 : 4);   // as many as registers allow
+        plan.own_parts = cut(ctas, paged_f32_blocks(d, true), keys, 64);
+        if (d.prefix_table) plan.prefix_parts = cut(ctas, paged_f32_blocks(d, false), before, 64);
         plan.partial = plan.prefix_parts + plan.own_parts > 1;
     } else {
         // the prefix of few queries: two key tiles to a part at least, one for each softmax group (32 x 16 heads behind
