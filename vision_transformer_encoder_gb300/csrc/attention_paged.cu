@@ -341,29 +341,48 @@ PagedPlan plan_paged(const PagedDesc& d, const DeviceInfo& dev) {
         z = z < n / least ? z : n / least;
         return (int)(z < 1 ? 1 : z > 32 ? 32 : z);
     };
+    // The same on tensor cores, a CTA to an SM. Where `blocks` leave SMs idle in the only round, or the last, smaller items can
+    // fill more rounds better: an item takes 4 us and 1.5 for each tile of 128 keys, its part of `rows` rows a write and a read.
+    auto cut_tc = [&](int64_t blocks, int64_t n, int64_t least, int64_t rows) {
+        const int first = cut(sms, blocks, n, least);
+        auto us = [&](int64_t z) {
+            return (double)((blocks * z + sms - 1) / sms) * (4.0 + 1.5 * (double)((n + 128 * z - 1) / (128 * z))) +
+                   (double)z * (0.3 + (double)(rows * d.dh) * 8.0 / 6.8e6);
+        };
+        int best = first;
+        for (int z = first + 1; z <= 32 && n >= z * least; ++z)
+            if (us(z) < us(best)) best = z;
+        return us(best) < 0.9 * us(first) ? best : first;
+    };
     const int RT = generic_rows(d);
     const int64_t G = d.H / d.Hkv, own_rb = (d.Tq * G + RT - 1) / RT, prefix_rb = (d.B / d.groups * d.Tq * G + RT - 1) / RT;
     if (plan.form == PAGED_TC) {
         // A CTA to an SM. Parts cost a write and a read of fp32 rows: items that fill the SMs once are not cut (2 x 1025
         // queries over 4100 keys, 120 items: 56 us, in two parts 65, in three 58).
         const bool apart = plan.prefix_tc && paged_tc_apart(d);
-        if (apart) plan.prefix_parts = cut(sms, paged_tc_items(d, false), before, 512);
-        plan.own_parts = cut(sms, paged_tc_items(d, true), keys + (apart ? 0 : before), 512);
+        if (apart) plan.prefix_parts = cut_tc(paged_tc_items(d, false), before, 512, d.B * d.Tq * d.H);
+        plan.own_parts = cut_tc(paged_tc_items(d, true), keys + (apart ? 0 : before), 512, d.B * d.Tq * d.H);
         const int least = (int)((keys + (apart ? 0 : before) + PAGED_TC_PART - 1) / PAGED_TC_PART);
         plan.own_parts = plan.own_parts < least ? least : plan.own_parts;
         plan.partial = plan.prefix_parts + plan.own_parts > 1;
     } else if (plan.form == PAGED_F32) {
-        // CTAs of four warps, four of them to an SM (8: 14.8 us, 16: 14.9, 4: 13.3 for 8 x 12 heads over 577 keys
-        // behind 197), parts of two steps to each warp at least
-        const int64_t ctas = sms * (d.dh > 64 && paged_f32_rows(d) == 4 ? 3 : 4);   // as many as registers allow
-        plan.own_parts = cut(ctas, paged_f32_blocks(d, true), keys, 64);
-        if (d.prefix_table) plan.prefix_parts = cut(ctas, paged_f32_blocks(d, false), before, 64);
+        // CTAs of four warps, as many as sit on the SMs at once (three to six to an SM by registers), dealt out to own keys and prefix
+        // by what there is to read (in turn, each for all SMs, 6 x 2 tokens of 12 / 3 heads of 96 over 300 keys behind 800 took 20.8 us
+        // instead of 14.9); parts of three or four steps to each warp at least (two: 16.1)
+        const int rows = paged_f32_rows(d);
+        const int64_t ctas = sms * (d.dh > 64 ? (rows == 4 ? 3 : 4) : rows == 1 ? 6 : 4), least = rows == 1 ? 96 : 128;
+        const int64_t own = paged_f32_blocks(d, true), ahead = d.prefix_table ? paged_f32_blocks(d, false) : 0;
+        int64_t per = (own * keys + ahead * before + ctas - 1) / ctas;
+        per = per < least ? least : per;
+        auto parts = [&](int64_t n) { return (int)(n / per < 1 ? 1 : n / per > 32 ? 32 : n / per); };
+        plan.own_parts = parts(keys);
+        if (ahead) plan.prefix_parts = parts(before);
         plan.partial = plan.prefix_parts + plan.own_parts > 1;
     } else {
         // the prefix of few queries: two key tiles to a part at least, one for each softmax group (32 x 16 heads behind
         // 1025 keys: 13.1 us, with four 13.8)
         if (d.prefix_table)
-            plan.prefix_parts = plan.prefix_tc ? cut(sms, paged_tc_items(d, false), before, 256)
+            plan.prefix_parts = plan.prefix_tc ? cut_tc(paged_tc_items(d, false), before, 256, d.B * d.Tq * d.H)
                                                : cut(8 * sms, d.groups * d.Hkv * prefix_rb, before, 128);
         // CTAs of four warps, some eight of them to an SM
         if (plan.form == PAGED_GENERIC) plan.own_parts = cut(8 * sms, d.B * d.Hkv * own_rb, keys, 128);
