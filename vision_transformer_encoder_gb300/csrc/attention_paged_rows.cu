@@ -552,12 +552,14 @@ cudaError_t launch_paged_rows(const PagedDesc& d, const PagedParts& prefix, cons
     // with an SM of their own where key heads are few, else three and two CTAs. Clusters, us at 1 / 2 / 4 / 8 CTAs per key
     // head for 16 heads of 128 over 8200 keys, six warps: 52 / 30 / 18.3 / 26.5 (clusters of eight CTAs that fill an SM
     // each do not pack into the GPU's SM groups). Parts joined by another kernel, on all SMs, were no faster: 18.4.
+    // A cluster doubles while every warp had two tiles, wide heads one: 16 heads over 1000 keys of 128 in 8 CTAs 7.1 us, in 4 7.6, in 2
+    // 8.2; over 128 keys of 64 in 1 CTA 3.4, in 2 4.4.
     const int64_t heads = d.B * d.Hkv, sms = dev.num_sms, keys = d.table_pages * d.page;
     const bool narrow = d.dh <= 64, many = d.Tq * (d.H / d.Hkv) > 8;
     const int warps = narrow || heads > sms / 2 ? 3 : 6;
     const int64_t ctas = warps == 3 ? 2 * sms : sms;   // aimed at; more CTAs only add joins
     int Z = 1;
-    while (Z < PR_MAXZ && heads * Z * 2 <= ctas && keys >= (int64_t)Z * 2 * warps * PR_KEYS * 2) Z *= 2;
+    while (Z < PR_MAXZ && heads * Z * 2 <= ctas && keys >= Z * warps * PR_KEYS * (narrow ? 2 : 1)) Z *= 2;
     if (warps == 6 && Z == 8 && heads * 8 > sms / 2) Z = 4;
     const PagedRowsParams p{d, prefix, (float)(d.scale * 1.4426950408889634), Z, dev.err_word};
     if (narrow) return many ? launch_rows<64, 2, 3, 2, 3>(p, s) : launch_rows<64, 1, 3, 2, 4>(p, s);
