@@ -6,7 +6,7 @@
 // together, those of the next step behind them. The 8 NR products' halves are added across the lanes while they are
 // handed out, so that each lane ends up with whole scores of its own: 31 exchanges for 32 scores. fp32 throughout, O in
 // registers. The warps of a CTA take every fourth step of its part of the keys and join in shared memory; parts are
-// joined as in attention_paged.cu. 8 sequences of up to 577 keys behind 197, 12 heads of 64: 13.3 us, two launches of latencies;
+// joined as in attention_paged.cu. 8 sequences of up to 577 keys behind 197, 12 heads of 64: 10.9 us, two launches of latencies;
 // 2 x 2048 queries of 12 heads of 64 over 2048 keys, bound by the CUDA cores: 1195 us (10.8 TFLOP/s).
 #include <cuda_runtime.h>
 

@@ -24,7 +24,7 @@
 // Bound by the matrix unit and, at widths below 128, by the softmax's instructions: 4 x 2048 queries behind 8200 keys, 16 heads of
 // 128 on 2 key heads, 540 us (1.14 PFLOP/s; a half tile of both groups 1720 cycles, its products 1280 of them); 2 x 1025 queries over 4100
 // keys, 12 heads of 64, 56 us (0.40 PFLOP/s: one round of 120 items, 1450 cycles to a half tile). With few rows, by HBM: 64 x 3
-// queries behind 16 prefixes of up to 8200 keys, 40.2 us with the own keys and the join.
+// queries behind 16 prefixes of up to 8200 keys, 39.9 us with the own keys and the join.
 //
 // Every wait is bounded; on expiry the kernel records an error bit and unwinds.
 #include <cuda.h>
