@@ -350,9 +350,14 @@ PagedPlan plan_paged(const PagedDesc& d, const DeviceInfo& dev) {
                    (double)z * (0.3 + (double)(rows * d.dh) * 8.0 / 6.8e6);
         };
         int best = first;
-        for (int z = first + 1; z <= 32 && n >= z * least; ++z)
-            if (us(z) < us(best)) best = z;
-        return us(best) < 0.9 * us(first) ? best : first;
+        double lowest = 0.9 * us(first);
+        for (int z = first + 1; z <= 32 && n >= z * least; ++z) {
+            const double t = us(z);
+            if (t >= lowest) continue;
+            best = z;
+            lowest = t;
+        }
+        return best;
     };
     const int RT = generic_rows(d);
     const int64_t G = d.H / d.Hkv, own_rb = (d.Tq * G + RT - 1) / RT, prefix_rb = (d.B / d.groups * d.Tq * G + RT - 1) / RT;
