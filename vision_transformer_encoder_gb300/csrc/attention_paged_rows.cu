@@ -518,6 +518,33 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     }
 }
 
+// Clusters of Z CTAs, an SM to each, that run at once (of the first device asked about).
+int clusters_at_once(int Z) {
+    static std::atomic<int> known[PR_MAXZ + 1];   // one more than that
+    int n = known[Z].load(std::memory_order_relaxed);
+    if (n) return n - 1;
+    auto k = paged_rows_kernel<128, 1, 6, 2, 1>;
+    constexpr int smem = 6 * 2 * PR_KEYS * 512 + 8 * 130 * 4 + 1024;   // as launch_rows asks for
+    static std::atomic<uint64_t> attr{0};
+    if (set_smem_limit_once(k, smem, attr) != cudaSuccess) return 0;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)Z;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)Z);
+    cfg.blockDim = dim3(6 * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    known[Z].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
 template <int DHT, int NR, int NW, int STAGES, int MINB>
 cudaError_t launch_rows(const PagedRowsParams& p, cudaStream_t s) {
     constexpr int STAGE = PR_KEYS * (DHT / 64) * 256;
@@ -547,24 +574,28 @@ bool paged_rows_supported(const PagedDesc& d) {
 
 cudaError_t launch_paged_rows(const PagedDesc& d, const PagedParts& prefix, const DeviceInfo& dev, cudaStream_t s) {
     // A warp takes 1.1 us for a tile, half of it the matrix instructions' own time, so what counts is to have many of them, each
-    // with two tiles at least, in one round of CTAs. Widths up to 64: three warps, four CTAs to an SM (32 heads x 16, 577
-    // keys: 10.2 us; with four warps, of which three CTAs fit and the rest are a second round, 15.2). Wider: six warps
-    // with an SM of their own where key heads are few, else three and two CTAs. Clusters, us at 1 / 2 / 4 / 8 CTAs per key
-    // head for 16 heads of 128 over 8200 keys, six warps: 52 / 30 / 18.3 / 26.5 (clusters of eight CTAs that fill an SM
-    // each do not pack into the GPU's SM groups). Parts joined by another kernel, on all SMs, were no faster: 18.4.
-    // A cluster doubles while every warp had two tiles, wide heads one: 16 heads over 1000 keys of 128 in 8 CTAs 7.1 us, in 4 7.6, in 2
-    // 8.2; over 128 keys of 64 in 1 CTA 3.4, in 2 4.4.
+    // with a tile at least, in one round of CTAs. Few key heads: six warps with an SM of their own, in clusters of as many CTAs as
+    // still run at once for all heads (eight for 15 heads, six for 23, five for 28, four for 36: a cluster lies in one of the GPU's
+    // SM groups). 16 heads of 128 over 8200 keys, us at 1 / 2 / 4 / 6 / 8 CTAs: 52 / 30 / 18.2 / 15.9 / 27; of 64 at 4 / 6
+    // 12.5 / 10.9, three warps and clusters of eight 13.1. Parts joined by another kernel, on all SMs, were no faster.
+    // Many: three warps, four CTAs to an SM for widths up to 64 (32 heads x 16, 577 keys: 10.2 us; with four warps, of which
+    // three CTAs fit and the rest are a second round, 15.2), two for wider ones; clusters double while every warp has
+    // two tiles, wide heads one.
     const int64_t heads = d.B * d.Hkv, sms = dev.num_sms, keys = d.table_pages * d.page;
     const bool narrow = d.dh <= 64, many = d.Tq * (d.H / d.Hkv) > 8;
-    const int warps = narrow || heads > sms / 2 ? 3 : 6;
-    const int64_t ctas = warps == 3 ? 2 * sms : sms;   // aimed at; more CTAs only add joins
     int Z = 1;
-    while (Z < PR_MAXZ && heads * Z * 2 <= ctas && keys >= Z * warps * PR_KEYS * (narrow ? 2 : 1)) Z *= 2;
-    if (warps == 6 && Z == 8 && heads * 8 > sms / 2) Z = 4;
+    if (heads <= sms / 2) {
+        const int64_t fill = (keys + 6 * PR_KEYS - 1) / (6 * PR_KEYS);
+        Z = (int)(fill < PR_MAXZ ? fill : PR_MAXZ);
+        while (Z > 1 && heads > clusters_at_once(Z)) --Z;
+        const PagedRowsParams p{d, prefix, (float)(d.scale * 1.4426950408889634), Z, dev.err_word};
+        if (narrow) return many ? launch_rows<64, 2, 6, 2, 1>(p, s) : launch_rows<64, 1, 6, 2, 1>(p, s);
+        return many ? launch_rows<128, 2, 6, 2, 1>(p, s) : launch_rows<128, 1, 6, 2, 1>(p, s);
+    }
+    while (Z < PR_MAXZ && heads * Z * 2 <= 2 * sms && keys >= Z * 3 * PR_KEYS * (narrow ? 2 : 1)) Z *= 2;
     const PagedRowsParams p{d, prefix, (float)(d.scale * 1.4426950408889634), Z, dev.err_word};
     if (narrow) return many ? launch_rows<64, 2, 3, 2, 3>(p, s) : launch_rows<64, 1, 3, 2, 4>(p, s);
-    if (warps == 3) return many ? launch_rows<128, 2, 3, 2, 2>(p, s) : launch_rows<128, 1, 3, 2, 2>(p, s);
-    return many ? launch_rows<128, 2, 6, 2, 1>(p, s) : launch_rows<128, 1, 6, 2, 1>(p, s);
+    return many ? launch_rows<128, 2, 3, 2, 2>(p, s) : launch_rows<128, 1, 3, 2, 2>(p, s);
 }
 
 }  // namespace vit
