@@ -6,9 +6,11 @@
 // each, to the warps of one CTA or of a cluster of CTAs; every warp looks its pages up one tile ahead of asking for them, keeps
 // its own running maximum, sum and output rows, joined at the end through shared memory and, between the CTAs of a cluster,
 // distributed shared memory. 32 sequences of up to 577 keys, 16 heads of 64: 12.2 us (4.6 TB/s), 4 us of it the latency of length,
-// page and first tile; 8 of up to 8200, 16 heads of 128 on 2 key heads: 19.2 us (2.6 TB/s), a warp's chain of products. The rows of the prefix, where there is one, were worked off by the kernel launched before this
-// one: its parts are joined here. This kernel starts beside that one and waits for it only then: its own keys, queries
-// and tables were there before that one began (it lets this one start behind its own wait).
+// page and first tile; 8 of up to 8200, 16 heads of 128 on 2 key heads: 16.6 us (3.0 TB/s), a warp's chain of products.
+//
+// The rows of the prefix, where there is one, were worked off by the kernel launched before this one: its parts are joined
+// here. This kernel starts beside that one and waits for it only then: its own keys, queries and tables were there before that
+// one began (it lets this one start behind its own wait).
 //
 // Rings and products are those of attention_cross_rows.cu: mma.m16n8k16 with the query rows as the n side,
 // S^T = K Q^T and O^T = V^T P^T, K and V by TMA into a ring of each warp's own. Weights are rounded to bf16 for the second
