@@ -615,6 +615,32 @@ def test_paged_attention_of_many_ragged_sequences(B):
         check_paged(Held(Tq, 6, 3, 64, 16, own, prefix, q_lens=lens))
 
 
+@pytest.mark.parametrize("dh", [40, 64, 96, 128])
+@pytest.mark.parametrize("Tq,H,Hkv", [(1, 12, 12), (1, 16, 8), (4, 24, 8), (8, 16, 8)])
+@pytest.mark.parametrize("most,prefix", [(1, []), (33, [70]), (64, []), (64, [300]), (65, [40]), (96, []), (97, []), (330, [])])
+def test_paged_attention_of_few_queries_and_many_heads(Tq, H, Hkv, dh, most, prefix):
+    """More key heads than half the SMs: short sequences, whose warps have a tile at most, some empty; absent values and
+    later tokens that are no numbers; any number of CTAs to a head."""
+    own = [Tq + (most - 1) * i // 12 for i in range(13)]
+    h = Held(Tq, H, Hkv, dh, 16, own, prefix, q_lens=[min(Tq, n) if i != 3 else 0 for i, n in enumerate(own)])
+    check_paged(h)
+    o, w, mag, n = h.ref(dh ** -0.5)
+    pg, s = slots(h.table, 12, own[12] - 1, 16)
+    h.vp[pg, s] = math.nan
+    got = h.call()
+    assert torch.isnan(got[12, Tq - 1]).all()
+    got[12, Tq - 1] = o[12, Tq - 1].to(got.dtype)
+    close(got, o, paged_tol(h, o, w, mag, n, dh))
+
+
+@pytest.mark.parametrize("dh", [64, 80, 128])
+@pytest.mark.parametrize("B", [1, 7, 9, 12, 14, 17, 36])
+def test_paged_attention_of_few_queries_in_any_cluster(B, dh):
+    """One to eight CTAs to a key head, as many as run at once."""
+    for n in (150, 190, 400, 770, 1000, 1200, 1500, 3000):
+        check_paged(Held(1 + n % 2, 8, 2, dh, 32, [n - n * b // (3 * B) for b in range(B)]))
+
+
 @pytest.mark.parametrize("Tq,H,Hkv,dh", [(1, 4, 2, 64), (2, 16, 2, 128), (100, 4, 2, 64), (260, 2, 2, 96)])
 def test_paged_attention_where_keys_are_dealt_out(Tq, H, Hkv, dh):
     """Few rows over many keys: parts go to different CTAs, some of them, or all but one key, without any."""
