@@ -596,9 +596,9 @@ cudaError_t launch_paged_rows(const PagedDesc& d, const PagedParts& prefix, cons
     }
     while (Z < PR_MAXZ && heads * Z * 2 <= 2 * sms && keys > Z * 3 * PR_KEYS * (narrow ? 2 : 1)) Z *= 2;
     const PagedRowsParams p{d, prefix, (float)(d.scale * 1.4426950408889634), Z, dev.err_word};
-    // Sequences of one tile to a warp, as behind a prefix, need no ring, and more CTAs sit on an SM: 32 sequences of up to 64 keys behind 500,
-    // 16 heads of 128, 16.9 -> 12.3 us with two warps (three: 15.1), up to 70 keys of five tokens 20.5 -> 16.4 with three (two: 18.0; spilling 200 bytes, but with two CTAs to an SM 20.9); 100 of up to 40,
-    // 8 heads of 64, 7.3 -> 4.2.
+    // Sequences of one tile to a warp, as behind a prefix, need no ring, and more CTAs sit on an SM: 32 sequences of up to 64 keys
+    // behind 500, 16 heads of 128, 16.9 -> 12.3 us with two warps (three: 15.1); up to 70 keys and five tokens 20.5 -> 16.4 with three
+    // (two: 18.0; sixteen rows then spill 200 bytes, but two CTAs to an SM take 20.9); 100 of up to 40, 8 heads of 64, 7.3 -> 4.2.
     if (keys <= 2 * PR_KEYS) {
         if (narrow) return many ? launch_rows<64, 2, 2, 1, 5>(p, s) : launch_rows<64, 1, 2, 1, 6>(p, s);
         return many ? launch_rows<128, 2, 2, 1, 4>(p, s) : launch_rows<128, 1, 2, 1, 5>(p, s);
