@@ -902,3 +902,32 @@ def test_the_binding_refuses_what_does_not_fit():
                lambda: h.call(q=rand(2, 2, 3, 64, dtype=BF))):                          # 3 heads on 2
         with pytest.raises(api.VitError):
             fn()
+
+
+@pytest.mark.parametrize("dt", [BF, F32, F64], ids=str)
+def test_an_output_at_the_inputs_address_is_the_input_or_is_refused(dt):
+    """Rows of a wider buffer, and an output that starts where they do but steps otherwise: refused, and nothing is written.
+    Dimensions of one have no stride to compare."""
+    B, T, H, dh, page = 2, 5, 4, 64, 16
+    buf, f = rand(B, T, H + 2, dh, seed=1, dtype=dt), api.rotary_frequencies(48, device=DEV)
+    k = rand(B, T, 2, dh, seed=2, dtype=dt)
+    table, pages = tables([T] * B, page)
+    pools = pool(pages, page, 2, dh, dt, fill=0.0)
+    keep = buf.clone()
+    x, packed = buf[:, :, :H], buf.view(-1)[:B * T * H * dh].view(B, T, H, dh)
+    for a, b in ((x, packed), (packed, x), (x, buf.as_strided(x.shape, (T * H * dh, dh, T * dh, 1)))):
+        with pytest.raises(ValueError):
+            api.rotary(a, f, out=b)
+        with pytest.raises(ValueError):
+            api.cache_append(k, k, *pools, table, ints([0] * B), q=a, frequencies=f, q_out=b)
+        assert same(buf, keep) and all((p == 0).all() for p in pools)
+    # one sequence of one token: whatever those strides say, it is x
+    for shape, at in (((1, 1, H, dh), (3, 7, dh, 1)), ((1, T, H, dh), (1, (H + 2) * dh, dh, 1)), ((B, 1, 1, dh), (T * (H + 2) * dh, 5, 11, 1))):
+        buf.copy_(keep)
+        x = buf[:shape[0], :shape[1], :shape[2]]
+        ref = api.rotary(x, f)
+        out = buf.as_strided(shape, at)
+        assert api.rotary(x, f, out=out) is out and same(x, ref)
+        buf.copy_(keep)
+        kk = k[:shape[0], :shape[1]].contiguous()
+        assert api.cache_append(kk, kk, *pools, table[:shape[0]].contiguous(), ints([0] * shape[0]), q=x, frequencies=f, q_out=out) is out and same(x, ref)

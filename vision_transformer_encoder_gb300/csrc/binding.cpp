@@ -342,12 +342,15 @@ const vit_rope* rope_of(PyObject* f, PyObject* layout, PyObject* scale, int64_t 
     return r;
 }
 
-// Where x (B, T, H, dh) goes rotated: into a new tensor, a contiguous one that is given, or x itself.
+// Where x (B, T, H, dh) goes rotated: into a new tensor, a contiguous one that is given, or x itself. The C call takes an
+// output at x's address for x, with x's strides, so one that steps otherwise is refused; dimensions of one are not stepped along.
 void* turned_output(PyObject* given, const char* name, const at::Tensor& x, PyObject** keep) {
     if (given != Py_None) {
         const at::Tensor& o = tensor(given, name);
-        if (o.is_cuda() && o.data_ptr() == x.data_ptr() && o.sizes() == x.sizes() && o.strides() == x.strides() &&
-            o.scalar_type() == x.scalar_type()) {
+        if (o.is_cuda() && o.data_ptr() == x.data_ptr() && o.sizes() == x.sizes() && o.scalar_type() == x.scalar_type()) {
+            for (int i = 0; i < 4; ++i)
+                if (x.size(i) > 1 && o.stride(i) != x.stride(i))
+                    refuse(name, " starts at the input's address with strides " + dims(o.strides()) + ", the input's are " + dims(x.strides()));
             Py_INCREF(given);
             *keep = given;
             return o.data_ptr();
