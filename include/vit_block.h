@@ -505,8 +505,9 @@ typedef enum {
 /*
  * Rotary positions: at position p, pair i (u, v) of the first 2 n columns of a head becomes
  *   scale (u cos a - v sin a, u sin a + v cos a),   a = p frequencies[i]
- * and the other columns stay. The angle is reduced to a turn exactly (64-bit fixed point), however far the
- * position; arithmetic in fp32 (fp64 for F64), rounded once.
+ * and the other columns stay. The angle is taken modulo a turn in 64-bit fixed point, exactly; what is off is the fraction of a turn
+ * of a frequency: the angle by p |frequencies[i]| 2^-52 + 2 pi |p| 2^-65 (F64, which keeps 128 bits: p |frequencies[i]| 2^-104).
+ * Arithmetic in fp32 (fp64 for F64), rounded once.
  */
 typedef struct {
     const double* frequencies;   /* (n) on the device, radians per position; finite */

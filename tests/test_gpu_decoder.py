@@ -931,3 +931,64 @@ def test_an_output_at_the_inputs_address_is_the_input_or_is_refused(dt):
         buf.copy_(keep)
         kk = k[:shape[0], :shape[1]].contiguous()
         assert api.cache_append(kk, kk, *pools, table[:shape[0]].contiguous(), ints([0] * shape[0]), q=x, frequencies=f, q_out=out) is out and same(x, ref)
+
+
+def pi_floor(bits):
+    """floor(2^bits pi), by 16 atan(1/5) - 4 atan(1/239)."""
+    def atan_of(n):   # 2^(bits + 32) atan(1/n), each term off by less than 1
+        term = total = (1 << (bits + 32)) // n
+        i = 1
+        while term:
+            term //= n * n
+            i += 2
+            total += term // i if i % 4 == 1 else -(term // i)
+        return total
+    return (16 * atan_of(5) - 4 * atan_of(239)) >> 32
+
+
+def cos_sin_exactly(pos, f):
+    """Cosines and sines (B, T, 1, n) in 64 bits of the angles positions * frequencies, reduced in whole numbers of 2^-256 turns."""
+    K = 256
+    pi = pi_floor(K)
+    c, s = [], []
+    for p in pos.reshape(-1).tolist():
+        for x in f.tolist():
+            num, den = float(x).as_integer_ratio()
+            r = ((p * num << 2 * K) // (2 * den * pi)) % (1 << K)
+            r -= (1 << K) if r >> (K - 1) else 0
+            a = (2 * r * pi) / (1 << 2 * K)   # rounded once
+            c.append(math.cos(a))
+            s.append(math.sin(a))
+    shape = tuple(pos.shape) + (1, f.numel())
+    return [torch.tensor(v, dtype=F64).view(shape).to(DEV) for v in (c, s)]
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_rotary_in_64_bits_at_any_position(layout):
+    """Angles from a reduction in whole numbers. Off by, in units of 2^-53 of |u| + |v|: the half turn in [-1, 1) by 1 (its
+    conversion and one sum), so the angle by pi; sincospi by 2 last places, 2; the factor 1; a product 1 and the rounding of the
+    result, counted apart. The reference: its angle's rounding 2, cos and sin 1, two products and a sum 3. 14 in all."""
+    assert abs(pi_floor(60) / (1 << 60) - math.pi) < 2.0 ** -51
+    x = rand(2, 8, 3, 64, seed=2, dtype=F64)
+    pos = ints([[0, 1, -1, 300, 4097, 99991, 1000000, -123456], [(1 << 31) - 1, -(1 << 31), 1 << 24, -(1 << 30) + 1, 7, 1 << 20, 2, 31]])
+    for f in (api.rotary_frequencies(64, device=DEV), api.rotary_frequencies(48, 500000.0, factor=8, trained=8192, device=DEV),
+              -api.rotary_frequencies(64, device=DEV),
+              torch.tensor([7.0, -3.0, 6.283185307179586, 0.0, 1e3, -1e-3, 1e-9, -1e-12, 1e-25, -3e-40], dtype=F64, device=DEV)):
+        n = f.numel()
+        c, s = cos_sin_exactly(pos, f)
+        i = torch.arange(n, device=DEV)
+        i, j = (i, i + n) if layout == api.ROTARY_HALF else (2 * i, 2 * i + 1)
+        y, w = x.clone(), torch.zeros_like(x)
+        y[..., i], y[..., j] = x[..., i] * c - x[..., j] * s, x[..., i] * s + x[..., j] * c
+        w[..., i] = w[..., j] = x[..., i].abs() + x[..., j].abs()
+        close(api.rotary(x, f, positions=pos, layout=layout), y, w * 14 * 2.0 ** -53 * 1.01 + HALF[F64] * y.abs() * 1.01)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("dt", [BF, F32, F64], ids=str)
+def test_rotary_by_a_negative_frequency_is_rotary_at_a_negative_position(dt, layout):
+    """The same angle, to the bit: a frequency's sign costs nothing of its turn's bits."""
+    x = rand(1, 6, 3, 64, seed=2, dtype=dt)
+    pos = ints([[0, 5, 1 << 20, -(1 << 24) + 1, (1 << 31) - 1, -(1 << 30)]])
+    f = torch.cat([api.rotary_frequencies(40), torch.tensor([1e-9, 3e-13, 0.7, 2.5], dtype=F64)]).to(DEV)
+    assert same(api.rotary(x, -f, positions=pos, layout=layout), api.rotary(x, f, positions=-pos, layout=layout))

@@ -3,10 +3,12 @@
 // One kernel turns the heads of the queries into their output and those of the keys into their pages, and copies
 // the values into theirs; without keys it is the plain rotation.
 //
-// The angle: f_i / 2 pi as a 64-bit fraction of a turn, once per block and pair (fp64, of which the GPU has little). A
-// position times that, modulo 2^64, is the fraction of a turn of p f_i, exact but for p 2^-64 and the rounding of f_i / 2 pi
-// (2^-52 of it): no range reduction, and far positions lose nothing. Sine and cosine are the hardware's on [-pi, pi] for
-// bf16 (off by 2^-20, where a result is rounded at 2^-9), sincospi for fp32 and fp64.
+// The angle: |f_i| / 2 pi as a 64-bit fraction of a turn with the sign put back, once per block and pair (fp64, of which the GPU
+// has little). A position times that, modulo 2^64, is the fraction of a turn of p f_i: the modulo is exact, so that there is no
+// range reduction, and what is off is p |f_i| 2^-52 for the rounding of f_i / 2 pi and 2 pi p 2^-65 for the fraction's (at
+// position 10^6 and f 1, 2.2e-10 in all). That is below what fp32 and bf16 keep; for fp64 f_i / 2 pi is kept in two words, 128 bits of a turn
+// (p |f_i| 2^-104). Sine and cosine are the hardware's on [-pi, pi] for bf16 (off by 2^-20, where a result is rounded at 2^-9),
+// sincospi for fp32 and fp64.
 //
 // Bound by reading and writing each head once. A block takes a few tokens: it makes their sines and cosines once, in shared
 // memory. A thread has one 16-byte unit (both halves of its pairs where they lie apart) of one head and walks over the tokens,
@@ -30,21 +32,44 @@ namespace {
 
 constexpr int RO_THREADS = 256, RO_MAXPAIRS = 256, RO_TOKENS = 32, RO_SINES = 1024, RO_MOST = 512, RO_AHEAD = 4;
 
-// f / 2 pi as a fraction of a turn in units of 2^-64
-__device__ __forceinline__ uint64_t turn_of(double f) {
-    double t = f * 0.15915494309189533577;
-    t -= floor(t);
-    return __double2ull_rn(t * 18446744073709551616.0);   // 1 itself saturates
+// f / 2 pi as a fraction of a turn: in units of 2^-64, and for fp64 of 2^-128.
+template <typename A> using TurnOf = typename std::conditional<std::is_same<A, double>::value, unsigned __int128, uint64_t>::type;
+
+template <typename U> __device__ __forceinline__ U turn_of(double f) {
+    // of the magnitude: a small negative number's fraction, next to 1, would keep 53 bits behind the point and no more
+    const double a = fabs(f), t = a * 0.15915494309189535, r = t - floor(t);
+    U turn;
+    if constexpr (sizeof(U) == 8) {
+        turn = __double2ull_rn(r * 18446744073709551616.0);
+    } else {
+        // t's rest: of the product, and of 1 / 2 pi behind its first 53 bits
+        double low = fma(a, 0.15915494309189535, -t) + a * -9.839338337591243e-18;
+        low -= rint(low);
+        const double high = r * 0x1p64, units = low * 0x1p64, whole = floor(high), down = floor(units);
+        turn = ((U)__double2ull_rz(whole) << 64) + __double2ull_rz((high - whole) * 0x1p64);
+        turn += ((U)(uint64_t)__double2ll_rz(down) << 64) + __double2ull_rz((units - down) * 0x1p64);
+    }
+    return f < 0 ? (U)0 - turn : turn;
 }
 
-// (cos, sin) of the angle that is `turn` 2^-64 of a turn, in half turns of [-1, 1)
-template <typename T, typename A> __device__ __forceinline__ void cos_sin(uint64_t turn, A scale, A& c, A& s) {
+// `turn` of 2^-64 or 2^-128 in half turns of [-1, 1)
+__device__ __forceinline__ double half_turns(uint64_t turn) { return (double)(int64_t)turn * 0x1p-63; }
+__device__ __forceinline__ double half_turns(unsigned __int128 turn) {
+    const bool below = (int64_t)(uint64_t)(turn >> 64) < 0;
+    if (below) turn = 0 - turn;
+    const double x = fma((double)(uint64_t)(turn >> 64), 0x1p-63, (double)(uint64_t)turn * 0x1p-127);
+    return below ? -x : x;
+}
+
+// (cos, sin) of the angle that is `turn` units of a turn
+template <typename T, typename A, typename U> __device__ __forceinline__ void cos_sin(U turn, A scale, A& c, A& s) {
     if constexpr (std::is_same<A, double>::value) {
-        sincospi((double)(int64_t)turn * 0x1p-63, &s, &c);
+        sincospi(half_turns(turn), &s, &c);
     } else if constexpr (std::is_same<T, float>::value) {
         sincospif((float)(int64_t)turn * 0x1p-63f, &s, &c);
     } else {
-        // 32 bits of the turn: off by pi 2^-32
+        // 32 bits of the turn, 24 in the float: the angle is off by 2 pi 2^-32, pi 2^-25 for the float, pi 2^-25 for pi's own
+        // rounding and 2^-23 for the product's
         __sincosf((float)(int32_t)(turn >> 32) * (0x1p-31f * 3.14159265358979f), &s, &c);
     }
     c *= scale;
@@ -149,7 +174,7 @@ __global__ void __launch_bounds__(RO_MOST) rotary_units_kernel(const __grid_cons
     const int items = (int)d.dh / N - half, heads = (int)d.H, Hkv = (int)d.Hkv, HH = heads + 2 * Hkv;
     const int64_t tokens = d.B * d.T, first = (int64_t)(blockIdx.x / groups) * tile;
     const int count = (int)min((int64_t)tile, tokens - first);
-    for (int i = threadIdx.x; i < n; i += blockDim.x) turns[i] = turn_of(d.frequencies[i]);
+    for (int i = threadIdx.x; i < n; i += blockDim.x) turns[i] = turn_of<uint64_t>(d.frequencies[i]);
     for (int i = threadIdx.x; i < count; i += blockDim.x) {
         const Token x = token_of(d, first + i);
         from[i][0] = x.b * d.qs[0] + x.t * d.qs[1];
@@ -233,10 +258,11 @@ __global__ void __launch_bounds__(RO_MOST) rotary_units_kernel(const __grid_cons
 // Any type, width, stride and alignment: a thread owns a pair, or a column behind them.
 template <typename T, typename A>
 __global__ void __launch_bounds__(RO_THREADS) rotary_generic_kernel(const __grid_constant__ RotaryDesc d, int groups) {
-    __shared__ uint64_t turns[RO_MAXPAIRS];
+    using U = TurnOf<A>;
+    __shared__ U turns[RO_MAXPAIRS];
     griddep_wait();
     griddep_launch_dependents();
-    for (int i = threadIdx.x; i < d.n; i += RO_THREADS) turns[i] = turn_of(d.frequencies[i]);
+    for (int i = threadIdx.x; i < d.n; i += RO_THREADS) turns[i] = turn_of<U>(d.frequencies[i]);
     __syncthreads();
     const int n = (int)d.n, items = (int)d.dh - n, HH = (int)(d.H + 2 * d.Hkv), per = groups * items;
     const int64_t total = d.B * d.T * per;
@@ -247,7 +273,7 @@ __global__ void __launch_bounds__(RO_THREADS) rotary_generic_kernel(const __grid
         const int at = !pair ? item + n : d.layout == VIT_ROTARY_HALF ? item : 2 * item;
         const int to = d.layout == VIT_ROTARY_HALF ? at + n : at + 1;
         A c = 1, s = 0;
-        if (pair) cos_sin<T, A>(turns[item] * (uint64_t)x.pos, (A)d.scale, c, s);
+        if (pair) cos_sin<T, A>(turns[item] * (U)x.pos, (A)d.scale, c, s);   // modulo a turn, negative positions too
         for (int h = group; h < HH; h += groups) {
             const T* src;
             T* dst;
