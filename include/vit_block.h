@@ -586,6 +586,33 @@ int vit_paged_attention(const void* q, const int64_t* q_strides, const vit_paged
                         const int32_t* prefix_table, int64_t prefix_pages, const int32_t* prefix_lens,
                         int64_t groups, int64_t B, int64_t Tq, int64_t H, double scale, void* o, void* stream);
 
+/* Kernels of vit_paged_attention. */
+typedef enum {
+    VIT_PAGED_GENERIC = 0,   /* CUDA cores, any call                                   */
+    VIT_PAGED_ROWS = 1,      /* bf16, at most 16 query rows per key head               */
+    VIT_PAGED_TC = 2,        /* bf16, tcgen05                                          */
+    VIT_PAGED_F32 = 3        /* fp32 on CUDA cores                                     */
+} vit_paged_kernel;
+
+typedef struct {
+    int kernel, prefix_kernel;      /* vit_paged_kernel of the own keys and of the prefix; -1 without a prefix */
+    int own_parts, prefix_parts;    /* parts along the keys; prefix_parts 0: none, or worked off in front of the own keys */
+    int own_rows, prefix_rows;      /* query rows of a key head that one read of a key serves, at most; 0 without a prefix */
+    int launches;                   /* kernels */
+    int64_t scratch;                /* bytes from the library's pool */
+} vit_paged_plan;
+
+/*
+ * vit_paged_attention_plan -- how vit_paged_attention would work a call with these arguments off on the current device: a
+ * diagnostic that launches and allocates nothing and reads no device memory. Sizes, strides, alignment and the room in the tables
+ * decide, lengths do not. The same errors.
+ */
+int vit_paged_attention_plan(const void* q, const int64_t* q_strides, const vit_paged_cache* cache, const int32_t* table,
+                             int64_t table_pages, const int32_t* kv_lens, const int32_t* q_lens,
+                             const int32_t* prefix_table, int64_t prefix_pages, const int32_t* prefix_lens,
+                             int64_t groups, int64_t B, int64_t Tq, int64_t H, double scale, const void* o,
+                             vit_paged_plan* plan);
+
 /* ------------------------------------------------------------------------------
  * Status, diagnostics and measurement
  * ------------------------------------------------------------------------------ */

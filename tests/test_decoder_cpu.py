@@ -166,3 +166,32 @@ def test_the_binding_refuses_layouts_past_32_bits(layout):
     x = torch.empty(2, 3, 4, 64, dtype=torch.bfloat16, device="meta")
     with pytest.raises(ValueError):
         api.rotary(x, x, layout=layout)
+
+
+class Plan(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("kernel", "prefix_kernel", "own_parts", "prefix_parts", "own_rows", "prefix_rows", "launches")]
+    _fields_ += [("scratch", I64)]
+
+
+def plan(lib, p="own", q=at(0), qs=None, c=None, table=at(1), tp=8, kv=at(2), ql=at(3), pt=at(4), pp=5, pl=at(5), groups=2, B=4, Tq=3, H=4,
+         scale=0.125, o=at(6)):
+    c = cache() if c is None else c
+    p = ctypes.byref(Plan()) if p == "own" else p
+    return lib.vit_paged_attention_plan(q, strides(qs), ctypes.byref(c) if c else None, table, tp, kv, ql, pt, pp, pl, groups, B, Tq, H, scale, o, p)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(p=None), dict(q=None), dict(c=0), dict(table=None), dict(kv=None), dict(o=None), dict(B=0), dict(Tq=0), dict(H=3), dict(tp=0),
+    dict(pl=None), dict(pp=0), dict(groups=3), dict(scale=float("nan")), dict(tp=1 << 27), dict(qs=(-1, 256, 64)), dict(q=at(0, 1)),
+    dict(o=at(10, 512)), dict(B=1 << 44), dict(c=cache(page=0)), dict(c=cache(k=at(10, 1)))], ids=str)
+def test_the_plan_of_paged_attention_refuses_what_the_call_refuses(lib, kw):
+    assert plan(lib, **kw) == ARG
+
+
+def test_the_plan_of_paged_attention_needs_a_device(lib):
+    assert plan(lib, c=cache(dh=513)) == UNSUPPORTED and plan(lib, c=cache(d=E4M3)) == DTYPE
+    if not torch.cuda.is_available():
+        assert plan(lib) == CUDA and plan(lib, pt=None, pl=None, pp=0, groups=1, ql=None) == CUDA
+    x, s = torch.zeros(2, 3, 4, 64, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        api.paged_attention_plan(x, x, x, torch.zeros(2, 1, dtype=torch.int32), s)

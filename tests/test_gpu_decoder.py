@@ -992,3 +992,89 @@ def test_rotary_by_a_negative_frequency_is_rotary_at_a_negative_position(dt, lay
     pos = ints([[0, 5, 1 << 20, -(1 << 24) + 1, (1 << 31) - 1, -(1 << 30)]])
     f = torch.cat([api.rotary_frequencies(40), torch.tensor([1e-9, 3e-13, 0.7, 2.5], dtype=F64)]).to(DEV)
     assert same(api.rotary(x, -f, positions=pos, layout=layout), api.rotary(x, f, positions=-pos, layout=layout))
+
+
+# --------------------------------------------------------------------- which kernel works a call off
+G_, R_, T_, F_ = api.PAGED_GENERIC, api.PAGED_ROWS, api.PAGED_TC, api.PAGED_F32
+
+
+def check_form(h, kernel, prefix_kernel=-1, scale=None, **kw):
+    """The call has this kernel, launches what its plan says, and is right."""
+    a = dict(q=h.q, k_pages=h.kp, v_pages=h.vp, page_table=h.table, kv_lens=h.kv_lens, q_lens=h.q_lens, prefix_table=h.prefix_table,
+             prefix_lens=h.prefix_lens, scale=scale) | kw
+    before = api.launch_count()
+    p = api.paged_attention_plan(**a)
+    assert api.launch_count() == before
+    assert (p["kernel"], p["prefix_kernel"]) == (kernel, prefix_kernel), p
+    check_paged(h, scale, **kw)
+    assert api.launch_count() - before == p["launches"]
+    assert (p["scratch"] > 0) == (p["launches"] > 1)
+    return p
+
+
+@pytest.mark.parametrize("dh", [8, 16, 24, 56, 64, 72, 80, 88, 96, 104, 120, 128, 136])
+@pytest.mark.parametrize("Tq,H,Hkv", [(1, 4, 4), (16, 2, 2), (2, 16, 2), (17, 2, 2), (3, 12, 2)])
+def test_which_kernel_bf16_has(Tq, H, Hkv, dh):
+    """At most 16 query rows per key head and widths of a multiple of 8 up to 128: the kernel of few queries. Prefixes, and more rows,
+    of widths 64, 80, 96 and 128: tensor cores. Just outside either: the generic one."""
+    few, wide, tc = Tq * H // Hkv <= 16, dh > 128, dh in (64, 80, 96, 128)
+    own = G_ if wide else R_ if few else T_ if tc else G_
+    check_form(Held(Tq, H, Hkv, dh, 16, [Tq, 40 + Tq, 100], []), own)
+    p = check_form(Held(Tq, H, Hkv, dh, 16, [Tq, 40 + Tq, 100, 30], [70, 200]), own, T_ if tc else G_)
+    assert p["own_rows"] == (min(Tq * H // Hkv, 4 if Tq * H // Hkv <= 4 else 16) if own == G_ else Tq * H // Hkv)
+
+
+@pytest.mark.parametrize("Tq,dh", [(1, 64), (5, 80), (40, 64), (40, 80), (40, 128)])
+def test_which_kernel_bf16_has_by_pages_scales_and_layouts(Tq, dh):
+    fast, H, Hkv = R_ if Tq <= 16 else T_, 2, 2
+    for page, kernel in ((16, fast), (48, fast), (8, G_), (24, G_), (1, G_)):
+        h = Held(Tq, H, Hkv, dh, page, [Tq, Tq + 90, 100], [50])
+        check_form(h, kernel, G_ if kernel == G_ else T_)
+    h = Held(Tq, H, Hkv, dh, 16, [Tq, Tq + 90], [50])
+    neg = G_ if fast == T_ else R_
+    check_form(h, neg, G_, scale=-0.1)
+    check_form(h, neg, G_, scale=0.0)
+    off = torch.empty(h.q.numel() + 1, dtype=BF, device=DEV)[1:].view(h.q.shape).copy_(h.q)
+    check_form(h, G_, G_, q=off)
+    odd = torch.empty(2, *h.kp.shape[:3], dh + 1, dtype=BF, device=DEV)[..., :dh]
+    odd[0].copy_(h.kp)
+    odd[1].copy_(h.vp)
+    check_form(h, G_, G_, k_pages=odd[0], v_pages=odd[1])
+    # tokens before sequences: a group's queries are no single run of rows
+    early = torch.empty(Tq, 2, H, dh, dtype=BF, device=DEV).transpose(0, 1).copy_(h.q)
+    p = check_form(h, fast, G_ if 1 < Tq <= 16 else T_, q=early)
+    if fast == T_:
+        assert p["prefix_parts"] == 0
+    wide = torch.empty(2, Tq, H + 2, dh, dtype=BF, device=DEV)[:, :, :H].copy_(h.q)
+    check_form(h, fast, T_, q=wide)
+
+
+@pytest.mark.parametrize("dh,page,kernel", [(4, 16, F_), (60, 8, F_), (64, 16, F_), (68, 24, F_), (128, 16, F_), (132, 16, G_), (66, 16, G_), (63, 16, G_),
+                                            (64, 12, G_), (64, 20, G_)])
+@pytest.mark.parametrize("Tq,H,Hkv", [(1, 3, 3), (1, 4, 2), (3, 4, 2), (30, 4, 2)])
+def test_which_kernel_fp32_has(Tq, H, Hkv, dh, page, kernel):
+    p = check_form(Held(Tq, H, Hkv, dh, page, [Tq, 70 + Tq], [], dt=F32), kernel)
+    R = Tq * H // Hkv
+    assert p["own_rows"] == min(R, 4 if kernel == F_ else 16)
+    check_form(Held(Tq, H, Hkv, dh, page, [Tq, 70 + Tq], [90], dt=F32), kernel, kernel)
+    h = Held(Tq, H, Hkv, dh, page, [Tq, 70 + Tq], [90], dt=F64)
+    check_form(h, G_, G_)
+    h = Held(Tq, H, Hkv, dh, page, [Tq, 70 + Tq], [90], dt=F32)
+    off = torch.empty(h.q.numel() + 1, dtype=F32, device=DEV)[1:].view(h.q.shape).copy_(h.q)
+    check_form(h, G_, G_, q=off)
+
+
+def test_which_work_is_cut_along_the_keys():
+    """Few rows over many keys are cut into parts, by the room in the tables; many are not."""
+    for Tq, dt, kernel in ((40, BF, T_), (1, F32, F_), (1, F64, G_)):
+        p = check_form(Held(Tq, 2, 2, 64, 64, [4000], [], dt=dt), kernel)
+        assert p["own_parts"] > 1 and p["launches"] == 2
+        h = Held(Tq, 2, 2, 64, 64, [Tq + 20], [], dt=dt)
+        p = check_form(h, kernel)
+        assert p["own_parts"] == 1 and p["launches"] == 1 and p["scratch"] == 0
+    p = check_form(Held(1, 2, 2, 64, 64, [4000], []), R_)
+    assert p["launches"] == 1 and p["scratch"] == 0
+    p = check_form(Held(1, 16, 16, 64, 16, [20] * 32, [1025]), R_, T_)   # rows of all sequences behind their prefix at once
+    assert p["prefix_rows"] == 32 and p["prefix_parts"] > 1
+    p = check_form(Held(300, 2, 2, 64, 16, [300, 310], [1000]), T_, T_)   # in front of the own keys
+    assert p["prefix_parts"] == 0 and p["prefix_rows"] == 256

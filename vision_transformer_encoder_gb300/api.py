@@ -21,6 +21,7 @@ LIB_PATH = os.path.join(_HERE, "libvit_block.so")
 VIT_F32, VIT_BF16, VIT_F64, VIT_E4M3 = 0, 1, 2, 3
 EPI_STORE, EPI_GELU, EPI_RESIDUAL = 0, 1, 2
 ROTARY_HALF, ROTARY_INTERLEAVED = 0, 1
+PAGED_GENERIC, PAGED_ROWS, PAGED_TC, PAGED_F32 = 0, 1, 2, 3
 
 _DT = {torch.float32: VIT_F32, torch.bfloat16: VIT_BF16, torch.float64: VIT_F64}
 
@@ -65,6 +66,7 @@ SIGNATURES = {
     "vit_rotary": (_int, [_vp] * 4 + [_i64] * 4 + [_int, _vp, _vp]),
     "vit_cache_append": (_int, [_vp] * 8 + [_i64] + [_vp] * 4 + [_i64] * 3 + [_vp, _vp]),
     "vit_paged_attention": (_int, [_vp] * 4 + [_i64] + [_vp] * 3 + [_i64, _vp] + [_i64] * 4 + [_dbl, _vp, _vp]),
+    "vit_paged_attention_plan": (_int, [_vp] * 4 + [_i64] + [_vp] * 3 + [_i64, _vp] + [_i64] * 4 + [_dbl, _vp, _vp]),
     "vit_status_string": (ctypes.c_char_p, [_int]),
     "vit_device_error": (_int, [ctypes.POINTER(ctypes.c_uint32)]),
     "vit_launch_count": (_i64, []),
@@ -486,7 +488,7 @@ def _serving():
 
         native.set_entry(on_error, *[ctypes.cast(getattr(lib, name), _vp).value for name in (
             "vit_rmsnorm", "vit_quantize", "vit_quantize_weight", "vit_linear_fp8", "vit_cross_attention", "vit_rotary",
-            "vit_cache_append", "vit_paged_attention")])
+            "vit_cache_append", "vit_paged_attention", "vit_paged_attention_plan")])
         _native = native
     return _native
 
@@ -643,6 +645,21 @@ def paged_attention(q, k_pages, v_pages, page_table, kv_lens, q_lens=None, prefi
     if stream is None:
         return fn(*a, scale, out)
     return _on(stream, a + (out,), fn, *a, scale, out)
+
+
+def paged_attention_plan(q, k_pages, v_pages, page_table, kv_lens, q_lens=None, prefix_table=None, prefix_lens=None,
+                         scale=None, out=None):
+    """How paged_attention would work this call off, as a dict: a diagnostic that launches nothing.
+
+    kernel, prefix_kernel: PAGED_GENERIC, PAGED_ROWS, PAGED_TC or PAGED_F32 (prefix_kernel -1 without a prefix).
+    own_parts, prefix_parts: parts along the keys. own_rows, prefix_rows: query rows of a key head that one read of a key
+    serves, at most. launches: kernels. scratch: bytes. Sizes, strides, alignment and the room in the tables decide,
+    lengths do not."""
+    if scale is None:
+        scale = (q.shape[-1] or 1) ** -0.5
+    names = ("kernel", "prefix_kernel", "own_parts", "prefix_parts", "own_rows", "prefix_rows", "launches", "scratch")
+    return dict(zip(names, (_native or _serving()).paged_attention_plan(
+        q, k_pages, v_pages, page_table, kv_lens, q_lens, prefix_table, prefix_lens, scale, out)))
 
 
 def device_error() -> int:

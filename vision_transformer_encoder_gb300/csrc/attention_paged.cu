@@ -400,6 +400,17 @@ PagedPlan plan_paged(const PagedDesc& d, const DeviceInfo& dev) {
     return plan;
 }
 
+int paged_rows_at_once(const PagedDesc& d, const PagedPlan& plan, bool own) {
+    const int64_t R = d.Tq * (d.H / d.Hkv);   // of a sequence; apart from the own keys, a prefix's are those of its group
+    const int64_t rows = own || (plan.form == PAGED_TC && !plan.prefix_parts) ? R : d.B / d.groups * R;
+    int64_t tile;
+    if (plan.form == PAGED_F32) tile = paged_f32_rows(d);
+    else if (plan.form == PAGED_TC || (!own && plan.prefix_tc)) tile = paged_tc_rows(d);
+    else if (plan.form == PAGED_ROWS && own) tile = R;
+    else tile = generic_rows(d);
+    return (int)(tile < rows ? tile : rows);
+}
+
 cudaError_t launch_paged_attention(const PagedDesc& d, const PagedPlan& plan, void* workspace, const DeviceInfo& dev,
                                    cudaStream_t s) {
     PagedParts parts{};

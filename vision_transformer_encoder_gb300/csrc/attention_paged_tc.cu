@@ -883,6 +883,11 @@ int64_t paged_tc_items(const PagedDesc& d, bool own) {
     return own ? d.B * d.Hkv * ceil_div(d.Tq, 2 * TT) : d.groups * d.Hkv * ceil_div(d.B / d.groups * d.Tq, 2 * TT);
 }
 
+int64_t paged_tc_rows(const PagedDesc& d) {
+    const int64_t G = d.H / d.Hkv;
+    return 2 * (PT_ROWS / G) * G;
+}
+
 bool paged_tc_apart(const PagedDesc& d) {
     // Rows of one sequence that leave their tiles mostly empty: packed with the others' they take half the tiles or less.
     const int64_t TT = PT_ROWS / (d.H / d.Hkv), S = d.B / d.groups;

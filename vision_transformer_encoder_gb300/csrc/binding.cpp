@@ -32,6 +32,7 @@ decltype(&vit_cross_attention) p_cross_attention;
 decltype(&vit_rotary) p_rotary;
 decltype(&vit_cache_append) p_cache_append;
 decltype(&vit_paged_attention) p_paged_attention;
+decltype(&vit_paged_attention_plan) p_paged_attention_plan;
 PyObject* g_on_error;   // called with (status, name)
 
 struct Refused : std::exception {
@@ -437,8 +438,8 @@ PyObject* cache_append(PyObject* const* a) {
     return keep.result(1);
 }
 
-// ---- (q, k_pages, v_pages, table, kv_lens, q_lens, prefix_table, prefix_lens, scale, out)
-PyObject* paged_attention(PyObject* const* a) {
+// ---- (q, k_pages, v_pages, table, kv_lens, q_lens, prefix_table, prefix_lens, scale, out): the attention, or its plan
+template <bool PLAN> PyObject* paged_attention(PyObject* const* a) {
     const at::Tensor &q = tensor(a[0], "q"), &kp = tensor(a[1], "k_pages"), &vp = tensor(a[2], "v_pages");
     const vit_paged_cache c = cache_of(kp, vp);
     const at::ScalarType dt = kp.scalar_type();
@@ -459,6 +460,14 @@ PyObject* paged_attention(PyObject* const* a) {
     const double scale = number(a[8]);
     Kept keep;
     void* op = output(a[9], "out", dt, q.sizes(), q, &keep.o[0]);
+    if constexpr (PLAN) {
+        vit_paged_plan p;
+        call("vit_paged_attention_plan", dev, [&](void*) {
+            return p_paged_attention_plan(q_, qs, &c, table, pages, kv, ql, before, prefix_pages, pl, groups, B, T, H, scale, op, &p);
+        });
+        return Py_BuildValue("iiiiiiiL", p.kernel, p.prefix_kernel, p.own_parts, p.prefix_parts, p.own_rows, p.prefix_rows, p.launches,
+                             (long long)p.scratch);
+    }
     call("vit_paged_attention", dev, [&](void* s) {
         return p_paged_attention(q_, qs, &c, table, pages, kv, ql, before, prefix_pages, pl, groups, B, T, H, scale, op, s);
     });
@@ -480,14 +489,14 @@ template <PyObject* (*F)(PyObject* const*), int N> PyObject* entry(PyObject*, Py
     END_HANDLE_TH_ERRORS
 }
 
-// set_entry(on_error, addresses of the eight entry points)
+// set_entry(on_error, addresses of the nine entry points)
 PyObject* set_entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
-    if (n != 9) {
-        PyErr_SetString(PyExc_TypeError, "set_entry takes a callable and eight addresses");
+    if (n != 10) {
+        PyErr_SetString(PyExc_TypeError, "set_entry takes a callable and nine addresses");
         return nullptr;
     }
-    void* p[8];
-    for (int i = 0; i < 8; ++i) {
+    void* p[9];
+    for (int i = 0; i < 9; ++i) {
         p[i] = PyLong_AsVoidPtr(args[i + 1]);
         if (PyErr_Occurred()) return nullptr;
     }
@@ -501,6 +510,7 @@ PyObject* set_entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     p_rotary = reinterpret_cast<decltype(p_rotary)>(p[5]);
     p_cache_append = reinterpret_cast<decltype(p_cache_append)>(p[6]);
     p_paged_attention = reinterpret_cast<decltype(p_paged_attention)>(p[7]);
+    p_paged_attention_plan = reinterpret_cast<decltype(p_paged_attention_plan)>(p[8]);
     Py_RETURN_NONE;
 }
 
@@ -512,7 +522,8 @@ PyMethodDef methods[] = {ENTRY("rmsnorm", rmsnorm, 8),
                          ENTRY("cross_attention", cross_attention, 6),
                          ENTRY("rotary", rotary, 6),
                          ENTRY("cache_append", cache_append, 13),
-                         ENTRY("paged_attention", paged_attention, 10),
+                         ENTRY("paged_attention", paged_attention<false>, 10),
+                         ENTRY("paged_attention_plan", paged_attention<true>, 10),
                          {"set_entry", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&set_entry)), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serving", "Marshalling of the serving stages.", -1, methods,

@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "vit_block.h"
+
 namespace vit {
 
 // Element type tags (values match vit_dtype).
@@ -323,7 +325,7 @@ struct PagedPlan {
 };
 // GENERIC: CUDA cores throughout. ROWS: the kernel of few queries for the own keys, joining the prefix's parts. TC: tensor
 // cores (tcgen05) throughout. F32: the fp32 kernel throughout.
-enum PagedForm : int { PAGED_GENERIC = 0, PAGED_ROWS = 1, PAGED_TC = 2, PAGED_F32 = 3 };
+enum PagedForm : int { PAGED_GENERIC = VIT_PAGED_GENERIC, PAGED_ROWS = VIT_PAGED_ROWS, PAGED_TC = VIT_PAGED_TC, PAGED_F32 = VIT_PAGED_F32 };
 // Few queries (attention_paged_rows.cu): bf16, at most 16 query rows per key head; joins the parts of the prefix that the
 // kernel launched before it leaves (n 0: there is none).
 bool paged_rows_supported(const PagedDesc& d);
@@ -333,6 +335,7 @@ cudaError_t launch_paged_rows(const PagedDesc& d, const PagedParts& prefix, cons
 constexpr int64_t PAGED_TC_PART = 1 << 17;              // own keys to a part, at most: made again key by key, a third of a wait's limit
 bool paged_tc_supported(const PagedDesc& d, bool own);
 int64_t paged_tc_items(const PagedDesc& d, bool own);   // of one part each
+int64_t paged_tc_rows(const PagedDesc& d);              // query rows of an item
 bool paged_tc_apart(const PagedDesc& d);                // whether the prefix is better worked off apart
 cudaError_t launch_paged_tc(const PagedDesc& d, const PagedPlan& plan, const PagedParts& parts, bool own, const DeviceInfo& dev,
                             cudaStream_t s);
@@ -342,6 +345,7 @@ int paged_f32_rows(const PagedDesc& d);                       // rows to a warp:
 int64_t paged_f32_blocks(const PagedDesc& d, bool own);   // CTAs of one part each
 cudaError_t launch_paged_f32(const PagedDesc& d, const PagedPlan& plan, const PagedParts& parts, cudaStream_t s);
 PagedPlan plan_paged(const PagedDesc& d, const DeviceInfo& dev);
+int paged_rows_at_once(const PagedDesc& d, const PagedPlan& plan, bool own);   // query rows that one read of a key serves, at most
 // workspace: plan.workspace bytes, 16-byte aligned.
 cudaError_t launch_paged_attention(const PagedDesc& d, const PagedPlan& plan, void* workspace, const DeviceInfo& dev,
                                    cudaStream_t s);

@@ -2061,14 +2061,16 @@ int vit_cache_append(const void* k, const int64_t* k_strides, const void* v, con
     return enqueue(stream, [&](const DeviceInfo& dev, cudaStream_t s) { return launch_rotary(d, dev, s); });
 }
 
-int vit_paged_attention(const void* q, const int64_t* q_strides, const vit_paged_cache* cache, const int32_t* table,
-                        int64_t table_pages, const int32_t* kv_lens, const int32_t* q_lens, const int32_t* prefix_table,
-                        int64_t prefix_pages, const int32_t* prefix_lens, int64_t groups, int64_t B, int64_t Tq, int64_t H,
-                        double scale, void* o, void* stream) {
+// Checks a call of vit_paged_attention and describes it; a status.
+static int take_paged(const void* q, const int64_t* q_strides, const vit_paged_cache* cache, const int32_t* table,
+                      int64_t table_pages, const int32_t* kv_lens, const int32_t* q_lens, const int32_t* prefix_table,
+                      int64_t prefix_pages, const int32_t* prefix_lens, int64_t groups, int64_t B, int64_t Tq, int64_t H,
+                      double scale, const void* o, PagedDesc* desc) {
     if (!q || !cache || !table || !kv_lens || !o || B <= 0 || Tq <= 0 || H <= 0 || table_pages <= 0) return VIT_ERR_ARG;
     if (!prefix_table != !prefix_lens || (prefix_table ? prefix_pages <= 0 : prefix_pages != 0)) return VIT_ERR_ARG;
     if (groups <= 0 || B % groups != 0 || (!prefix_table && groups != 1)) return VIT_ERR_ARG;
-    PagedDesc d{};
+    PagedDesc& d = *desc;
+    d = PagedDesc{};
     int64_t k_last, v_last, q_last;
     const int rc = take_cache(cache, d.ks, d.vs, &k_last, &v_last);
     if (rc != VIT_OK) return rc;
@@ -2081,7 +2083,7 @@ int vit_paged_attention(const void* q, const int64_t* q_strides, const vit_paged
     d.q = q; d.k = cache->k; d.v = cache->v; d.table = table; d.table_pages = table_pages; d.kv_lens = kv_lens;
     d.q_lens = q_lens; d.prefix_table = prefix_table; d.prefix_pages = prefix_pages; d.prefix_lens = prefix_lens;
     d.groups = groups; d.B = B; d.Tq = Tq; d.H = H; d.Hkv = Hkv; d.dh = dh; d.pages = cache->pages; d.page = cache->page;
-    d.scale = scale; d.dt = cache->dtype; d.o = o;
+    d.scale = scale; d.dt = cache->dtype; d.o = const_cast<void*>(o);
     const int64_t nq[3] = {B, Tq, H};
     if (!row_strides(q_strides, nq, dh, d.qs, &q_last)) return VIT_ERR_ARG;
     const size_t es = dt_size(d.dt), ob = (size_t)(B * Tq * H * dh) * es;
@@ -2094,6 +2096,17 @@ int vit_paged_attention(const void* q, const int64_t* q_strides, const vit_paged
     if (!aligned_to(q, d.dt) || !aligned_to(o, d.dt) || !aligned_to(table, DT_F32) || !aligned_to(kv_lens, DT_F32) ||
         !aligned_to(q_lens, DT_F32) || !aligned_to(prefix_table, DT_F32) || !aligned_to(prefix_lens, DT_F32))
         return VIT_ERR_ARG;
+    return VIT_OK;
+}
+
+int vit_paged_attention(const void* q, const int64_t* q_strides, const vit_paged_cache* cache, const int32_t* table,
+                        int64_t table_pages, const int32_t* kv_lens, const int32_t* q_lens, const int32_t* prefix_table,
+                        int64_t prefix_pages, const int32_t* prefix_lens, int64_t groups, int64_t B, int64_t Tq, int64_t H,
+                        double scale, void* o, void* stream) {
+    PagedDesc d;
+    const int rc = take_paged(q, q_strides, cache, table, table_pages, kv_lens, q_lens, prefix_table, prefix_pages, prefix_lens,
+                              groups, B, Tq, H, scale, o, &d);
+    if (rc != VIT_OK) return rc;
     DeviceState* st = nullptr;
     const int on = current_device(&st);
     if (on != VIT_OK) return on;
@@ -2116,6 +2129,30 @@ int vit_paged_attention(const void* q, const int64_t* q_strides, const vit_paged
         return ran != VIT_OK ? ran : VIT_ERR_CUDA;
     }
     return ran;
+}
+
+int vit_paged_attention_plan(const void* q, const int64_t* q_strides, const vit_paged_cache* cache, const int32_t* table,
+                             int64_t table_pages, const int32_t* kv_lens, const int32_t* q_lens, const int32_t* prefix_table,
+                             int64_t prefix_pages, const int32_t* prefix_lens, int64_t groups, int64_t B, int64_t Tq, int64_t H,
+                             double scale, const void* o, vit_paged_plan* plan) {
+    if (!plan) return VIT_ERR_ARG;
+    PagedDesc d;
+    const int rc = take_paged(q, q_strides, cache, table, table_pages, kv_lens, q_lens, prefix_table, prefix_pages, prefix_lens,
+                              groups, B, Tq, H, scale, o, &d);
+    if (rc != VIT_OK) return rc;
+    DeviceState* st = nullptr;
+    const int on = current_device(&st);
+    if (on != VIT_OK) return on;
+    const PagedPlan p = plan_paged(d, st->info);
+    plan->kernel = p.form;
+    plan->prefix_kernel = !d.prefix_table ? -1 : p.form != PAGED_ROWS ? p.form : p.prefix_tc ? PAGED_TC : PAGED_GENERIC;
+    plan->own_parts = p.own_parts > 0 ? p.own_parts : 1;
+    plan->prefix_parts = p.prefix_parts;
+    plan->own_rows = paged_rows_at_once(d, p, true);
+    plan->prefix_rows = d.prefix_table ? paged_rows_at_once(d, p, false) : 0;
+    plan->launches = p.launches;
+    plan->scratch = (int64_t)p.workspace;
+    return VIT_OK;
 }
 
 int vit_block_noalloc(const void* x, const void* w_q, const void* w_k, const void* w_v,
