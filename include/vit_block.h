@@ -564,7 +564,8 @@ int vit_cache_append(const void* k, const int64_t* k_strides, const void* v, con
  *   o[b, t, h] = sum_u softmax_u(scale q[b, t, h] . k[u, h / G]) v[u, h / G],   G = H / heads
  * over the keys u of the sequence with u < kv_lens[b] - (q_lens[b] - 1 - t), so that the last query sees them all, and,
  * in front of them, over the prefix of its group. The sequences fall into `groups` groups of B / groups in turn, each
- * with a prefix of its own, whose keys are read and scored for the whole group at once.
+ * with a prefix of its own, whose keys are read and scored for many rows of the group at once: BF16 on tensor cores up to 256, the
+ * other kernels two to sixteen.
  *   q             (B, Tq, H, dh) with strides as vit_rotary's; H % heads == 0
  *   table         (B, table_pages); kv_lens (B), clamped to [0, table_pages page], the new tokens counted in
  *   q_lens        (B), nullable (then Tq; clamped to [0, Tq]): rows t >= q_lens[b] of o are zeros

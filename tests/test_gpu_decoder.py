@@ -1078,3 +1078,33 @@ def test_which_work_is_cut_along_the_keys():
     assert p["prefix_rows"] == 32 and p["prefix_parts"] > 1
     p = check_form(Held(300, 2, 2, 64, 16, [300, 310], [1000]), T_, T_)   # in front of the own keys
     assert p["prefix_parts"] == 0 and p["prefix_rows"] == 256
+
+
+@pytest.mark.parametrize("dh", [60, 64, 96, 128])
+@pytest.mark.parametrize("S,Tq,G,own_rows,prefix_rows", [(1, 1, 1, 1, 1), (2, 1, 1, 1, 2), (3, 1, 1, 1, 2), (8, 1, 1, 1, 2), (9, 1, 1, 1, 4), (33, 1, 1, 1, 4),
+                                                         (1, 2, 1, 2, 2), (3, 1, 2, 2, 4), (1, 1, 3, 3, 3), (5, 1, 3, 3, 4), (2, 3, 2, 4, 4)])
+def test_an_fp32_prefix_is_read_for_several_sequences_at_once(S, Tq, G, own_rows, prefix_rows, dh):
+    """Rows of different sequences in one warp: empty ones among them, pages that are absent, and a prefix cut along its keys."""
+    for prefix in ([77], [700, 33]):
+        n = S * len(prefix)
+        own = [(Tq + 40 * b) % 130 + (Tq if b % 4 != 2 else 0) for b in range(n)]
+        lens = [min(Tq, own[b]) if b % 4 != 3 else 0 for b in range(n)]
+        for q_lens in (None, lens):
+            h = Held(Tq, 2 * G, 2, dh, 16, own, prefix, dt=F32, q_lens=q_lens)
+            p = check_form(h, F_, F_)
+            assert (p["own_rows"], p["prefix_rows"]) == (own_rows, prefix_rows)
+            assert same(h.call(), h.call())
+        h = Held(Tq, 2 * G, 2, dh, 16, own, prefix, dt=F32)
+        ref = h.call()
+        pg, s = slots(h.prefix_table, len(prefix) - 1, 5, 16)
+        h.vp[pg, s, 0] = math.nan   # one key head of the last group's prefix: its sequences' rows, no others
+        got = h.call()
+        assert torch.isnan(got[n - S:, :, :G]).all() and same(got[:n - S], ref[:n - S]) and same(got[n - S:, :, G:], ref[n - S:, :, G:])
+        h.prefix_table[len(prefix) - 1, 0] = -1   # with the page that holds it absent, the value is not there
+        assert torch.isfinite(h.call()).all()
+
+
+def test_a_generic_prefix_is_read_for_several_rows_at_once():
+    for Tq, G, rows in ((1, 1, 4), (2, 2, 4), (1, 5, 16), (9, 2, 16)):
+        p = check_form(Held(Tq, 2 * G, 2, 40, 20, [Tq + 3 * b for b in range(6)], [77], dt=F32), G_, G_)
+        assert p["prefix_rows"] == rows

@@ -636,8 +636,8 @@ def paged_attention(q, k_pages, v_pages, page_table, kv_lens, q_lens=None, prefi
     the new tokens in; q_lens (B) int32 says how many those are, Tq when not given. Rows behind them are zeros.
     page_table: (B, table_pages) int32; keys on absent pages (entries outside [0, pages)) are not seen.
     prefix_table (groups, prefix_pages) and prefix_lens (groups), int32: keys in front of all those, the same for the
-    B / groups sequences of a group (the first B / groups sequences are the first group), read once for all of
-    them. A row that sees nothing is zeros. scale: 1 / sqrt(dh) by default."""
+    B / groups sequences of a group (the first B / groups sequences are the first group), read for many of
+    their rows at once. A row that sees nothing is zeros. scale: 1 / sqrt(dh) by default."""
     fn = (_native or _serving()).paged_attention
     if scale is None:
         scale = (q.shape[-1] or 1) ** -0.5

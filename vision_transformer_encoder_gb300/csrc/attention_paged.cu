@@ -4,7 +4,8 @@
 // over the prefix of b's group and b's own keys u < lim(b, t) = kv_len - (q_len - 1 - t). G = H / Hkv query heads share a
 // key head.
 //
-// The prefix of a group is worked off for the rows of all its sequences at once, apart from their own keys; either can be
+// The prefix of a group is worked off for the rows of all its sequences in turn, apart from their own keys, as many rows to a read of
+// a key as a kernel's tile has: up to 256 on tensor cores, four in fp32, 4 or 16 in the generic kernel. Either can be
 // cut along the keys too. Such a part leaves an unnormalised row, its maximum and its sum of weights in a workspace
 // (PagedParts), and what runs last joins them, always in the same order. Without a prefix and with one part, rows are
 // stored directly.
@@ -12,7 +13,8 @@
 // Generic kernel: any type, head width up to 512, page size, stride and alignment. A CTA takes up to RT rows of one key
 // head and 32 keys at a time: keys to shared memory, scores, the running maximum and sum, values over the keys, sums in
 // registers. Bound by the reads of shared memory for its products: 2 x 512 queries of 12 heads of 64 over 512 keys in pages of 20,
-// fp32, 209 us; 252 us in bf16 with heads of 72.
+// fp32, 209 us; 252 us in bf16 with heads of 72. A prefix has a sequence's RT too: with 16 rows of a group where a sequence has
+// one, 32 x 1 behind 4100 keys 190 -> 125 us, but 8 x 1 over 577 behind 197 52 -> 72 and 8 x 1 of fp64 and heads of 512 397 -> 1490.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -371,11 +373,13 @@ PagedPlan plan_paged(const PagedDesc& d, const DeviceInfo& dev) {
         plan.own_parts = plan.own_parts < least ? least : plan.own_parts;
         plan.partial = plan.prefix_parts + plan.own_parts > 1;
     } else if (plan.form == PAGED_F32) {
-        // CTAs of four warps, as many as sit on the SMs at once (three to six to an SM by registers), dealt out to own keys and prefix
+        // CTAs of four warps, as many as sit on the SMs at once (three to six to an SM by the registers of own keys' rows or, where they
+        // are more, the prefix's), dealt out to own keys and prefix
         // by what there is to read (in turn, each for all SMs, 6 x 2 tokens of 12 / 3 heads of 96 over 300 keys behind 800 took 20.8 us
         // instead of 14.9); parts of three or four steps to each warp at least (two: 16.1)
-        const int rows = paged_f32_rows(d);
-        const int64_t ctas = sms * (d.dh > 64 ? (rows == 4 ? 3 : 4) : rows == 1 ? 6 : 4), least = rows == 1 ? 96 : 128;
+        const int one = paged_f32_rows(d, true), rows = d.prefix_table ? paged_f32_rows(d, false) : one;
+        const int64_t ctas = sms * (d.dh > 64 ? (rows == 4 ? 3 : 4) : rows == 1 ? 6 : rows == 2 && one == 1 ? 5 : 4);
+        const int64_t least = one == 1 ? 96 : 128;
         const int64_t own = paged_f32_blocks(d, true), ahead = d.prefix_table ? paged_f32_blocks(d, false) : 0;
         int64_t per = (own * keys + ahead * before + ctas - 1) / ctas;
         per = per < least ? least : per;
@@ -404,7 +408,7 @@ int paged_rows_at_once(const PagedDesc& d, const PagedPlan& plan, bool own) {
     const int64_t R = d.Tq * (d.H / d.Hkv);   // of a sequence; apart from the own keys, a prefix's are those of its group
     const int64_t rows = own || (plan.form == PAGED_TC && !plan.prefix_parts) ? R : d.B / d.groups * R;
     int64_t tile;
-    if (plan.form == PAGED_F32) tile = paged_f32_rows(d);
+    if (plan.form == PAGED_F32) tile = paged_f32_rows(d, own);
     else if (plan.form == PAGED_TC || (!own && plan.prefix_tc)) tile = paged_tc_rows(d);
     else if (plan.form == PAGED_ROWS && own) tile = R;
     else tile = generic_rows(d);

@@ -1,7 +1,8 @@
 // attention_paged_f32.cu -- paged attention in fp32: the mathematics of attention_paged.cu for head widths up to 128 in steps
 // of 4 and pages of a multiple of 8 tokens.
 //
-// Bound by reading keys and values once. A warp takes up to four rows (NR) of one key head and 8 keys, which lie in one page, at
+// Bound by reading keys and values once for every four rows. A warp takes up to four rows (NR) of one key head, of a sequence or for a
+// prefix of all its group's, and 8 keys, which lie in one page, at
 // a time: its lanes hold VEC columns each, so that a key is one coalesced load, and all 16 loads of a step are in flight
 // together, those of the next step behind them. The 8 NR products' halves are added across the lanes while they are
 // handed out, so that each lane ends up with whole scores of its own: 31 exchanges for 32 scores. fp32 throughout, O in
@@ -62,19 +63,15 @@ template <int N> __device__ __forceinline__ void hand_out(float (&x)[N], int lan
     }
 }
 
+// CTA i of the prefixes, or of the own keys. sO: a row of O for each warp and row, sml: its maximum and sum.
 template <int VEC, int NR>
-__global__ void __launch_bounds__(PF_WARPS * 32) paged_f32_kernel(const __grid_constant__ PagedF32Params p) {
+__device__ __forceinline__ void paged_f32_rows_of(const PagedF32Params& p, bool prefix, int i, float* sO, float* sml) {
     constexpr int N = PF_KEYS * NR;   // scores of a step: value key * NR + row
     // lanes that differ in these bits hold the same score; those of one row's keys differ in `across`
     constexpr int ROWBIT = NR == 1 ? 0 : NR == 2 ? 1 : 2;
     const PagedDesc& d = p.d;
-    __shared__ float sO[PF_WARPS][NR][32 * VEC], sml[PF_WARPS][NR][2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, dh = (int)d.dh;
-    griddep_wait();
-    griddep_launch_dependents();
     const int G = (int)(d.H / d.Hkv), Tq = (int)d.Tq, S = (int)(d.B / d.groups);
-    const bool prefix = blockIdx.x < p.prefix_blocks;
-    int i = (int)(prefix ? blockIdx.x : blockIdx.x - p.prefix_blocks);
     const int Z = prefix ? p.prefix_parts : p.own_parts, nrb = prefix ? p.prefix_rb : p.own_rb;
     const int z = i % Z;
     i /= Z;
@@ -199,13 +196,13 @@ __global__ void __launch_bounds__(PF_WARPS * 32) paged_f32_kernel(const __grid_c
 #pragma unroll
     for (int w = 16; w >= (1 << (5 - BITS + ROWBIT)); w /= 2) l += __shfl_xor_sync(0xffffffffu, l, w);
     if (my_key == 0 && (lane & ((1 << (5 - BITS)) - 1)) == 0) {
-        sml[warp][my_row][0] = m;
-        sml[warp][my_row][1] = l;
+        sml[2 * (warp * NR + my_row)] = m;
+        sml[2 * (warp * NR + my_row) + 1] = l;
     }
 #pragma unroll
     for (int r = 0; r < NR; ++r)
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) sO[warp][r][col + c] = o[r][c];
+        for (int c = 0; c < VEC; ++c) sO[(warp * NR + r) * 32 * VEC + col + c] = o[r][c];
     __syncthreads();
     // join the warps, a row to a warp in turn
 #pragma unroll
@@ -218,15 +215,15 @@ __global__ void __launch_bounds__(PF_WARPS * 32) paged_f32_kernel(const __grid_c
         if (to < 0) continue;
         float top = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < PF_WARPS; ++w) top = fmaxf(top, sml[w][r][0]);
+        for (int w = 0; w < PF_WARPS; ++w) top = fmaxf(top, sml[2 * (w * NR + r)]);
         const float base = top == -INFINITY ? 0.f : top;
         float acc[VEC] = {}, sum = 0.f;
 #pragma unroll
         for (int w = 0; w < PF_WARPS; ++w) {
-            const float f = exp2f(sml[w][r][0] - base);
-            sum = fmaf(f, sml[w][r][1], sum);
+            const float f = exp2f(sml[2 * (w * NR + r)] - base);
+            sum = fmaf(f, sml[2 * (w * NR + r) + 1], sum);
 #pragma unroll
-            for (int c = 0; c < VEC; ++c) acc[c] = fmaf(f, sO[w][r][col + c], acc[c]);
+            for (int c = 0; c < VEC; ++c) acc[c] = fmaf(f, sO[(w * NR + r) * 32 * VEC + col + c], acc[c]);
         }
         float* dst;
         if (p.parts.n) {
@@ -244,11 +241,32 @@ __global__ void __launch_bounds__(PF_WARPS * 32) paged_f32_kernel(const __grid_c
     }
 }
 
-template <int VEC> cudaError_t launch_f32(const PagedF32Params& p, int NR, int64_t blocks, cudaStream_t s) {
+// NR rows to a warp for own keys, NP for the prefixes, whose rows are those of all sequences of a group.
+template <int VEC, int NR, int NP>
+__global__ void __launch_bounds__(PF_WARPS * 32) paged_f32_kernel(const __grid_constant__ PagedF32Params p) {
+    static_assert(NP >= NR, "a group has a sequence's rows at least");
+    __shared__ float sO[PF_WARPS * NP * 32 * VEC], sml[PF_WARPS * NP * 2];
+    griddep_wait();
+    griddep_launch_dependents();
+    const bool prefix = blockIdx.x < p.prefix_blocks;
+    const int i = (int)(prefix ? blockIdx.x : blockIdx.x - p.prefix_blocks);
+    if constexpr (NR == NP) {
+        paged_f32_rows_of<VEC, NR>(p, prefix, i, sO, sml);
+    } else {
+        if (prefix) paged_f32_rows_of<VEC, NP>(p, true, i, sO, sml);
+        else paged_f32_rows_of<VEC, NR>(p, false, i, sO, sml);
+    }
+}
+
+template <int VEC> cudaError_t launch_f32(const PagedF32Params& p, int NR, int NP, int64_t blocks, cudaStream_t s) {
     const dim3 grid((unsigned)blocks), block(PF_WARPS * 32);
-    if (NR == 1) return launch_dependent(paged_f32_kernel<VEC, 1>, grid, block, 0, s, p);
-    if (NR == 2) return launch_dependent(paged_f32_kernel<VEC, 2>, grid, block, 0, s, p);
-    return launch_dependent(paged_f32_kernel<VEC, 4>, grid, block, 0, s, p);
+    if (NR == 4) return launch_dependent(paged_f32_kernel<VEC, 4, 4>, grid, block, 0, s, p);
+    if (NR == 2)
+        return NP == 2 ? launch_dependent(paged_f32_kernel<VEC, 2, 2>, grid, block, 0, s, p)
+                       : launch_dependent(paged_f32_kernel<VEC, 2, 4>, grid, block, 0, s, p);
+    if (NP == 1) return launch_dependent(paged_f32_kernel<VEC, 1, 1>, grid, block, 0, s, p);
+    return NP == 2 ? launch_dependent(paged_f32_kernel<VEC, 1, 2>, grid, block, 0, s, p)
+                   : launch_dependent(paged_f32_kernel<VEC, 1, 4>, grid, block, 0, s, p);
 }
 
 bool columns_fit(const void* p, const int64_t st[3], int64_t unit) {
@@ -257,13 +275,16 @@ bool columns_fit(const void* p, const int64_t st[3], int64_t unit) {
 
 }  // namespace
 
-int paged_f32_rows(const PagedDesc& d) {
-    const int64_t R = d.Tq * (d.H / d.Hkv);
-    return R == 1 ? 1 : R == 2 ? 2 : 4;
+// Rows that share a key's load. A prefix's are those of all sequences of its group: 32 x 1 over 64 keys behind 4100, 12 heads of 64, 88
+// us with one row, 47 with four; of 128, 164 -> 65. With few sequences of one row, four rows' registers cost the own keys
+// more than their sharing gains: 8 x 1 over 577 keys behind 197, 11.9 us with four, 11.3 with two (one: 11.4).
+int paged_f32_rows(const PagedDesc& d, bool own) {
+    const int64_t one = d.Tq * (d.H / d.Hkv), R = (own ? 1 : d.B / d.groups) * one;
+    return R == 1 ? 1 : R == 2 || (one == 1 && R <= 8) ? 2 : 4;
 }
 
 int64_t paged_f32_blocks(const PagedDesc& d, bool own) {
-    const int64_t NR = paged_f32_rows(d), R = (own ? 1 : d.B / d.groups) * d.Tq * (d.H / d.Hkv);
+    const int64_t NR = paged_f32_rows(d, own), R = (own ? 1 : d.B / d.groups) * d.Tq * (d.H / d.Hkv);
     return (own ? d.B : d.groups) * d.Hkv * ((R + NR - 1) / NR);
 }
 
@@ -276,7 +297,7 @@ bool paged_f32_supported(const PagedDesc& d) {
 }
 
 cudaError_t launch_paged_f32(const PagedDesc& d, const PagedPlan& plan, const PagedParts& parts, cudaStream_t s) {
-    const int NR = paged_f32_rows(d);
+    const int NR = paged_f32_rows(d, true), NP = plan.prefix_parts ? paged_f32_rows(d, false) : NR;
     const int64_t G = d.H / d.Hkv;
     PagedF32Params p{};
     p.d = d;
@@ -284,11 +305,11 @@ cudaError_t launch_paged_f32(const PagedDesc& d, const PagedPlan& plan, const Pa
     p.prefix_parts = plan.prefix_parts;
     p.own_parts = plan.own_parts;
     p.own_rb = (int)((d.Tq * G + NR - 1) / NR);
-    p.prefix_rb = (int)((d.B / d.groups * d.Tq * G + NR - 1) / NR);
+    p.prefix_rb = (int)((d.B / d.groups * d.Tq * G + NP - 1) / NP);
     p.prefix_blocks = plan.prefix_parts ? paged_f32_blocks(d, false) * plan.prefix_parts : 0;
     p.scale_log2 = (float)(d.scale * 1.4426950408889634);
     const int64_t blocks = p.prefix_blocks + paged_f32_blocks(d, true) * plan.own_parts;
-    return d.dh <= 64 ? launch_f32<2>(p, NR, blocks, s) : launch_f32<4>(p, NR, blocks, s);
+    return d.dh <= 64 ? launch_f32<2>(p, NR, NP, blocks, s) : launch_f32<4>(p, NR, NP, blocks, s);
 }
 
 }  // namespace vit

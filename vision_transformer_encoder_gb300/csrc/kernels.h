@@ -341,7 +341,7 @@ cudaError_t launch_paged_tc(const PagedDesc& d, const PagedPlan& plan, const Pag
                             cudaStream_t s);
 // fp32 (attention_paged_f32.cu): head widths up to 128 in steps of 4, pages of a multiple of 8.
 bool paged_f32_supported(const PagedDesc& d);
-int paged_f32_rows(const PagedDesc& d);                       // rows to a warp: 1, 2 or 4
+int paged_f32_rows(const PagedDesc& d, bool own);         // rows to a warp: 1, 2 or 4
 int64_t paged_f32_blocks(const PagedDesc& d, bool own);   // CTAs of one part each
 cudaError_t launch_paged_f32(const PagedDesc& d, const PagedPlan& plan, const PagedParts& parts, cudaStream_t s);
 PagedPlan plan_paged(const PagedDesc& d, const DeviceInfo& dev);
