@@ -381,12 +381,6 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&a)[32], float& top) 
     tmem_ld_wait_for(a);
     asm volatile("" : "+f"(top)::"memory");
 }
-__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[8]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
-                 :
-                 : "memory");
-}
 __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
