@@ -195,3 +195,20 @@ def test_the_plan_of_paged_attention_needs_a_device(lib):
     x, s = torch.zeros(2, 3, 4, 64, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
     with pytest.raises(ValueError):
         api.paged_attention_plan(x, x, x, torch.zeros(2, 1, dtype=torch.int32), s)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(base=float("nan")), dict(base=0.0), dict(base=-2.0), dict(factor=float("nan")), dict(factor=-1.0), dict(trained=float("nan")),
+    dict(trained=4096, slow=float("-inf")), dict(trained=4096, slow=float("nan")), dict(trained=4096, slow=32.0),
+    dict(base=1e-300, width=512, factor=1e-30)], ids=str)
+def test_rotary_frequencies_are_finite_or_refused(kw):
+    """The kernels take finite frequencies only, and cannot look at them before they run."""
+    kw = dict(dict(width=64, factor=8.0), **kw)
+    with pytest.raises(ValueError):
+        api.rotary_frequencies(**kw)
+
+
+def test_rotary_frequencies_that_are_taken():
+    for kw in (dict(), dict(factor=0.25), dict(factor=8, trained=1), dict(factor=8, trained=4096.0, slow=-1, fast=0.5), dict(factor=float("inf")), dict(trained=float("inf")), dict(base=0.5), dict(width=2, base=1e300)):
+        f = api.rotary_frequencies(**dict(dict(width=64), **kw))
+        assert f.dtype == torch.float64 and torch.isfinite(f).all()

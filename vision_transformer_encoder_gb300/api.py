@@ -592,7 +592,10 @@ def rotary_frequencies(width, base=10000.0, factor=1.0, trained=None, slow=1.0, 
     keep = torch.zeros_like(f)
     if trained is not None:
         keep = ((trained * f / (2 * torch.pi) - slow) / (fast - slow)).clamp(0, 1)
-    return (f * (keep + (1 - keep) / factor)).to(device)
+    f = f * (keep + (1 - keep) / factor)
+    if not torch.isfinite(f).all():
+        raise ValueError("these arguments give frequencies that are not finite")
+    return f.to(device)
 
 
 def rotary(x, frequencies, positions=None, layout=ROTARY_HALF, scale=1.0, out=None, stream=None):
