@@ -1108,3 +1108,138 @@ def test_a_generic_prefix_is_read_for_several_rows_at_once():
     for Tq, G, rows in ((1, 1, 4), (2, 2, 4), (1, 5, 16), (9, 2, 16)):
         p = check_form(Held(Tq, 2 * G, 2, 40, 20, [Tq + 3 * b for b in range(6)], [77], dt=F32), G_, G_)
         assert p["prefix_rows"] == rows
+
+
+# ------------------------------------------------------------------- tables as a server keeps them
+FORMS = [(1, 4, 2, 64, 16, BF), (3, 8, 2, 128, 64, BF), (2, 4, 2, 72, 16, BF), (40, 4, 4, 64, 16, BF), (200, 4, 2, 80, 32, BF), (140, 2, 2, 128, 128, BF),
+         (20, 4, 2, 72, 16, BF), (1, 4, 4, 64, 16, F32), (2, 4, 2, 128, 8, F32), (30, 4, 2, 64, 16, F32), (1, 4, 2, 64, 12, F32), (2, 2, 1, 64, 16, F64)]
+
+
+def widened(table, by, pages, seed):
+    """A table with room for `by` times as many pages: entries behind the held ones are any numbers, pages of the pool among them."""
+    g = torch.Generator().manual_seed(seed)
+    t = torch.randint(-3, pages + 3, (table.shape[0], table.shape[1] * by), generator=g, dtype=torch.int32)
+    t[:, 3::7] = torch.randint(-(1 << 31), (1 << 31) - 1, t[:, 3::7].shape, generator=g).int()
+    t[:, :table.shape[1]] = table.cpu()
+    return t.to(DEV)
+
+
+@pytest.mark.parametrize("by", [16, 128, 3000])
+@pytest.mark.parametrize("Tq,H,Hkv,dh,page,dt", FORMS, ids=str)
+def test_paged_attention_of_tables_much_wider_than_what_is_held(Tq, H, Hkv, dh, page, dt, by):
+    """Room for long texts, and short ones in it: the same results, whatever stands behind the held pages."""
+    for prefix in ([], [130, 33]):
+        h = Held(Tq, H, Hkv, dh, page, [Tq, Tq + 90, 2 * Tq, 100 + Tq], prefix, dt=dt)
+        P = h.kp.shape[0]
+        # rubbish stands in the spare entry behind the last page too
+        h.table = widened(h.table, by, P, by)
+        if prefix:
+            h.prefix_table = widened(h.prefix_table, by, P, by + 1)
+        got = check_paged(h)
+        assert same(h.call(), got)
+
+
+@pytest.mark.parametrize("Tq,H,Hkv,dh,page,dt", FORMS, ids=str)
+def test_paged_attention_reads_a_page_as_often_as_tables_name_it(Tq, H, Hkv, dh, page, dt):
+    """The same page twice in a sequence, in several sequences and in a prefix."""
+    n = 5 * page + 3
+    n = max(n, Tq)
+    need = -(-n // page)
+    P = 3
+    kp, vp = rand(P, page, Hkv, dh, seed=1, dtype=dt), rand(P, page, Hkv, dh, seed=2, dtype=dt)
+    order = [[(i * i + b) % P for i in range(need)] for b in range(2)]
+    table, pre = ints(order), ints([[1, 1, 0, 1]])
+    q = rand(2, Tq, H, dh, seed=3, dtype=dt)
+    got = api.paged_attention(q, kp, vp, table, ints([n, n]), prefix_table=pre, prefix_lens=ints([3 * page + 1]))
+    # the same keys, each in a page of its own
+    rows = order + [[1, 1, 0, 1]]
+    own = [torch.cat([p[i] for r in rows for i in r]).view(-1, page, Hkv, dh) for p in (kp, vp)]
+    t2 = torch.arange(2 * need, dtype=torch.int32, device=DEV).view(2, need)
+    p2 = torch.arange(2 * need, 2 * need + 4, dtype=torch.int32, device=DEV).view(1, 4)
+    assert same(got, api.paged_attention(q, own[0], own[1], t2, ints([n, n]), prefix_table=p2, prefix_lens=ints([3 * page + 1])))
+    assert torch.isfinite(got).all()
+
+
+@pytest.mark.parametrize("Tq,H,Hkv,dh,page,dt", FORMS, ids=str)
+def test_paged_attention_of_nothing_and_of_padding_that_is_no_number(Tq, H, Hkv, dh, page, dt):
+    """Lengths of zero throughout; a prefix of nothing; and queries behind a sequence's new tokens that are NaN."""
+    B = 4
+    h = Held(Tq, H, Hkv, dh, page, [Tq + 50 * b for b in range(B)], [90, 40], dt=dt)
+    zero, none = ints([0] * B), ints([0, -5])
+    assert (h.call(kv_lens=zero, prefix_lens=none) == 0).all()
+    assert (h.call(q_lens=zero) == 0).all() and (h.call(q_lens=zero, kv_lens=zero, prefix_lens=none) == 0).all()
+    alone = h.call(prefix_table=None, prefix_lens=None)
+    h.prefix, h.prefix_lens = [0, 0], none   # the same rows without one
+    keep, h.where = h.where, h.where[:B] + [(0, 0), (0, 0)]
+    o, w, mag, n = h.ref(dh ** -0.5)
+    close(h.call(), o, paged_tol(h, o, w, mag, n, dh))
+    close(alone, o, paged_tol(h, o, w, mag, n, dh))
+    h.where, h.prefix, h.prefix_lens = keep, [90, 40], ints([90, 40])
+    lens = [Tq, max(1, Tq // 2), 0, max(1, Tq - 1)]
+    h.q_lens = ints(lens)
+    ref = check_paged(h)
+    for b, m in enumerate(lens):
+        h.q[b, m:] = math.nan
+    assert same(h.call(), ref)
+
+
+@pytest.mark.parametrize("B,Tq,H,Hkv,dh,dt", [(2500, 1, 4, 4, 64, BF), (1200, 2, 4, 2, 128, BF), (500, 20, 2, 2, 64, BF), (1200, 1, 4, 2, 64, F32), (400, 1, 2, 2, 40, F64)], ids=str)
+def test_paged_attention_of_thousands_of_sequences(B, Tq, H, Hkv, dh, dt):
+    g = torch.Generator().manual_seed(B)
+    own = (torch.randint(0, 70, (B,), generator=g)).tolist()
+    for prefix, groups in ((0, 0), (50, 1), (20, B // 4)):
+        h = Held(Tq, H, Hkv, dh, 16, own, [prefix] * groups, dt=dt)
+        got = h.call()
+        some = list(range(0, B, 97)) + [B - 1]
+        small = Held.__new__(Held)
+        small.__dict__.update(h.__dict__)
+        S = B // groups if groups else 0
+        small.B, small.own, small.q, small.q_lens = len(some), [own[b] for b in some], h.q[some], None
+        small.where = [h.where[b] for b in some] + ([h.where[B + b // S] for b in some] if groups else [])
+        small.prefix = [prefix] * len(some) if groups else []
+        o, w, mag, n = small.ref(dh ** -0.5)
+        close(got[some], o, paged_tol(small, o, w, mag, n, dh))
+
+
+@pytest.mark.parametrize("H,Hkv,dh,dt", [(8, 2, 64, BF), (4, 4, 72, BF), (4, 4, 64, F32)], ids=str)
+@pytest.mark.parametrize("T", [1, 2, 24])
+def test_a_text_grows_without_waiting_as_it_grows_with_waiting(T, H, Hkv, dh, dt):
+    """Append and attention in turn, each launched while the one before still runs, against the same with a wait behind each
+    call: tokens, lengths, starts and page tables are all made on the stream."""
+    B, page, steps = 6, 16, 12
+    h = Held(T, H, Hkv, dh, page, [30 + 9 * b for b in range(B)], [300, 77, 500], dt=dt)
+    f = api.rotary_frequencies(dh if dh != 72 else 64, device=DEV)
+    x = rand(steps, B, T, H + 2 * Hkv, dh, seed=5, dtype=dt)
+    width = -(-(80 + steps * T + page) // page)
+    P0 = h.kp.shape[0]
+
+    def run(wait):
+        kp, vp = (torch.cat([p, torch.full((B * width,) + p.shape[1:], math.nan, dtype=dt, device=DEV)]) for p in (h.kp, h.vp))
+        table = torch.full((B, width), -1, dtype=torch.int32, device=DEV)
+        held = h.table[:, :6]   # of at most 75 keys; what is behind a sequence's own is rubbish
+        table[:, :6] = torch.where((held < P0) & (page * torch.arange(6, device=DEV) < h.kv_lens[:, None]), held, -1)
+        lens, q, outs = h.kv_lens.clone(), torch.empty(B, T, H, dh, dtype=dt, device=DEV), []
+        torch.cuda.synchronize()
+        for i in range(steps):
+            sync = torch.cuda.synchronize if wait else (lambda: None)
+            starts = lens.clone()
+            lens += T
+            for j in range(width):   # a page for each slot that starts to be used
+                table[:, j] = torch.where((table[:, j] < 0) & (lens > j * page), P0 + j + width * torch.arange(B, device=DEV), table[:, j]).int()
+            sync()
+            a = x[i]
+            api.cache_append(a[:, :, H:H + Hkv], a[:, :, H + Hkv:], kp, vp, table, starts, q=a[:, :, :H], frequencies=f, q_out=q)
+            sync()
+            o = api.paged_attention(q, kp, vp, table, lens, prefix_table=h.prefix_table, prefix_lens=h.prefix_lens)
+            sync()
+            x2 = o + 0   # an ordinary kernel between
+            outs.append(api.paged_attention(x2, kp, vp, table, lens, prefix_table=h.prefix_table, prefix_lens=h.prefix_lens, out=o))
+            sync()
+        torch.cuda.synchronize()
+        return outs, kp, vp
+
+    ref, rk, rv = run(True)
+    assert all(torch.isfinite(o).all() for o in ref)
+    for _ in range(3):
+        got, gk, gv = run(False)
+        assert all(same(a, b) for a, b in zip(got, ref)) and same(gk, rk) and same(gv, rv)
