@@ -579,7 +579,13 @@ int vit_cache_append(const void* k, const int64_t* k_strides, const void* v, con
  * (their sum is not), with pages of a multiple of 16 tokens and 16-byte aligned rows: own keys with dh a multiple of 8 up
  * to 128 where a key head has at most 16 query rows (Tq G); more rows, and prefixes, with dh 64, 80, 96 or 128 and
  * positive scales, up to 2^22 keys (prefixes of few rows 2^26). F32 has a kernel for dh a multiple of 4 up to 128, pages of a
- * multiple of 8 and aligned rows. A generic one takes everything else, a few times slower. dh up to 512.
+ * multiple of 8 and aligned rows. A generic one takes everything else: for few rows some five times slower (fp32, pages of 20), for many
+ * rows of bf16 twenty to eighty times (3.6 to 5.4 TFLOP/s). dh up to 512.
+ * How a call is cut along the keys follows the room in the tables (pages of a row), as lengths are on the device. Parts of many rows go
+ * through scratch from the library's pool, fp32 rows for each part of up to 32, whatever the lengths: tables with room for
+ * many times what is held cost time and memory (4 x 2048 queries of 16 heads of 128: none at room for 10,000 keys, 325 MiB and a fifth
+ * more time at 164,000, 715 MiB and 1.6 times the time at 1.3 million), and VIT_ERR_NOMEM where that is not to be had. Keep them
+ * near the longest length. vit_paged_attention_plan says what a call takes.
  * Errors: VIT_ERR_ARG, VIT_ERR_DTYPE, VIT_ERR_UNSUPPORTED (dh), VIT_ERR_NOMEM, VIT_ERR_CUDA.
  */
 int vit_paged_attention(const void* q, const int64_t* q_strides, const vit_paged_cache* cache, const int32_t* table,

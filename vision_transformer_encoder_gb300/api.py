@@ -640,7 +640,8 @@ def paged_attention(q, k_pages, v_pages, page_table, kv_lens, q_lens=None, prefi
     page_table: (B, table_pages) int32; keys on absent pages (entries outside [0, pages)) are not seen.
     prefix_table (groups, prefix_pages) and prefix_lens (groups), int32: keys in front of all those, the same for the
     B / groups sequences of a group (the first B / groups sequences are the first group), read for many of
-    their rows at once. A row that sees nothing is zeros. scale: 1 / sqrt(dh) by default."""
+    their rows at once. A row that sees nothing is zeros. scale: 1 / sqrt(dh) by default.
+    Results do not depend on how wide the tables are, time and scratch memory do: keep them near the longest length."""
     fn = (_native or _serving()).paged_attention
     if scale is None:
         scale = (q.shape[-1] or 1) ** -0.5

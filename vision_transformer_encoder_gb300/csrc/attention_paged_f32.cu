@@ -4,7 +4,7 @@
 // Bound by reading keys and values once for every four rows. A warp takes up to four rows (NR) of one key head, of a sequence or for a
 // prefix of all its group's, and 8 keys, which lie in one page, at
 // a time: its lanes hold VEC columns each, so that a key is one coalesced load, and all 16 loads of a step are in flight
-// together, those of the next step behind them. The 8 NR products' halves are added across the lanes while they are
+// together; those of the next step, into the same registers, are asked for when its products are done, its pages two steps ahead. The 8 NR products' halves are added across the lanes while they are
 // handed out, so that each lane ends up with whole scores of its own: 31 exchanges for 32 scores. fp32 throughout, O in
 // registers. The warps of a CTA take every fourth step of its part of the keys and join in shared memory; parts are
 // joined as in attention_paged.cu. 8 sequences of up to 577 keys behind 197, 12 heads of 64: 10.9 us, two launches of latencies;

@@ -520,7 +520,9 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     }
 }
 
-// Clusters of Z CTAs, an SM to each, that run at once (of the first device asked about).
+// Clusters of Z CTAs, an SM to each, that run at once: asked once, of the first device that calls and of the instance for width 128
+// and eight rows, whose shared memory leaves room for one CTA to an SM. The others are given an SM to each CTA as well. Another
+// device, or a part of one, may run fewer at once and be slower for it; the results do not depend on it but for their rounding.
 int clusters_at_once(int Z) {
     static std::atomic<int> known[PR_MAXZ + 1];   // one more than that
     int n = known[Z].load(std::memory_order_relaxed);

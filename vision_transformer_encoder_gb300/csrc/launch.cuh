@@ -2,11 +2,19 @@
 //
 // A kernel launched here may start its CTAs while the previous kernel in the stream is
 // still running (CUDA's programmatic stream serialisation). Every kernel launched this way
-// calls griddep_wait() (common.cuh) in every CTA before its first access to global memory, which
-// blocks until the previous grid has completed and its writes are visible; its own setup
-// (barrier initialisation, tensor-memory allocation, tensor-map prefetch) runs before that
-// and overlaps the previous kernel's last CTAs. Because each such kernel waits for its
-// predecessor before it can complete, the ordering is transitive along the stream.
+// calls griddep_wait() (common.cuh) in every CTA, which blocks until the previous grid has
+// completed and its writes are visible; its own setup (barrier initialisation, tensor-memory
+// allocation, tensor-map prefetch) runs before that and overlaps the previous kernel's last CTAs.
+// Because each such kernel waits for its predecessor before it can complete, the ordering is
+// transitive along the stream.
+// In front of the wait a kernel writes no global memory and uses none that it reads, with two exceptions, both in paged
+// attention:
+//  - attention_paged_rows.cu and attention_paged_tc.cu prefetch to L2 there, by lengths and page entries that may still change:
+//    bounds are checked, nothing of it is used, and all is read again behind the wait.
+//  - attention_paged_rows.cu behind a prefix reads lengths, tables, queries and own keys before it waits. The grid in front of it
+//    is the prefix's, of the same call, which writes scratch alone and lets dependents start only behind its own wait: what those
+//    reads need was complete by then. Its wait, for the prefix's parts, stands before its first store.
+// A kernel that lets dependents start (griddep_launch_dependents) does so behind its own wait.
 // VIT_PDL=0 launches without the attribute (plain stream order).
 #pragma once
 
