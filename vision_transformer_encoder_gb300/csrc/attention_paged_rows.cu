@@ -14,7 +14,9 @@
 //
 // Rings and products are those of attention_cross_rows.cu: mma.m16n8k16 with the query rows as the n side,
 // S^T = K Q^T and O^T = V^T P^T, K and V by TMA into a ring of each warp's own. Weights are rounded to bf16 for the second
-// product (their sum is not).
+// product, whose operands have one type, V's (their sum is not rounded): outputs are off by 2.3e-3 in the 2-norm where their own rounding
+// alone leaves 1.7e-3. Weights as two numbers of bf16 would take that back at twice the second product. Exponentials are the
+// hardware's, good to 2^-22, where a weight then keeps 2^-8.
 //
 // A query does not see later tokens, but the product adds their values times weights of zero. Where such a value is
 // not finite, the tile is multiplied once per token with what that token does not see cleared.
